@@ -19,7 +19,17 @@ import ctypes
 import os
 import threading
 
+from . import _latent_abi
 from ._build import LIB_PATH, build
+
+
+def __getattr__(name: str):
+    # The latent-cache operators import torch when first used, as the functions below do.
+    if name in ("latent_append", "latent_attend_selected", "latent_attend_paged", "latent_workspace"):
+        from . import latent
+        value = globals()[name] = getattr(latent, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 TOKEN = 0
 BLOCK8 = 1
@@ -97,6 +107,7 @@ def load(path: str | None = None):
         lib.topk_bf16_plan.restype = ctypes.c_int
         lib.topk_bf16_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]
         lib.topk_bf16_device_status.restype = ctypes.c_int
+        _latent_abi.declare(lib)
         if path is None:
             _lib = lib
         return lib

@@ -14,6 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 HEADER = os.path.join(ROOT, "include", "topk_bf16.h")
+LATENT_HEADER = os.path.join(ROOT, "include", "latent_bf16.h")
 LIB_PATH = os.path.join(PKG, "libtopk_bf16.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -26,7 +27,7 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return [*sources(), *glob.glob(os.path.join(CSRC, "*.cuh")), *glob.glob(os.path.join(CSRC, "*.h")),
-            HEADER, __file__]
+            HEADER, LATENT_HEADER, __file__]
 
 
 def _nvcc() -> str:
