@@ -49,6 +49,7 @@ topk_status_t check_attend(const latent_bf16_attend_t *a, bool paged) {
     if (!a || a->tokens < 0 || a->cache_rows < 0) return TOPK_ERR_ARG;
     if (bad_latent(a->latent)) return TOPK_ERR_WIDTH;
     if (a->heads < 1 || a->heads > LATENT_MAX_HEADS || !std::isfinite(a->scale)) return TOPK_ERR_ARG;
+    if (static_cast<int64_t>(a->tokens) * a->heads > INT32_MAX) return TOPK_ERR_ARG;
     if (paged) {
         if (a->width < 0) return TOPK_ERR_WIDTH;
         if (a->page_size < 1 || (a->page_size & (a->page_size - 1)) || a->block_rows < a->page_size ||
@@ -69,7 +70,9 @@ topk_status_t check_attend(const latent_bf16_attend_t *a, bool paged) {
         off4(a->selected) || off4(a->valid_len) || off4(a->block_table))
         return TOPK_ERR_ALIGN;
     if ((a->cache_stride | a->query_token_stride | a->query_head_stride) & 7) return TOPK_ERR_ALIGN;
-    if (a->workspace_bytes < latent_bf16_workspace_bytes()) return TOPK_ERR_ARG;
+    const int64_t need = workspace_bytes();
+    if (need <= 0) return TOPK_ERR_CUDA;
+    if (a->workspace_bytes < need) return TOPK_ERR_ARG;
     return TOPK_OK;
 }
 
@@ -101,6 +104,7 @@ topk_status_t attend(const latent_bf16_attend_t *a, bool paged, void *stream) {
     p.block_rows = a->block_rows;
     p.rows_per_request = paged ? a->rows_per_request : 1;
     p.scale = a->scale;
+    p.workspace = a->workspace;
     return launch_attend(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TOPK_OK : TOPK_ERR_CUDA;
 }
 
@@ -129,6 +133,6 @@ topk_status_t latent_bf16_attend_paged(const latent_bf16_attend_t *args, void *s
     return topk::latent::attend(args, true, stream);
 }
 
-int64_t latent_bf16_workspace_bytes(void) { return 256; }
+int64_t latent_bf16_workspace_bytes(void) { return topk::latent::workspace_bytes(); }
 
 }  // extern "C"

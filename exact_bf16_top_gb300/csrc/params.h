@@ -86,5 +86,8 @@ cudaError_t status_stream(uint32_t *v, bool clear);
 cudaError_t status_direct(uint32_t *v, bool clear);
 cudaError_t status_one(uint32_t *v, bool clear);
 cudaError_t status_ordered(uint32_t *v, bool clear);
+namespace latent {
+cudaError_t status_attend(uint32_t *v, bool clear);   // latent_attend.cu
+}
 
 }  // namespace topk
