@@ -1,8 +1,6 @@
 // Attention over latent cache rows on the tensor cores: one persistent kernel
 // for both forms, and the kernel that joins the parts of split tiles.
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <mutex>
@@ -14,13 +12,16 @@ namespace topk::latent {
 
 namespace {
 
-constexpr int NT = 256;
+constexpr int SOFT = 128;                    // warps 0 to 3: softmax and outputs
+constexpr int LOAD = 128;                    // warps 4 to 7: cache rows
+constexpr int QLOAD = 64;                    // warps 8 and 9: query rows
+constexpr int NT = SOFT + LOAD + QLOAD + 32; // warp 10: the tensor cores
+constexpr int NT_JOIN = 256;
 constexpr int ROWS = 64;                     // query rows of a tile
 constexpr int KEYS = 64;                     // cache rows of a block
 constexpr int CHUNK = 64 * 128;              // bytes of 64 rows of 64 values
 constexpr int CHUNKS = 27;                   // chunks of shared memory: the query's and the stages'
 constexpr int MAX_STAGES = 4;
-constexpr int SOFT = 128;                    // threads of the softmax warps (4 to 7)
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: output (4 x NR), scores (2 x 64)
 constexpr float LAZY = 8.0f;                 // the reference maximum may lag by this much (log2)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -32,7 +33,6 @@ struct Ctrl {
     u64 p_full, o_done;                        // a block's weights are in / its product is added
     u64 q_full, q_empty;                       // the query tile is in / used up
     u64 drain;
-    u64 mask[MAX_STAGES];                      // which rows of the stage hold a cache row
     u64 bad;
     long long sums[NT / 32];
     int32_t first_tile, first_block;
@@ -40,6 +40,7 @@ struct Ctrl {
     uint32_t tmem;
     volatile uint32_t abort;
     float factor[ROWS], m[ROWS], l[ROWS];
+    uint8_t there[MAX_STAGES][KEYS];           // which rows of the stage hold a cache row
 };
 
 constexpr int SMEM = CHUNKS * CHUNK + static_cast<int>(sizeof(Ctrl)) + 1024;
@@ -132,13 +133,14 @@ __device__ __forceinline__ void tc_store16(uint32_t addr, const float (&v)[16]) 
         : "memory");
 }
 
-// Four cache rows' 64 values at column x, by row number (one past the last: zeros).
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap *map, int x, int4 rows, u64 *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_addr(bar))
-        : "memory");
+// 16 bytes from global to shared memory, or zeros (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+// An arrival on `bar` once this thread's copies so far are done.
+__device__ __forceinline__ void copies_arrive(u64 *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -293,12 +295,15 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
 
 // ------------------------------------------------------------------ the warps' parts
 
-// Cache rows into the stages, gathered four at a time by row number; entries
-// that hold no cache row are filled with zeros and masked.
-__device__ void load_rows(const AttendParams &p, const CUtensorMap *map, Ctrl &c, uint32_t stages, int chunks,
-                          int stage_count) {
-    const int lane = threadIdx.x & 31;
-    const int32_t none = max(p.cache_rows, 1);
+// Cache rows into the stages, swizzled as the products read them. Eight threads
+// copy a row's 128-byte chunks, 16 rows at a time; places that hold no cache
+// row are filled with zeros and marked. (Measured: the same rows gathered four
+// at a time by TMA come at 12 bytes a nanosecond per SM, a third of what these
+// copies reach.)
+__device__ void load_rows(const AttendParams &p, Ctrl &c, uint32_t stages, int chunks, int stage_count) {
+    const int tid = threadIdx.x - SOFT, lane = tid & 31, piece = tid & 7, r = tid >> 3;
+    const int64_t pitch = p.cache_stride * 2;
+    const char *cache = reinterpret_cast<const char *>(p.cache) + piece * 16;
     Cursor at(c);
     uint32_t st = 0, use = 0;
     bool ok = true;
@@ -306,58 +311,43 @@ __device__ void load_rows(const AttendParams &p, const CUtensorMap *map, Ctrl &c
         const int32_t *list = p.paged ? p.table + static_cast<int64_t>(at.tile.request) * p.table_stride
                                       : p.selected + static_cast<int64_t>(at.tile.token) * p.selected_stride;
         auto row = [&](int32_t i) -> int32_t {
-            if (i >= at.len) return none;
-            int64_t r;
+            if (i >= at.len) return -1;
+            int64_t v;
             if (p.paged)
-                r = static_cast<int64_t>(__ldg(list + (i >> p.page_shift))) * p.block_rows +
+                v = static_cast<int64_t>(__ldg(list + (i >> p.page_shift))) * p.block_rows +
                     (i & ((1 << p.page_shift) - 1));
             else
-                r = __ldg(list + i);
-            return r >= 0 && r < p.cache_rows ? static_cast<int32_t>(r) : none;
+                v = __ldg(list + i);
+            return v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
         };
-        int32_t r0 = row(at.b0 * KEYS + lane), r1 = row(at.b0 * KEYS + 32 + lane);
+        int32_t now[4], then[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) now[i] = row(at.b0 * KEYS + r + 16 * i);
         for (int32_t b = at.b0; b < at.b1; ++b) {
-            int32_t n0 = none, n1 = none;
             if (b + 1 < at.b1) {
-                n0 = row((b + 1) * KEYS + lane);
-                n1 = row((b + 1) * KEYS + 32 + lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) then[i] = row((b + 1) * KEYS + r + 16 * i);
             }
-            const u64 mask = static_cast<u64>(__ballot_sync(0xFFFFFFFFu, r0 < p.cache_rows)) |
-                             static_cast<u64>(__ballot_sync(0xFFFFFFFFu, r1 < p.cache_rows)) << 32;
             if (!(ok = wait(&c.empty[st], use + 1, c))) break;
-            if (lane == 0) {
-                c.mask[st] = mask;
-                mbar_expect_tx(&c.full[st], static_cast<uint32_t>(chunks) * CHUNK);
-            }
-            __syncwarp();
-            const int group = lane & 15, from = 4 * (group & 7);
-            int4 rows;
-            int32_t *rr = &rows.x;
+            const uint32_t stage = stages + st * chunks * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int32_t lo = __shfl_sync(0xFFFFFFFFu, r0, from + i), hi = __shfl_sync(0xFFFFFFFFu, r1, from + i);
-                rr[i] = group < 8 ? lo : hi;
+                const bool on = now[i] >= 0;
+                const char *src = cache + (on ? now[i] * pitch : 0);
+                for (int k = 0; k < chunks; ++k) copy16(stage + i * 16 * 128 + k * CHUNK, src + k * 128, on);
+                if (piece == 0) c.there[st][r + 16 * i] = on ? 1 : 0;
+                now[i] = then[i];
             }
-            const uint32_t dst = stages + st * chunks * CHUNK + group * 512;
-            for (int k = lane >> 4; k < chunks; k += 2) gather4(dst + k * CHUNK, map, k * 64, rows, &c.full[st]);
-            r0 = n0;
-            r1 = n1;
+            copies_arrive(&c.full[st]);
+            __syncwarp();
+            if (lane == 0) arrive(&c.full[st]);
             if (++st == static_cast<uint32_t>(stage_count)) {
                 st = 0;
                 ++use;
             }
         }
     }
-    // Nothing may be in flight into shared memory when the CTA ends: after a
-    // wait that gave up, wait (with its own limit) for the copies still out.
-    if (!ok) {
-        const uint64_t t0 = global_timer_ns();
-        for (int s = 0; s < stage_count; ++s) {
-            const uint32_t uses = use + (s < static_cast<int>(st) ? 1u : 0u);
-            while (uses > 0 && !mbar_try_wait(&c.full[s], (uses - 1) & 1u) && global_timer_ns() - t0 < WAIT_LIMIT_NS) {
-            }
-        }
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // The products: scores of block i, then the weighted sum of block i - 1, so
@@ -400,6 +390,7 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, uint32_t query, uint32_
                 if (!(ok = wait(&c.q_full, piece, c))) break;
             }
             if (!(ok = wait(&c.full[st], use, c))) break;
+            fence_proxy_async();              // (the stage was written by ordinary copies)
             if (!(ok = wait(&c.s_empty[i & 1], (i >> 1) + 1, c))) break;
             tc_fence_after();
             if (lane == 0) {
@@ -438,17 +429,17 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, uint32_t query, uint32_
 // Rows past the tile's are left as they are: every row is apart in scores,
 // weights and sums, and nothing is written for those.
 __device__ void load_query(const AttendParams &p, Ctrl &c, char *query, int chunks) {
-    const int tid = threadIdx.x - 64, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x - SOFT - LOAD, lane = threadIdx.x & 31;
     Cursor at(c);
     uint32_t piece = 0;
     while (at.next(p, lane)) {
         if (!wait(&c.q_empty, piece + 1, c)) return;
         const int vecs = chunks * 8, n = at.tile.rows * vecs;
-        for (int i0 = tid; i0 < n; i0 += 64 * 8) {
+        for (int i0 = tid; i0 < n; i0 += QLOAD * 8) {
             uint4 v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int i = i0 + e * 64;
+                const int i = i0 + e * QLOAD;
                 if (i < n) {
                     const int r = i / vecs, k = i - r * vecs;
                     const int32_t flat = at.tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
@@ -458,7 +449,7 @@ __device__ void load_query(const AttendParams &p, Ctrl &c, char *query, int chun
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int i = i0 + e * 64;
+                const int i = i0 + e * QLOAD;
                 if (i < n) {
                     const int r = i / vecs, k = i - r * vecs;
                     *reinterpret_cast<uint4 *>(query + (k >> 3) * CHUNK + r * 128 + (((k & 7) ^ (r & 7)) << 4)) = v[e];
@@ -487,7 +478,7 @@ __device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f :
 // warp w holds rows 16 w + t / 4 and 8 further, a quarter of each one's columns.
 template <int NR>
 __device__ void soften(const AttendParams &p, Ctrl &c, char *stages, int chunks, int stage_count, uint32_t tmem) {
-    const int tid = threadIdx.x - (NT - SOFT), lane = tid & 31, w = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const bool active = w * 16 < NR;
     const int row0 = w * 16 + lane / 4, quad = lane & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
@@ -513,7 +504,8 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *stages, int chunks,
             mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
             mbar_wait(&c.full[st], use & 1u, &c.abort);   // (complete: makes the mask visible)
             __syncwarp();
-            const u64 mask = c.mask[st];
+            const u64 mask = static_cast<u64>(__ballot_sync(0xFFFFFFFFu, c.there[st][lane] != 0)) |
+                             static_cast<u64>(__ballot_sync(0xFFFFFFFFu, c.there[st][lane + 32] != 0)) << 32;
             float x[32];
             if (active) {
                 tc_fence_after();
@@ -706,8 +698,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *stages, int chunks,
 }
 
 template <int NR>
-__global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ AttendParams p,
-                                                       const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ AttendParams p) {
     extern __shared__ char raw[];
     char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     Ctrl &c = *reinterpret_cast<Ctrl *>(smem + CHUNKS * CHUNK);
@@ -716,7 +707,7 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     const int stage_count = min(MAX_STAGES, (CHUNKS - chunks) / chunks);
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_STAGES; ++s) {
-            mbar_init(&c.full[s], 1);
+            mbar_init(&c.full[s], LOAD + LOAD / 32);
             mbar_init(&c.empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -725,14 +716,14 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
         }
         mbar_init(&c.p_full, SOFT / 32);
         mbar_init(&c.o_done, 1);
-        mbar_init(&c.q_full, 64);
+        mbar_init(&c.q_full, QLOAD);
         mbar_init(&c.q_empty, 1);
         mbar_init(&c.drain, 1);
         c.bad = 0;
         c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == NT / 32 - 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&c.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -745,14 +736,14 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     char *stages = smem + chunks * CHUNK;
-    if (warp == 0) load_rows(p, &map, c, smem_addr(stages), chunks, stage_count);
-    else if (warp == 1) multiply<NR>(p, c, smem_addr(smem), smem_addr(stages), chunks, stage_count, tmem);
-    else if (warp < 4) load_query(p, c, smem, chunks);
-    else soften<NR>(p, c, stages, chunks, stage_count, tmem);
+    if (warp < SOFT / 32) soften<NR>(p, c, stages, chunks, stage_count, tmem);
+    else if (warp < (SOFT + LOAD) / 32) load_rows(p, c, smem_addr(stages), chunks, stage_count);
+    else if (warp < (SOFT + LOAD + QLOAD) / 32) load_query(p, c, smem, chunks);
+    else multiply<NR>(p, c, smem_addr(smem), smem_addr(stages), chunks, stage_count, tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == NT / 32 - 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
@@ -761,9 +752,9 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
 // Joins a split tile's parts, one CTA per row: each part's sum weighs
 // 2^(its maximum - the largest). Parts are added in order: results do not
 // depend on which CTA finished first.
-__global__ void __launch_bounds__(NT) join_kernel(const __grid_constant__ AttendParams p) {
-    __shared__ float weight[512], red[NT / 32];
-    __shared__ __align__(16) float partial[NT * 4];
+__global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ AttendParams p) {
+    __shared__ float weight[512], red[NT_JOIN / 32];
+    __shared__ __align__(16) float partial[NT_JOIN * 4];
     grid_dependents_release();
     grid_dependency_wait();
     const Part *parts = reinterpret_cast<const Part *>(p.workspace);
@@ -774,17 +765,17 @@ __global__ void __launch_bounds__(NT) join_kernel(const __grid_constant__ Attend
     if (row >= t.rows) return;
     auto part = [&](int i) -> const Part & { return parts[2 * (j.cta + i) + (i == 0 ? 1 : 0)]; };
     float mine = -INFINITY;
-    for (int i = tid; i < j.parts; i += NT) mine = fmaxf(mine, part(i).m[row]);
+    for (int i = tid; i < j.parts; i += NT_JOIN) mine = fmaxf(mine, part(i).m[row]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mine = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
     if ((tid & 31) == 0) red[tid >> 5] = mine;
     __syncthreads();
     float top = red[0];
 #pragma unroll
-    for (int i = 1; i < NT / 32; ++i) top = fmaxf(top, red[i]);
+    for (int i = 1; i < NT_JOIN / 32; ++i) top = fmaxf(top, red[i]);
     __syncthreads();
     float sum = 0.0f;
-    for (int i = tid; i < j.parts; i += NT) {
+    for (int i = tid; i < j.parts; i += NT_JOIN) {
         const float m = part(i).m[row];
         const float f = m == -INFINITY ? 0.0f : exp2_fast(m - top);
         weight[i] = f;
@@ -796,8 +787,8 @@ __global__ void __launch_bounds__(NT) join_kernel(const __grid_constant__ Attend
     __syncthreads();
     float l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) l += red[i];
-    const int vecs = p.latent / 4, groups = NT / vecs, g = tid / vecs, v = tid - g * vecs;
+    for (int i = 0; i < NT_JOIN / 32; ++i) l += red[i];
+    const int vecs = p.latent / 4, groups = NT_JOIN / vecs, g = tid / vecs, v = tid - g * vecs;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (g < groups) {
 #pragma unroll 8
@@ -841,7 +832,6 @@ struct Device {
     std::once_flag once;
     cudaError_t err = cudaSuccess;
     int sms = 0;
-    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 Device g_device[64];
 
@@ -860,12 +850,6 @@ cudaError_t device(Device *&out) {
         cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
         for (const void *fn : {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()})
             if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        cudaDriverEntryPointQueryResult found;
-        void *f = nullptr;
-        if (e == cudaSuccess)
-            e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
-        if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !f)) e = cudaErrorNotSupported;
-        d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
         if (e == cudaSuccess && d.sms > 512) e = cudaErrorNotSupported;   // (join_kernel's weights)
         d.err = e;
     });
@@ -899,18 +883,6 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     const int64_t rows = full > 0 ? per : rest;
     const int nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 
-    CUtensorMap map;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.latent + LATENT_ROPE),
-                                static_cast<cuuint64_t>(p.cache_rows > 0 ? p.cache_rows : 1)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.cache_stride) * 2};
-    const cuuint32_t box[2] = {64, 1}, steps[2] = {1, 1};
-    // (With an empty cache nothing is read: any address will do.)
-    void *base = const_cast<uint16_t *>(p.cache_rows > 0 ? p.cache : p.query);
-    if (d->encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -921,9 +893,10 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void *args[] = {&p, &map};
+    void *args[] = {&p};
     e = cudaLaunchKernelExC(&cfg, nr == 16 ? attend_fn<16>() : nr == 32 ? attend_fn<32>() : attend_fn<64>(), args);
     if (e != cudaSuccess || most_blocks <= 1) return e;   // tiles of one block are never split
+    cfg.blockDim = dim3(NT_JOIN, 1, 1);
     cfg.gridDim = dim3(static_cast<unsigned>(p.tiles < static_cast<int32_t>(grid) ? p.tiles : grid),
                        static_cast<unsigned>(nr), 1);
     cfg.dynamicSmemBytes = 0;
