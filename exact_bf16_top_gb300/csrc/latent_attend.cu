@@ -18,32 +18,57 @@ constexpr int QLOAD = 64;                    // warps 8 and 9: query rows
 constexpr int NT = SOFT + LOAD + QLOAD + 32; // warp 10: the tensor cores
 constexpr int NT_JOIN = 256;
 constexpr int ROWS = 64;                     // query rows of a tile
-constexpr int KEYS = 64;                     // cache rows of a block
-constexpr int CHUNK = 64 * 128;              // bytes of 64 rows of 64 values
-constexpr int CHUNKS = 27;                   // chunks of shared memory: the query's and the stages'
-constexpr int MAX_STAGES = 4;
-constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: output (4 x NR), scores (2 x 64)
-constexpr float LAZY = 8.0f;                 // the reference maximum may lag by this much (log2)
+constexpr int KEYS = 128;                    // cache rows of a block
+constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
+constexpr int MAX_SLOTS = 6;                 // most slots of either ring
+constexpr int ROW_SETS = 8;                  // blocks whose row numbers are kept
+constexpr int SMEM = 232448;                 // all of a CTA's shared memory
+constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
+constexpr float LAZY = 60.0f;                // the reference may lag the maximum by this much (log2)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 using u64 = unsigned long long;
 
 struct Ctrl {
-    u64 full[MAX_STAGES], empty[MAX_STAGES];   // a stage's rows are in / its values are used up
+    u64 full[2][MAX_SLOTS], empty[2][MAX_SLOTS];   // a slot's rows are in / used up; [0] pairs, [1] ropes
     u64 s_full[2], s_empty[2];                 // scores written / read
-    u64 p_full, o_done;                        // a block's weights are in / its product is added
+    u64 p_full[2], o_done[2];                  // a block's weights are in / its sums are added (by turns: who
+                                               // waits for block i - 1 may meet block i's, and two phases of one
+                                               // barrier look like none)
     u64 q_full, q_empty;                       // the query tile is in / used up
     u64 drain;
-    u64 bad;
     long long sums[NT / 32];
     int32_t first_tile, first_block;
     long long begin, share, total;
     uint32_t tmem;
     volatile uint32_t abort;
-    float factor[ROWS], m[ROWS], l[ROWS];
-    uint8_t there[MAX_STAGES][KEYS];           // which rows of the stage hold a cache row
+    alignas(16) float ref[ROWS];               // reference maximum (log2); +inf: a row that sees nothing here
+    alignas(16) float factor[ROWS];
+    float l[ROWS];
+    int32_t lim[ROWS];                         // tokens a row may see
+    float across[4][ROWS];
+    int32_t rows[ROW_SETS][KEYS];              // cache row numbers of a block, -1: none
 };
 
-constexpr int SMEM = CHUNKS * CHUNK + static_cast<int>(sizeof(Ctrl)) + 1024;
+// Shared memory: the query tile (chunks of 64 values, NR rows of 128 bytes
+// each), a ring of pairs of latent chunks, a ring of rotary chunks (where a
+// block's weights go once its scores are out), the control block.
+struct Plan {
+    int pairs, pair_slots, rope_slots, ahead;  // pairs per block; slots; units of the next block loadable ahead
+    uint32_t query_bytes;
+};
+
+template <int NR>
+__device__ __forceinline__ Plan make_plan(int latent) {
+    Plan r;
+    r.pairs = latent / 128;
+    r.query_bytes = (2 * r.pairs + 1) * NR * 128;
+    const int units = static_cast<int>((SMEM - 1024 - sizeof(Ctrl) - r.query_bytes) / CHUNK);
+    r.rope_slots = max(1, units / (2 * r.pairs + 1));
+    r.pair_slots = min(MAX_SLOTS, (units - r.rope_slots) / 2);
+    r.rope_slots = min(MAX_SLOTS, units - 2 * r.pair_slots);
+    r.ahead = r.pair_slots >= 2 * r.pairs && r.rope_slots >= 2 ? r.pairs + 1 : min(r.pairs, r.pair_slots - r.pairs);
+    return r;
+}
 
 __device__ __forceinline__ void arrive(u64 *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -60,6 +85,13 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 
 __device__ __forceinline__ void tc_commit(u64 *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -82,30 +114,11 @@ __device__ __forceinline__ uint64_t matrix(uint32_t addr, uint32_t lead) {
            (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: BF16 x BF16 -> FP32, M x N; a_major: A is stored with
-// its rows' dimension contiguous.
-__host__ __device__ constexpr uint32_t instruction(int m, int n, bool a_major) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (a_major ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+// Instruction descriptor: BF16 x BF16 -> FP32, M x N; `along`: both operands are
+// stored with the summed dimension across rows (else along them).
+__host__ __device__ constexpr uint32_t instruction(int m, int n, bool along) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (along ? 3u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// 64 columns of 16 lanes: thread t gets of every group of 8 columns j the
-// values of row t / 4 (v[4 j], v[4 j + 1]) and row t / 4 + 8 (v[4 j + 2], v[4 j + 3])
-// at columns 8 j + 2 (t % 4) and the next.
-__device__ __forceinline__ void tc_load_scores(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-        "%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-    tc_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 16 columns of this warp's 32 lanes, one lane per thread.
@@ -295,130 +308,171 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
 
 // ------------------------------------------------------------------ the warps' parts
 
-// Cache rows into the stages, swizzled as the products read them. Eight threads
-// copy a row's 128-byte chunks, 16 rows at a time; places that hold no cache
-// row are filled with zeros and marked. (Measured: the same rows gathered four
-// at a time by TMA come at 12 bytes a nanosecond per SM, a third of what these
-// copies reach.)
-__device__ void load_rows(const AttendParams &p, Ctrl &c, uint32_t stages, int chunks, int stage_count) {
-    const int tid = threadIdx.x - SOFT, lane = tid & 31, piece = tid & 7, r = tid >> 3;
+// Cache rows into the rings, swizzled as the products read them: 16 threads
+// copy a row's 256 bytes of a pair, 8 a row's 128 rotary bytes. Places that
+// hold no cache row are filled with zeros. (Measured: the same rows gathered
+// four at a time by TMA come at 12 bytes a nanosecond per SM, a third of what
+// these copies reach.)
+__device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t pairs, uint32_t ropes) {
+    const int tid = threadIdx.x - SOFT, lane = tid & 31;
     const int64_t pitch = p.cache_stride * 2;
-    const char *cache = reinterpret_cast<const char *>(p.cache) + piece * 16;
+    const char *cache = reinterpret_cast<const char *>(p.cache);
     Cursor at(c);
-    uint32_t st = 0, use = 0;
-    bool ok = true;
-    while (ok && at.next(p, lane)) {
+    uint32_t i = 0, ps = 0, pu = 0, rs = 0, ru = 0;   // block; pair slot and its use; rope slot and its use
+    // (These warps meet at barriers, so none leaves early: after a wait that gave up,
+    // all go on copying without waiting, inside the same bounds.)
+    while (at.next(p, lane)) {
         const int32_t *list = p.paged ? p.table + static_cast<int64_t>(at.tile.request) * p.table_stride
                                       : p.selected + static_cast<int64_t>(at.tile.token) * p.selected_stride;
-        auto row = [&](int32_t i) -> int32_t {
-            if (i >= at.len) return -1;
+        auto row = [&](int32_t j) -> int32_t {
+            if (j >= at.len) return -1;
             int64_t v;
             if (p.paged)
-                v = static_cast<int64_t>(__ldg(list + (i >> p.page_shift))) * p.block_rows +
-                    (i & ((1 << p.page_shift) - 1));
+                v = static_cast<int64_t>(__ldg(list + (j >> p.page_shift))) * p.block_rows +
+                    (j & ((1 << p.page_shift) - 1));
             else
-                v = __ldg(list + i);
+                v = __ldg(list + j);
             return v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
         };
-        int32_t now[4], then[4];
+        int32_t now = row(at.b0 * KEYS + tid);
+        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+            int32_t *rows = c.rows[i % ROW_SETS];
+            rows[tid] = now;
+            asm volatile("bar.sync 2, %0;" ::"n"(LOAD) : "memory");
+            if (b + 1 < at.b1) now = row((b + 1) * KEYS + tid);
+            {
+                const int piece = tid & 15, r = tid >> 4;
+                const uint32_t dst = (piece >> 3) * CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                for (int u = 0; u < plan.pairs; ++u) {
+                    mbar_wait(&c.empty[0][ps], (pu + 1) & 1u, &c.abort);
+                    const char *src = cache + u * 256 + piece * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) now[i] = row(at.b0 * KEYS + r + 16 * i);
-        for (int32_t b = at.b0; b < at.b1; ++b) {
-            if (b + 1 < at.b1) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) then[i] = row((b + 1) * KEYS + r + 16 * i);
+                    for (int k = 0; k < KEYS / 8; ++k) {
+                        const int32_t v = rows[r + 8 * k];
+                        copy16(pairs + ps * 2 * CHUNK + dst + k * 1024, src + (v >= 0 ? v * pitch : 0), v >= 0);
+                    }
+                    copies_arrive(&c.full[0][ps]);
+                    if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
+                        ps = 0;
+                        ++pu;
+                    }
+                }
             }
-            if (!(ok = wait(&c.empty[st], use + 1, c))) break;
-            const uint32_t stage = stages + st * chunks * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4);
+            mbar_wait(&c.empty[1][rs], (ru + 1) & 1u, &c.abort);
+            const int piece = tid & 7, r = tid >> 3;
+            const uint32_t dst = ropes + rs * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4);
+            const char *src = cache + plan.pairs * 256 + piece * 16;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool on = now[i] >= 0;
-                const char *src = cache + (on ? now[i] * pitch : 0);
-                for (int k = 0; k < chunks; ++k) copy16(stage + i * 16 * 128 + k * CHUNK, src + k * 128, on);
-                if (piece == 0) c.there[st][r + 16 * i] = on ? 1 : 0;
-                now[i] = then[i];
+            for (int k = 0; k < KEYS / 16; ++k) {
+                const int32_t v = rows[r + 16 * k];
+                copy16(dst + k * 2048, src + (v >= 0 ? v * pitch : 0), v >= 0);
             }
-            copies_arrive(&c.full[st]);
+            copies_arrive(&c.full[1][rs]);
             __syncwarp();
-            if (lane == 0) arrive(&c.full[st]);
-            if (++st == static_cast<uint32_t>(stage_count)) {
-                st = 0;
-                ++use;
+            if (lane == 0) arrive(&c.full[1][rs]);     // (makes the row numbers visible)
+            if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
+                rs = 0;
+                ++ru;
             }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The products: scores of block i, then the weighted sum of block i - 1, so
-// that the tensor cores work while the softmax warps turn scores into weights.
+// The products, both with the cache as the 128-row operand (tokens for the
+// scores, latent values for the sums) and the query rows as columns: the tensor
+// cores take 42 + N / 2 cycles for 128 x N x 16 with both operands in shared
+// memory, so few columns cost little and 64 rows are never half of an operand.
+//   scores[token][row] = sum over chunks of K chunk x Q chunk
+//   sums[value][row]  += V pair (values x tokens) x weights (tokens x rows)
+// Block i's scores start with what its ring slots hold before block i - 1's are
+// given back, then comes block i - 1's sum, then the rest.
 template <int NR>
-__device__ void multiply(const AttendParams &p, Ctrl &c, uint32_t query, uint32_t stages, int chunks, int stage_count,
-                         uint32_t tmem) {
+__device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, uint32_t pairs,
+                         uint32_t ropes, uint32_t tmem) {
     const int lane = threadIdx.x & 31;
-    constexpr uint32_t QK = instruction(ROWS, KEYS, false), PV = instruction(128, NR, true);
-    const int halves = (chunks - 1) / 2;      // 128-value blocks of the latent part
+    constexpr uint32_t QK = instruction(KEYS, NR, false), PV = instruction(128, NR, true);
+    constexpr int QCHUNK = NR * 128;
     Cursor at(c);
-    uint32_t i = 0, st = 0, use = 0, piece = 0;
-    uint32_t prev_st = 0;
-    bool prev_first = true, ok = true;
-    auto sum = [&]() -> bool {                // the weighted sum of block i - 1, in stage prev_st
-        if (!wait(&c.p_full, i - 1, c)) return false;
+    uint32_t i = 0, piece = 0, ps = 0, pu = 0, rs = 0, ru = 0;
+    uint32_t last_ps = 0, last_rs = 0;       // where block i - 1 begins
+    bool first = true, pending = false, ok = true;
+    auto sum = [&]() -> bool {                // of block i - 1
+        pending = false;
+        if (!wait(&c.p_full[(i - 1) & 1], (i - 1) >> 1, c)) return false;
         tc_fence_after();
-        if (lane == 0) {
-            const uint32_t base = stages + prev_st * chunks * CHUNK;
-            const uint64_t b = matrix(base + (chunks - 1) * CHUNK, 16);
-            for (int h = 0; h < halves; ++h) {
-                const uint64_t a = matrix(base + 2 * h * CHUNK, CHUNK);
+        if (elected()) {
+            const uint64_t w = matrix(ropes + last_rs * CHUNK, 16);
+            uint32_t s = last_ps;
+            for (int h = 0; h < plan.pairs; ++h) {
+                const uint64_t v = matrix(pairs + s * 2 * CHUNK, CHUNK);
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k)
-                    tc_mma(tmem + O_COL + h * NR, a + k * (16 * 128 >> 4), b + k * 2, PV, !prev_first || k > 0);
+                    tc_mma(tmem + O_COL + h * NR, v + k * 128, w + k * 128, PV, !first || k > 0);
+                tc_commit(&c.empty[0][s]);
+                if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
             }
-            tc_commit(&c.empty[prev_st]);
-            tc_commit(&c.o_done);
+            tc_commit(&c.empty[1][last_rs]);
+            tc_commit(&c.o_done[(i - 1) & 1]);
         }
         __syncwarp();
         return true;
     };
-    bool pending = false;
     while (ok && at.next(p, lane)) {
-        for (int32_t b = at.b0; b < at.b1; ++b) {
+        for (int32_t b = at.b0; ok && b < at.b1; ++b, ++i) {
             if (b == at.b0) {
-                // A new query tile waits for its loads: finish the last tile's sum first.
+                // A new query tile waits for its loads: finish the last tile's sums first.
                 if (pending && !(ok = sum())) break;
-                pending = false;
                 if (!(ok = wait(&c.q_full, piece, c))) break;
             }
-            if (!(ok = wait(&c.full[st], use, c))) break;
-            fence_proxy_async();              // (the stage was written by ordinary copies)
             if (!(ok = wait(&c.s_empty[i & 1], (i >> 1) + 1, c))) break;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t a = matrix(query, 16), k0 = matrix(stages + st * chunks * CHUNK, 16);
-                for (int k = 0; k < chunks; ++k)
+            const uint32_t this_ps = ps, this_rs = rs, d = tmem + S_COL + (i & 1) * NR;
+            const uint64_t q = matrix(query, 16);
+            for (int u = 0; u <= plan.pairs; ++u) {
+                if (pending && u == plan.ahead && !(ok = sum())) break;
+                const bool rope = u == plan.pairs;
+                if (!(ok = rope ? wait(&c.full[1][rs], ru, c) : wait(&c.full[0][ps], pu, c))) break;
+                fence_proxy_async();          // (the rows were written by ordinary copies)
+                tc_fence_after();
+                if (elected()) {
+                    const uint64_t k = matrix(rope ? ropes + rs * CHUNK : pairs + ps * 2 * CHUNK, 16);
+                    const uint64_t qu = q + u * (2 * QCHUNK >> 4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        tc_mma(tmem + S_COL + (i & 1) * KEYS, a + k * (CHUNK >> 4) + e * 2, k0 + k * (CHUNK >> 4) + e * 2,
-                               QK, k > 0 || e > 0);
+                    for (int e = 0; e < 4; ++e) tc_mma(d, k + e * 2, qu + e * 2, QK, u > 0 || e > 0);
+                    if (!rope) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            tc_mma(d, k + (CHUNK >> 4) + e * 2, qu + (QCHUNK >> 4) + e * 2, QK, true);
+                    }
+                }
+                __syncwarp();
+                if (rope) {
+                    if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
+                        rs = 0;
+                        ++ru;
+                    }
+                } else if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
+                    ps = 0;
+                    ++pu;
+                }
+            }
+            if (!ok) break;
+            if (elected()) {
                 tc_commit(&c.s_full[i & 1]);
                 if (b + 1 == at.b1) tc_commit(&c.q_empty);
             }
             __syncwarp();
             if (pending && !(ok = sum())) break;
             pending = true;
-            prev_st = st;
-            prev_first = b == at.b0;
-            ++i;
-            if (++st == static_cast<uint32_t>(stage_count)) {
-                st = 0;
-                ++use;
-            }
+            last_ps = this_ps;
+            last_rs = this_rs;
+            first = b == at.b0;
         }
         ++piece;
     }
-    if (ok && pending) ok = sum();
+    if (ok && pending) sum();
     // Nothing may be running on the tensor cores when their memory is freed.
-    if (lane == 0) tc_commit(&c.drain);
+    if (elected()) tc_commit(&c.drain);
     __syncwarp();
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&c.drain, 0) && global_timer_ns() - t0 < WAIT_LIMIT_NS) {
@@ -428,37 +482,24 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, uint32_t query, uint32_
 // A tile's query rows into shared memory, swizzled as the products read them.
 // Rows past the tile's are left as they are: every row is apart in scores,
 // weights and sums, and nothing is written for those.
-__device__ void load_query(const AttendParams &p, Ctrl &c, char *query, int chunks) {
+template <int NR>
+__device__ void load_query(const AttendParams &p, Ctrl &c, uint32_t query, int chunks) {
     const int tid = threadIdx.x - SOFT - LOAD, lane = threadIdx.x & 31;
     Cursor at(c);
-    uint32_t piece = 0;
+    uint32_t n = 0;
     while (at.next(p, lane)) {
-        if (!wait(&c.q_empty, piece + 1, c)) return;
-        const int vecs = chunks * 8, n = at.tile.rows * vecs;
-        for (int i0 = tid; i0 < n; i0 += QLOAD * 8) {
-            uint4 v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = i0 + e * QLOAD;
-                if (i < n) {
-                    const int r = i / vecs, k = i - r * vecs;
-                    const int32_t flat = at.tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
-                    v[e] = __ldg(reinterpret_cast<const uint4 *>(p.query + token * p.query_token_stride +
-                                                                 head * p.query_head_stride) + k);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = i0 + e * QLOAD;
-                if (i < n) {
-                    const int r = i / vecs, k = i - r * vecs;
-                    *reinterpret_cast<uint4 *>(query + (k >> 3) * CHUNK + r * 128 + (((k & 7) ^ (r & 7)) << 4)) = v[e];
-                }
-            }
+        if (!wait(&c.q_empty, n + 1, c)) break;
+        const int piece = tid & 7;
+        for (int r = tid >> 3; r < at.tile.rows; r += QLOAD / 8) {
+            const int32_t flat = at.tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
+            const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
+            const uint32_t dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
+            for (int k = 0; k < chunks; ++k) copy16(dst + k * NR * 128, src + k * 64, true);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async();
         arrive(&c.q_full);
-        ++piece;
+        ++n;
     }
 }
 
@@ -472,15 +513,50 @@ struct Joint {                                 // a split tile: where its parts 
 };
 
 __device__ __forceinline__ float finished_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2; }
-__device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }   // NaN stays NaN
+__device__ __forceinline__ float finished(float sum, float l) { return l == 0.0f ? 0.0f : sum / l; }   // NaN stays NaN
 
-// Scores to weights, the running maximum and sum, and the outputs. Thread t of
-// warp w holds rows 16 w + t / 4 and 8 further, a quarter of each one's columns.
+// Combines v[0 .. NR) over the warp's lanes: afterwards lane's v[j] is the
+// whole warp's value `index(lane) + j` (NR / 32 of them; NR = 16: lanes l and
+// l ^ 1 hold the same one).
+template <int N, int O = 16, int SIZE, class Op>
+__device__ __forceinline__ void across_lanes(float (&v)[SIZE], Op op) {
+    if constexpr (O > 0) {
+        constexpr int H = N / 2;
+        if constexpr (H > 0) {
+            const bool up = (threadIdx.x & O) != 0;
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + H], O);
+                v[j] = op(up ? v[j + H] : v[j], other);
+            }
+            across_lanes<H, O / 2>(v, op);
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], O));
+            across_lanes<1, O / 2>(v, op);
+        }
+    }
+}
+
+// The first row whose value across_lanes leaves in this lane.
 template <int NR>
-__device__ void soften(const AttendParams &p, Ctrl &c, char *stages, int chunks, int stage_count, uint32_t tmem) {
+__device__ __forceinline__ int across_index() {
+    const int lane = threadIdx.x & 31;
+    int r = 0;
+#pragma unroll
+    for (int o = 16, n = NR / 2; o && n; o >>= 1, n /= 2) r += lane & o ? n : 0;
+    return r;
+}
+
+// Scores to weights, the running reference and sums, and the outputs. Thread t
+// holds token t of a block against all rows of the tile, so that masks and the
+// weights' layout (tokens x rows, a token's 128 bytes together) are its own,
+// and a row's sum over tokens stays in one register per row until the piece is
+// done. The weights' reference is the maximum of the row's first block; weights
+// may grow to 2^60 before it moves (FP32 sums and BF16 weights lose nothing by
+// that), which is seen from the packed weights and almost never happens.
+template <int NR>
+__device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *pairs, char *ropes, uint32_t tmem) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const bool active = w * 16 < NR;
-    const int row0 = w * 16 + lane / 4, quad = lane & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
     const float scale = p.scale * LOG2E;
     Part *parts = reinterpret_cast<Part *>(p.workspace);
@@ -488,198 +564,212 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *stages, int chunks,
     const bool by_tile = p.tiles <= static_cast<int32_t>(gridDim.x);
     bool split_here = false;
     Cursor at(c);
-    uint32_t i = 0, st = 0, use = 0;
+    uint32_t i = 0, ps = 0, rs = 0, ru = 0;
     long long done = c.begin;
     while (at.next(p, lane)) {
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-        int32_t lim[2] = {0, 0};
+        const int32_t start = at.b0 * KEYS;
+        // A row that sees nothing of this piece has an infinite reference: whatever its
+        // scores, its weights never move it, and its results are written as empty.
+        int32_t low = INT32_MAX;
+        if (tid < ROWS) {
+            int32_t lim = 0;
+            if (tid < at.tile.rows) lim = p.paged ? token_len(p, (at.tile.base + tid) / p.heads) : INT32_MAX;
+            c.lim[tid] = lim;
+            c.ref[tid] = lim > start ? -INFINITY : INFINITY;
+        }
+        soft_sync();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (row0 + 8 * h < at.tile.rows)
-                lim[h] = p.paged ? token_len(p, (at.tile.base + row0 + 8 * h) / p.heads) : INT32_MAX;
-        for (int32_t b = at.b0; b < at.b1; ++b) {
-            char *stage = stages + st * chunks * CHUNK;
+        for (int r = 0; r < ROWS; r += 32) {
+            const int32_t lim = c.lim[r + lane];
+            low = min(low, lim > start ? lim : INT32_MAX);
+        }
+        low = __reduce_min_sync(0xFFFFFFFFu, low);
+        float l[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
             // (These warps meet at barriers, so none leaves early: after a wait that gave
             // up, all go on without waiting, on whatever the memories hold.)
             mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
-            mbar_wait(&c.full[st], use & 1u, &c.abort);   // (complete: makes the mask visible)
+            mbar_wait(&c.full[1][rs], ru & 1u, &c.abort);   // (complete: makes the row numbers visible)
             __syncwarp();
-            const u64 mask = static_cast<u64>(__ballot_sync(0xFFFFFFFFu, c.there[st][lane] != 0)) |
-                             static_cast<u64>(__ballot_sync(0xFFFFFFFFu, c.there[st][lane + 32] != 0)) << 32;
-            float x[32];
-            if (active) {
+            const int32_t token = b * KEYS + tid;
+            const bool there = c.rows[i % ROW_SETS][tid] >= 0;
+            const bool whole = __all_sync(0xFFFFFFFFu, there) && (b + 1) * KEYS <= low;
+            const uint32_t scores = lanes + S_COL + (i & 1) * NR;
+            char *weights = ropes + rs * CHUNK + tid * 128;
+            float x[NR];
+            bool bad = false;
+            // Scores in log2 units; where masked, -inf. A cache row that only some of the
+            // tile's rows see must not reach the others through 0 x inf: where a score that
+            // is masked here is not finite (every row sees a cache row's NaN and infinities
+            // in its score), the cache row is zeroed and the weights of the rows that do
+            // see it are NaN.
+            auto take = [&]() {
                 tc_fence_after();
-                tc_load_scores(lanes + S_COL + (i & 1) * KEYS, x);
+#pragma unroll
+                for (int r = 0; r < NR; r += 16) {
+                    float v[16];
+                    tc_load16(scores + r, v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[r + e] = v[e] * scale;
+                }
                 tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) arrive(&c.s_empty[i & 1]);
-            bool grow[2] = {false, false};
-            float old[2] = {m[0], m[1]};
-            if (active) {
+                if (!whole) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] *= scale;
-            }
-            const bool whole = mask == ~0ull && at.low >= (b + 1) * KEYS && at.tile.rows == NR;
-            if (!whole) {
-                // Keep an entry if its place holds a cache row that this row may see. A
-                // cache row that only some of the tile's rows see must not reach the others
-                // through 0 x inf: where a score that is masked here is not finite (every
-                // row sees its NaN and infinities in its score), the cache row is zeroed and
-                // the weights of the rows that do see it are NaN.
-                const u64 mine = mask >> (2 * quad);
-                u64 bad = 0;
-                uint32_t keep = 0;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int h = (e >> 1) & 1, col = (e >> 2) * 8 + (e & 1);
-                    const bool there = (mine >> col) & 1;
-                    const bool seen = there && b * KEYS + col + 2 * quad < lim[h];
-                    keep |= seen ? 1u << e : 0u;
-                    if (active && there && !seen && lim[h] >= 0 && row0 + 8 * h < at.tile.rows &&
-                        !(fabsf(x[e]) < INFINITY))
-                        bad |= 1ull << (col + 2 * quad);
-                }
-                if (p.paged && soft_any(bad != 0)) {
-                    if (bad) atomicOr(&c.bad, bad);
-                    soft_sync();
-                    const u64 all = c.bad;
-                    const u64 here = all >> (2 * quad);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if ((here >> ((e >> 2) * 8 + (e & 1))) & 1) x[e] = __uint_as_float(0x7FC00000u);
-                    for (int v = tid; v < KEYS * (chunks - 1) * 8; v += SOFT) {
-                        const int r = v / ((chunks - 1) * 8), k = v - r * (chunks - 1) * 8;
-                        if ((all >> r) & 1)
-                            *reinterpret_cast<uint4 *>(stage + (k >> 3) * CHUNK + r * 128 + (k & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                    for (int r = 0; r < NR; ++r) {
+                        const bool seen = there && token < c.lim[r];
+                        bad |= there && !seen && r < at.tile.rows && !(fabsf(x[r]) < INFINITY);
+                        x[r] = seen ? x[r] : -INFINITY;
                     }
-                    soft_sync();
-                    if (tid == 0) c.bad = 0;
-                }
+                    if (bad) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!((keep >> e) & 1)) x[e] = -INFINITY;
-            }
-            if (active) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (((e >> 1) & 1) == h) mx = fmaxf(mx, x[e]);
-                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                    grow[h] = mx > m[h] + LAZY || (m[h] == -INFINITY && mx > m[h]);
-                    if (grow[h]) m[h] = mx;
-                }
-            }
-            // The reference maximum only moves when it lags by more than 2^8 (the weights
-            // then stay below 2^8 and lose nothing): the sums so far are rescaled then.
-            if (b > at.b0 && soft_any(grow[0] || grow[1])) {
-                if (active) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float f = !grow[h] ? 1.0f : old[h] == -INFINITY ? 0.0f : exp2_fast(old[h] - m[h]);
-                        l[h] *= f;
-                        if (quad == 0) c.factor[row0 + 8 * h] = f;
+                        for (int r = 0; r < NR; ++r)
+                            if (there && token < c.lim[r]) x[r] = __uint_as_float(0x7FC00000u);
                     }
+                }
+            };
+            // Weights from scores, rounded once to BF16 for the tensor cores; true if one
+            // outgrew the reference.
+            auto weigh = [&]() -> bool {
+                __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+                for (int g = 0; g < NR / 8; ++g) {
+                    __nv_bfloat162 v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 8 * g + 2 * e;
+                        const float2 ref = *reinterpret_cast<const float2 *>(&c.ref[r]);
+                        x[r] = whole || x[r] != -INFINITY ? exp2_fast(x[r] - ref.x) : 0.0f;
+                        x[r + 1] = whole || x[r + 1] != -INFINITY ? exp2_fast(x[r + 1] - ref.y) : 0.0f;
+                        v[e] = __floats2bfloat162_rn(x[r], x[r + 1]);
+                        top = __hmax2(top, v[e]);
+                    }
+                    *reinterpret_cast<uint4 *>(weights + ((g ^ (tid & 7)) << 4)) = *reinterpret_cast<uint4 *>(v);
+                }
+                return fmaxf(__low2float(top), __high2float(top)) > 1.152921504606846976e18f;   // 2^60
+            };
+            take();
+            bool moved = b == at.b0;
+            if (!moved) moved = soft_any(weigh());
+            if (moved) {
+                // New references: the rows' largest scores of this block where they are 2^60
+                // above the old ones (or the first the row sees).
+                if (b > at.b0) take();
+                float top[NR];
+#pragma unroll
+                for (int r = 0; r < NR; ++r) top[r] = x[r];
+                across_lanes<NR>(top, [](float a, float d) { return fmaxf(a, d); });
+                const int mine = across_index<NR>();
+#pragma unroll
+                for (int j = 0; j < (NR + 31) / 32; ++j) c.across[w][mine + j] = top[j];
+                soft_sync();
+                if (tid < NR) {
+                    const float t = fmaxf(fmaxf(c.across[0][tid], c.across[1][tid]),
+                                          fmaxf(c.across[2][tid], c.across[3][tid]));
+                    const float old = c.ref[tid];
+                    const bool move = t > old + LAZY || (old == -INFINITY && t > old);
+                    c.factor[tid] = !move ? 1.0f : old == -INFINITY ? 0.0f : exp2_fast(old - t);
+                    if (move) c.ref[tid] = t;
                 }
                 soft_sync();
-                mbar_wait(&c.o_done, (i - 1) & 1u, &c.abort);
-                __syncwarp();
-                tc_fence_after();
-                for (int v = 0; v < (chunks - 1) / 2 * NR; v += 16) {
-                    float o[16];
-                    tc_load16(lanes + O_COL + v, o);
+                weigh();
+                if (b > at.b0) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] *= c.factor[(v + e) % NR];
-                    tc_store16(lanes + O_COL + v, o);
+                    for (int r = 0; r < NR; ++r) l[r] *= c.factor[r];
+                    mbar_wait(&c.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1u, &c.abort);
+                    __syncwarp();
+                    tc_fence_after();
+                    for (int h = 0; h < plan.pairs; ++h)
+#pragma unroll
+                        for (int v = 0; v < NR; v += 16) {
+                            float o[16];
+                            tc_load16(lanes + O_COL + h * NR + v, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= c.factor[v + e];
+                            tc_store16(lanes + O_COL + h * NR + v, o);
+                        }
+                    tc_wait_st();
+                    tc_fence_before();
                 }
-                tc_wait_st();
-                tc_fence_before();
             }
-            if (active) {
-                // Weights, rounded once to BF16 for the tensor cores; their sum is of the
-                // unrounded ones, in 32 bits, a block's 16 per thread first.
-                char *weights = stage + (chunks - 1) * CHUNK;
+            // The sums are of the unrounded weights, in 32 bits.
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float ref = m[h] == -INFINITY ? 0.0f : m[h];
-                    float s = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float a = exp2_fast(x[4 * j + 2 * h] - ref), d = exp2_fast(x[4 * j + 2 * h + 1] - ref);
-                        s += a + d;
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
-                        const int r = row0 + 8 * h;
-                        *reinterpret_cast<__nv_bfloat162 *>(weights + r * 128 + ((j ^ (r & 7)) << 4) + quad * 4) = v;
-                    }
-                    l[h] += s;
+            for (int r = 0; r < NR; ++r) l[r] += x[r];
+            if (bad) {
+                uint32_t s = ps;
+                for (int u = 0; u < plan.pairs; ++u) {
+                    for (int k = 0; k < 16; ++k)
+                        *reinterpret_cast<uint4 *>(pairs + s * 2 * CHUNK + (k >> 3) * CHUNK + tid * 128 + (k & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
                 }
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive(&c.p_full);
-            ++i;
-            if (++st == static_cast<uint32_t>(stage_count)) {
-                st = 0;
-                ++use;
+            if (lane == 0) {
+                arrive(&c.s_empty[i & 1]);
+                arrive(&c.p_full[i & 1]);
+            }
+            ps = (ps + plan.pairs) % plan.pair_slots;
+            if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
+                rs = 0;
+                ++ru;
             }
         }
         // The piece is done: write its rows, or its part of them.
-        if (active) {
+        across_lanes<NR>(l, [](float a, float d) { return a + d; });
+        const int mine = across_index<NR>();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
-                l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
-                if (quad == 0) {
-                    c.m[row0 + 8 * h] = m[h];
-                    c.l[row0 + 8 * h] = l[h];
-                }
-            }
+        for (int j = 0; j < (NR + 31) / 32; ++j) c.across[w][mine + j] = l[j];
+        soft_sync();
+        if (tid < NR) {
+            const bool sees = c.lim[tid] > start;
+            const float sum = c.across[0][tid] + c.across[1][tid] + c.across[2][tid] + c.across[3][tid];
+            c.l[tid] = sees ? sum : 0.0f;
+            if (!sees) c.ref[tid] = -INFINITY;
         }
         soft_sync();
-        // (One phase at a time: block i - 1's scores say that block i - 3's sum is done.)
-        if (i > 1) mbar_wait(&c.o_done, i & 1u, &c.abort);
-        mbar_wait(&c.o_done, (i - 1) & 1u, &c.abort);
+        mbar_wait(&c.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1u, &c.abort);
         __syncwarp();
         tc_fence_after();
         const bool direct = at.b0 == 0 && at.b1 == at.blocks;
         if (direct) {
-            if (p.lse && tid < at.tile.rows) p.lse[at.tile.base + tid] = finished_lse(c.m[tid], c.l[tid]);
-            uint16_t *out = p.out + static_cast<int64_t>(at.tile.base) * p.latent;
-            for (int v = 0; v < (chunks - 1) / 2 * NR; v += 16) {
-                float o[16];
-                tc_load16(lanes + O_COL + v, o);
-                const int d = v / NR * 128 + w * 32 + lane;
+            if (p.lse && tid < at.tile.rows) p.lse[at.tile.base + tid] = finished_lse(c.ref[tid], c.l[tid]);
+            uint16_t *out = p.out + static_cast<int64_t>(at.tile.base) * p.latent + w * 32 + (lane & ~1);
+            for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    // Even lanes take the pair's values of one row, odd lanes of the next.
-                    const int r = v % NR + e;
-                    const float a = o[e] * reciprocal(c.l[r]), a1 = o[e + 1] * reciprocal(c.l[r + 1]);
-                    const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : a1, 1);
-                    const int mine = r + (lane & 1);
-                    const __nv_bfloat162 pair = lane & 1 ? __floats2bfloat162_rn(other, a1)
-                                                         : __floats2bfloat162_rn(a, other);
-                    if (mine < at.tile.rows)
-                        *reinterpret_cast<__nv_bfloat162 *>(out + static_cast<int64_t>(mine) * p.latent + (d & ~1)) =
-                            pair;
+                for (int v = 0; v < NR; v += 16) {
+                    float o[16];
+                    tc_load16(lanes + O_COL + h * NR + v, o);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        // Even lanes take the pair's values of one row, odd lanes of the next.
+                        const float a = finished(o[e], c.l[v + e]), a1 = finished(o[e + 1], c.l[v + e + 1]);
+                        const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : a1, 1);
+                        const int row = v + e + (lane & 1);
+                        const __nv_bfloat162 two = lane & 1 ? __floats2bfloat162_rn(other, a1)
+                                                            : __floats2bfloat162_rn(a, other);
+                        if (row < at.tile.rows)
+                            *reinterpret_cast<__nv_bfloat162 *>(out + static_cast<int64_t>(row) * p.latent + h * 128) =
+                                two;
+                    }
                 }
-            }
         } else {
             Part &part = parts[2 * blockIdx.x + (at.b0 == 0 ? 1 : 0)];
             if (tid < NR) {
-                part.m[tid] = c.m[tid];
+                part.m[tid] = c.ref[tid];
                 part.l[tid] = c.l[tid];
             }
-            for (int v = 0; v < (chunks - 1) / 2 * NR; v += 16) {
-                float o[16];
-                tc_load16(lanes + O_COL + v, o);
-                const int d = v / NR * 128 + w * 32 + lane;
+            for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) part.sum[(v % NR + e) * p.latent + d] = o[e];
-            }
+                for (int v = 0; v < NR; v += 16) {
+                    float o[16];
+                    tc_load16(lanes + O_COL + h * NR + v, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        part.sum[(v + e) * p.latent + h * 128 + w * 32 + lane] = c.l[v + e] == 0.0f ? 0.0f : o[e];
+                }
         }
         if (at.b0 == 0 && tid == 0 && (by_tile || !direct)) {
             Joint j;
@@ -701,25 +791,26 @@ template <int NR>
 __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ AttendParams p) {
     extern __shared__ char raw[];
     char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    Ctrl &c = *reinterpret_cast<Ctrl *>(smem + CHUNKS * CHUNK);
+    const Plan plan = make_plan<NR>(p.latent);
+    char *pairs = smem + plan.query_bytes, *ropes = pairs + plan.pair_slots * 2 * CHUNK;
+    Ctrl &c = *reinterpret_cast<Ctrl *>(ropes + plan.rope_slots * CHUNK);
     const int warp = threadIdx.x >> 5;
-    const int chunks = p.latent / 64 + 1;
-    const int stage_count = min(MAX_STAGES, (CHUNKS - chunks) / chunks);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < MAX_STAGES; ++s) {
-            mbar_init(&c.full[s], LOAD + LOAD / 32);
-            mbar_init(&c.empty[s], 1);
+        for (int s = 0; s < MAX_SLOTS; ++s) {
+            mbar_init(&c.full[0][s], LOAD);
+            mbar_init(&c.full[1][s], LOAD + LOAD / 32);
+            mbar_init(&c.empty[0][s], 1);
+            mbar_init(&c.empty[1][s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&c.s_full[s], 1);
             mbar_init(&c.s_empty[s], SOFT / 32);
+            mbar_init(&c.p_full[s], SOFT / 32);
+            mbar_init(&c.o_done[s], 1);
         }
-        mbar_init(&c.p_full, SOFT / 32);
-        mbar_init(&c.o_done, 1);
         mbar_init(&c.q_full, QLOAD);
         mbar_init(&c.q_empty, 1);
         mbar_init(&c.drain, 1);
-        c.bad = 0;
         c.abort = 0;
         fence_mbar_init();
     }
@@ -735,11 +826,10 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
-    char *stages = smem + chunks * CHUNK;
-    if (warp < SOFT / 32) soften<NR>(p, c, stages, chunks, stage_count, tmem);
-    else if (warp < (SOFT + LOAD) / 32) load_rows(p, c, smem_addr(stages), chunks, stage_count);
-    else if (warp < (SOFT + LOAD + QLOAD) / 32) load_query(p, c, smem, chunks);
-    else multiply<NR>(p, c, smem_addr(smem), smem_addr(stages), chunks, stage_count, tmem);
+    if (warp < SOFT / 32) soften<NR>(p, c, plan, pairs, ropes, tmem);
+    else if (warp < (SOFT + LOAD) / 32) load_rows(p, c, plan, smem_addr(pairs), smem_addr(ropes));
+    else if (warp < (SOFT + LOAD + QLOAD) / 32) load_query<NR>(p, c, smem_addr(smem), 2 * plan.pairs + 1);
+    else multiply<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -811,9 +901,8 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ A
             acc.z += x.z;
             acc.w += x.w;
         }
-        const float inv = reciprocal(l);
-        const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        const __nv_bfloat162 a = __floats2bfloat162_rn(finished(acc.x, l), finished(acc.y, l));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(finished(acc.z, l), finished(acc.w, l));
         uint2 o;
         o.x = *reinterpret_cast<const uint32_t *>(&a);
         o.y = *reinterpret_cast<const uint32_t *>(&b);
@@ -875,7 +964,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     const int64_t full = p.tokens / p.rows_per_request, rest = p.tokens % p.rows_per_request * static_cast<int64_t>(p.heads);
     p.tiles_per_request = static_cast<int32_t>((per + ROWS - 1) / ROWS);
     p.tiles = static_cast<int32_t>(full * p.tiles_per_request + (rest + ROWS - 1) / ROWS);
-    p.min_share = 2;
+    p.min_share = 1;
     p.sms = d->sms;
     const int64_t most_blocks = (static_cast<int64_t>(p.paged ? p.width : p.k) + KEYS - 1) / KEYS;
     const int64_t want = (p.tiles * (most_blocks > 1 ? most_blocks : 1) + p.min_share - 1) / p.min_share;
