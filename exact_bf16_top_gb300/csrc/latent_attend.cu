@@ -13,15 +13,15 @@ namespace topk::latent {
 namespace {
 
 constexpr int SOFT = 128;                    // warps 0 to 3: softmax and outputs
-constexpr int LOAD = 128;                    // warps 4 to 7: cache rows
-constexpr int QLOAD = 64;                    // warps 8 and 9: query rows
-constexpr int NT = SOFT + LOAD + QLOAD + 32; // warp 10: the tensor cores
+constexpr int LOAD = 256;                    // warps 4 to 11: cache rows
+constexpr int QLOAD = 64;                    // warps 12 and 13: query rows
+constexpr int NT = SOFT + LOAD + QLOAD + 32; // warp 14: the tensor cores
 constexpr int NT_JOIN = 256;
 constexpr int ROWS = 64;                     // query rows of a tile
-constexpr int KEYS = 128;                    // cache rows of a block
+constexpr int KEYS = 64;                     // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
-constexpr int MAX_SLOTS = 6;                 // most slots of either ring
-constexpr int ROW_SETS = 8;                  // blocks whose row numbers are kept
+constexpr int MAX_SLOTS = 12;                // most slots of either ring
+constexpr int ROW_SETS = 16;                 // blocks whose row numbers are kept: more than the rings hold
 constexpr int SMEM = 232448;                 // all of a CTA's shared memory
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
 constexpr float LAZY = 60.0f;                // the reference may lag the maximum by this much (log2)
@@ -45,7 +45,7 @@ struct Ctrl {
     alignas(16) float factor[ROWS];
     float l[ROWS];
     int32_t lim[ROWS];                         // tokens a row may see
-    float across[4][ROWS];
+    float across[SOFT / 32][ROWS];
     int32_t rows[ROW_SETS][KEYS];              // cache row numbers of a block, -1: none
 };
 
@@ -53,22 +53,25 @@ struct Ctrl {
 // each), a ring of pairs of latent chunks, a ring of rotary chunks (where a
 // block's weights go once its scores are out), the control block.
 struct Plan {
-    int pairs, pair_slots, rope_slots, ahead;  // pairs per block; slots; units of the next block loadable ahead
+    int pairs, pair_slots, rope_slots;         // pairs per block; slots: two blocks' at least
     uint32_t query_bytes;
 };
 
 template <int NR>
-__device__ __forceinline__ Plan make_plan(int latent) {
-    Plan r;
+__host__ __device__ constexpr Plan make_plan(int latent) {
+    Plan r = {};
     r.pairs = latent / 128;
-    r.query_bytes = (2 * r.pairs + 1) * NR * 128;
+    r.query_bytes = static_cast<uint32_t>((2 * r.pairs + 1) * NR * 128);
     const int units = static_cast<int>((SMEM - 1024 - sizeof(Ctrl) - r.query_bytes) / CHUNK);
-    r.rope_slots = max(1, units / (2 * r.pairs + 1));
-    r.pair_slots = min(MAX_SLOTS, (units - r.rope_slots) / 2);
-    r.rope_slots = min(MAX_SLOTS, units - 2 * r.pair_slots);
-    r.ahead = r.pair_slots >= 2 * r.pairs && r.rope_slots >= 2 ? r.pairs + 1 : min(r.pairs, r.pair_slots - r.pairs);
+    r.rope_slots = units / (2 * r.pairs + 1);
+    r.pair_slots = (units - r.rope_slots) / 2;
+    if (r.pair_slots > MAX_SLOTS) r.pair_slots = MAX_SLOTS;
+    r.rope_slots = units - 2 * r.pair_slots;
+    if (r.rope_slots > MAX_SLOTS) r.rope_slots = MAX_SLOTS;
     return r;
 }
+static_assert(make_plan<ROWS>(LATENT_MAX).pair_slots >= 2 * LATENT_MAX / 128 &&
+              make_plan<ROWS>(LATENT_MAX).rope_slots >= 2);
 
 __device__ __forceinline__ void arrive(u64 *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -119,6 +122,37 @@ __device__ __forceinline__ uint64_t matrix(uint32_t addr, uint32_t lead) {
 __host__ __device__ constexpr uint32_t instruction(int m, int n, bool along) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (along ? 3u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Eight columns of this warp's first 16 lanes, N groups of them: thread t gets
+// of group j the values of lane t / 4 (v[4 j], v[4 j + 1]) and of lane t / 4 + 8
+// (v[4 j + 2], v[4 j + 3]) at columns 8 j + 2 (t % 4) and the next.
+template <int N>
+__device__ __forceinline__ void tc_load_groups(uint32_t addr, float (&v)[4 * N]) {
+    uint32_t r[4 * N];
+    if constexpr (N == 2)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr));
+    else if constexpr (N == 4)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(addr));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+            "%28,%29,%30,%31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+              "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+              "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(addr));
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 16 columns of this warp's 32 lanes, one lane per thread.
@@ -334,23 +368,29 @@ __device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint
                 v = __ldg(list + j);
             return v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
         };
-        int32_t now = row(at.b0 * KEYS + tid);
+        int32_t now = tid < KEYS ? row(at.b0 * KEYS + tid) : -1;
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
             int32_t *rows = c.rows[i % ROW_SETS];
-            rows[tid] = now;
+            if (tid < KEYS) rows[tid] = now;
             asm volatile("bar.sync 2, %0;" ::"n"(LOAD) : "memory");
-            if (b + 1 < at.b1) now = row((b + 1) * KEYS + tid);
+            if (tid < KEYS && b + 1 < at.b1) now = row((b + 1) * KEYS + tid);
             {
+                constexpr int STEP = LOAD / 16;
                 const int piece = tid & 15, r = tid >> 4;
                 const uint32_t dst = (piece >> 3) * CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                const char *src[KEYS / STEP];
+                bool on[KEYS / STEP];
+#pragma unroll
+                for (int k = 0; k < KEYS / STEP; ++k) {
+                    const int32_t v = rows[r + STEP * k];
+                    on[k] = v >= 0;
+                    src[k] = cache + (on[k] ? v * pitch : 0) + piece * 16;
+                }
                 for (int u = 0; u < plan.pairs; ++u) {
                     mbar_wait(&c.empty[0][ps], (pu + 1) & 1u, &c.abort);
-                    const char *src = cache + u * 256 + piece * 16;
 #pragma unroll
-                    for (int k = 0; k < KEYS / 8; ++k) {
-                        const int32_t v = rows[r + 8 * k];
-                        copy16(pairs + ps * 2 * CHUNK + dst + k * 1024, src + (v >= 0 ? v * pitch : 0), v >= 0);
-                    }
+                    for (int k = 0; k < KEYS / STEP; ++k)
+                        copy16(pairs + ps * 2 * CHUNK + dst + k * STEP * 128, src[k] + u * 256, on[k]);
                     copies_arrive(&c.full[0][ps]);
                     if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
                         ps = 0;
@@ -359,13 +399,14 @@ __device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint
                 }
             }
             mbar_wait(&c.empty[1][rs], (ru + 1) & 1u, &c.abort);
+            constexpr int STEP = LOAD / 8;
             const int piece = tid & 7, r = tid >> 3;
             const uint32_t dst = ropes + rs * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4);
             const char *src = cache + plan.pairs * 256 + piece * 16;
 #pragma unroll
-            for (int k = 0; k < KEYS / 16; ++k) {
-                const int32_t v = rows[r + 16 * k];
-                copy16(dst + k * 2048, src + (v >= 0 ? v * pitch : 0), v >= 0);
+            for (int k = 0; k < KEYS / STEP; ++k) {
+                const int32_t v = rows[r + STEP * k];
+                copy16(dst + k * STEP * 128, src + (v >= 0 ? v * pitch : 0), v >= 0);
             }
             copies_arrive(&c.full[1][rs]);
             __syncwarp();
@@ -379,14 +420,14 @@ __device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The products, both with the cache as the 128-row operand (tokens for the
-// scores, latent values for the sums) and the query rows as columns: the tensor
-// cores take 42 + N / 2 cycles for 128 x N x 16 with both operands in shared
-// memory, so few columns cost little and 64 rows are never half of an operand.
-//   scores[token][row] = sum over chunks of K chunk x Q chunk
-//   sums[value][row]  += V pair (values x tokens) x weights (tokens x rows)
-// Block i's scores start with what its ring slots hold before block i - 1's are
-// given back, then comes block i - 1's sum, then the rest.
+// The products, both with the cache as the left operand and the query rows as
+// columns, so that few query rows cost little:
+//   scores[token][row] = sum over chunks of K chunk x Q chunk       (64 x NR x 16 a step)
+//   sums[value][row]  += V pair (values x tokens) x weights         (128 x NR x 16 a step)
+// A step takes the longer of its arithmetic and its operands' way out of shared
+// memory at 128 bytes a cycle (measured: 23 and 39 cycles at NR = 16, 32 and 48
+// at NR = 64). Block i's scores are issued before block i - 1's sums, so that
+// the tensor cores work while the softmax warps turn scores into weights.
 template <int NR>
 __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, uint32_t pairs,
                          uint32_t ropes, uint32_t tmem) {
@@ -429,7 +470,6 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
             const uint32_t this_ps = ps, this_rs = rs, d = tmem + S_COL + (i & 1) * NR;
             const uint64_t q = matrix(query, 16);
             for (int u = 0; u <= plan.pairs; ++u) {
-                if (pending && u == plan.ahead && !(ok = sum())) break;
                 const bool rope = u == plan.pairs;
                 if (!(ok = rope ? wait(&c.full[1][rs], ru, c) : wait(&c.full[0][ps], pu, c))) break;
                 fence_proxy_async();          // (the rows were written by ordinary copies)
@@ -515,12 +555,11 @@ struct Joint {                                 // a split tile: where its parts 
 __device__ __forceinline__ float finished_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * LN2; }
 __device__ __forceinline__ float finished(float sum, float l) { return l == 0.0f ? 0.0f : sum / l; }   // NaN stays NaN
 
-// Combines v[0 .. NR) over the warp's lanes: afterwards lane's v[j] is the
-// whole warp's value `index(lane) + j` (NR / 32 of them; NR = 16: lanes l and
-// l ^ 1 hold the same one).
+// Combines v[0 .. N) over the eight lanes that share lane % 4: afterwards a
+// lane's v[j] is the eight lanes' value across_index() + j (N / 8 of them).
 template <int N, int O = 16, int SIZE, class Op>
 __device__ __forceinline__ void across_lanes(float (&v)[SIZE], Op op) {
-    if constexpr (O > 0) {
+    if constexpr (O >= 4) {
         constexpr int H = N / 2;
         if constexpr (H > 0) {
             const bool up = (threadIdx.x & O) != 0;
@@ -537,31 +576,32 @@ __device__ __forceinline__ void across_lanes(float (&v)[SIZE], Op op) {
     }
 }
 
-// The first row whose value across_lanes leaves in this lane.
-template <int NR>
+template <int N>
 __device__ __forceinline__ int across_index() {
-    const int lane = threadIdx.x & 31;
     int r = 0;
 #pragma unroll
-    for (int o = 16, n = NR / 2; o && n; o >>= 1, n /= 2) r += lane & o ? n : 0;
+    for (int o = 16, n = N / 2; o >= 4 && n; o >>= 1, n /= 2) r += threadIdx.x & o ? n : 0;
     return r;
 }
 
 // Scores to weights, the running reference and sums, and the outputs. Thread t
-// holds token t of a block against all rows of the tile, so that masks and the
-// weights' layout (tokens x rows, a token's 128 bytes together) are its own,
-// and a row's sum over tokens stays in one register per row until the piece is
-// done. The weights' reference is the maximum of the row's first block; weights
-// may grow to 2^60 before it moves (FP32 sums and BF16 weights lose nothing by
-// that), which is seen from the packed weights and almost never happens.
+// of warp w holds tokens 16 w + t / 4 and 8 further of a block, against the
+// query rows 8 j + 2 (t % 4) and the next: their references and sums stay in
+// its registers. The weights' reference is the maximum of the row's first
+// block; weights may grow to 2^60 before it moves (FP32 sums and BF16 weights
+// lose nothing by that), which is seen from the packed weights and almost never
+// happens.
 template <int NR>
 __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *pairs, char *ropes, uint32_t tmem) {
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    constexpr int N = NR / 4;                  // query rows of a thread
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, quad = lane & 3;
+    const int t0 = w * 16 + lane / 4;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
     const float scale = p.scale * LOG2E;
     Part *parts = reinterpret_cast<Part *>(p.workspace);
     Joint *joints = reinterpret_cast<Joint *>(parts + 2 * p.sms);
     const bool by_tile = p.tiles <= static_cast<int32_t>(gridDim.x);
+    auto row_of = [&](int n) { return 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
     bool split_here = false;
     Cursor at(c);
     uint32_t i = 0, ps = 0, rs = 0, ru = 0;
@@ -570,7 +610,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
         const int32_t start = at.b0 * KEYS;
         // A row that sees nothing of this piece has an infinite reference: whatever its
         // scores, its weights never move it, and its results are written as empty.
-        int32_t low = INT32_MAX;
         if (tid < ROWS) {
             int32_t lim = 0;
             if (tid < at.tile.rows) lim = p.paged ? token_len(p, (at.tile.base + tid) / p.heads) : INT32_MAX;
@@ -578,28 +617,32 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             c.ref[tid] = lim > start ? -INFINITY : INFINITY;
         }
         soft_sync();
+        int32_t low = INT32_MAX;
 #pragma unroll
         for (int r = 0; r < ROWS; r += 32) {
             const int32_t lim = c.lim[r + lane];
             low = min(low, lim > start ? lim : INT32_MAX);
         }
         low = __reduce_min_sync(0xFFFFFFFFu, low);
-        float l[NR];
+        float l[N], ref[N];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+        for (int n = 0; n < N; ++n) {
+            l[n] = 0.0f;
+            ref[n] = c.ref[row_of(n)];
+        }
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
             // (These warps meet at barriers, so none leaves early: after a wait that gave
             // up, all go on without waiting, on whatever the memories hold.)
             mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
             mbar_wait(&c.full[1][rs], ru & 1u, &c.abort);   // (complete: makes the row numbers visible)
             __syncwarp();
-            const int32_t token = b * KEYS + tid;
-            const bool there = c.rows[i % ROW_SETS][tid] >= 0;
-            const bool whole = __all_sync(0xFFFFFFFFu, there) && (b + 1) * KEYS <= low;
+            const int32_t token = b * KEYS + t0;
+            const bool there[2] = {c.rows[i % ROW_SETS][t0] >= 0, c.rows[i % ROW_SETS][t0 + 8] >= 0};
+            const bool whole = __all_sync(0xFFFFFFFFu, there[0] && there[1]) && (b + 1) * KEYS <= low;
             const uint32_t scores = lanes + S_COL + (i & 1) * NR;
-            char *weights = ropes + rs * CHUNK + tid * 128;
-            float x[NR];
-            bool bad = false;
+            char *weights = ropes + rs * CHUNK + t0 * 128 + quad * 4;
+            float x[2 * N];                    // x[4 j + 2 h + e]: token h, row 8 j + 2 quad + e
+            bool bad[2] = {false, false};
             // Scores in log2 units; where masked, -inf. A cache row that only some of the
             // tile's rows see must not reach the others through 0 x inf: where a score that
             // is masked here is not finite (every row sees a cache row's NaN and infinities
@@ -607,25 +650,31 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             // see it are NaN.
             auto take = [&]() {
                 tc_fence_after();
-#pragma unroll
-                for (int r = 0; r < NR; r += 16) {
-                    float v[16];
-                    tc_load16(scores + r, v);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[r + e] = v[e] * scale;
-                }
+                tc_load_groups<NR / 8>(scores, x);
                 tc_fence_before();
+#pragma unroll
+                for (int e = 0; e < 2 * N; ++e) x[e] *= scale;
                 if (!whole) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        const bool seen = there && token < c.lim[r];
-                        bad |= there && !seen && r < at.tile.rows && !(fabsf(x[r]) < INFINITY);
-                        x[r] = seen ? x[r] : -INFINITY;
-                    }
-                    if (bad) {
+                    for (int h = 0; h < 2; ++h) {
+                        bool odd = false;
 #pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            if (there && token < c.lim[r]) x[r] = __uint_as_float(0x7FC00000u);
+                        for (int n = 0; n < N; ++n) {
+                            float &v = x[4 * (n >> 1) + 2 * h + (n & 1)];
+                            const int r = row_of(n);
+                            const bool seen = there[h] && token + 8 * h < c.lim[r];
+                            odd |= there[h] && !seen && r < at.tile.rows && !(fabsf(v) < INFINITY);
+                            v = seen ? v : -INFINITY;
+                        }
+                        odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, 1);
+                        odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, 2);
+                        bad[h] = odd;
+                        if (odd) {
+#pragma unroll
+                            for (int n = 0; n < N; ++n)
+                                if (token + 8 * h < c.lim[row_of(n)])
+                                    x[4 * (n >> 1) + 2 * h + (n & 1)] = __uint_as_float(0x7FC00000u);
+                        }
                     }
                 }
             };
@@ -634,19 +683,16 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             auto weigh = [&]() -> bool {
                 __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-                for (int g = 0; g < NR / 8; ++g) {
-                    __nv_bfloat162 v[4];
+                for (int j = 0; j < NR / 8; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 8 * g + 2 * e;
-                        const float2 ref = *reinterpret_cast<const float2 *>(&c.ref[r]);
-                        x[r] = whole || x[r] != -INFINITY ? exp2_fast(x[r] - ref.x) : 0.0f;
-                        x[r + 1] = whole || x[r + 1] != -INFINITY ? exp2_fast(x[r + 1] - ref.y) : 0.0f;
-                        v[e] = __floats2bfloat162_rn(x[r], x[r + 1]);
-                        top = __hmax2(top, v[e]);
+                    for (int h = 0; h < 2; ++h) {
+                        float &a = x[4 * j + 2 * h], &d = x[4 * j + 2 * h + 1];
+                        a = whole || a != -INFINITY ? exp2_fast(a - ref[2 * j]) : 0.0f;
+                        d = whole || d != -INFINITY ? exp2_fast(d - ref[2 * j + 1]) : 0.0f;
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
+                        top = __hmax2(top, v);
+                        *reinterpret_cast<__nv_bfloat162 *>(weights + h * 1024 + ((j ^ (t0 & 7)) << 4)) = v;
                     }
-                    *reinterpret_cast<uint4 *>(weights + ((g ^ (tid & 7)) << 4)) = *reinterpret_cast<uint4 *>(v);
-                }
                 return fmaxf(__low2float(top), __high2float(top)) > 1.152921504606846976e18f;   // 2^60
             };
             take();
@@ -656,13 +702,13 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                 // New references: the rows' largest scores of this block where they are 2^60
                 // above the old ones (or the first the row sees).
                 if (b > at.b0) take();
-                float top[NR];
+                float top[N];
 #pragma unroll
-                for (int r = 0; r < NR; ++r) top[r] = x[r];
-                across_lanes<NR>(top, [](float a, float d) { return fmaxf(a, d); });
-                const int mine = across_index<NR>();
+                for (int n = 0; n < N; ++n) top[n] = fmaxf(x[4 * (n >> 1) + (n & 1)], x[4 * (n >> 1) + 2 + (n & 1)]);
+                across_lanes<N>(top, [](float a, float d) { return fmaxf(a, d); });
+                const int mine = across_index<N>();
 #pragma unroll
-                for (int j = 0; j < (NR + 31) / 32; ++j) c.across[w][mine + j] = top[j];
+                for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = top[j];
                 soft_sync();
                 if (tid < NR) {
                     const float t = fmaxf(fmaxf(c.across[0][tid], c.across[1][tid]),
@@ -673,10 +719,13 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                     if (move) c.ref[tid] = t;
                 }
                 soft_sync();
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    ref[n] = c.ref[row_of(n)];
+                    l[n] *= c.factor[row_of(n)];
+                }
                 weigh();
                 if (b > at.b0) {
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= c.factor[r];
                     mbar_wait(&c.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1u, &c.abort);
                     __syncwarp();
                     tc_fence_after();
@@ -695,38 +744,42 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             }
             // The sums are of the unrounded weights, in 32 bits.
 #pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] += x[r];
-            if (bad) {
-                uint32_t s = ps;
-                for (int u = 0; u < plan.pairs; ++u) {
-                    for (int k = 0; k < 16; ++k)
-                        *reinterpret_cast<uint4 *>(pairs + s * 2 * CHUNK + (k >> 3) * CHUNK + tid * 128 + (k & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
+            for (int n = 0; n < N; ++n) l[n] += x[4 * (n >> 1) + (n & 1)] + x[4 * (n >> 1) + 2 + (n & 1)];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (bad[h]) {
+                    uint32_t s = ps;
+                    for (int u = 0; u < plan.pairs; ++u) {
+                        for (int k = quad; k < 16; k += 4)
+                            *reinterpret_cast<uint4 *>(pairs + s * 2 * CHUNK + (k >> 3) * CHUNK + (t0 + 8 * h) * 128 +
+                                                       (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
+                    }
                 }
-            }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
                 arrive(&c.s_empty[i & 1]);
                 arrive(&c.p_full[i & 1]);
             }
-            ps = (ps + plan.pairs) % plan.pair_slots;
+            ps += plan.pairs;
+            if (ps >= static_cast<uint32_t>(plan.pair_slots)) ps -= plan.pair_slots;
             if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
                 rs = 0;
                 ++ru;
             }
         }
         // The piece is done: write its rows, or its part of them.
-        across_lanes<NR>(l, [](float a, float d) { return a + d; });
-        const int mine = across_index<NR>();
+        across_lanes<N>(l, [](float a, float d) { return a + d; });
+        const int mine = across_index<N>();
 #pragma unroll
-        for (int j = 0; j < (NR + 31) / 32; ++j) c.across[w][mine + j] = l[j];
+        for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = l[j];
         soft_sync();
         if (tid < NR) {
             const bool sees = c.lim[tid] > start;
             const float sum = c.across[0][tid] + c.across[1][tid] + c.across[2][tid] + c.across[3][tid];
             c.l[tid] = sees ? sum : 0.0f;
+            c.factor[tid] = 1.0f / sum;
             if (!sees) c.ref[tid] = -INFINITY;
         }
         soft_sync();
@@ -745,7 +798,8 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         // Even lanes take the pair's values of one row, odd lanes of the next.
-                        const float a = finished(o[e], c.l[v + e]), a1 = finished(o[e + 1], c.l[v + e + 1]);
+                        const float a = c.l[v + e] == 0.0f ? 0.0f : o[e] * c.factor[v + e];
+                        const float a1 = c.l[v + e + 1] == 0.0f ? 0.0f : o[e + 1] * c.factor[v + e + 1];
                         const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : a1, 1);
                         const int row = v + e + (lane & 1);
                         const __nv_bfloat162 two = lane & 1 ? __floats2bfloat162_rn(other, a1)
@@ -964,7 +1018,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     const int64_t full = p.tokens / p.rows_per_request, rest = p.tokens % p.rows_per_request * static_cast<int64_t>(p.heads);
     p.tiles_per_request = static_cast<int32_t>((per + ROWS - 1) / ROWS);
     p.tiles = static_cast<int32_t>(full * p.tiles_per_request + (rest + ROWS - 1) / ROWS);
-    p.min_share = 1;
+    p.min_share = 2;
     p.sms = d->sms;
     const int64_t most_blocks = (static_cast<int64_t>(p.paged ? p.width : p.k) + KEYS - 1) / KEYS;
     const int64_t want = (p.tiles * (most_blocks > 1 ? most_blocks : 1) + p.min_share - 1) / p.min_share;
