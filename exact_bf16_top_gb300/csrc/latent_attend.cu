@@ -687,8 +687,9 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float &a = x[4 * j + 2 * h], &d = x[4 * j + 2 * h + 1];
-                        a = whole || a != -INFINITY ? exp2_fast(a - ref[2 * j]) : 0.0f;
-                        d = whole || d != -INFINITY ? exp2_fast(d - ref[2 * j + 1]) : 0.0f;
+                        const float ea = exp2_fast(a - ref[2 * j]), ed = exp2_fast(d - ref[2 * j + 1]);
+                        a = a == -INFINITY ? 0.0f : ea;      // (masked: the reference may be -inf too)
+                        d = d == -INFINITY ? 0.0f : ed;
                         const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
                         top = __hmax2(top, v);
                         *reinterpret_cast<__nv_bfloat162 *>(weights + h * 1024 + ((j ^ (t0 & 7)) << 4)) = v;
