@@ -21,7 +21,8 @@ constexpr int ROWS = 64;                     // query rows of a tile
 constexpr int KEYS = 64;                     // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
 constexpr int MAX_SLOTS = 12;                // most slots of either ring
-constexpr int ROW_SETS = 16;                 // blocks whose row numbers are kept: more than the rings hold
+constexpr int BLOCKS = 16;                   // blocks that have barriers and row numbers of their own: more than
+                                             // the rings hold
 constexpr int SMEM = 232448;                 // all of a CTA's shared memory
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
 constexpr float LAZY = 60.0f;                // the reference may lag the maximum by this much (log2)
@@ -29,7 +30,8 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 using u64 = unsigned long long;
 
 struct Ctrl {
-    u64 full[2][MAX_SLOTS], empty[2][MAX_SLOTS];   // a slot's rows are in / used up; [0] pairs, [1] ropes
+    u64 full[BLOCKS];                          // a block's rows are in
+    u64 pair_empty[MAX_SLOTS], rope_empty[MAX_SLOTS];   // a slot is used up
     u64 s_full[2], s_empty[2];                 // scores written / read
     u64 p_full[2], o_done[2];                  // a block's weights are in / its sums are added (by turns: who
                                                // waits for block i - 1 may meet block i's, and two phases of one
@@ -46,7 +48,7 @@ struct Ctrl {
     float l[ROWS];
     int32_t lim[ROWS];                         // tokens a row may see
     float across[SOFT / 32][ROWS];
-    int32_t rows[ROW_SETS][KEYS];              // cache row numbers of a block, -1: none
+    int32_t rows[BLOCKS][KEYS];                // cache row numbers of a block, -1: none
 };
 
 // Shared memory: the query tile (chunks of 64 values, NR rows of 128 bytes
@@ -77,11 +79,13 @@ __device__ __forceinline__ void arrive(u64 *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Bounded wait by a whole warp; false, on every lane, once any wait of the CTA
-// gave up.
-__device__ __forceinline__ bool wait(u64 *bar, uint32_t parity, Ctrl &c) {
+// Bounded wait by a whole warp. Once a wait of the CTA gave up, every later one
+// returns at once and all warps go on to the end of the schedule on whatever the
+// memories hold, inside the same bounds: they meet at barriers, so none may leave
+// early.
+__device__ __forceinline__ void wait(u64 *bar, uint32_t parity, Ctrl &c) {
     mbar_wait(bar, parity & 1u, &c.abort);
-    return __all_sync(0xFFFFFFFFu, c.abort == 0);
+    __syncwarp();
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -342,24 +346,28 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
 
 // ------------------------------------------------------------------ the warps' parts
 
-// Cache rows into the rings, swizzled as the products read them: 16 threads
-// copy a row's 256 bytes of a pair, 8 a row's 128 rotary bytes. Places that
-// hold no cache row are filled with zeros. (Measured: the same rows gathered
-// four at a time by TMA come at 12 bytes a nanosecond per SM, a third of what
-// these copies reach.)
+// Cache rows into the rings, swizzled as the products read them. A warp copies
+// eight rows of every block: half a warp a row's 256 bytes of a pair, a quarter
+// its 128 rotary bytes. Places that hold no cache row are filled with zeros.
+// (Measured: the same rows gathered four at a time by TMA come at 12 bytes a
+// nanosecond per SM; copies of 16 bytes reach 100 from L2 with four warps.)
 __device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t pairs, uint32_t ropes) {
-    const int tid = threadIdx.x - SOFT, lane = tid & 31;
+    constexpr int WARPS = LOAD / 32;
+    static_assert(KEYS == 8 * WARPS);
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x - SOFT) >> 5;
     const int64_t pitch = p.cache_stride * 2;
     const char *cache = reinterpret_cast<const char *>(p.cache);
+    // Row j of the warp's eight is row `place(j)` of the block.
+    auto place = [&](int j) { return 2 * warp + (j & 1) + 2 * WARPS * (j >> 1); };
+    const int half = lane >> 4, piece = lane & 15, quarter = lane >> 3, rope_piece = lane & 7;
     Cursor at(c);
     uint32_t i = 0, ps = 0, pu = 0, rs = 0, ru = 0;   // block; pair slot and its use; rope slot and its use
-    // (These warps meet at barriers, so none leaves early: after a wait that gave up,
-    // all go on copying without waiting, inside the same bounds.)
     while (at.next(p, lane)) {
         const int32_t *list = p.paged ? p.table + static_cast<int64_t>(at.tile.request) * p.table_stride
                                       : p.selected + static_cast<int64_t>(at.tile.token) * p.selected_stride;
-        auto row = [&](int32_t j) -> int32_t {
-            if (j >= at.len) return -1;
+        auto row = [&](int32_t b) -> int32_t {         // lane's (lane & 7)th row of block b
+            const int32_t j = b * KEYS + place(lane & 7);
+            if (b >= at.b1 || j >= at.len) return -1;
             int64_t v;
             if (p.paged)
                 v = static_cast<int64_t>(__ldg(list + (j >> p.page_shift))) * p.block_rows +
@@ -368,53 +376,46 @@ __device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint
                 v = __ldg(list + j);
             return v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
         };
-        int32_t now = tid < KEYS ? row(at.b0 * KEYS + tid) : -1;
+        int32_t now = row(at.b0);
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
-            int32_t *rows = c.rows[i % ROW_SETS];
-            if (tid < KEYS) rows[tid] = now;
-            asm volatile("bar.sync 2, %0;" ::"n"(LOAD) : "memory");
-            if (tid < KEYS && b + 1 < at.b1) now = row((b + 1) * KEYS + tid);
-            {
-                constexpr int STEP = LOAD / 16;
-                const int piece = tid & 15, r = tid >> 4;
-                const uint32_t dst = (piece >> 3) * CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-                const char *src[KEYS / STEP];
-                bool on[KEYS / STEP];
+            const int32_t then = row(b + 1);
+            if (lane < 8) c.rows[i % BLOCKS][place(lane)] = now;
+            const char *src[4];
+            bool on[4];
 #pragma unroll
-                for (int k = 0; k < KEYS / STEP; ++k) {
-                    const int32_t v = rows[r + STEP * k];
-                    on[k] = v >= 0;
-                    src[k] = cache + (on[k] ? v * pitch : 0) + piece * 16;
-                }
-                for (int u = 0; u < plan.pairs; ++u) {
-                    mbar_wait(&c.empty[0][ps], (pu + 1) & 1u, &c.abort);
+            for (int k = 0; k < 4; ++k) {
+                const int32_t v = __shfl_sync(0xFFFFFFFFu, now, 2 * k + half);
+                on[k] = v >= 0;
+                src[k] = cache + (on[k] ? v * pitch : 0) + piece * 16;
+            }
+            const int r = place(half);
+            const uint32_t dst = (piece >> 3) * CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+            for (int u = 0; u < plan.pairs; ++u) {
+                wait(&c.pair_empty[ps], pu + 1, c);
 #pragma unroll
-                    for (int k = 0; k < KEYS / STEP; ++k)
-                        copy16(pairs + ps * 2 * CHUNK + dst + k * STEP * 128, src[k] + u * 256, on[k]);
-                    copies_arrive(&c.full[0][ps]);
-                    if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
-                        ps = 0;
-                        ++pu;
-                    }
+                for (int k = 0; k < 4; ++k)
+                    copy16(pairs + ps * 2 * CHUNK + dst + k * 2 * WARPS * 128, src[k] + u * 256, on[k]);
+                if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
+                    ps = 0;
+                    ++pu;
                 }
             }
-            mbar_wait(&c.empty[1][rs], (ru + 1) & 1u, &c.abort);
-            constexpr int STEP = LOAD / 8;
-            const int piece = tid & 7, r = tid >> 3;
-            const uint32_t dst = ropes + rs * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4);
-            const char *src = cache + plan.pairs * 256 + piece * 16;
+            wait(&c.rope_empty[rs], ru + 1, c);
 #pragma unroll
-            for (int k = 0; k < KEYS / STEP; ++k) {
-                const int32_t v = rows[r + STEP * k];
-                copy16(dst + k * STEP * 128, src + (v >= 0 ? v * pitch : 0), v >= 0);
+            for (int k = 0; k < 2; ++k) {
+                const int j = quarter + 4 * k, at_row = place(j);
+                const int32_t v = __shfl_sync(0xFFFFFFFFu, now, j);
+                copy16(ropes + rs * CHUNK + at_row * 128 + ((rope_piece ^ (at_row & 7)) << 4),
+                       cache + (v >= 0 ? v * pitch : 0) + plan.pairs * 256 + rope_piece * 16, v >= 0);
             }
-            copies_arrive(&c.full[1][rs]);
+            copies_arrive(&c.full[i % BLOCKS]);
             __syncwarp();
-            if (lane == 0) arrive(&c.full[1][rs]);     // (makes the row numbers visible)
+            if (lane == 0) arrive(&c.full[i % BLOCKS]);     // (makes the row numbers visible)
             if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
                 rs = 0;
                 ++ru;
             }
+            now = then;
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -435,12 +436,12 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
     constexpr uint32_t QK = instruction(KEYS, NR, false), PV = instruction(128, NR, true);
     constexpr int QCHUNK = NR * 128;
     Cursor at(c);
-    uint32_t i = 0, piece = 0, ps = 0, pu = 0, rs = 0, ru = 0;
+    uint32_t i = 0, piece = 0, ps = 0, rs = 0;
     uint32_t last_ps = 0, last_rs = 0;       // where block i - 1 begins
-    bool first = true, pending = false, ok = true;
-    auto sum = [&]() -> bool {                // of block i - 1
-        pending = false;
-        if (!wait(&c.p_full[(i - 1) & 1], (i - 1) >> 1, c)) return false;
+    bool first = true, pending = false;
+    const uint64_t q = matrix(query, 16);
+    auto sum = [&]() {                        // of block i - 1
+        wait(&c.p_full[(i - 1) & 1], (i - 1) >> 1, c);
         tc_fence_after();
         if (elected()) {
             const uint64_t w = matrix(ropes + last_rs * CHUNK, 16);
@@ -450,67 +451,57 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
 #pragma unroll
                 for (int k = 0; k < KEYS / 16; ++k)
                     tc_mma(tmem + O_COL + h * NR, v + k * 128, w + k * 128, PV, !first || k > 0);
-                tc_commit(&c.empty[0][s]);
+                tc_commit(&c.pair_empty[s]);
                 if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
             }
-            tc_commit(&c.empty[1][last_rs]);
+            tc_commit(&c.rope_empty[last_rs]);
             tc_commit(&c.o_done[(i - 1) & 1]);
         }
         __syncwarp();
-        return true;
     };
-    while (ok && at.next(p, lane)) {
-        for (int32_t b = at.b0; ok && b < at.b1; ++b, ++i) {
+    while (at.next(p, lane)) {
+        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
             if (b == at.b0) {
                 // A new query tile waits for its loads: finish the last tile's sums first.
-                if (pending && !(ok = sum())) break;
-                if (!(ok = wait(&c.q_full, piece, c))) break;
+                if (pending) sum();
+                pending = false;
+                wait(&c.q_full, piece, c);
             }
-            if (!(ok = wait(&c.s_empty[i & 1], (i >> 1) + 1, c))) break;
-            const uint32_t this_ps = ps, this_rs = rs, d = tmem + S_COL + (i & 1) * NR;
-            const uint64_t q = matrix(query, 16);
-            for (int u = 0; u <= plan.pairs; ++u) {
-                const bool rope = u == plan.pairs;
-                if (!(ok = rope ? wait(&c.full[1][rs], ru, c) : wait(&c.full[0][ps], pu, c))) break;
-                fence_proxy_async();          // (the rows were written by ordinary copies)
-                tc_fence_after();
-                if (elected()) {
-                    const uint64_t k = matrix(rope ? ropes + rs * CHUNK : pairs + ps * 2 * CHUNK, 16);
-                    const uint64_t qu = q + u * (2 * QCHUNK >> 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) tc_mma(d, k + e * 2, qu + e * 2, QK, u > 0 || e > 0);
-                    if (!rope) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            tc_mma(d, k + (CHUNK >> 4) + e * 2, qu + (QCHUNK >> 4) + e * 2, QK, true);
-                    }
-                }
-                __syncwarp();
-                if (rope) {
-                    if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
-                        rs = 0;
-                        ++ru;
-                    }
-                } else if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
-                    ps = 0;
-                    ++pu;
-                }
-            }
-            if (!ok) break;
+            wait(&c.s_empty[i & 1], (i >> 1) + 1, c);
+            wait(&c.full[i % BLOCKS], i / BLOCKS, c);
+            fence_proxy_async();              // (the rows were written by ordinary copies)
+            tc_fence_after();
+            const uint32_t this_ps = ps;
             if (elected()) {
+                const uint32_t d = tmem + S_COL + (i & 1) * NR;
+                uint32_t s = ps;
+                for (int u = 0; u < plan.pairs; ++u) {
+                    const uint64_t k = matrix(pairs + s * 2 * CHUNK, 16), qu = q + u * (2 * QCHUNK >> 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        tc_mma(d, k + (e >> 2) * (CHUNK >> 4) + (e & 3) * 2, qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2,
+                               QK, u > 0 || e > 0);
+                    if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
+                }
+                const uint64_t k = matrix(ropes + rs * CHUNK, 16), qu = q + plan.pairs * (2 * QCHUNK >> 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tc_mma(d, k + e * 2, qu + e * 2, QK, true);
                 tc_commit(&c.s_full[i & 1]);
                 if (b + 1 == at.b1) tc_commit(&c.q_empty);
             }
             __syncwarp();
-            if (pending && !(ok = sum())) break;
+            if (pending) sum();
             pending = true;
-            last_ps = this_ps;
-            last_rs = this_rs;
             first = b == at.b0;
+            last_ps = this_ps;
+            last_rs = rs;
+            ps += plan.pairs;
+            if (ps >= static_cast<uint32_t>(plan.pair_slots)) ps -= plan.pair_slots;
+            if (++rs == static_cast<uint32_t>(plan.rope_slots)) rs = 0;
         }
         ++piece;
     }
-    if (ok && pending) sum();
+    if (pending) sum();
     // Nothing may be running on the tensor cores when their memory is freed.
     if (elected()) tc_commit(&c.drain);
     __syncwarp();
@@ -528,7 +519,7 @@ __device__ void load_query(const AttendParams &p, Ctrl &c, uint32_t query, int c
     Cursor at(c);
     uint32_t n = 0;
     while (at.next(p, lane)) {
-        if (!wait(&c.q_empty, n + 1, c)) break;
+        wait(&c.q_empty, n + 1, c);
         const int piece = tid & 7;
         for (int r = tid >> 3; r < at.tile.rows; r += QLOAD / 8) {
             const int32_t flat = at.tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
@@ -604,7 +595,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
     auto row_of = [&](int n) { return 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
     bool split_here = false;
     Cursor at(c);
-    uint32_t i = 0, ps = 0, rs = 0, ru = 0;
+    uint32_t i = 0, ps = 0, rs = 0;
     long long done = c.begin;
     while (at.next(p, lane)) {
         const int32_t start = at.b0 * KEYS;
@@ -631,13 +622,10 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             ref[n] = c.ref[row_of(n)];
         }
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
-            // (These warps meet at barriers, so none leaves early: after a wait that gave
-            // up, all go on without waiting, on whatever the memories hold.)
             mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
-            mbar_wait(&c.full[1][rs], ru & 1u, &c.abort);   // (complete: makes the row numbers visible)
-            __syncwarp();
+            wait(&c.full[i % BLOCKS], i / BLOCKS, c);       // (complete: makes the row numbers visible)
             const int32_t token = b * KEYS + t0;
-            const bool there[2] = {c.rows[i % ROW_SETS][t0] >= 0, c.rows[i % ROW_SETS][t0 + 8] >= 0};
+            const bool there[2] = {c.rows[i % BLOCKS][t0] >= 0, c.rows[i % BLOCKS][t0 + 8] >= 0};
             const bool whole = __all_sync(0xFFFFFFFFu, there[0] && there[1]) && (b + 1) * KEYS <= low;
             const uint32_t scores = lanes + S_COL + (i & 1) * NR;
             char *weights = ropes + rs * CHUNK + t0 * 128 + quad * 4;
@@ -727,8 +715,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                 }
                 weigh();
                 if (b > at.b0) {
-                    mbar_wait(&c.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1u, &c.abort);
-                    __syncwarp();
+                    wait(&c.o_done[(i - 1) & 1], (i - 1) >> 1, c);
                     tc_fence_after();
                     for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
@@ -765,10 +752,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             }
             ps += plan.pairs;
             if (ps >= static_cast<uint32_t>(plan.pair_slots)) ps -= plan.pair_slots;
-            if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
-                rs = 0;
-                ++ru;
-            }
+            if (++rs == static_cast<uint32_t>(plan.rope_slots)) rs = 0;
         }
         // The piece is done: write its rows, or its part of them.
         across_lanes<N>(l, [](float a, float d) { return a + d; });
@@ -784,8 +768,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             if (!sees) c.ref[tid] = -INFINITY;
         }
         soft_sync();
-        mbar_wait(&c.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1u, &c.abort);
-        __syncwarp();
+        wait(&c.o_done[(i - 1) & 1], (i - 1) >> 1, c);
         tc_fence_after();
         const bool direct = at.b0 == 0 && at.b1 == at.blocks;
         if (direct) {
@@ -851,11 +834,10 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     Ctrl &c = *reinterpret_cast<Ctrl *>(ropes + plan.rope_slots * CHUNK);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
+        for (int s = 0; s < BLOCKS; ++s) mbar_init(&c.full[s], LOAD + LOAD / 32);
         for (int s = 0; s < MAX_SLOTS; ++s) {
-            mbar_init(&c.full[0][s], LOAD);
-            mbar_init(&c.full[1][s], LOAD + LOAD / 32);
-            mbar_init(&c.empty[0][s], 1);
-            mbar_init(&c.empty[1][s], 1);
+            mbar_init(&c.pair_empty[s], 1);
+            mbar_init(&c.rope_empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&c.s_full[s], 1);
