@@ -51,12 +51,12 @@ topk_status_t check_attend(const latent_bf16_attend_t *a, bool paged) {
     if (a->heads < 1 || a->heads > LATENT_MAX_HEADS || !std::isfinite(a->scale)) return TOPK_ERR_ARG;
     if (static_cast<int64_t>(a->tokens) * a->heads > INT32_MAX) return TOPK_ERR_ARG;
     if (paged) {
-        if (a->width < 0) return TOPK_ERR_WIDTH;
+        if (a->width < 0 || a->width > LATENT_MAX_LENGTH) return TOPK_ERR_WIDTH;
         if (a->page_size < 1 || (a->page_size & (a->page_size - 1)) || a->block_rows < a->page_size ||
             a->rows_per_request < 1)
             return TOPK_ERR_ARG;
         if (a->table_stride < (static_cast<int64_t>(a->width) + a->page_size - 1) / a->page_size) return TOPK_ERR_ARG;
-    } else if (a->k < 0) {
+    } else if (a->k < 0 || a->k > LATENT_MAX_LENGTH) {
         return TOPK_ERR_ARG;
     } else if (a->selected_stride < a->k) {
         return TOPK_ERR_WIDTH;

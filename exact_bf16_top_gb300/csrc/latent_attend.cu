@@ -13,9 +13,10 @@ namespace topk::latent {
 namespace {
 
 constexpr int SOFT = 128;                    // warps 0 to 3: softmax and outputs
-constexpr int LOAD = 256;                    // warps 4 to 11: cache rows
-constexpr int QLOAD = 64;                    // warps 12 and 13: query rows
-constexpr int NT = SOFT + LOAD + QLOAD + 32; // warp 14: the tensor cores
+constexpr int LOAD = 256;                    // warps 4 to 11: the latent part of cache rows
+constexpr int ROPE_LOAD = 32;                // warp 12: their rotary part
+constexpr int QLOAD = 64;                    // warps 13 and 14: query rows
+constexpr int NT = SOFT + LOAD + ROPE_LOAD + QLOAD + 32; // warp 15: the tensor cores
 constexpr int NT_JOIN = 256;
 constexpr int ROWS = 64;                     // query rows of a tile
 constexpr int KEYS = 64;                     // cache rows of a block
@@ -25,6 +26,7 @@ constexpr int BLOCKS = 16;                   // blocks that have barriers and ro
                                              // the rings hold
 constexpr int SMEM = 232448;                 // all of a CTA's shared memory
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
+constexpr int POLLS = 1 << 16;               // tries before a choice between two arrivals becomes a wait
 constexpr float LAZY = 60.0f;                // the reference may lag the maximum by this much (log2)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 using u64 = unsigned long long;
@@ -55,6 +57,7 @@ struct Ctrl {
 // each), a ring of pairs of latent chunks, a ring of rotary chunks (where a
 // block's weights go once its scores are out), the control block.
 struct Plan {
+    int parts;                                 // warps that load one pair of a block
     int pairs, pair_slots, rope_slots;         // pairs per block; slots: two blocks' at least
     uint32_t query_bytes;
 };
@@ -63,6 +66,7 @@ template <int NR>
 __host__ __device__ constexpr Plan make_plan(int latent) {
     Plan r = {};
     r.pairs = latent / 128;
+    r.parts = r.pairs == 1 ? 8 : r.pairs == 2 ? 4 : 2;
     r.query_bytes = static_cast<uint32_t>((2 * r.pairs + 1) * NR * 128);
     const int units = static_cast<int>((SMEM - 1024 - sizeof(Ctrl) - r.query_bytes) / CHUNK);
     r.rope_slots = units / (2 * r.pairs + 1);
@@ -86,6 +90,17 @@ __device__ __forceinline__ void arrive(u64 *bar) {
 __device__ __forceinline__ void wait(u64 *bar, uint32_t parity, Ctrl &c) {
     mbar_wait(bar, parity & 1u, &c.abort);
     __syncwarp();
+}
+
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool arrived(u64 *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity & 1u)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -346,67 +361,91 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
 
 // ------------------------------------------------------------------ the warps' parts
 
-// Cache rows into the rings, swizzled as the products read them. A warp copies
-// eight rows of every block: half a warp a row's 256 bytes of a pair, a quarter
-// its 128 rotary bytes. Places that hold no cache row are filled with zeros.
-// (Measured: the same rows gathered four at a time by TMA come at 12 bytes a
-// nanosecond per SM; copies of 16 bytes reach 100 from L2 with four warps.)
-__device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t pairs, uint32_t ropes) {
-    constexpr int WARPS = LOAD / 32;
-    static_assert(KEYS == 8 * WARPS);
+// The row numbers of a tile's blocks: entry j of its list or pages, -1 for none.
+struct RowList {
+    const int32_t *list;
+    int32_t len;
+    __device__ RowList(const AttendParams &p, const Cursor &at)
+        : list(p.paged ? p.table + static_cast<int64_t>(at.tile.request) * p.table_stride
+                       : p.selected + static_cast<int64_t>(at.tile.token) * p.selected_stride),
+          len(min(at.len, at.b1 * KEYS)) {}
+    __device__ int32_t row(const AttendParams &p, int32_t j) const {
+        if (j >= len) return -1;
+        int64_t v;
+        if (p.paged)
+            v = static_cast<int64_t>(__ldg(list + (j >> p.page_shift))) * p.block_rows + (j & ((1 << p.page_shift) - 1));
+        else
+            v = __ldg(list + j);
+        return v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
+    }
+};
+
+// Cache rows into the rings, swizzled as the products read them. Each warp has
+// one pair of every block (and with few pairs only some of its rows), so that
+// it waits for one slot a block and the pairs of a block are copied side by
+// side as their slots come free. Places that hold no cache row are filled with
+// zeros. (Measured: the same rows gathered four at a time by TMA come at 12
+// bytes a nanosecond per SM; copies of 16 bytes reach 100 from L2 with four
+// warps.)
+__device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t pairs) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - SOFT) >> 5;
+    const int unit = warp % plan.pairs, part = warp / plan.pairs;
+    if (part >= plan.parts) return;
     const int64_t pitch = p.cache_stride * 2;
-    const char *cache = reinterpret_cast<const char *>(p.cache);
-    // Row j of the warp's eight is row `place(j)` of the block.
-    auto place = [&](int j) { return 2 * warp + (j & 1) + 2 * WARPS * (j >> 1); };
-    const int half = lane >> 4, piece = lane & 15, quarter = lane >> 3, rope_piece = lane & 7;
+    const int rows = KEYS / plan.parts, half = lane >> 4, piece = lane & 15;
+    const char *cache = reinterpret_cast<const char *>(p.cache) + unit * 256 + piece * 16;
+    const int r0 = part * rows + half;         // this lane copies rows r0, r0 + 2, ..
+    const uint32_t dst = pairs + (piece >> 3) * CHUNK + r0 * 128;
     Cursor at(c);
-    uint32_t i = 0, ps = 0, pu = 0, rs = 0, ru = 0;   // block; pair slot and its use; rope slot and its use
+    uint32_t i = 0, ps = unit, pu = 0;         // block; slot and its use
     while (at.next(p, lane)) {
-        const int32_t *list = p.paged ? p.table + static_cast<int64_t>(at.tile.request) * p.table_stride
-                                      : p.selected + static_cast<int64_t>(at.tile.token) * p.selected_stride;
-        auto row = [&](int32_t b) -> int32_t {         // lane's (lane & 7)th row of block b
-            const int32_t j = b * KEYS + place(lane & 7);
-            if (b >= at.b1 || j >= at.len) return -1;
-            int64_t v;
-            if (p.paged)
-                v = static_cast<int64_t>(__ldg(list + (j >> p.page_shift))) * p.block_rows +
-                    (j & ((1 << p.page_shift) - 1));
-            else
-                v = __ldg(list + j);
-            return v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
-        };
-        int32_t now = row(at.b0);
+        const RowList list(p, at);
+        const int mine = part * rows + (lane & (rows - 1));
+        int32_t now = list.row(p, at.b0 * KEYS + mine);
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
-            const int32_t then = row(b + 1);
-            if (lane < 8) c.rows[i % BLOCKS][place(lane)] = now;
-            const char *src[4];
-            bool on[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            const int32_t then = list.row(p, (b + 1) * KEYS + mine);
+            wait(&c.pair_empty[ps], pu + 1, c);
+            const uint32_t to = dst + ps * 2 * CHUNK;
+#pragma unroll 4
+            for (int k = 0; k < rows / 2; ++k) {
                 const int32_t v = __shfl_sync(0xFFFFFFFFu, now, 2 * k + half);
-                on[k] = v >= 0;
-                src[k] = cache + (on[k] ? v * pitch : 0) + piece * 16;
+                copy16(to + k * 256 + (((piece ^ (r0 + 2 * k)) & 7) << 4), cache + (v >= 0 ? v * pitch : 0), v >= 0);
             }
-            const int r = place(half);
-            const uint32_t dst = (piece >> 3) * CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-            for (int u = 0; u < plan.pairs; ++u) {
-                wait(&c.pair_empty[ps], pu + 1, c);
+            copies_arrive(&c.full[i % BLOCKS]);
+            ps += plan.pairs;
+            if (ps >= static_cast<uint32_t>(plan.pair_slots)) {
+                ps -= plan.pair_slots;
+                ++pu;
+            }
+            now = then;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ void load_ropes(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t ropes) {
+    const int lane = threadIdx.x & 31, quarter = lane >> 3, piece = lane & 7;
+    const int64_t pitch = p.cache_stride * 2;
+    const char *cache = reinterpret_cast<const char *>(p.cache) + plan.pairs * 256 + piece * 16;
+    Cursor at(c);
+    uint32_t i = 0, rs = 0, ru = 0;
+    while (at.next(p, lane)) {
+        const RowList list(p, at);
+        int32_t now[2], then[2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    copy16(pairs + ps * 2 * CHUNK + dst + k * 2 * WARPS * 128, src[k] + u * 256, on[k]);
-                if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
-                    ps = 0;
-                    ++pu;
-                }
+        for (int h = 0; h < 2; ++h) now[h] = list.row(p, at.b0 * KEYS + 32 * h + lane);
+        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                then[h] = list.row(p, (b + 1) * KEYS + 32 * h + lane);
+                c.rows[i % BLOCKS][32 * h + lane] = now[h];
             }
             wait(&c.rope_empty[rs], ru + 1, c);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int j = quarter + 4 * k, at_row = place(j);
-                const int32_t v = __shfl_sync(0xFFFFFFFFu, now, j);
-                copy16(ropes + rs * CHUNK + at_row * 128 + ((rope_piece ^ (at_row & 7)) << 4),
-                       cache + (v >= 0 ? v * pitch : 0) + plan.pairs * 256 + rope_piece * 16, v >= 0);
+            for (int k = 0; k < KEYS / 4; ++k) {
+                const int r = 4 * k + quarter;
+                const int32_t v = __shfl_sync(0xFFFFFFFFu, now[k / 8], r & 31);
+                copy16(ropes + rs * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4), cache + (v >= 0 ? v * pitch : 0), v >= 0);
             }
             copies_arrive(&c.full[i % BLOCKS]);
             __syncwarp();
@@ -415,7 +454,8 @@ __device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint
                 rs = 0;
                 ++ru;
             }
-            now = then;
+            now[0] = then[0];
+            now[1] = then[1];
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -427,8 +467,10 @@ __device__ void load_rows(const AttendParams &p, Ctrl &c, const Plan &plan, uint
 //   sums[value][row]  += V pair (values x tokens) x weights         (128 x NR x 16 a step)
 // A step takes the longer of its arithmetic and its operands' way out of shared
 // memory at 128 bytes a cycle (measured: 23 and 39 cycles at NR = 16, 32 and 48
-// at NR = 64). Block i's scores are issued before block i - 1's sums, so that
-// the tensor cores work while the softmax warps turn scores into weights.
+// at NR = 64). Block i's scores and block i - 1's sums are issued in the order
+// in which their operands arrive: the scores first while loads keep up (the
+// tensor cores then work while the softmax warps turn scores into weights), the
+// sums first where they do not, which frees their slots for the loads.
 template <int NR>
 __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, uint32_t pairs,
                          uint32_t ropes, uint32_t tmem) {
@@ -468,6 +510,13 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
                 wait(&c.q_full, piece, c);
             }
             wait(&c.s_empty[i & 1], (i >> 1) + 1, c);
+            for (int n = 0; pending && n < POLLS; ++n) {
+                if (__any_sync(0xFFFFFFFFu, arrived(&c.full[i % BLOCKS], i / BLOCKS) || c.abort)) break;
+                if (__any_sync(0xFFFFFFFFu, arrived(&c.p_full[(i - 1) & 1], (i - 1) >> 1))) {
+                    sum();
+                    pending = false;
+                }
+            }
             wait(&c.full[i % BLOCKS], i / BLOCKS, c);
             fence_proxy_async();              // (the rows were written by ordinary copies)
             tc_fence_after();
@@ -515,7 +564,7 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
 // weights and sums, and nothing is written for those.
 template <int NR>
 __device__ void load_query(const AttendParams &p, Ctrl &c, uint32_t query, int chunks) {
-    const int tid = threadIdx.x - SOFT - LOAD, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x - SOFT - LOAD - ROPE_LOAD, lane = threadIdx.x & 31;
     Cursor at(c);
     uint32_t n = 0;
     while (at.next(p, lane)) {
@@ -834,7 +883,7 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     Ctrl &c = *reinterpret_cast<Ctrl *>(ropes + plan.rope_slots * CHUNK);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < BLOCKS; ++s) mbar_init(&c.full[s], LOAD + LOAD / 32);
+        for (int s = 0; s < BLOCKS; ++s) mbar_init(&c.full[s], 32 * plan.pairs * plan.parts + ROPE_LOAD + 1);
         for (int s = 0; s < MAX_SLOTS; ++s) {
             mbar_init(&c.pair_empty[s], 1);
             mbar_init(&c.rope_empty[s], 1);
@@ -864,8 +913,9 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     if (warp < SOFT / 32) soften<NR>(p, c, plan, pairs, ropes, tmem);
-    else if (warp < (SOFT + LOAD) / 32) load_rows(p, c, plan, smem_addr(pairs), smem_addr(ropes));
-    else if (warp < (SOFT + LOAD + QLOAD) / 32) load_query<NR>(p, c, smem_addr(smem), 2 * plan.pairs + 1);
+    else if (warp < (SOFT + LOAD) / 32) load_pairs(p, c, plan, smem_addr(pairs));
+    else if (warp < (SOFT + LOAD + ROPE_LOAD) / 32) load_ropes(p, c, plan, smem_addr(ropes));
+    else if (warp < NT / 32 - 1) load_query<NR>(p, c, smem_addr(smem), 2 * plan.pairs + 1);
     else multiply<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
     __syncwarp();
     tc_fence_before();

@@ -41,6 +41,7 @@ extern "C" {
 #define LATENT_ROPE 64        /* rotated values of a cache row */
 #define LATENT_MAX 512        /* largest latent */
 #define LATENT_MAX_HEADS 256  /* query heads per token */
+#define LATENT_MAX_LENGTH (1 << 30)  /* list entries or width of an attention call */
 
 /*
  * Appends tokens to the cache: for token t with row slots[t] in [0, cache_rows)
@@ -121,7 +122,7 @@ topk_status_t latent_bf16_append(const latent_bf16_append_t *args, void *stream)
  * table_stride >= ceil(width / page_size).
  *
  * Errors: TOPK_ERR_ARG (null pointer, negative count, heads outside
- * [1, LATENT_MAX_HEADS], a bad page size, block_rows, table stride, workspace
+ * [1, LATENT_MAX_HEADS], k above LATENT_MAX_LENGTH, a bad page size, block_rows, table stride, workspace
  * size or rows_per_request, a scale that is not finite), TOPK_ERR_WIDTH
  * (latent, width, or a stride below its row), TOPK_ERR_ALIGN, TOPK_ERR_CUDA.
  */
