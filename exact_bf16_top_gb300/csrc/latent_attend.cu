@@ -12,8 +12,8 @@ namespace topk::latent {
 
 namespace {
 
-constexpr int SOFT = 128;                    // warps 0 to 3: softmax and outputs
-constexpr int LOAD = 256;                    // warps 4 to 11: the latent part of cache rows
+constexpr int SOFT = 256;                    // warps 0 to 7: softmax and outputs, in two groups
+constexpr int LOAD = 128;                    // warps 8 to 11: the latent part of cache rows
 constexpr int ROPE_LOAD = 32;                // warp 12: their rotary part
 constexpr int QLOAD = 64;                    // warps 13 and 14: query rows
 constexpr int NT = SOFT + LOAD + ROPE_LOAD + QLOAD + 32; // warp 15: the tensor cores
@@ -22,8 +22,7 @@ constexpr int ROWS = 64;                     // query rows of a tile
 constexpr int KEYS = 64;                     // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
 constexpr int MAX_SLOTS = 12;                // most slots of either ring
-constexpr int BLOCKS = 16;                   // blocks that have barriers and row numbers of their own: more than
-                                             // the rings hold
+constexpr int BLOCKS = 16;                   // blocks whose row numbers are kept: more than the rings hold
 constexpr int SMEM = 232448;                 // all of a CTA's shared memory
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
 constexpr int POLLS = 1 << 16;               // tries before a choice between two arrivals becomes a wait
@@ -32,7 +31,7 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 using u64 = unsigned long long;
 
 struct Ctrl {
-    u64 full[BLOCKS];                          // a block's rows are in
+    u64 pair_full[MAX_SLOTS], rope_full[MAX_SLOTS];     // a slot's rows are in
     u64 pair_empty[MAX_SLOTS], rope_empty[MAX_SLOTS];   // a slot is used up
     u64 s_full[2], s_empty[2];                 // scores written / read
     u64 p_full[2], o_done[2];                  // a block's weights are in / its sums are added (by turns: who
@@ -49,7 +48,7 @@ struct Ctrl {
     alignas(16) float factor[ROWS];
     float l[ROWS];
     int32_t lim[ROWS];                         // tokens a row may see
-    float across[SOFT / 32][ROWS];
+    float across[4][ROWS];
     int32_t rows[BLOCKS][KEYS];                // cache row numbers of a block, -1: none
 };
 
@@ -66,7 +65,7 @@ template <int NR>
 __host__ __device__ constexpr Plan make_plan(int latent) {
     Plan r = {};
     r.pairs = latent / 128;
-    r.parts = r.pairs == 1 ? 8 : r.pairs == 2 ? 4 : 2;
+    r.parts = r.pairs == 1 ? 4 : r.pairs == 2 ? 2 : 1;
     r.query_bytes = static_cast<uint32_t>((2 * r.pairs + 1) * NR * 128);
     const int units = static_cast<int>((SMEM - 1024 - sizeof(Ctrl) - r.query_bytes) / CHUNK);
     r.rope_slots = units / (2 * r.pairs + 1);
@@ -149,25 +148,19 @@ __host__ __device__ constexpr uint32_t instruction(int m, int n, bool along) {
 template <int N>
 __device__ __forceinline__ void tc_load_groups(uint32_t addr, float (&v)[4 * N]) {
     uint32_t r[4 * N];
-    if constexpr (N == 2)
+    if constexpr (N == 1)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+    else if constexpr (N == 2)
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(addr));
-    else if constexpr (N == 4)
+    else
         asm volatile(
             "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
               "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(addr));
-    else
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
-            "%28,%29,%30,%31}, [%32];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-              "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-              "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
             : "r"(addr));
     tc_wait_ld();
 #pragma unroll
@@ -397,27 +390,36 @@ __device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uin
     const int r0 = part * rows + half;         // this lane copies rows r0, r0 + 2, ..
     const uint32_t dst = pairs + (piece >> 3) * CHUNK + r0 * 128;
     Cursor at(c);
-    uint32_t i = 0, ps = unit, pu = 0;         // block; slot and its use
+    uint32_t ps = unit, pu = 0;                // slot and its use
     while (at.next(p, lane)) {
         const RowList list(p, at);
         const int mine = part * rows + (lane & (rows - 1));
-        int32_t now = list.row(p, at.b0 * KEYS + mine);
-        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
-            const int32_t then = list.row(p, (b + 1) * KEYS + mine);
+        int32_t now[2], then[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) now[h] = list.row(p, at.b0 * KEYS + mine + 32 * h);
+        for (int32_t b = at.b0; b < at.b1; ++b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) then[h] = list.row(p, (b + 1) * KEYS + mine + 32 * h);
             wait(&c.pair_empty[ps], pu + 1, c);
             const uint32_t to = dst + ps * 2 * CHUNK;
-#pragma unroll 4
-            for (int k = 0; k < rows / 2; ++k) {
-                const int32_t v = __shfl_sync(0xFFFFFFFFu, now, 2 * k + half);
-                copy16(to + k * 256 + (((piece ^ (r0 + 2 * k)) & 7) << 4), cache + (v >= 0 ? v * pitch : 0), v >= 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (32 * h >= rows) break;
+#pragma unroll 8
+                for (int k = 0; k < min(rows, 32) / 2; ++k) {
+                    const int32_t v = __shfl_sync(0xFFFFFFFFu, now[h], 2 * k + half);
+                    copy16(to + h * 32 * 128 + k * 256 + (((piece ^ (r0 + 2 * k)) & 7) << 4),
+                           cache + (v >= 0 ? v * pitch : 0), v >= 0);
+                }
             }
-            copies_arrive(&c.full[i % BLOCKS]);
+            copies_arrive(&c.pair_full[ps]);
             ps += plan.pairs;
             if (ps >= static_cast<uint32_t>(plan.pair_slots)) {
                 ps -= plan.pair_slots;
                 ++pu;
             }
-            now = then;
+            now[0] = then[0];
+            now[1] = then[1];
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -447,9 +449,9 @@ __device__ void load_ropes(const AttendParams &p, Ctrl &c, const Plan &plan, uin
                 const int32_t v = __shfl_sync(0xFFFFFFFFu, now[k / 8], r & 31);
                 copy16(ropes + rs * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4), cache + (v >= 0 ? v * pitch : 0), v >= 0);
             }
-            copies_arrive(&c.full[i % BLOCKS]);
+            copies_arrive(&c.rope_full[rs]);
             __syncwarp();
-            if (lane == 0) arrive(&c.full[i % BLOCKS]);     // (makes the row numbers visible)
+            if (lane == 0) arrive(&c.rope_full[rs]);   // (makes the row numbers visible)
             if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
                 rs = 0;
                 ++ru;
@@ -478,7 +480,7 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
     constexpr uint32_t QK = instruction(KEYS, NR, false), PV = instruction(128, NR, true);
     constexpr int QCHUNK = NR * 128;
     Cursor at(c);
-    uint32_t i = 0, piece = 0, ps = 0, rs = 0;
+    uint32_t i = 0, piece = 0, ps = 0, pu = 0, rs = 0, ru = 0;
     uint32_t last_ps = 0, last_rs = 0;       // where block i - 1 begins
     bool first = true, pending = false;
     const uint64_t q = matrix(query, 16);
@@ -511,32 +513,39 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
             }
             wait(&c.s_empty[i & 1], (i >> 1) + 1, c);
             for (int n = 0; pending && n < POLLS; ++n) {
-                if (__any_sync(0xFFFFFFFFu, arrived(&c.full[i % BLOCKS], i / BLOCKS) || c.abort)) break;
+                if (__any_sync(0xFFFFFFFFu, arrived(&c.pair_full[ps], pu) || c.abort)) break;
                 if (__any_sync(0xFFFFFFFFu, arrived(&c.p_full[(i - 1) & 1], (i - 1) >> 1))) {
                     sum();
                     pending = false;
                 }
             }
-            wait(&c.full[i % BLOCKS], i / BLOCKS, c);
-            fence_proxy_async();              // (the rows were written by ordinary copies)
-            tc_fence_after();
-            const uint32_t this_ps = ps;
-            if (elected()) {
-                const uint32_t d = tmem + S_COL + (i & 1) * NR;
-                uint32_t s = ps;
-                for (int u = 0; u < plan.pairs; ++u) {
-                    const uint64_t k = matrix(pairs + s * 2 * CHUNK, 16), qu = q + u * (2 * QCHUNK >> 4);
+            const uint32_t this_ps = ps, d = tmem + S_COL + (i & 1) * NR;
+            for (int u = 0; u <= plan.pairs; ++u) {
+                const bool rope = u == plan.pairs;
+                if (rope)
+                    wait(&c.rope_full[rs], ru, c);
+                else
+                    wait(&c.pair_full[ps], pu, c);
+                fence_proxy_async();          // (the rows were written by ordinary copies)
+                tc_fence_after();
+                if (elected()) {
+                    const uint64_t k = matrix(rope ? ropes + rs * CHUNK : pairs + ps * 2 * CHUNK, 16);
+                    const uint64_t qu = q + u * (2 * QCHUNK >> 4);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        tc_mma(d, k + (e >> 2) * (CHUNK >> 4) + (e & 3) * 2, qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2,
-                               QK, u > 0 || e > 0);
-                    if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
+                    for (int e = 0; e < 4; ++e) tc_mma(d, k + e * 2, qu + e * 2, QK, u > 0 || e > 0);
+                    if (!rope) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            tc_mma(d, k + (CHUNK >> 4) + e * 2, qu + (QCHUNK >> 4) + e * 2, QK, true);
+                    } else {
+                        tc_commit(&c.s_full[i & 1]);
+                        if (b + 1 == at.b1) tc_commit(&c.q_empty);
+                    }
                 }
-                const uint64_t k = matrix(ropes + rs * CHUNK, 16), qu = q + plan.pairs * (2 * QCHUNK >> 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) tc_mma(d, k + e * 2, qu + e * 2, QK, true);
-                tc_commit(&c.s_full[i & 1]);
-                if (b + 1 == at.b1) tc_commit(&c.q_empty);
+                if (!rope && ++ps == static_cast<uint32_t>(plan.pair_slots)) {
+                    ps = 0;
+                    ++pu;
+                }
             }
             __syncwarp();
             if (pending) sum();
@@ -544,9 +553,10 @@ __device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint3
             first = b == at.b0;
             last_ps = this_ps;
             last_rs = rs;
-            ps += plan.pairs;
-            if (ps >= static_cast<uint32_t>(plan.pair_slots)) ps -= plan.pair_slots;
-            if (++rs == static_cast<uint32_t>(plan.rope_slots)) rs = 0;
+            if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
+                rs = 0;
+                ++ru;
+            }
         }
         ++piece;
     }
@@ -624,27 +634,27 @@ __device__ __forceinline__ int across_index() {
     return r;
 }
 
-// Scores to weights, the running reference and sums, and the outputs. Thread t
-// of warp w holds tokens 16 w + t / 4 and 8 further of a block, against the
-// query rows 8 j + 2 (t % 4) and the next: their references and sums stay in
-// its registers. The weights' reference is the maximum of the row's first
+// Scores to weights, the running reference and sums, and the outputs. Each group
+// of four warps has half of the query rows. Thread t of a group's warp w holds
+// tokens 16 w + t / 4 and 8 further of a block, against the rows 8 j + 2 (t % 4)
+// and the next of its half: their references and sums stay in its registers. The weights' reference is the maximum of the row's first
 // block; weights may grow to 2^60 before it moves (FP32 sums and BF16 weights
 // lose nothing by that), which is seen from the packed weights and almost never
 // happens.
 template <int NR>
 __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *pairs, char *ropes, uint32_t tmem) {
-    constexpr int N = NR / 4;                  // query rows of a thread
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, quad = lane & 3;
+    constexpr int N = NR / 8;                  // query rows of a thread
+    const int tid = threadIdx.x, lane = tid & 31, w = (tid >> 5) & 3, group = tid >> 7, quad = lane & 3;
     const int t0 = w * 16 + lane / 4;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
     const float scale = p.scale * LOG2E;
     Part *parts = reinterpret_cast<Part *>(p.workspace);
     Joint *joints = reinterpret_cast<Joint *>(parts + 2 * p.sms);
     const bool by_tile = p.tiles <= static_cast<int32_t>(gridDim.x);
-    auto row_of = [&](int n) { return 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
+    auto row_of = [&](int n) { return group * (NR / 2) + 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
     bool split_here = false;
     Cursor at(c);
-    uint32_t i = 0, ps = 0, rs = 0;
+    uint32_t i = 0, ps = 0, rs = 0, ru = 0;
     long long done = c.begin;
     while (at.next(p, lane)) {
         const int32_t start = at.b0 * KEYS;
@@ -672,13 +682,13 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
         }
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
             mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
-            wait(&c.full[i % BLOCKS], i / BLOCKS, c);       // (complete: makes the row numbers visible)
+            wait(&c.rope_full[rs], ru, c);             // (complete: makes the row numbers visible)
             const int32_t token = b * KEYS + t0;
             const bool there[2] = {c.rows[i % BLOCKS][t0] >= 0, c.rows[i % BLOCKS][t0 + 8] >= 0};
             const bool whole = __all_sync(0xFFFFFFFFu, there[0] && there[1]) && (b + 1) * KEYS <= low;
-            const uint32_t scores = lanes + S_COL + (i & 1) * NR;
+            const uint32_t scores = lanes + S_COL + (i & 1) * NR + group * (NR / 2);
             char *weights = ropes + rs * CHUNK + t0 * 128 + quad * 4;
-            float x[2 * N];                    // x[4 j + 2 h + e]: token h, row 8 j + 2 quad + e
+            float x[2 * N];                    // x[4 j + 2 h + e]: token h, the thread's row 2 j + e
             bool bad[2] = {false, false};
             // Scores in log2 units; where masked, -inf. A cache row that only some of the
             // tile's rows see must not reach the others through 0 x inf: where a score that
@@ -687,11 +697,14 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             // see it are NaN.
             auto take = [&]() {
                 tc_fence_after();
-                tc_load_groups<NR / 8>(scores, x);
+                tc_load_groups<NR / 16>(scores, x);
                 tc_fence_before();
 #pragma unroll
                 for (int e = 0; e < 2 * N; ++e) x[e] *= scale;
-                if (!whole) {
+                if (!whole && !p.paged) {      // a place that holds no cache row is masked for every row
+#pragma unroll
+                    for (int e = 0; e < 2 * N; ++e) x[e] = there[(e >> 1) & 1] ? x[e] : -INFINITY;
+                } else if (!whole) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         bool odd = false;
@@ -720,7 +733,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             auto weigh = [&]() -> bool {
                 __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-                for (int j = 0; j < NR / 8; ++j)
+                for (int j = 0; j < N / 2; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float &a = x[4 * j + 2 * h], &d = x[4 * j + 2 * h + 1];
@@ -729,7 +742,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                         d = d == -INFINITY ? 0.0f : ed;
                         const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
                         top = __hmax2(top, v);
-                        *reinterpret_cast<__nv_bfloat162 *>(weights + h * 1024 + ((j ^ (t0 & 7)) << 4)) = v;
+                        *reinterpret_cast<__nv_bfloat162 *>(weights + h * 1024 + (((group * (N / 2) + j) ^ (t0 & 7)) << 4)) = v;
                     }
                 return fmaxf(__low2float(top), __high2float(top)) > 1.152921504606846976e18f;   // 2^60
             };
@@ -769,6 +782,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                     for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
                         for (int v = 0; v < NR; v += 16) {
+                            if (((h * (NR / 16) + v / 16) & 1) != group) continue;
                             float o[16];
                             tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
@@ -801,7 +815,10 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             }
             ps += plan.pairs;
             if (ps >= static_cast<uint32_t>(plan.pair_slots)) ps -= plan.pair_slots;
-            if (++rs == static_cast<uint32_t>(plan.rope_slots)) rs = 0;
+            if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
+                rs = 0;
+                ++ru;
+            }
         }
         // The piece is done: write its rows, or its part of them.
         across_lanes<N>(l, [](float a, float d) { return a + d; });
@@ -826,6 +843,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
                 for (int v = 0; v < NR; v += 16) {
+                    if (((h * (NR / 16) + v / 16) & 1) != group) continue;
                     float o[16];
                     tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
@@ -851,6 +869,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
                 for (int v = 0; v < NR; v += 16) {
+                    if (((h * (NR / 16) + v / 16) & 1) != group) continue;
                     float o[16];
                     tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
@@ -883,8 +902,9 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     Ctrl &c = *reinterpret_cast<Ctrl *>(ropes + plan.rope_slots * CHUNK);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < BLOCKS; ++s) mbar_init(&c.full[s], 32 * plan.pairs * plan.parts + ROPE_LOAD + 1);
         for (int s = 0; s < MAX_SLOTS; ++s) {
+            mbar_init(&c.pair_full[s], 32 * plan.parts);
+            mbar_init(&c.rope_full[s], ROPE_LOAD + 1);
             mbar_init(&c.pair_empty[s], 1);
             mbar_init(&c.rope_empty[s], 1);
         }
