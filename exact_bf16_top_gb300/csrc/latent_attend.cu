@@ -13,19 +13,18 @@ namespace topk::latent {
 namespace {
 
 constexpr int SOFT = 256;                    // warps 0 to 7: softmax and outputs, in two groups
-constexpr int LOAD = 128;                    // warps 8 to 11: the latent part of cache rows
-constexpr int ROPE_LOAD = 32;                // warp 12: their rotary part
-constexpr int QLOAD = 64;                    // warps 13 and 14: query rows
-constexpr int NT = SOFT + LOAD + ROPE_LOAD + QLOAD + 32; // warp 15: the tensor cores
+constexpr int LOAD = 128;                    // warps 8 to 11: query rows, the latent part of cache rows
+constexpr int ROPE_LOAD = 32;                // warp 12: the rotary part
+constexpr int NT = SOFT + LOAD + ROPE_LOAD + 64;   // warps 13 and 14: the tensor cores (scores, sums)
 constexpr int NT_JOIN = 256;
 constexpr int ROWS = 64;                     // query rows of a tile
 constexpr int KEYS = 64;                     // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
 constexpr int MAX_SLOTS = 12;                // most slots of either ring
-constexpr int BLOCKS = 16;                   // blocks whose row numbers are kept: more than the rings hold
+constexpr int BLOCKS = 16;                   // blocks that have row numbers and barriers of their own: more
+                                             // than the rings hold
 constexpr int SMEM = 232448;                 // all of a CTA's shared memory
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
-constexpr int POLLS = 1 << 16;               // tries before a choice between two arrivals becomes a wait
 constexpr float LAZY = 60.0f;                // the reference may lag the maximum by this much (log2)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 using u64 = unsigned long long;
@@ -34,11 +33,11 @@ struct Ctrl {
     u64 pair_full[MAX_SLOTS], rope_full[MAX_SLOTS];     // a slot's rows are in
     u64 pair_empty[MAX_SLOTS], rope_empty[MAX_SLOTS];   // a slot is used up
     u64 s_full[2], s_empty[2];                 // scores written / read
-    u64 p_full[2], o_done[2];                  // a block's weights are in / its sums are added (by turns: who
-                                               // waits for block i - 1 may meet block i's, and two phases of one
+    u64 p_full[BLOCKS], o_done[BLOCKS];        // a block's weights are in / its sums are added (one each: who waits
+                                               // for one block may find later ones done, and two phases of one
                                                // barrier look like none)
     u64 q_full, q_empty;                       // the query tile is in / used up
-    u64 drain;
+    u64 drain[2];
     long long sums[NT / 32];
     int32_t first_tile, first_block;
     long long begin, share, total;
@@ -91,23 +90,14 @@ __device__ __forceinline__ void wait(u64 *bar, uint32_t parity, Ctrl &c) {
     __syncwarp();
 }
 
-// Whether a phase is over, without waiting.
-__device__ __forceinline__ bool arrived(u64 *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity & 1u)
-        : "memory");
-    return ok != 0;
-}
-
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// One lane of a converged warp.
+// One lane of a converged warp, by elect.sync: the compiler then knows that what
+// follows is one thread's and keeps descriptors in uniform registers (with
+// `lane == 0` in its place a step takes twice as long to issue).
 __device__ __forceinline__ bool elected() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -125,6 +115,16 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
         : "memory");
+}
+
+// Waits for all that the warp's elected lane issued: nothing may be running on
+// the tensor cores when their memory is freed.
+__device__ __forceinline__ void drain(u64 *bar, bool one) {
+    if (one) tc_commit(bar);
+    __syncwarp();
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, 0) && global_timer_ns() - t0 < WAIT_LIMIT_NS) {
+    }
 }
 
 // Matrix descriptor of a 128-byte-swizzled operand. `lead`: bytes between
@@ -373,24 +373,40 @@ struct RowList {
     }
 };
 
-// Cache rows into the rings, swizzled as the products read them. Each warp has
-// one pair of every block (and with few pairs only some of its rows), so that
-// it waits for one slot a block and the pairs of a block are copied side by
-// side as their slots come free. Places that hold no cache row are filled with
-// zeros. (Measured: the same rows gathered four at a time by TMA come at 12
-// bytes a nanosecond per SM; copies of 16 bytes reach 100 from L2 with four
-// warps.)
-__device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t pairs) {
+// A tile's query rows into shared memory, swizzled as the products read them, a
+// row's eighth of every chunk per thread. Rows past the tile's are left as they
+// are: every row is apart in scores, weights and sums, and nothing is written
+// for those.
+template <int NR>
+__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, uint32_t query, int chunks) {
+    const int tid = threadIdx.x - SOFT, piece = tid & 7;
+    for (int r = tid >> 3; r < tile.rows; r += LOAD / 8) {
+        const int32_t flat = tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
+        const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
+        const uint32_t dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
+        for (int k = 0; k < chunks; ++k) copy16(dst + k * NR * 128, src + k * 64, true);
+    }
+}
+
+// Query and cache rows into shared memory. Each warp has one pair of every
+// block (and with few pairs only some of its rows), so that it waits for one
+// slot a block and the pairs of a block are copied side by side as their slots
+// come free. Places that hold no cache row are filled with zeros. The first
+// tile's query is copied first, a later one's when its first block is on its way. (Measured: the same cache
+// rows gathered four at a time by TMA come at 12 bytes a nanosecond per SM;
+// copies of 16 bytes reach 100 from L2 with four warps.)
+template <int NR>
+__device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, uint32_t pairs) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - SOFT) >> 5;
     const int unit = warp % plan.pairs, part = warp / plan.pairs;
-    if (part >= plan.parts) return;
+    const bool idle = part >= plan.parts;      // (three pairs: one warp only helps with the query)
     const int64_t pitch = p.cache_stride * 2;
     const int rows = KEYS / plan.parts, half = lane >> 4, piece = lane & 15;
     const char *cache = reinterpret_cast<const char *>(p.cache) + unit * 256 + piece * 16;
     const int r0 = part * rows + half;         // this lane copies rows r0, r0 + 2, ..
     const uint32_t dst = pairs + (piece >> 3) * CHUNK + r0 * 128;
     Cursor at(c);
-    uint32_t ps = unit, pu = 0;                // slot and its use
+    uint32_t ps = unit, pu = 0, piece_no = 0;  // slot and its use
     while (at.next(p, lane)) {
         const RowList list(p, at);
         const int mine = part * rows + (lane & (rows - 1));
@@ -400,6 +416,12 @@ __device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uin
         for (int32_t b = at.b0; b < at.b1; ++b) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) then[h] = list.row(p, (b + 1) * KEYS + mine + 32 * h);
+            if (b == at.b0 + (piece_no ? 1 : 0)) {
+                wait(&c.q_empty, piece_no + 1, c);
+                load_query<NR>(p, at.tile, query, 2 * plan.pairs + 1);
+                copies_arrive(&c.q_full);
+            }
+            if (idle) continue;
             wait(&c.pair_empty[ps], pu + 1, c);
             const uint32_t to = dst + ps * 2 * CHUNK;
 #pragma unroll
@@ -421,6 +443,12 @@ __device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uin
             now[0] = then[0];
             now[1] = then[1];
         }
+        if (piece_no && at.b1 == at.b0 + 1) {
+            wait(&c.q_empty, piece_no + 1, c);
+            load_query<NR>(p, at.tile, query, 2 * plan.pairs + 1);
+            copies_arrive(&c.q_full);
+        }
+        ++piece_no;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -469,128 +497,90 @@ __device__ void load_ropes(const AttendParams &p, Ctrl &c, const Plan &plan, uin
 //   sums[value][row]  += V pair (values x tokens) x weights         (128 x NR x 16 a step)
 // A step takes the longer of its arithmetic and its operands' way out of shared
 // memory at 128 bytes a cycle (measured: 23 and 39 cycles at NR = 16, 32 and 48
-// at NR = 64). Block i's scores and block i - 1's sums are issued in the order
-// in which their operands arrive: the scores first while loads keep up (the
-// tensor cores then work while the softmax warps turn scores into weights), the
-// sums first where they do not, which frees their slots for the loads.
+// at NR = 64). Each product has a warp of its own, of which one lane issues: the
+// tensor cores take the steps in the order in which operands arrive, and one
+// product's waiting does not hold up the other.
 template <int NR>
-__device__ void multiply(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, uint32_t pairs,
-                         uint32_t ropes, uint32_t tmem) {
+__device__ void multiply_scores(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, uint32_t pairs,
+                                uint32_t ropes, uint32_t tmem) {
     const int lane = threadIdx.x & 31;
-    constexpr uint32_t QK = instruction(KEYS, NR, false), PV = instruction(128, NR, true);
+    const bool one = elected();
+    constexpr uint32_t KIND = instruction(KEYS, NR, false);
     constexpr int QCHUNK = NR * 128;
     Cursor at(c);
     uint32_t i = 0, piece = 0, ps = 0, pu = 0, rs = 0, ru = 0;
-    uint32_t last_ps = 0, last_rs = 0;       // where block i - 1 begins
-    bool first = true, pending = false;
     const uint64_t q = matrix(query, 16);
-    auto sum = [&]() {                        // of block i - 1
-        wait(&c.p_full[(i - 1) & 1], (i - 1) >> 1, c);
-        tc_fence_after();
-        if (elected()) {
-            const uint64_t w = matrix(ropes + last_rs * CHUNK, 16);
-            uint32_t s = last_ps;
-            for (int h = 0; h < plan.pairs; ++h) {
-                const uint64_t v = matrix(pairs + s * 2 * CHUNK, CHUNK);
-#pragma unroll
-                for (int k = 0; k < KEYS / 16; ++k)
-                    tc_mma(tmem + O_COL + h * NR, v + k * 128, w + k * 128, PV, !first || k > 0);
-                tc_commit(&c.pair_empty[s]);
-                if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
-            }
-            tc_commit(&c.rope_empty[last_rs]);
-            tc_commit(&c.o_done[(i - 1) & 1]);
-        }
-        __syncwarp();
-    };
     while (at.next(p, lane)) {
-        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
-            if (b == at.b0) {
-                // A new query tile waits for its loads: finish the last tile's sums first.
-                if (pending) sum();
-                pending = false;
-                wait(&c.q_full, piece, c);
-            }
-            wait(&c.s_empty[i & 1], (i >> 1) + 1, c);
-            for (int n = 0; pending && n < POLLS; ++n) {
-                if (__any_sync(0xFFFFFFFFu, arrived(&c.pair_full[ps], pu) || c.abort)) break;
-                if (__any_sync(0xFFFFFFFFu, arrived(&c.p_full[(i - 1) & 1], (i - 1) >> 1))) {
-                    sum();
-                    pending = false;
-                }
-            }
-            const uint32_t this_ps = ps, d = tmem + S_COL + (i & 1) * NR;
-            for (int u = 0; u <= plan.pairs; ++u) {
-                const bool rope = u == plan.pairs;
-                if (rope)
-                    wait(&c.rope_full[rs], ru, c);
-                else
-                    wait(&c.pair_full[ps], pu, c);
-                fence_proxy_async();          // (the rows were written by ordinary copies)
-                tc_fence_after();
-                if (elected()) {
-                    const uint64_t k = matrix(rope ? ropes + rs * CHUNK : pairs + ps * 2 * CHUNK, 16);
-                    const uint64_t qu = q + u * (2 * QCHUNK >> 4);
+        if (one) {
+            for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+                const uint32_t d = tmem + S_COL + (i & 1) * NR;
+                mbar_wait(&c.s_empty[i & 1], ((i >> 1) + 1) & 1u, &c.abort);
+                if (b == at.b0) mbar_wait(&c.q_full, piece & 1u, &c.abort);
+                for (int u = 0; u < plan.pairs; ++u) {
+                    mbar_wait(&c.pair_full[ps], pu & 1u, &c.abort);
+                    fence_proxy_async();      // (the rows were written by ordinary copies)
+                    tc_fence_after();
+                    const uint64_t k = matrix(pairs + ps * 2 * CHUNK, 16), qu = q + u * (2 * QCHUNK >> 4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) tc_mma(d, k + e * 2, qu + e * 2, QK, u > 0 || e > 0);
-                    if (!rope) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            tc_mma(d, k + (CHUNK >> 4) + e * 2, qu + (QCHUNK >> 4) + e * 2, QK, true);
-                    } else {
-                        tc_commit(&c.s_full[i & 1]);
-                        if (b + 1 == at.b1) tc_commit(&c.q_empty);
+                    for (int e = 0; e < 8; ++e)
+                        tc_mma(d, k + (e >> 2) * (CHUNK >> 4) + (e & 3) * 2, qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2,
+                               KIND, u > 0 || e > 0);
+                    if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
+                        ps = 0;
+                        ++pu;
                     }
                 }
-                if (!rope && ++ps == static_cast<uint32_t>(plan.pair_slots)) {
-                    ps = 0;
-                    ++pu;
+                mbar_wait(&c.rope_full[rs], ru & 1u, &c.abort);
+                fence_proxy_async();
+                tc_fence_after();
+                const uint64_t k = matrix(ropes + rs * CHUNK, 16), qu = q + plan.pairs * (2 * QCHUNK >> 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tc_mma(d, k + e * 2, qu + e * 2, KIND, true);
+                tc_commit(&c.s_full[i & 1]);
+                if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
+                    rs = 0;
+                    ++ru;
                 }
             }
-            __syncwarp();
-            if (pending) sum();
-            pending = true;
-            first = b == at.b0;
-            last_ps = this_ps;
-            last_rs = rs;
-            if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
-                rs = 0;
-                ++ru;
-            }
+            tc_commit(&c.q_empty);
         }
+        __syncwarp();
         ++piece;
     }
-    if (pending) sum();
-    // Nothing may be running on the tensor cores when their memory is freed.
-    if (elected()) tc_commit(&c.drain);
-    __syncwarp();
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(&c.drain, 0) && global_timer_ns() - t0 < WAIT_LIMIT_NS) {
-    }
+    drain(&c.drain[0], one);
 }
 
-// A tile's query rows into shared memory, swizzled as the products read them.
-// Rows past the tile's are left as they are: every row is apart in scores,
-// weights and sums, and nothing is written for those.
 template <int NR>
-__device__ void load_query(const AttendParams &p, Ctrl &c, uint32_t query, int chunks) {
-    const int tid = threadIdx.x - SOFT - LOAD - ROPE_LOAD, lane = threadIdx.x & 31;
+__device__ void multiply_sums(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t pairs, uint32_t ropes,
+                              uint32_t tmem) {
+    const int lane = threadIdx.x & 31;
+    const bool one = elected();
+    constexpr uint32_t KIND = instruction(128, NR, true);
     Cursor at(c);
-    uint32_t n = 0;
+    uint32_t i = 0, ps = 0, rs = 0;
     while (at.next(p, lane)) {
-        wait(&c.q_empty, n + 1, c);
-        const int piece = tid & 7;
-        for (int r = tid >> 3; r < at.tile.rows; r += QLOAD / 8) {
-            const int32_t flat = at.tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
-            const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
-            const uint32_t dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
-            for (int k = 0; k < chunks; ++k) copy16(dst + k * NR * 128, src + k * 64, true);
+        if (one) {
+            for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+                mbar_wait(&c.p_full[i % BLOCKS], (i / BLOCKS) & 1u, &c.abort);
+                fence_proxy_async();
+                tc_fence_after();
+                const uint64_t w = matrix(ropes + rs * CHUNK, 16);
+                for (int h = 0; h < plan.pairs; ++h) {
+                    const uint64_t v = matrix(pairs + ps * 2 * CHUNK, CHUNK);
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k)
+                        tc_mma(tmem + O_COL + h * NR, v + k * 128, w + k * 128, KIND, b > at.b0 || k > 0);
+                    tc_commit(&c.pair_empty[ps]);
+                    if (++ps == static_cast<uint32_t>(plan.pair_slots)) ps = 0;
+                }
+                tc_commit(&c.rope_empty[rs]);
+                tc_commit(&c.o_done[i % BLOCKS]);
+                if (++rs == static_cast<uint32_t>(plan.rope_slots)) rs = 0;
+            }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async();
-        arrive(&c.q_full);
-        ++n;
+        __syncwarp();
     }
+    drain(&c.drain[1], one);
 }
 
 struct Part {                                  // a piece's unfinished rows in the workspace
@@ -777,7 +767,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                 }
                 weigh();
                 if (b > at.b0) {
-                    wait(&c.o_done[(i - 1) & 1], (i - 1) >> 1, c);
+                    wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
                     tc_fence_after();
                     for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
@@ -811,7 +801,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             __syncwarp();
             if (lane == 0) {
                 arrive(&c.s_empty[i & 1]);
-                arrive(&c.p_full[i & 1]);
+                arrive(&c.p_full[i % BLOCKS]);
             }
             ps += plan.pairs;
             if (ps >= static_cast<uint32_t>(plan.pair_slots)) ps -= plan.pair_slots;
@@ -834,7 +824,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             if (!sees) c.ref[tid] = -INFINITY;
         }
         soft_sync();
-        wait(&c.o_done[(i - 1) & 1], (i - 1) >> 1, c);
+        wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
         tc_fence_after();
         const bool direct = at.b0 == 0 && at.b1 == at.blocks;
         if (direct) {
@@ -911,12 +901,14 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
         for (int s = 0; s < 2; ++s) {
             mbar_init(&c.s_full[s], 1);
             mbar_init(&c.s_empty[s], SOFT / 32);
+            mbar_init(&c.drain[s], 1);
+        }
+        for (int s = 0; s < BLOCKS; ++s) {
             mbar_init(&c.p_full[s], SOFT / 32);
             mbar_init(&c.o_done[s], 1);
         }
-        mbar_init(&c.q_full, QLOAD);
+        mbar_init(&c.q_full, LOAD);
         mbar_init(&c.q_empty, 1);
-        mbar_init(&c.drain, 1);
         c.abort = 0;
         fence_mbar_init();
     }
@@ -933,10 +925,10 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     if (warp < SOFT / 32) soften<NR>(p, c, plan, pairs, ropes, tmem);
-    else if (warp < (SOFT + LOAD) / 32) load_pairs(p, c, plan, smem_addr(pairs));
+    else if (warp < (SOFT + LOAD) / 32) load_pairs<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs));
     else if (warp < (SOFT + LOAD + ROPE_LOAD) / 32) load_ropes(p, c, plan, smem_addr(ropes));
-    else if (warp < NT / 32 - 1) load_query<NR>(p, c, smem_addr(smem), 2 * plan.pairs + 1);
-    else multiply<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
+    else if (warp < NT / 32 - 1) multiply_scores<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
+    else multiply_sums<NR>(p, c, plan, smem_addr(pairs), smem_addr(ropes), tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
