@@ -1,6 +1,8 @@
 // Attention over latent cache rows on the tensor cores: one persistent kernel
 // for both forms, and the kernel that joins the parts of split tiles.
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <mutex>
@@ -197,6 +199,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
+// 64 rows of 64 values from column x and row y, completing on `bar`.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, u64 *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // An arrival on `bar` once this thread's copies so far are done.
 __device__ __forceinline__ void copies_arrive(u64 *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -354,7 +365,9 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
 
 // ------------------------------------------------------------------ the warps' parts
 
-// The row numbers of a tile's blocks: entry j of its list or pages, -1 for none.
+// The row numbers of a tile's blocks. fetch() only loads entry j of the list or
+// pages, row() makes the cache row of it (-1 for none) a block later: a warp
+// that looked at the value at once would stand still until it came.
 struct RowList {
     const int32_t *list;
     int32_t len;
@@ -362,14 +375,13 @@ struct RowList {
         : list(p.paged ? p.table + static_cast<int64_t>(at.tile.request) * p.table_stride
                        : p.selected + static_cast<int64_t>(at.tile.token) * p.selected_stride),
           len(min(at.len, at.b1 * KEYS)) {}
-    __device__ int32_t row(const AttendParams &p, int32_t j) const {
-        if (j >= len) return -1;
-        int64_t v;
-        if (p.paged)
-            v = static_cast<int64_t>(__ldg(list + (j >> p.page_shift))) * p.block_rows + (j & ((1 << p.page_shift) - 1));
-        else
-            v = __ldg(list + j);
-        return v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
+    __device__ int32_t fetch(const AttendParams &p, int32_t j) const {
+        return j < len ? __ldg(list + (p.paged ? j >> p.page_shift : j)) : -1;
+    }
+    __device__ int32_t row(const AttendParams &p, int32_t fetched, int32_t j) const {
+        const int64_t v = p.paged ? static_cast<int64_t>(fetched) * p.block_rows + (j & ((1 << p.page_shift) - 1))
+                                  : fetched;
+        return j < len && v >= 0 && v < p.cache_rows ? static_cast<int32_t>(v) : -1;
     }
 };
 
@@ -391,15 +403,19 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
 // Query and cache rows into shared memory. Each warp has one pair of every
 // block (and with few pairs only some of its rows), so that it waits for one
 // slot a block and the pairs of a block are copied side by side as their slots
-// come free. Places that hold no cache row are filled with zeros. The first
+// come free. Places that hold no cache row are filled with zeros. Pages that hold
+// whole blocks come by TMA, 64 rows of 64 values a copy; their rows past the
+// context's end then hold whatever the page does, and are masked. The first
 // tile's query is copied first, a later one's when its first block is on its way. (Measured: the same cache
 // rows gathered four at a time by TMA come at 12 bytes a nanosecond per SM;
 // copies of 16 bytes reach 100 from L2 with four warps.)
 template <int NR>
-__device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, uint32_t pairs) {
+__device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &c, const Plan &plan, uint32_t query,
+                           uint32_t pairs) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - SOFT) >> 5;
     const int unit = warp % plan.pairs, part = warp / plan.pairs;
-    const bool idle = part >= plan.parts;      // (three pairs: one warp only helps with the query)
+    // (Three pairs: one warp only helps with the query; by TMA, one warp a pair.)
+    const bool idle = part >= (p.tiled ? 1 : plan.parts);
     const int64_t pitch = p.cache_stride * 2;
     const int rows = KEYS / plan.parts, half = lane >> 4, piece = lane & 15;
     const char *cache = reinterpret_cast<const char *>(p.cache) + unit * 256 + piece * 16;
@@ -412,10 +428,10 @@ __device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uin
         const int mine = part * rows + (lane & (rows - 1));
         int32_t now[2], then[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) now[h] = list.row(p, at.b0 * KEYS + mine + 32 * h);
+        for (int h = 0; h < 2; ++h) now[h] = list.fetch(p, at.b0 * KEYS + mine + 32 * h);
         for (int32_t b = at.b0; b < at.b1; ++b) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) then[h] = list.row(p, (b + 1) * KEYS + mine + 32 * h);
+            for (int h = 0; h < 2; ++h) then[h] = list.fetch(p, (b + 1) * KEYS + mine + 32 * h);
             if (b == at.b0 + (piece_no ? 1 : 0)) {
                 wait(&c.q_empty, piece_no + 1, c);
                 load_query<NR>(p, at.tile, query, 2 * plan.pairs + 1);
@@ -423,18 +439,30 @@ __device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uin
             }
             if (idle) continue;
             wait(&c.pair_empty[ps], pu + 1, c);
-            const uint32_t to = dst + ps * 2 * CHUNK;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (32 * h >= rows) break;
-#pragma unroll 8
-                for (int k = 0; k < min(rows, 32) / 2; ++k) {
-                    const int32_t v = __shfl_sync(0xFFFFFFFFu, now[h], 2 * k + half);
-                    copy16(to + h * 32 * 128 + k * 256 + (((piece ^ (r0 + 2 * k)) & 7) << 4),
-                           cache + (v >= 0 ? v * pitch : 0), v >= 0);
+            if (p.tiled) {
+                const int32_t first = list.row(p, now[0], b * KEYS);
+                if (lane == 0) {
+                    mbar_expect_tx(&c.pair_full[ps], 2 * CHUNK);
+                    for (int k = 0; k < 2; ++k)
+                        copy_box(pairs + (2 * ps + k) * CHUNK, map, (2 * unit + k) * 64, first < 0 ? p.cache_rows : first,
+                                 &c.pair_full[ps]);
                 }
+                __syncwarp();
+            } else {
+                const uint32_t to = dst + ps * 2 * CHUNK;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (32 * h >= rows) break;
+                    const int32_t here = list.row(p, now[h], b * KEYS + mine + 32 * h);
+#pragma unroll 8
+                    for (int k = 0; k < min(rows, 32) / 2; ++k) {
+                        const int32_t v = __shfl_sync(0xFFFFFFFFu, here, 2 * k + half);
+                        copy16(to + h * 32 * 128 + k * 256 + (((piece ^ (r0 + 2 * k)) & 7) << 4),
+                               cache + (v >= 0 ? v * pitch : 0), v >= 0);
+                    }
+                }
+                copies_arrive(&c.pair_full[ps]);
             }
-            copies_arrive(&c.pair_full[ps]);
             ps += plan.pairs;
             if (ps >= static_cast<uint32_t>(plan.pair_slots)) {
                 ps -= plan.pair_slots;
@@ -453,7 +481,7 @@ __device__ void load_pairs(const AttendParams &p, Ctrl &c, const Plan &plan, uin
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-__device__ void load_ropes(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t ropes) {
+__device__ void load_ropes(const AttendParams &p, const CUtensorMap *map, Ctrl &c, const Plan &plan, uint32_t ropes) {
     const int lane = threadIdx.x & 31, quarter = lane >> 3, piece = lane & 7;
     const int64_t pitch = p.cache_stride * 2;
     const char *cache = reinterpret_cast<const char *>(p.cache) + plan.pairs * 256 + piece * 16;
@@ -461,23 +489,33 @@ __device__ void load_ropes(const AttendParams &p, Ctrl &c, const Plan &plan, uin
     uint32_t i = 0, rs = 0, ru = 0;
     while (at.next(p, lane)) {
         const RowList list(p, at);
-        int32_t now[2], then[2];
+        int32_t now[2], then[2], here[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) now[h] = list.row(p, at.b0 * KEYS + 32 * h + lane);
+        for (int h = 0; h < 2; ++h) now[h] = list.fetch(p, at.b0 * KEYS + 32 * h + lane);
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                then[h] = list.row(p, (b + 1) * KEYS + 32 * h + lane);
-                c.rows[i % BLOCKS][32 * h + lane] = now[h];
+                then[h] = list.fetch(p, (b + 1) * KEYS + 32 * h + lane);
+                here[h] = list.row(p, now[h], b * KEYS + 32 * h + lane);
+                c.rows[i % BLOCKS][32 * h + lane] = here[h];
             }
             wait(&c.rope_empty[rs], ru + 1, c);
+            if (p.tiled) {
+                if (lane == 0) {
+                    mbar_expect_tx(&c.rope_full[rs], CHUNK);
+                    copy_box(ropes + rs * CHUNK, map, plan.pairs * 128, here[0] < 0 ? p.cache_rows : here[0],
+                             &c.rope_full[rs]);
+                }
+            } else {
 #pragma unroll
-            for (int k = 0; k < KEYS / 4; ++k) {
-                const int r = 4 * k + quarter;
-                const int32_t v = __shfl_sync(0xFFFFFFFFu, now[k / 8], r & 31);
-                copy16(ropes + rs * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4), cache + (v >= 0 ? v * pitch : 0), v >= 0);
+                for (int k = 0; k < KEYS / 4; ++k) {
+                    const int r = 4 * k + quarter;
+                    const int32_t v = __shfl_sync(0xFFFFFFFFu, here[k / 8], r & 31);
+                    copy16(ropes + rs * CHUNK + r * 128 + ((piece ^ (r & 7)) << 4), cache + (v >= 0 ? v * pitch : 0),
+                           v >= 0);
+                }
+                copies_arrive(&c.rope_full[rs]);
             }
-            copies_arrive(&c.rope_full[rs]);
             __syncwarp();
             if (lane == 0) arrive(&c.rope_full[rs]);   // (makes the row numbers visible)
             if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
@@ -680,11 +718,11 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
             char *weights = ropes + rs * CHUNK + t0 * 128 + quad * 4;
             float x[2 * N];                    // x[4 j + 2 h + e]: token h, the thread's row 2 j + e
             bool bad[2] = {false, false};
-            // Scores in log2 units; where masked, -inf. A cache row that only some of the
-            // tile's rows see must not reach the others through 0 x inf: where a score that
-            // is masked here is not finite (every row sees a cache row's NaN and infinities
-            // in its score), the cache row is zeroed and the weights of the rows that do
-            // see it are NaN.
+            // Scores in log2 units; where masked, -inf. A cache row that some or all of the
+            // tile's rows may not see must not reach them through 0 x inf: where a score that
+            // is masked here is not finite (a cache row's NaN and infinities show in the
+            // scores of all rows), the cache row is zeroed and the weights of the rows that
+            // do see it are NaN.
             auto take = [&]() {
                 tc_fence_after();
                 tc_load_groups<NR / 16>(scores, x);
@@ -703,7 +741,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                             float &v = x[4 * (n >> 1) + 2 * h + (n & 1)];
                             const int r = row_of(n);
                             const bool seen = there[h] && token + 8 * h < c.lim[r];
-                            odd |= there[h] && !seen && r < at.tile.rows && !(fabsf(v) < INFINITY);
+                            odd |= !seen && r < at.tile.rows && !(fabsf(v) < INFINITY);
                             v = seen ? v : -INFINITY;
                         }
                         odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, 1);
@@ -712,7 +750,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
                         if (odd) {
 #pragma unroll
                             for (int n = 0; n < N; ++n)
-                                if (token + 8 * h < c.lim[row_of(n)])
+                                if (there[h] && token + 8 * h < c.lim[row_of(n)])
                                     x[4 * (n >> 1) + 2 * h + (n & 1)] = __uint_as_float(0x7FC00000u);
                         }
                     }
@@ -884,7 +922,8 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
 }
 
 template <int NR>
-__global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ AttendParams p,
+                                                       const __grid_constant__ CUtensorMap map) {
     extern __shared__ char raw[];
     char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const Plan plan = make_plan<NR>(p.latent);
@@ -893,8 +932,8 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_SLOTS; ++s) {
-            mbar_init(&c.pair_full[s], 32 * plan.parts);
-            mbar_init(&c.rope_full[s], ROPE_LOAD + 1);
+            mbar_init(&c.pair_full[s], p.tiled ? 1 : 32 * plan.parts);
+            mbar_init(&c.rope_full[s], p.tiled ? 2 : ROPE_LOAD + 1);
             mbar_init(&c.pair_empty[s], 1);
             mbar_init(&c.rope_empty[s], 1);
         }
@@ -925,8 +964,8 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     if (warp < SOFT / 32) soften<NR>(p, c, plan, pairs, ropes, tmem);
-    else if (warp < (SOFT + LOAD) / 32) load_pairs<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs));
-    else if (warp < (SOFT + LOAD + ROPE_LOAD) / 32) load_ropes(p, c, plan, smem_addr(ropes));
+    else if (warp < (SOFT + LOAD) / 32) load_pairs<NR>(p, &map, c, plan, smem_addr(smem), smem_addr(pairs));
+    else if (warp < (SOFT + LOAD + ROPE_LOAD) / 32) load_ropes(p, &map, c, plan, smem_addr(ropes));
     else if (warp < NT / 32 - 1) multiply_scores<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
     else multiply_sums<NR>(p, c, plan, smem_addr(pairs), smem_addr(ropes), tmem);
     __syncwarp();
@@ -1020,6 +1059,7 @@ struct Device {
     std::once_flag once;
     cudaError_t err = cudaSuccess;
     int sms = 0;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 Device g_device[64];
 
@@ -1038,6 +1078,12 @@ cudaError_t device(Device *&out) {
         cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
         for (const void *fn : {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()})
             if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        cudaDriverEntryPointQueryResult found;
+        void *f = nullptr;
+        if (e == cudaSuccess)
+            e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !f)) e = cudaErrorNotSupported;
+        d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
         if (e == cudaSuccess && d.sms > 512) e = cudaErrorNotSupported;   // (join_kernel's weights)
         d.err = e;
     });
@@ -1071,6 +1117,19 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     const int64_t rows = full > 0 ? per : rest;
     const int nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 
+    // Pages that hold whole blocks: a block is 64 consecutive rows of the cache.
+    CUtensorMap map = {};
+    p.tiled = p.paged && (1 << p.page_shift) % KEYS == 0 && p.cache_rows >= KEYS ? 1 : 0;
+    if (p.tiled) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.latent + LATENT_ROPE), static_cast<cuuint64_t>(p.cache_rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.cache_stride) * 2};
+        const cuuint32_t box[2] = {64, KEYS}, steps[2] = {1, 1};
+        if (d->encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(p.cache), dims, strides, box,
+                      steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1081,7 +1140,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void *args[] = {&p};
+    void *args[] = {&p, &map};
     e = cudaLaunchKernelExC(&cfg, nr == 16 ? attend_fn<16>() : nr == 32 ? attend_fn<32>() : attend_fn<64>(), args);
     if (e != cudaSuccess || most_blocks <= 1) return e;   // tiles of one block are never split
     cfg.blockDim = dim3(NT_JOIN, 1, 1);
