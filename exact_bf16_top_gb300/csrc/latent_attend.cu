@@ -38,7 +38,7 @@ struct Ctrl {
     u64 p_full[BLOCKS], o_done[BLOCKS];        // a block's weights are in / its sums are added (one each: who waits
                                                // for one block may find later ones done, and two phases of one
                                                // barrier look like none)
-    u64 q_full, q_empty;                       // the query tile is in / used up
+    u64 q_first, q_full, q_empty;              // the first query tile, a later one is in / it is used up
     u64 drain[2];
     long long sums[NT / 32];
     int32_t first_tile, first_block;
@@ -389,10 +389,10 @@ struct RowList {
 // row's eighth of every chunk per thread. Rows past the tile's are left as they
 // are: every row is apart in scores, weights and sums, and nothing is written
 // for those.
-template <int NR>
-__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, uint32_t query, int chunks) {
-    const int tid = threadIdx.x - SOFT, piece = tid & 7;
-    for (int r = tid >> 3; r < tile.rows; r += LOAD / 8) {
+template <int NR, int THREADS>
+__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, uint32_t query, int chunks, int tid) {
+    const int piece = tid & 7;
+    for (int r = tid >> 3; r < tile.rows; r += THREADS / 8) {
         const int32_t flat = tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
         const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
         const uint32_t dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
@@ -405,8 +405,9 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
 // slot a block and the pairs of a block are copied side by side as their slots
 // come free. Places that hold no cache row are filled with zeros. Pages that hold
 // whole blocks come by TMA, 64 rows of 64 values a copy; their rows past the
-// context's end then hold whatever the page does, and are masked. The first
-// tile's query is copied first, a later one's when its first block is on its way. (Measured: the same cache
+// context's end then hold whatever the page does, and are masked. A tile's query is
+// copied when its first block is on its way (the first tile's by the softmax
+// warps, which have nothing else to do yet). (Measured: the same cache
 // rows gathered four at a time by TMA come at 12 bytes a nanosecond per SM;
 // copies of 16 bytes reach 100 from L2 with four warps.)
 template <int NR>
@@ -432,9 +433,9 @@ __device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &
         for (int32_t b = at.b0; b < at.b1; ++b) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) then[h] = list.fetch(p, (b + 1) * KEYS + mine + 32 * h);
-            if (b == at.b0 + (piece_no ? 1 : 0)) {
+            if (piece_no && b == at.b0 + 1) {
                 wait(&c.q_empty, piece_no + 1, c);
-                load_query<NR>(p, at.tile, query, 2 * plan.pairs + 1);
+                load_query<NR, LOAD>(p, at.tile, query, 2 * plan.pairs + 1, threadIdx.x - SOFT);
                 copies_arrive(&c.q_full);
             }
             if (idle) continue;
@@ -473,7 +474,7 @@ __device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &
         }
         if (piece_no && at.b1 == at.b0 + 1) {
             wait(&c.q_empty, piece_no + 1, c);
-            load_query<NR>(p, at.tile, query, 2 * plan.pairs + 1);
+            load_query<NR, LOAD>(p, at.tile, query, 2 * plan.pairs + 1, threadIdx.x - SOFT);
             copies_arrive(&c.q_full);
         }
         ++piece_no;
@@ -553,7 +554,7 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, const Plan &plan
             for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
                 const uint32_t d = tmem + S_COL + (i & 1) * NR;
                 mbar_wait(&c.s_empty[i & 1], ((i >> 1) + 1) & 1u, &c.abort);
-                if (b == at.b0) mbar_wait(&c.q_full, piece & 1u, &c.abort);
+                if (b == at.b0) mbar_wait(piece ? &c.q_full : &c.q_first, piece ? (piece - 1) & 1u : 0u, &c.abort);
                 for (int u = 0; u < plan.pairs; ++u) {
                     mbar_wait(&c.pair_full[ps], pu & 1u, &c.abort);
                     fence_proxy_async();      // (the rows were written by ordinary copies)
@@ -670,7 +671,8 @@ __device__ __forceinline__ int across_index() {
 // lose nothing by that), which is seen from the packed weights and almost never
 // happens.
 template <int NR>
-__device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *pairs, char *ropes, uint32_t tmem) {
+__device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, char *pairs, char *ropes,
+                       uint32_t tmem) {
     constexpr int N = NR / 8;                  // query rows of a thread
     const int tid = threadIdx.x, lane = tid & 31, w = (tid >> 5) & 3, group = tid >> 7, quad = lane & 3;
     const int t0 = w * 16 + lane / 4;
@@ -686,6 +688,10 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, char *p
     long long done = c.begin;
     while (at.next(p, lane)) {
         const int32_t start = at.b0 * KEYS;
+        if (i == 0) {
+            load_query<NR, SOFT>(p, at.tile, query, 2 * plan.pairs + 1, tid);
+            copies_arrive(&c.q_first);
+        }
         // A row that sees nothing of this piece has an infinite reference: whatever its
         // scores, its weights never move it, and its results are written as empty.
         if (tid < ROWS) {
@@ -946,6 +952,7 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
             mbar_init(&c.p_full[s], SOFT / 32);
             mbar_init(&c.o_done[s], 1);
         }
+        mbar_init(&c.q_first, SOFT);
         mbar_init(&c.q_full, LOAD);
         mbar_init(&c.q_empty, 1);
         c.abort = 0;
@@ -963,7 +970,7 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
-    if (warp < SOFT / 32) soften<NR>(p, c, plan, pairs, ropes, tmem);
+    if (warp < SOFT / 32) soften<NR>(p, c, plan, smem_addr(smem), pairs, ropes, tmem);
     else if (warp < (SOFT + LOAD) / 32) load_pairs<NR>(p, &map, c, plan, smem_addr(smem), smem_addr(pairs));
     else if (warp < (SOFT + LOAD + ROPE_LOAD) / 32) load_ropes(p, &map, c, plan, smem_addr(ropes));
     else if (warp < NT / 32 - 1) multiply_scores<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
@@ -977,23 +984,38 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     }
 }
 
-// Joins a split tile's parts, one CTA per row: each part's sum weighs
-// 2^(its maximum - the largest). Parts are added in order: results do not
-// depend on which CTA finished first.
-__global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ AttendParams p) {
+// Joins a split tile's parts: each part's sum weighs 2^(its maximum - the
+// largest). Parts are added in an order of their own: results do not depend on
+// which CTA finished first.
+__device__ __forceinline__ const Part &part_of(const Part *parts, const Joint &j, int i) {
+    return parts[2 * (j.cta + i) + (i == 0 ? 1 : 0)];
+}
+
+__device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.0f : exp2_fast(m - top); }
+
+__device__ __forceinline__ void add4(float4 &a, float f, const float4 &x) {
+    a.x += f * x.x;
+    a.y += f * x.y;
+    a.z += f * x.z;
+    a.w += f * x.w;
+}
+
+__device__ __forceinline__ void write4(const AttendParams &p, int64_t row, int v, const float4 &a, float l) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(finished(a.x, l), finished(a.y, l));
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(finished(a.z, l), finished(a.w, l));
+    uint2 o;
+    o.x = *reinterpret_cast<const uint32_t *>(&lo);
+    o.y = *reinterpret_cast<const uint32_t *>(&hi);
+    reinterpret_cast<uint2 *>(p.out + row * p.latent)[v] = o;
+}
+
+// Many parts of few tiles: a CTA per row, the parts dealt to groups of threads.
+__device__ void join_wide(const AttendParams &p, const Part *parts, const Joint &j, const Tile &t, int row) {
     __shared__ float weight[512], red[NT_JOIN / 32];
     __shared__ __align__(16) float partial[NT_JOIN * 4];
-    grid_dependents_release();
-    grid_dependency_wait();
-    const Part *parts = reinterpret_cast<const Part *>(p.workspace);
-    const Joint j = reinterpret_cast<const Joint *>(parts + 2 * p.sms)[blockIdx.x];
-    if (j.parts < 2) return;
-    const Tile t = tile_at(p, j.tile);
-    const int row = blockIdx.y, tid = threadIdx.x;
-    if (row >= t.rows) return;
-    auto part = [&](int i) -> const Part & { return parts[2 * (j.cta + i) + (i == 0 ? 1 : 0)]; };
+    const int tid = threadIdx.x;
     float mine = -INFINITY;
-    for (int i = tid; i < j.parts; i += NT_JOIN) mine = fmaxf(mine, part(i).m[row]);
+    for (int i = tid; i < j.parts; i += NT_JOIN) mine = fmaxf(mine, part_of(parts, j, i).m[row]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mine = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
     if ((tid & 31) == 0) red[tid >> 5] = mine;
@@ -1004,10 +1026,9 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ A
     __syncthreads();
     float sum = 0.0f;
     for (int i = tid; i < j.parts; i += NT_JOIN) {
-        const float m = part(i).m[row];
-        const float f = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+        const float f = part_weight(part_of(parts, j, i).m[row], top);
         weight[i] = f;
-        sum += f * part(i).l[row];
+        sum += f * part_of(parts, j, i).l[row];
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -1020,33 +1041,56 @@ __global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ A
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (g < groups) {
 #pragma unroll 8
-        for (int i = g; i < j.parts; i += groups) {
-            const float4 x = reinterpret_cast<const float4 *>(part(i).sum + row * p.latent)[v];
-            const float f = weight[i];
-            acc.x += f * x.x;
-            acc.y += f * x.y;
-            acc.z += f * x.z;
-            acc.w += f * x.w;
-        }
+        for (int i = g; i < j.parts; i += groups)
+            add4(acc, weight[i], reinterpret_cast<const float4 *>(part_of(parts, j, i).sum + row * p.latent)[v]);
         reinterpret_cast<float4 *>(partial)[tid] = acc;
     }
     __syncthreads();
     if (g == 0) {
-        for (int k = 1; k < groups; ++k) {
-            const float4 x = reinterpret_cast<const float4 *>(partial)[k * vecs + v];
-            acc.x += x.x;
-            acc.y += x.y;
-            acc.z += x.z;
-            acc.w += x.w;
-        }
-        const __nv_bfloat162 a = __floats2bfloat162_rn(finished(acc.x, l), finished(acc.y, l));
-        const __nv_bfloat162 b = __floats2bfloat162_rn(finished(acc.z, l), finished(acc.w, l));
-        uint2 o;
-        o.x = *reinterpret_cast<const uint32_t *>(&a);
-        o.y = *reinterpret_cast<const uint32_t *>(&b);
-        reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(t.base) + row) * p.latent)[v] = o;
+        for (int k = 1; k < groups; ++k) add4(acc, 1.0f, reinterpret_cast<const float4 *>(partial)[k * vecs + v]);
+        write4(p, static_cast<int64_t>(t.base) + row, v, acc, l);
         if (v == 0 && p.lse) p.lse[t.base + row] = finished_lse(top, l);
     }
+}
+
+// Few parts of many tiles: a warp per row.
+__device__ void join_narrow(const AttendParams &p, const Part *parts, const Joint &j, const Tile &t, int row) {
+    const int lane = threadIdx.x & 31;
+    float top = -INFINITY;
+    for (int i = 0; i < j.parts; ++i) top = fmaxf(top, part_of(parts, j, i).m[row]);
+    float l = 0.0f;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int quads = p.latent / 128;
+#pragma unroll 2
+    for (int i = 0; i < j.parts; ++i) {
+        const Part &part = part_of(parts, j, i);
+        const float f = part_weight(part.m[row], top);
+        l += f * part.l[row];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < quads) add4(acc[k], f, reinterpret_cast<const float4 *>(part.sum + row * p.latent)[k * 32 + lane]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < quads) write4(p, static_cast<int64_t>(t.base) + row, k * 32 + lane, acc[k], l);
+    if (lane == 0 && p.lse) p.lse[t.base + row] = finished_lse(top, l);
+}
+
+__global__ void __launch_bounds__(NT_JOIN) join_kernel(const __grid_constant__ AttendParams p, int rows) {
+    grid_dependents_release();
+    grid_dependency_wait();
+    const Part *parts = reinterpret_cast<const Part *>(p.workspace);
+    const Joint j = reinterpret_cast<const Joint *>(parts + 2 * p.sms)[blockIdx.x];
+    if (j.parts < 2) return;
+    const Tile t = tile_at(p, j.tile);
+    if (rows == 1) {
+        if (static_cast<int>(blockIdx.y) < t.rows) join_wide(p, parts, j, t, blockIdx.y);
+        return;
+    }
+    const int row = blockIdx.y * rows + (threadIdx.x >> 5);
+    if (row < t.rows) join_narrow(p, parts, j, t, row);
 }
 
 }  // namespace
@@ -1144,10 +1188,14 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     e = cudaLaunchKernelExC(&cfg, nr == 16 ? attend_fn<16>() : nr == 32 ? attend_fn<32>() : attend_fn<64>(), args);
     if (e != cudaSuccess || most_blocks <= 1) return e;   // tiles of one block are never split
     cfg.blockDim = dim3(NT_JOIN, 1, 1);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles < static_cast<int32_t>(grid) ? p.tiles : grid),
-                       static_cast<unsigned>(nr), 1);
+    // A CTA per row where that is few enough CTAs to run at once (many parts each
+    // then), else a warp per row.
+    const unsigned tiles = static_cast<unsigned>(p.tiles) < grid ? static_cast<unsigned>(p.tiles) : grid;
+    int per_cta = tiles * static_cast<unsigned>(nr) <= 8u * static_cast<unsigned>(d->sms) ? 1 : NT_JOIN / 32;
+    cfg.gridDim = dim3(tiles, static_cast<unsigned>(nr / per_cta), 1);
+    cfg.blockDim = dim3(NT_JOIN, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    void *join_args[] = {&p};
+    void *join_args[] = {&p, &per_cta};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&join_kernel), join_args);
 }
 
