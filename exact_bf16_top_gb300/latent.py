@@ -10,23 +10,44 @@ from __future__ import annotations
 
 import torch
 
+from . import TopkError, load
 from ._latent_abi import Append, Attend
 
 ROPE = 64
 LATENTS = (128, 256, 384, 512)
 MAX_HEADS = 256
 
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+# (The handle alone: a step's smallest calls take a few microseconds on the host.)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_workspace_bytes: dict[int, int] = {}
 
-def _tensor(t, name: str, dtype, dim: int, device=None):
-    """Checks one argument: a CUDA tensor of this type and rank with unit inner stride, on `device`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must have {dim} dimension(s) with unit inner stride")
+
+def _fits(t, dev: int, dtype, dim: int) -> bool:
+    """A CUDA tensor on device index dev of this type and rank with unit inner stride."""
+    return (t.get_device() == dev and t.dtype is dtype and t.dim() == dim
+            and (t.stride(-1) == 1 or t.shape[-1] <= 1))
+
+
+def _refuse(**tensors):
+    """Raises for the first of name=(tensor, dtype, rank) that does not fit, on the first one's device."""
+    dev = None
+    for name, (t, dtype, dim) in tensors.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        dev = t.device if dev is None else dev
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+        if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+            raise ValueError(f"{name} must have {dim} dimension(s) with unit inner stride")
+
+
+def _check(fine: bool, **tensors):
+    if not fine:
+        _refuse(**tensors)
+        raise ValueError("tensors do not fit the call")
 
 
 def _row_stride(t) -> int:
@@ -36,21 +57,22 @@ def _row_stride(t) -> int:
 
 def _head_strides(t) -> tuple[int, int]:
     """Token and head stride of a [tokens, heads, n] tensor (immaterial ones of single rows made plain)."""
-    n = -(-t.shape[2] // 8) * 8
-    head = t.stride(1) if t.shape[1] > 1 else n
-    return (t.stride(0) if t.shape[0] > 1 else max(n, head * t.shape[1])), head
+    tokens, heads, n = t.shape
+    token, head, _ = t.stride()
+    if heads == 1:
+        head = -(-n // 8) * 8
+    return (token if tokens > 1 else max(-(-n // 8) * 8, head * heads)), head
 
 
-def _launch(function, args, device, stream):
-    from . import _check
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        status = function(args, stream.cuda_stream)
+def _launch(function, args, dev: int, stream):
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = function(args, handle)
     else:
-        with torch.cuda.device(device):
-            status = function(args, stream.cuda_stream)
-    _check(status)
+        with torch.cuda.device(dev):
+            status = function(args, handle)
+    if status:
+        raise TopkError(status)
 
 
 def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=None, eps: float = 1e-6,
@@ -69,44 +91,45 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
     query[..., latent:]; the rest of query is left alone.
     Rows may be strided: strides multiples of 8, 16-byte aligned.
     """
-    from . import load
-    bf16, i32 = torch.bfloat16, torch.int32
-    _tensor(cache, "cache", bf16, 2)
-    dev = cache.device
-    _tensor(latent, "latent", bf16, 2, dev)
-    _tensor(key_rope, "key_rope", bf16, 2, dev)
-    _tensor(positions, "positions", i32, 1, dev)
-    _tensor(cos_sin, "cos_sin", torch.float32, 2, dev)
-    _tensor(slots, "slots", i32, 1, dev)
+    dev = cache.get_device() if isinstance(cache, torch.Tensor) else -1
+    _check(dev >= 0 and _fits(cache, dev, _BF16, 2) and _fits(latent, dev, _BF16, 2)
+           and _fits(key_rope, dev, _BF16, 2) and _fits(positions, dev, _I32, 1)
+           and _fits(cos_sin, dev, _F32, 2) and _fits(slots, dev, _I32, 1),
+           cache=(cache, _BF16, 2), latent=(latent, _BF16, 2), key_rope=(key_rope, _BF16, 2),
+           positions=(positions, _I32, 1), cos_sin=(cos_sin, _F32, 2), slots=(slots, _I32, 1))
     tokens, width = latent.shape
-    if width not in LATENTS or cache.shape[1] != width + ROPE:
+    rows, dim = cache.shape
+    if width not in LATENTS or dim != width + ROPE:
         raise ValueError(f"latent must have one of {LATENTS} columns and cache {ROPE} more")
     if key_rope.shape != (tokens, ROPE) or positions.shape[0] != tokens or slots.shape[0] != tokens:
         raise ValueError("key_rope, positions and slots must have one row per token (key_rope of 64)")
-    if cos_sin.shape[1] != ROPE or cos_sin.shape[0] < 1 or not cos_sin.is_contiguous():
+    positions_known, angles = cos_sin.shape
+    if angles != ROPE or positions_known < 1 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous [positions, 64]")
+    weight_ptr = None
     if weight is not None:
-        _tensor(weight, "weight", bf16, 1, dev)
+        _check(_fits(weight, dev, _BF16, 1), cache=(cache, _BF16, 2), weight=(weight, _BF16, 1))
         if weight.shape[0] != width:
             raise ValueError("weight must have one entry per latent column")
+        weight_ptr = weight.data_ptr()
     if (query is None) != (query_rope is None):
         raise ValueError("query and query_rope come together")
-    heads, q, r = 0, (0, 0), (0, 0)
-    if query is not None:
-        _tensor(query, "query", bf16, 3, dev)
-        _tensor(query_rope, "query_rope", bf16, 3, dev)
+    if query is None:
+        heads, r, q = 0, (None, 0, 0), (None, 0, 0)
+    else:
+        _check(_fits(query, dev, _BF16, 3) and _fits(query_rope, dev, _BF16, 3), cache=(cache, _BF16, 2),
+               query=(query, _BF16, 3), query_rope=(query_rope, _BF16, 3))
         heads = query.shape[1]
-        if query.shape != (tokens, heads, width + ROPE) or query_rope.shape != (tokens, heads, ROPE):
+        if query.shape != (tokens, heads, dim) or query_rope.shape != (tokens, heads, ROPE):
             raise ValueError("query must be [tokens, heads, latent + 64] and query_rope [tokens, heads, 64]")
         if not 1 <= heads <= MAX_HEADS:
             raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
-        q, r = _head_strides(query), _head_strides(query_rope)
+        r = (query_rope.data_ptr(), *_head_strides(query_rope))
+        q = (query.data_ptr(), *_head_strides(query))
     args = Append(cache.data_ptr(), _row_stride(cache), latent.data_ptr(), _row_stride(latent),
-                   key_rope.data_ptr(), _row_stride(key_rope), positions.data_ptr(), cos_sin.data_ptr(),
-                   slots.data_ptr(), None if weight is None else weight.data_ptr(),
-                   None if query is None else query_rope.data_ptr(), r[0], r[1],
-                   None if query is None else query.data_ptr(), q[0], q[1], cache.shape[0], tokens, width,
-                   heads, cos_sin.shape[0], 1 if interleaved else 0, eps)
+                  key_rope.data_ptr(), _row_stride(key_rope), positions.data_ptr(), cos_sin.data_ptr(),
+                  slots.data_ptr(), weight_ptr, *r, *q, rows, tokens, width, heads, positions_known,
+                  1 if interleaved else 0, eps)
     _launch(load().latent_bf16_append, args, dev, stream)
     return cache
 
@@ -123,13 +146,15 @@ def latent_attend_selected(query, cache, selected, scale: float, *, latent: int 
     sees nothing), else None is returned for it. workspace: None, or scratch
     from latent_workspace() that no other call uses at the same time.
     """
-    _tensor(selected, "selected", torch.int32, 2)
-    if selected.shape[0] != query.shape[0]:
+    dev = query.get_device() if isinstance(query, torch.Tensor) else -1
+    _check(dev >= 0 and _fits(query, dev, _BF16, 3) and _fits(cache, dev, _BF16, 2)
+           and _fits(selected, dev, _I32, 2),
+           query=(query, _BF16, 3), cache=(cache, _BF16, 2), selected=(selected, _I32, 2))
+    lists, k = selected.shape
+    if lists != query.shape[0]:
         raise ValueError("selected must have one row per query token")
-    k = selected.shape[1]
-    stride = selected.stride(0) if selected.shape[0] > 1 else k
-    return _attend("latent_bf16_attend_selected", query, cache, scale, latent, out, lse, workspace, stream,
-                   (selected,), (selected.data_ptr() if k else None, stride, None, None),
+    return _attend(load().latent_bf16_attend_selected, dev, query, cache, scale, latent, out, lse, workspace, stream,
+                   (selected.data_ptr() if k else None, selected.stride(0) if lists > 1 else k, None, None),
                    (k, 0, 0, 1, 1, 1))
 
 
@@ -145,8 +170,11 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     chunk of new tokens after n others has valid_len n + 1, n + 2, ...; a padded
     token has 0. Other arguments and results as latent_attend_selected.
     """
-    _tensor(valid_len, "valid_len", torch.int32, 1)
-    _tensor(block_table, "block_table", torch.int32, 2)
+    dev = query.get_device() if isinstance(query, torch.Tensor) else -1
+    _check(dev >= 0 and _fits(query, dev, _BF16, 3) and _fits(cache, dev, _BF16, 2)
+           and _fits(valid_len, dev, _I32, 1) and _fits(block_table, dev, _I32, 2),
+           query=(query, _BF16, 3), cache=(cache, _BF16, 2), valid_len=(valid_len, _I32, 1),
+           block_table=(block_table, _I32, 2))
     page_size, rows_per_request = int(page_size), int(rows_per_request)
     if page_size < 1 or page_size & (page_size - 1) or rows_per_request < 1:
         raise ValueError("page_size must be a power of two and rows_per_request at least 1")
@@ -156,77 +184,64 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     width = pages * page_size if width is None else int(width)
     if not 0 <= width <= pages * page_size:
         raise ValueError("width exceeds the block table")
-    stride = block_table.stride(0) if requests > 1 else pages
-    return _attend("latent_bf16_attend_paged", query, cache, scale, latent, out, lse, workspace, stream,
-                   (valid_len, block_table), (None, 0, valid_len.data_ptr(), block_table.data_ptr()),
-                   (0, width, stride, page_size, page_size if block_rows is None else int(block_rows),
-                    rows_per_request))
+    return _attend(load().latent_bf16_attend_paged, dev, query, cache, scale, latent, out, lse, workspace, stream,
+                   (None, 0, valid_len.data_ptr(), block_table.data_ptr()),
+                   (0, width, block_table.stride(0) if requests > 1 else pages, page_size,
+                    page_size if block_rows is None else int(block_rows), rows_per_request))
 
 
 def latent_workspace(device=None):
     """Scratch for one attention call at a time on a device (uint8)."""
-    from . import load
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with torch.cuda.device(device):
-        n = load().latent_bf16_workspace_bytes()
+    dev = torch.cuda.current_device() if device is None else torch.empty(0, device=device).get_device()
+    return torch.empty(_scratch(dev), dtype=_U8, device=torch.device("cuda", dev))
+
+
+def _scratch(dev: int) -> int:
+    n = _workspace_bytes.get(dev)
+    if n is None:
+        with torch.cuda.device(dev):
+            n = load().latent_bf16_workspace_bytes()
         if n <= 0:
             raise RuntimeError("no usable CUDA device")
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        _workspace_bytes[dev] = n
+    return n
 
 
-_workspace_bytes: dict[int, int] = {}
-
-
-def _attend(name, query, cache, scale, latent, out, lse, workspace, stream, others, pointers, sizes):
-    from . import load
-    bf16 = torch.bfloat16
-    _tensor(query, "query", bf16, 3)
-    dev = query.device
-    _tensor(cache, "cache", bf16, 2, dev)
-    for t in others:
-        if t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}")
+def _attend(function, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes):
     tokens, heads, dim = query.shape
-    if latent not in LATENTS or dim != latent + ROPE or cache.shape[1] != dim:
+    rows, cache_dim = cache.shape
+    if latent not in LATENTS or dim != latent + ROPE or cache_dim != dim:
         raise ValueError(f"latent must be one of {LATENTS}, query and cache rows latent + {ROPE} values")
     if not 1 <= heads <= MAX_HEADS:
         raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
-    if stream is not None:
-        # Allocated on the stream that uses them.
-        with torch.cuda.stream(stream):
-            out, lse, workspace = _outputs(out, lse, workspace, dev, tokens, heads, latent)
+    if stream is None:
+        out, lse, workspace = _outputs(out, lse, workspace, query.device, tokens, heads, latent)
     else:
-        out, lse, workspace = _outputs(out, lse, workspace, dev, tokens, heads, latent)
-    if tokens == 0:
-        return out, lse
-    q = _head_strides(query)
-    args = Attend(query.data_ptr(), q[0], q[1], cache.data_ptr(), _row_stride(cache), *pointers,
-                   out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                   workspace.numel(), cache.shape[0], tokens, heads, latent, *sizes, scale)
-    _launch(getattr(load(), name), args, dev, stream)
+        with torch.cuda.stream(stream):     # allocated on the stream that uses them
+            out, lse, workspace = _outputs(out, lse, workspace, query.device, tokens, heads, latent)
+    if tokens:
+        args = Attend(query.data_ptr(), *_head_strides(query), cache.data_ptr(), _row_stride(cache), *pointers,
+                      out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                      workspace.numel(), rows, tokens, heads, latent, *sizes, scale)
+        _launch(function, args, dev, stream)
     return out, lse
 
 
-def _outputs(out, lse, workspace, dev, tokens, heads, latent):
+def _outputs(out, lse, workspace, device, tokens, heads, latent):
     """The caller's tensors, checked, or new ones."""
     if out is None:
-        out = torch.empty((tokens, heads, latent), dtype=torch.bfloat16, device=dev)
-    elif not (out.dtype == torch.bfloat16 and out.device == dev and out.shape == (tokens, heads, latent)
+        out = torch.empty((tokens, heads, latent), dtype=_BF16, device=device)
+    elif not (out.dtype is _BF16 and out.device == device and out.shape == (tokens, heads, latent)
               and out.is_contiguous()):
         raise ValueError("out must be a contiguous bfloat16 [tokens, heads, latent] on the query's device")
-    if isinstance(lse, torch.Tensor):
-        if not (lse.dtype == torch.float32 and lse.device == dev and lse.shape == (tokens, heads)
-                and lse.is_contiguous()):
-            raise ValueError("lse must be a contiguous float32 [tokens, heads] on the query's device")
-    else:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if lse else None
+    if lse is True:
+        lse = torch.empty((tokens, heads), dtype=_F32, device=device)
+    elif not isinstance(lse, torch.Tensor):
+        lse = None
+    elif not (lse.dtype is _F32 and lse.device == device and lse.shape == (tokens, heads) and lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] on the query's device")
     if workspace is None:
-        n = _workspace_bytes.get(dev.index)
-        if n is None:
-            workspace = latent_workspace(dev)
-            _workspace_bytes[dev.index] = workspace.numel()
-        else:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    elif not (workspace.dtype == torch.uint8 and workspace.device == dev and workspace.is_contiguous()):
+        workspace = torch.empty(_scratch(device.index), dtype=_U8, device=device)
+    elif not (workspace.dtype is _U8 and workspace.device == device and workspace.is_contiguous()):
         raise ValueError("workspace must be a uint8 tensor from latent_workspace() on the query's device")
     return out, lse, workspace
