@@ -17,7 +17,7 @@ bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 bool bad_latent(int32_t v) { return v != 128 && v != 256 && v != 384 && v != 512; }
 
 topk_status_t check_append(const latent_bf16_append_t *a) {
-    if (!a || a->tokens < 0 || a->cache_rows < 0) return TOPK_ERR_ARG;
+    if (!a || a->tokens < 0 || a->tokens > (1 << 27) || a->cache_rows < 0) return TOPK_ERR_ARG;
     if (bad_latent(a->latent)) return TOPK_ERR_WIDTH;
     if (a->tokens == 0) return TOPK_OK;
     if ((!a->cache && a->cache_rows > 0) || !a->latents || !a->key_rope || !a->positions || !a->cos_sin || !a->slots) return TOPK_ERR_ARG;

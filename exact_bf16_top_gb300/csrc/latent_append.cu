@@ -12,6 +12,7 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int ROPE = LATENT_ROPE;
+constexpr int HEADS = 16;                    // query heads of a unit
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -22,71 +23,82 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Rotates 64 values held as eight consecutive ones by each of eight lanes
-// (`part` = lane & 7) by the angles of one position. Interleaved: the pairs lie
-// inside a lane's eight values; halves: value i pairs with i + 32, which the
-// lane four parts away holds.
-__device__ __forceinline__ uint4 rotate8(uint4 v, const float *__restrict__ cs, int part, bool interleaved) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t r[4];
-    if (interleaved) {
-        const float4 c = *reinterpret_cast<const float4 *>(cs + 4 * part);
-        const float4 s = *reinterpret_cast<const float4 *>(cs + 32 + 4 * part);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+// The cosines and sines that turn eight consecutive values of 64, held by each
+// of eight lanes (`part` = lane & 7). Interleaved: the pairs lie inside a lane's
+// eight values; halves: value i pairs with i + 32, which the lane four parts
+// away holds.
+struct Turn {
+    float c[8], s[8];   // interleaved: four of each
+    __device__ __forceinline__ Turn(const float *__restrict__ cs, int part, bool interleaved) {
+        const int at = interleaved ? 4 * part : 8 * (part & 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = lo_f(w[i]), b = hi_f(w[i]);
-            r[i] = pack(a * cc[i] - b * ss[i], a * ss[i] + b * cc[i]);
-        }
-    } else {
-        const int at = 8 * (part & 3);
-        const float sign = part < 4 ? -1.0f : 1.0f;   // (a cos - b sin, b cos + a sin)
-        float c[8], s[8];
-        *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(cs + at);
-        *reinterpret_cast<float4 *>(c + 4) = *reinterpret_cast<const float4 *>(cs + at + 4);
-        *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(cs + 32 + at);
-        *reinterpret_cast<float4 *>(s + 4) = *reinterpret_cast<const float4 *>(cs + 32 + at + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w[i], 4);
-            r[i] = pack(lo_f(w[i]) * c[2 * i] + sign * lo_f(o) * s[2 * i],
-                        hi_f(w[i]) * c[2 * i + 1] + sign * hi_f(o) * s[2 * i + 1]);
+        for (int i = 0; i < 2; ++i) {
+            if (interleaved && i) break;
+            *reinterpret_cast<float4 *>(c + 4 * i) = __ldg(reinterpret_cast<const float4 *>(cs + at + 4 * i));
+            *reinterpret_cast<float4 *>(s + 4 * i) = __ldg(reinterpret_cast<const float4 *>(cs + 32 + at + 4 * i));
         }
     }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
+    __device__ __forceinline__ uint4 operator()(uint4 v, int part, bool interleaved) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t r[4];
+        if (interleaved) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = lo_f(w[i]), b = hi_f(w[i]);
+                r[i] = pack(a * c[i] - b * s[i], a * s[i] + b * c[i]);
+            }
+        } else {
+            const float sign = part < 4 ? -1.0f : 1.0f;   // (a cos - b sin, b cos + a sin)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w[i], 4);
+                r[i] = pack(lo_f(w[i]) * c[2 * i] + sign * lo_f(o) * s[2 * i],
+                            hi_f(w[i]) * c[2 * i + 1] + sign * hi_f(o) * s[2 * i + 1]);
+            }
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+};
 
-// One warp per unit of work: a token's cache row, or four of a token's query
-// heads (eight lanes each, 16 bytes a lane). Both are one dependent round of
-// loads and one of stores, so the kernel is bound by DRAM on long chunks and by
-// the launch and that round on short ones.
+// One warp per unit of work: a token's cache row, or up to 16 of a token's query
+// heads (eight lanes a head, four heads a round, all rounds' loads together).
+// Each is one dependent round of loads (position, angles) and one of stores, so
+// the kernel is bound by DRAM on long chunks and by the launch and that round on
+// short ones. Measured: @APPEND@
 template <int VECS>   // 16-byte vectors of the latent part per lane pair: latent / 256 rounded up
-__global__ void __launch_bounds__(NT) append_kernel(const latent_bf16_append_t a, int64_t units, int32_t quads) {
+__global__ void __launch_bounds__(NT) append_kernel(const latent_bf16_append_t a, uint32_t units, uint32_t groups) {
     grid_dependents_release();
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (NT / 32);
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (NT / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const bool key = u < a.tokens;
-        const int64_t q = u - a.tokens;
-        const int32_t t = static_cast<int32_t>(key ? u : q / quads);
-        int32_t pos = a.positions[t];
-        pos = pos < 0 ? 0 : pos >= a.max_positions ? a.max_positions - 1 : pos;
-        const float *cs = a.cos_sin + static_cast<int64_t>(pos) * ROPE;
-        const int part = lane & 7;
+    const int lane = threadIdx.x & 31, part = lane & 7;
+    const bool interleaved = a.interleaved != 0;
+    const uint32_t step = gridDim.x * (NT / 32);
+    for (uint32_t u = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); u < units; u += step) {
+        const bool key = u < static_cast<uint32_t>(a.tokens);
+        const uint32_t q = u - a.tokens;
+        const int32_t t = static_cast<int32_t>(key ? u : q / groups);
+        int32_t pos = __ldg(a.positions + t);
         if (!key) {
-            const int32_t h = static_cast<int32_t>(q % quads) * 4 + (lane >> 3);
-            const bool on = h < a.heads;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (on)
-                v = __ldg(reinterpret_cast<const uint4 *>(a.query_rope + t * a.query_rope_token_stride +
-                                                          h * a.query_rope_head_stride) + part);
-            v = rotate8(v, cs, part, a.interleaved != 0);
-            if (on)
-                reinterpret_cast<uint4 *>(a.query + t * a.query_token_stride + h * a.query_head_stride +
-                                          a.latent)[part] = v;
+            const int32_t h0 = static_cast<int32_t>(q - t * groups) * HEADS + (lane >> 3);
+            const uint16_t *from = a.query_rope + t * a.query_rope_token_stride;
+            uint4 v[HEADS / 4];
+#pragma unroll
+            for (int i = 0; i < HEADS / 4; ++i)
+                v[i] = h0 + 4 * i < a.heads
+                           ? __ldg(reinterpret_cast<const uint4 *>(from + (h0 + 4 * i) * a.query_rope_head_stride) + part)
+                           : make_uint4(0, 0, 0, 0);
+            pos = pos < 0 ? 0 : pos >= a.max_positions ? a.max_positions - 1 : pos;
+            const Turn turn(a.cos_sin + static_cast<int64_t>(pos) * ROPE, part, interleaved);
+            uint16_t *to = a.query + t * a.query_token_stride + a.latent;
+#pragma unroll
+            for (int i = 0; i < HEADS / 4; ++i) {
+                const uint4 r = turn(v[i], part, interleaved);
+                if (h0 + 4 * i < a.heads)
+                    reinterpret_cast<uint4 *>(to + (h0 + 4 * i) * a.query_head_stride)[part] = r;
+            }
             continue;
         }
+        pos = pos < 0 ? 0 : pos >= a.max_positions ? a.max_positions - 1 : pos;
+        const float *cs = a.cos_sin + static_cast<int64_t>(pos) * ROPE;
         const int32_t slot = a.slots[t];
         if (slot < 0 || slot >= a.cache_rows) continue;
         uint16_t *row = a.cache + static_cast<int64_t>(slot) * a.cache_stride;
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(NT) append_kernel(const latent_bf16_append_t a
             const int j = i * 32 + lane;
             if (j < vecs) reinterpret_cast<uint4 *>(row)[j] = x[i];
         }
-        const uint4 r = rotate8(k, cs, part, a.interleaved != 0);
+        const uint4 r = Turn(cs, part, interleaved)(k, part, interleaved);
         if (lane < 8) reinterpret_cast<uint4 *>(row + a.latent)[part] = r;
     }
 }
@@ -138,9 +150,9 @@ __global__ void __launch_bounds__(NT) append_kernel(const latent_bf16_append_t a
 }  // namespace
 
 cudaError_t launch_append(const latent_bf16_append_t &a, int sms, cudaStream_t stream) {
-    int32_t quads = a.query_rope ? (a.heads + 3) / 4 : 0;
-    int64_t units = a.tokens + static_cast<int64_t>(a.tokens) * quads;
-    const int64_t want = (units + NT / 32 - 1) / (NT / 32);
+    uint32_t groups = a.query_rope ? static_cast<uint32_t>((a.heads + HEADS - 1) / HEADS) : 0u;
+    uint32_t units = static_cast<uint32_t>(a.tokens) * (1u + groups);   // (at most 2^27 tokens: checked)
+    const int64_t want = (static_cast<int64_t>(units) + NT / 32 - 1) / (NT / 32);
     const int64_t most = static_cast<int64_t>(sms) * (2048 / NT);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most), 1, 1);
@@ -152,7 +164,7 @@ cudaError_t launch_append(const latent_bf16_append_t &a, int sms, cudaStream_t s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     latent_bf16_append_t arg = a;
-    void *args[] = {&arg, &units, &quads};
+    void *args[] = {&arg, &units, &groups};
     const void *fn = a.latent <= 256 ? reinterpret_cast<const void *>(&append_kernel<1>)
                                      : reinterpret_cast<const void *>(&append_kernel<2>);
     return cudaLaunchKernelExC(&cfg, fn, args);

@@ -69,8 +69,8 @@ extern "C" {
  * All BF16 pointers are 16-byte aligned and all strides multiples of 8 elements.
  * Outputs must not overlap inputs.
  *
- * Errors: TOPK_ERR_ARG (null pointer, negative count, heads outside
- * [1, LATENT_MAX_HEADS] with query_rope, max_positions < 1, query_rope without
+ * Errors: TOPK_ERR_ARG (null pointer, negative count, more than 2^27 tokens, heads
+ * outside [1, LATENT_MAX_HEADS] with query_rope, max_positions < 1, query_rope without
  * query), TOPK_ERR_WIDTH (latent, or a stride below its row), TOPK_ERR_ALIGN.
  */
 typedef struct {
