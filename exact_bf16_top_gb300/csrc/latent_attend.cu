@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "latent.h"
@@ -715,8 +716,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             ref[n] = c.ref[row_of(n)];
         }
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
-            mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
-            wait(&c.rope_full[rs], ru, c);             // (complete: makes the row numbers visible)
+            wait(&c.rope_full[rs], ru, c);             // (makes the row numbers visible)
             const int32_t token = b * KEYS + t0;
             const bool there[2] = {c.rows[i % BLOCKS][t0] >= 0, c.rows[i % BLOCKS][t0 + 8] >= 0};
             const bool whole = __all_sync(0xFFFFFFFFu, there[0] && there[1]) && (b + 1) * KEYS <= low;
@@ -730,7 +730,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             // scores of all rows), the cache row is zeroed and the weights of the rows that
             // do see it are NaN.
             auto take = [&]() {
-                tc_fence_after();
                 tc_load_groups<NR / 16>(scores, x);
                 tc_fence_before();
 #pragma unroll
@@ -762,27 +761,43 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                     }
                 }
             };
-            // Weights from scores, rounded once to BF16 for the tensor cores; true if one
-            // outgrew the reference.
-            auto weigh = [&]() -> bool {
+            // Weights from scores (or from the unscaled scores of a whole block), rounded once
+            // to BF16 for the tensor cores; true if one outgrew the reference.
+            auto weigh = [&](auto unscaled) -> bool {
                 __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
                 for (int j = 0; j < N / 2; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float &a = x[4 * j + 2 * h], &d = x[4 * j + 2 * h + 1];
-                        const float ea = exp2_fast(a - ref[2 * j]), ed = exp2_fast(d - ref[2 * j + 1]);
-                        a = a == -INFINITY ? 0.0f : ea;      // (masked: the reference may be -inf too)
-                        d = d == -INFINITY ? 0.0f : ed;
+                        if constexpr (decltype(unscaled)::value) {
+                            a = exp2_fast(fmaf(a, scale, -ref[2 * j]));
+                            d = exp2_fast(fmaf(d, scale, -ref[2 * j + 1]));
+                        } else {
+                            const float ea = exp2_fast(a - ref[2 * j]), ed = exp2_fast(d - ref[2 * j + 1]);
+                            a = a == -INFINITY ? 0.0f : ea;      // (masked: the reference may be -inf too)
+                            d = d == -INFINITY ? 0.0f : ed;
+                        }
                         const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
                         top = __hmax2(top, v);
                         *reinterpret_cast<__nv_bfloat162 *>(weights + h * 1024 + (((group * (N / 2) + j) ^ (t0 & 7)) << 4)) = v;
                     }
                 return fmaxf(__low2float(top), __high2float(top)) > 1.152921504606846976e18f;   // 2^60
             };
-            take();
-            bool moved = b == at.b0;
-            if (!moved) moved = soft_any(weigh());
+            mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
+            __syncwarp();
+            tc_fence_after();
+            bool moved = true;
+            if (b == at.b0) {
+                take();
+            } else if (whole) {
+                tc_load_groups<NR / 16>(scores, x);
+                tc_fence_before();
+                moved = soft_any(weigh(std::true_type{}));
+            } else {
+                take();
+                moved = soft_any(weigh(std::false_type{}));
+            }
             if (moved) {
                 // New references: the rows' largest scores of this block where they are 2^60
                 // above the old ones (or the first the row sees).
@@ -809,7 +824,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                     ref[n] = c.ref[row_of(n)];
                     l[n] *= c.factor[row_of(n)];
                 }
-                weigh();
+                weigh(std::false_type{});
                 if (b > at.b0) {
                     wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
                     tc_fence_after();
@@ -827,9 +842,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                     tc_fence_before();
                 }
             }
-            // The sums are of the unrounded weights, in 32 bits.
-#pragma unroll
-            for (int n = 0; n < N; ++n) l[n] += x[4 * (n >> 1) + (n & 1)] + x[4 * (n >> 1) + 2 + (n & 1)];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (bad[h]) {
@@ -847,6 +859,9 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                 arrive(&c.s_empty[i & 1]);
                 arrive(&c.p_full[i % BLOCKS]);
             }
+            // The sums are of the unrounded weights, in 32 bits.
+#pragma unroll
+            for (int n = 0; n < N; ++n) l[n] += x[4 * (n >> 1) + (n & 1)] + x[4 * (n >> 1) + 2 + (n & 1)];
             ps += plan.pairs;
             if (ps >= static_cast<uint32_t>(plan.pair_slots)) ps -= plan.pair_slots;
             if (++rs == static_cast<uint32_t>(plan.rope_slots)) {
