@@ -31,5 +31,7 @@ def declare(lib) -> None:
     lib.latent_bf16_attend_paged.argtypes = [ctypes.POINTER(Attend), _P]
     for f in (lib.latent_bf16_append, lib.latent_bf16_attend_selected, lib.latent_bf16_attend_paged):
         f.restype = ctypes.c_int
+    lib.latent_bf16_attend_workspace.argtypes = [ctypes.POINTER(Attend), ctypes.c_int32]
+    lib.latent_bf16_attend_workspace.restype = ctypes.c_int64
     lib.latent_bf16_workspace_bytes.argtypes = []
     lib.latent_bf16_workspace_bytes.restype = ctypes.c_int64

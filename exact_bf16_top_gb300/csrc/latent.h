@@ -28,11 +28,12 @@ struct AttendParams {
     int32_t width, table_stride, page_shift, block_rows, rows_per_request;
     float scale;
     void *workspace;
-    int32_t tiles, tiles_per_request, min_share, sms, tiled;   // filled in by launch_attend
+    int32_t tiles, tiles_per_request, min_share, sms, tiled, cluster;   // filled in by launch_attend
 };
 
 cudaError_t launch_append(const latent_bf16_append_t &a, int sms, cudaStream_t stream);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
+int64_t attend_workspace(const AttendParams &p);   // bytes this call needs, -1 if the device cannot be asked
 int64_t workspace_bytes();   // 0 if the device cannot be asked
 
 }  // namespace topk::latent

@@ -62,7 +62,7 @@ topk_status_t check_attend(const latent_bf16_attend_t *a, bool paged) {
         return TOPK_ERR_WIDTH;
     }
     if (a->tokens == 0) return TOPK_OK;
-    if (!a->query || (!a->cache && a->cache_rows > 0) || !a->out || !a->workspace) return TOPK_ERR_ARG;
+    if (!a->query || (!a->cache && a->cache_rows > 0) || !a->out) return TOPK_ERR_ARG;
     if (paged ? (!a->valid_len || !a->block_table) : (!a->selected && a->k > 0)) return TOPK_ERR_ARG;
     const int64_t dim = a->latent + LATENT_ROPE;
     if (a->cache_stride < dim || a->query_head_stride < 0 || a->query_token_stride < 0) return TOPK_ERR_WIDTH;
@@ -70,15 +70,10 @@ topk_status_t check_attend(const latent_bf16_attend_t *a, bool paged) {
         off4(a->selected) || off4(a->valid_len) || off4(a->block_table))
         return TOPK_ERR_ALIGN;
     if ((a->cache_stride | a->query_token_stride | a->query_head_stride) & 7) return TOPK_ERR_ALIGN;
-    const int64_t need = workspace_bytes();
-    if (need <= 0) return TOPK_ERR_CUDA;
-    if (a->workspace_bytes < need) return TOPK_ERR_ARG;
     return TOPK_OK;
 }
 
-topk_status_t attend(const latent_bf16_attend_t *a, bool paged, void *stream) {
-    const topk_status_t st = check_attend(a, paged);
-    if (st != TOPK_OK || a->tokens == 0) return st;
+AttendParams params_of(const latent_bf16_attend_t *a, bool paged) {
     AttendParams p = {};
     p.query = a->query;
     p.query_token_stride = a->query_token_stride;
@@ -105,6 +100,16 @@ topk_status_t attend(const latent_bf16_attend_t *a, bool paged, void *stream) {
     p.rows_per_request = paged ? a->rows_per_request : 1;
     p.scale = a->scale;
     p.workspace = a->workspace;
+    return p;
+}
+
+topk_status_t attend(const latent_bf16_attend_t *a, bool paged, void *stream) {
+    const topk_status_t st = check_attend(a, paged);
+    if (st != TOPK_OK || a->tokens == 0) return st;
+    const AttendParams p = params_of(a, paged);
+    const int64_t need = attend_workspace(p);
+    if (need < 0) return TOPK_ERR_CUDA;
+    if (need > 0 && (!a->workspace || a->workspace_bytes < need)) return TOPK_ERR_ARG;
     return launch_attend(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TOPK_OK : TOPK_ERR_CUDA;
 }
 
@@ -131,6 +136,11 @@ topk_status_t latent_bf16_attend_selected(const latent_bf16_attend_t *args, void
 
 topk_status_t latent_bf16_attend_paged(const latent_bf16_attend_t *args, void *stream) {
     return topk::latent::attend(args, true, stream);
+}
+
+int64_t latent_bf16_attend_workspace(const latent_bf16_attend_t *args, int32_t paged) {
+    if (topk::latent::check_attend(args, paged != 0) != TOPK_OK) return -1;
+    return args->tokens == 0 ? 0 : topk::latent::attend_workspace(topk::latent::params_of(args, paged != 0));
 }
 
 int64_t latent_bf16_workspace_bytes(void) { return topk::latent::workspace_bytes(); }

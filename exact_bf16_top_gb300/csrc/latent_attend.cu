@@ -7,6 +7,7 @@
 
 #include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "common.cuh"
 #include "latent.h"
@@ -43,6 +44,7 @@ struct Ctrl {
     u64 drain[2];
     long long sums[NT / 32];
     int32_t first_tile, first_block;
+    int32_t ranks;                             // CTAs of the cluster that have blocks
     long long begin, share, total;
     uint32_t tmem;
     volatile uint32_t abort;
@@ -285,7 +287,8 @@ __device__ __forceinline__ int32_t tile_len_warp(const AttendParams &p, const Ti
 }
 
 // All blocks of all tiles in order are cut into equal shares, one per CTA: a
-// CTA's share is a run of pieces, each part or all of one tile's blocks.
+// CTA's share is a run of pieces, each part or all of one tile's blocks. (Or,
+// where the host chose so, a cluster's CTAs share one tile.)
 struct Cursor {
     int32_t next_tile, next_block;
     long long left;
@@ -311,6 +314,23 @@ struct Cursor {
 // The CTA's share, by all threads of the CTA.
 __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.cluster) {                           // a tile per cluster, its blocks in equal runs
+        if (warp == 0) {
+            const int32_t tile = blockIdx.x / p.cluster, rank = blockIdx.x - tile * p.cluster;
+            int32_t low;
+            const int32_t n = blocks_of(tile_len_warp(p, tile_at(p, tile), lane, low));
+            const int32_t per = (n + p.cluster - 1) / p.cluster;
+            if (lane == 0) {
+                c.first_tile = tile;
+                c.first_block = rank * per;
+                c.begin = 0;
+                c.share = c.total = max(0, min(per, n - rank * per));
+                c.ranks = (n + per - 1) / per;
+            }
+        }
+        __syncthreads();
+        return;
+    }
     if (!p.paged) {
         if (tid == 0) {
             const long long n = blocks_of(p.k);
@@ -909,6 +929,19 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                                 two;
                     }
                 }
+        } else if (p.cluster) {
+            // The rings are used up: this CTA's part stays there for the cluster to join.
+            float *sums = reinterpret_cast<float *>(pairs);
+            for (int h = 0; h < plan.pairs; ++h)
+#pragma unroll
+                for (int v = 0; v < NR; v += 16) {
+                    if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                    float o[16];
+                    tc_load16(lanes + O_COL + h * NR + v, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        sums[(v + e) * p.latent + h * 128 + w * 32 + lane] = c.l[v + e] == 0.0f ? 0.0f : o[e];
+                }
         } else {
             Part &part = parts[2 * blockIdx.x + (at.b0 == 0 ? 1 : 0)];
             if (tid < NR) {
@@ -926,7 +959,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                         part.sum[(v + e) * p.latent + h * 128 + w * 32 + lane] = c.l[v + e] == 0.0f ? 0.0f : o[e];
                 }
         }
-        if (at.b0 == 0 && tid == 0 && (by_tile || !direct)) {
+        if (!p.cluster && at.b0 == 0 && tid == 0 && (by_tile || !direct)) {
             Joint j;
             j.tile = at.next_tile - 1;
             j.cta = static_cast<int32_t>(blockIdx.x);
@@ -939,7 +972,58 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
         tc_fence_before();
         soft_sync();
     }
-    if (!by_tile && !split_here && tid == 0) joints[blockIdx.x] = Joint{0, 0, 0, 0};
+    if (!p.cluster && !by_tile && !split_here && tid == 0) joints[blockIdx.x] = Joint{0, 0, 0, 0};
+}
+
+__device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.0f : exp2_fast(m - top); }
+
+__device__ __forceinline__ void add4(float4 &a, float f, const float4 &x) {
+    a.x += f * x.x;
+    a.y += f * x.y;
+    a.z += f * x.z;
+    a.w += f * x.w;
+}
+
+__device__ __forceinline__ void write4(const AttendParams &p, int64_t row, int v, const float4 &a, float l) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(finished(a.x, l), finished(a.y, l));
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(finished(a.z, l), finished(a.w, l));
+    uint2 o;
+    o.x = *reinterpret_cast<const uint32_t *>(&lo);
+    o.y = *reinterpret_cast<const uint32_t *>(&hi);
+    reinterpret_cast<uint2 *>(p.out + row * p.latent)[v] = o;
+}
+
+__device__ __forceinline__ float ld_peer_f(const void *p, uint32_t rank) { return __uint_as_float(ld_peer(peer_addr(p, rank))); }
+
+__device__ __forceinline__ float4 ld_peer4(const void *p, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(peer_addr(p, rank))
+                 : "memory");
+    return v;
+}
+
+// Joins a cluster's parts of its tile out of its CTAs' shared memory: each CTA
+// takes every cluster-th row, the parts are added in the CTAs' order.
+__device__ void join_cluster(const AttendParams &p, const Ctrl &c, const char *sums) {
+    const Tile t = tile_at(p, c.first_tile);
+    const int vecs = p.latent / 4, groups = NT / vecs, g = threadIdx.x / vecs, v = threadIdx.x - g * vecs;
+    const int rank = static_cast<int>(cluster_rank());
+    if (g >= groups) return;
+    for (int row = rank + p.cluster * g; row < t.rows; row += p.cluster * groups) {
+        float top = -INFINITY, l = 0.0f;
+        for (int i = 0; i < c.ranks; ++i) top = fmaxf(top, ld_peer_f(&c.ref[row], i));
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int i = 0; i < c.ranks; ++i) {
+            const float f = part_weight(ld_peer_f(&c.ref[row], i), top);
+            l += f * ld_peer_f(&c.l[row], i);
+            add4(acc, f, ld_peer4(sums + (row * p.latent + v * 4) * 4, i));
+        }
+        write4(p, static_cast<int64_t>(t.base) + row, v, acc, l);
+        if (v == 0 && p.lse) p.lse[t.base + row] = finished_lse(top, l);
+    }
 }
 
 template <int NR>
@@ -997,6 +1081,15 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
+    if (p.cluster > 1) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        if (c.ranks > 1) join_cluster(p, c, pairs);
+        __syncwarp();
+        cluster_arrive();                      // no CTA leaves while others read its part
+        cluster_wait();
+    }
 }
 
 // Joins a split tile's parts: each part's sum weighs 2^(its maximum - the
@@ -1004,24 +1097,6 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
 // which CTA finished first.
 __device__ __forceinline__ const Part &part_of(const Part *parts, const Joint &j, int i) {
     return parts[2 * (j.cta + i) + (i == 0 ? 1 : 0)];
-}
-
-__device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.0f : exp2_fast(m - top); }
-
-__device__ __forceinline__ void add4(float4 &a, float f, const float4 &x) {
-    a.x += f * x.x;
-    a.y += f * x.y;
-    a.z += f * x.z;
-    a.w += f * x.w;
-}
-
-__device__ __forceinline__ void write4(const AttendParams &p, int64_t row, int v, const float4 &a, float l) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(finished(a.x, l), finished(a.y, l));
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(finished(a.z, l), finished(a.w, l));
-    uint2 o;
-    o.x = *reinterpret_cast<const uint32_t *>(&lo);
-    o.y = *reinterpret_cast<const uint32_t *>(&hi);
-    reinterpret_cast<uint2 *>(p.out + row * p.latent)[v] = o;
 }
 
 // Many parts of few tiles: a CTA per row, the parts dealt to groups of threads.
@@ -1118,6 +1193,7 @@ struct Device {
     std::once_flag once;
     cudaError_t err = cudaSuccess;
     int sms = 0;
+    int clusters[5] = {};                      // of 1, 2, 4, 8, 16 CTAs that run at once
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 Device g_device[64];
@@ -1136,7 +1212,26 @@ cudaError_t device(Device *&out) {
     std::call_once(d.once, [&]() {
         cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
         for (const void *fn : {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()})
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            for (const auto &set : {std::pair{cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM},
+                                    std::pair{cudaFuncAttributeNonPortableClusterSizeAllowed, 1}})
+                if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, set.first, set.second);
+        d.clusters[0] = d.sms;
+        for (int i = 1; i < 5 && e == cudaSuccess; ++i) {
+            cudaLaunchAttribute a = {};
+            a.id = cudaLaunchAttributeClusterDimension;
+            a.val.clusterDim.x = 1u << i;
+            a.val.clusterDim.y = a.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1u << i, 1, 1);
+            cfg.blockDim = dim3(NT, 1, 1);
+            cfg.dynamicSmemBytes = SMEM;
+            cfg.attrs = &a;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&d.clusters[i], attend_fn<64>(), &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                d.clusters[i] = 0;             // (a size that the device does not take)
+            }
+        }
         cudaDriverEntryPointQueryResult found;
         void *f = nullptr;
         if (e == cudaSuccess)
@@ -1160,21 +1255,66 @@ int64_t workspace_bytes() {
 
 cudaError_t status_attend(uint32_t *v, bool clear) { return unit_status(v, clear); }
 
+namespace {
+
+// How a call's blocks are dealt: the tiles, and either equal shares of all blocks
+// for every SM with the split tiles joined by a second kernel, or (cluster > 0)
+// one cluster per tile, joined through its shared memory.
+struct Deal {
+    int64_t tiles, blocks;                     // tiles; blocks of a tile at most
+    int32_t tiles_per_request, cluster;
+    unsigned grid;
+    int nr;
+};
+
+constexpr int MIN_SHARE = 2;                   // blocks of a CTA in equal shares
+constexpr int JOIN_BLOCKS = 5;                 // blocks that cost what the second kernel does
+
+Deal deal(const AttendParams &p, const Device &d) {
+    Deal r = {};
+    const int64_t per = static_cast<int64_t>(p.rows_per_request) * p.heads;
+    const int64_t full = p.tokens / p.rows_per_request;
+    const int64_t rest = p.tokens % p.rows_per_request * static_cast<int64_t>(p.heads);
+    r.tiles_per_request = static_cast<int32_t>((per + ROWS - 1) / ROWS);
+    r.tiles = full * r.tiles_per_request + (rest + ROWS - 1) / ROWS;
+    const int64_t rows = full > 0 ? per : rest;
+    r.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    r.blocks = (static_cast<int64_t>(p.paged ? p.width : p.k) + KEYS - 1) / KEYS;
+    if (r.blocks < 1) r.blocks = 1;
+    const int64_t even = (r.tiles * r.blocks + d.sms - 1) / d.sms;
+    const int64_t share = even > MIN_SHARE ? even : MIN_SHARE;
+    // The largest cluster whose CTAs do not get more blocks than equal shares and
+    // the second kernel cost. (Measured: @DEAL@)
+    for (int i = 4; i >= 0 && !r.cluster; --i) {
+        const int64_t size = 1 << i;
+        if (size <= r.blocks && r.tiles <= d.clusters[i] && (r.blocks + size - 1) / size <= share + JOIN_BLOCKS)
+            r.cluster = static_cast<int32_t>(size);
+    }
+    const int64_t want = r.cluster ? r.tiles * r.cluster : (r.tiles * r.blocks + MIN_SHARE - 1) / MIN_SHARE;
+    r.grid = static_cast<unsigned>(r.cluster || want < d.sms ? want : d.sms);
+    return r;
+}
+
+}  // namespace
+
+int64_t attend_workspace(const AttendParams &p) {
+    Device *d = nullptr;
+    if (device(d) != cudaSuccess) return -1;
+    return deal(p, *d).cluster ? 0 : workspace_bytes();
+}
+
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     Device *d = nullptr;
     cudaError_t e = device(d);
     if (e != cudaSuccess) return e;
-    const int64_t per = static_cast<int64_t>(p.rows_per_request) * p.heads;
-    const int64_t full = p.tokens / p.rows_per_request, rest = p.tokens % p.rows_per_request * static_cast<int64_t>(p.heads);
-    p.tiles_per_request = static_cast<int32_t>((per + ROWS - 1) / ROWS);
-    p.tiles = static_cast<int32_t>(full * p.tiles_per_request + (rest + ROWS - 1) / ROWS);
-    p.min_share = 2;
+    const Deal plan = deal(p, *d);
+    p.tiles_per_request = plan.tiles_per_request;
+    p.tiles = static_cast<int32_t>(plan.tiles);
+    p.cluster = plan.cluster;
+    p.min_share = MIN_SHARE;
     p.sms = d->sms;
-    const int64_t most_blocks = (static_cast<int64_t>(p.paged ? p.width : p.k) + KEYS - 1) / KEYS;
-    const int64_t want = (p.tiles * (most_blocks > 1 ? most_blocks : 1) + p.min_share - 1) / p.min_share;
-    const unsigned grid = static_cast<unsigned>(want < d->sms ? want : d->sms);
-    const int64_t rows = full > 0 ? per : rest;
-    const int nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    const unsigned grid = plan.grid;
+    const int nr = plan.nr;
 
     // Pages that hold whole blocks: a block is 64 consecutive rows of the cache.
     CUtensorMap map = {};
@@ -1189,20 +1329,23 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
             return cudaErrorInvalidValue;
     }
 
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(NT, 1, 1);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
     void *args[] = {&p, &map};
     e = cudaLaunchKernelExC(&cfg, nr == 16 ? attend_fn<16>() : nr == 32 ? attend_fn<32>() : attend_fn<64>(), args);
-    if (e != cudaSuccess || most_blocks <= 1) return e;   // tiles of one block are never split
-    cfg.blockDim = dim3(NT_JOIN, 1, 1);
+    if (e != cudaSuccess || p.cluster || plan.blocks <= 1) return e;   // tiles of one block are never split
+    cfg.numAttrs = 1;
     // A CTA per row where that is few enough CTAs to run at once (many parts each
     // then), else a warp per row.
     const unsigned tiles = static_cast<unsigned>(p.tiles) < grid ? static_cast<unsigned>(p.tiles) : grid;

@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import torch
 
+import exact_bf16_top_gb300 as _package
+
 from . import TopkError, load
 from ._latent_abi import Append, Attend
 
@@ -18,15 +20,8 @@ LATENTS = (128, 256, 384, 512)
 MAX_HEADS = 256
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
-# (The handle alone: a step's smallest calls take a few microseconds on the host.)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_workspace_bytes: dict[int, int] = {}
-
-
-def _fits(t, dev: int, dtype, dim: int) -> bool:
-    """A CUDA tensor on device index dev of this type and rank with unit inner stride."""
-    return (t.get_device() == dev and t.dtype is dtype and t.dim() == dim
-            and (t.stride(-1) == 1 or t.shape[-1] <= 1))
+# (Plain integers: a step's smallest calls take a few microseconds on the host.)
+_raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _refuse(**tensors):
@@ -42,17 +37,12 @@ def _refuse(**tensors):
             raise ValueError(f"{name} must be on {dev}")
         if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
             raise ValueError(f"{name} must have {dim} dimension(s) with unit inner stride")
+    raise ValueError("tensors do not fit the call")
 
 
-def _check(fine: bool, **tensors):
-    if not fine:
-        _refuse(**tensors)
-        raise ValueError("tensors do not fit the call")
-
-
-def _row_stride(t) -> int:
+def _row_stride(rows: int, width: int, stride: int) -> int:
     """Row stride of a 2-D tensor; a single row's is immaterial, its width rounded up is given."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+    return stride if rows > 1 else -(-width // 8) * 8
 
 
 def _head_strides(t) -> tuple[int, int]:
@@ -62,17 +52,6 @@ def _head_strides(t) -> tuple[int, int]:
     if heads == 1:
         head = -(-n // 8) * 8
     return (token if tokens > 1 else max(-(-n // 8) * 8, head * heads)), head
-
-
-def _launch(function, args, dev: int, stream):
-    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
-        status = function(args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = function(args, handle)
-    if status:
-        raise TopkError(status)
 
 
 def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=None, eps: float = 1e-6,
@@ -91,14 +70,24 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
     query[..., latent:]; the rest of query is left alone.
     Rows may be strided: strides multiples of 8, 16-byte aligned.
     """
-    dev = cache.get_device() if isinstance(cache, torch.Tensor) else -1
-    _check(dev >= 0 and _fits(cache, dev, _BF16, 2) and _fits(latent, dev, _BF16, 2)
-           and _fits(key_rope, dev, _BF16, 2) and _fits(positions, dev, _I32, 1)
-           and _fits(cos_sin, dev, _F32, 2) and _fits(slots, dev, _I32, 1),
-           cache=(cache, _BF16, 2), latent=(latent, _BF16, 2), key_rope=(key_rope, _BF16, 2),
-           positions=(positions, _I32, 1), cos_sin=(cos_sin, _F32, 2), slots=(slots, _I32, 1))
-    tokens, width = latent.shape
-    rows, dim = cache.shape
+    try:
+        dev = cache.get_device()
+        rows, dim = cache.shape
+        cache_stride, c1 = cache.stride()
+        tokens, width = latent.shape
+        latent_stride, l1 = latent.stride()
+        key_stride, k1 = key_rope.stride()
+        fine = (dev >= 0 and latent.get_device() == key_rope.get_device() == positions.get_device() == dev
+                and cos_sin.get_device() == slots.get_device() == dev
+                and cache.dtype is latent.dtype is key_rope.dtype is _BF16
+                and positions.dtype is slots.dtype is _I32 and cos_sin.dtype is _F32
+                and c1 == l1 == k1 == 1 and positions.is_contiguous() and slots.is_contiguous()
+                and positions.dim() == slots.dim() == 1 and cos_sin.dim() == 2)
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse(cache=(cache, _BF16, 2), latent=(latent, _BF16, 2), key_rope=(key_rope, _BF16, 2),
+                positions=(positions, _I32, 1), cos_sin=(cos_sin, _F32, 2), slots=(slots, _I32, 1))
     if width not in LATENTS or dim != width + ROPE:
         raise ValueError(f"latent must have one of {LATENTS} columns and cache {ROPE} more")
     if key_rope.shape != (tokens, ROPE) or positions.shape[0] != tokens or slots.shape[0] != tokens:
@@ -108,7 +97,9 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
         raise ValueError("cos_sin must be contiguous [positions, 64]")
     weight_ptr = None
     if weight is not None:
-        _check(_fits(weight, dev, _BF16, 1), cache=(cache, _BF16, 2), weight=(weight, _BF16, 1))
+        if not (isinstance(weight, torch.Tensor) and weight.get_device() == dev and weight.dtype is _BF16
+                and weight.dim() == 1 and weight.is_contiguous()):
+            _refuse(cache=(cache, _BF16, 2), weight=(weight, _BF16, 1))
         if weight.shape[0] != width:
             raise ValueError("weight must have one entry per latent column")
         weight_ptr = weight.data_ptr()
@@ -117,8 +108,11 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
     if query is None:
         heads, r, q = 0, (None, 0, 0), (None, 0, 0)
     else:
-        _check(_fits(query, dev, _BF16, 3) and _fits(query_rope, dev, _BF16, 3), cache=(cache, _BF16, 2),
-               query=(query, _BF16, 3), query_rope=(query_rope, _BF16, 3))
+        if not (isinstance(query, torch.Tensor) and isinstance(query_rope, torch.Tensor)
+                and query.get_device() == query_rope.get_device() == dev
+                and query.dtype is query_rope.dtype is _BF16 and query.dim() == query_rope.dim() == 3
+                and query.stride(2) == query_rope.stride(2) == 1):
+            _refuse(cache=(cache, _BF16, 2), query=(query, _BF16, 3), query_rope=(query_rope, _BF16, 3))
         heads = query.shape[1]
         if query.shape != (tokens, heads, dim) or query_rope.shape != (tokens, heads, ROPE):
             raise ValueError("query must be [tokens, heads, latent + 64] and query_rope [tokens, heads, 64]")
@@ -126,11 +120,20 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
             raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
         r = (query_rope.data_ptr(), *_head_strides(query_rope))
         q = (query.data_ptr(), *_head_strides(query))
-    args = Append(cache.data_ptr(), _row_stride(cache), latent.data_ptr(), _row_stride(latent),
-                  key_rope.data_ptr(), _row_stride(key_rope), positions.data_ptr(), cos_sin.data_ptr(),
+    args = Append(cache.data_ptr(), _row_stride(rows, dim, cache_stride), latent.data_ptr(),
+                  _row_stride(tokens, width, latent_stride), key_rope.data_ptr(),
+                  _row_stride(tokens, ROPE, key_stride), positions.data_ptr(), cos_sin.data_ptr(),
                   slots.data_ptr(), weight_ptr, *r, *q, rows, tokens, width, heads, positions_known,
                   1 if interleaved else 0, eps)
-    _launch(load().latent_bf16_append, args, dev, stream)
+    function = (_package._lib or load()).latent_bf16_append
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if _raw_device() == dev:
+        status = function(args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = function(args, handle)
+    if status:
+        raise TopkError(status)
     return cache
 
 
@@ -146,15 +149,19 @@ def latent_attend_selected(query, cache, selected, scale: float, *, latent: int 
     sees nothing), else None is returned for it. workspace: None, or scratch
     from latent_workspace() that no other call uses at the same time.
     """
-    dev = query.get_device() if isinstance(query, torch.Tensor) else -1
-    _check(dev >= 0 and _fits(query, dev, _BF16, 3) and _fits(cache, dev, _BF16, 2)
-           and _fits(selected, dev, _I32, 2),
-           query=(query, _BF16, 3), cache=(cache, _BF16, 2), selected=(selected, _I32, 2))
-    lists, k = selected.shape
+    try:
+        dev = query.get_device()
+        lists, k = selected.shape
+        stride, s1 = selected.stride()
+        fine = (selected.get_device() == dev and selected.dtype is _I32 and (s1 == 1 or k <= 1))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2), selected=(selected, _I32, 2))
     if lists != query.shape[0]:
         raise ValueError("selected must have one row per query token")
-    return _attend(load().latent_bf16_attend_selected, dev, query, cache, scale, latent, out, lse, workspace, stream,
-                   (selected.data_ptr() if k else None, selected.stride(0) if lists > 1 else k, None, None),
+    return _attend(0, dev, query, cache, scale, latent, out, lse, workspace, stream,
+                   (selected.data_ptr() if k else None, stride if lists > 1 else k, None, None),
                    (k, 0, 0, 1, 1, 1))
 
 
@@ -170,78 +177,94 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     chunk of new tokens after n others has valid_len n + 1, n + 2, ...; a padded
     token has 0. Other arguments and results as latent_attend_selected.
     """
-    dev = query.get_device() if isinstance(query, torch.Tensor) else -1
-    _check(dev >= 0 and _fits(query, dev, _BF16, 3) and _fits(cache, dev, _BF16, 2)
-           and _fits(valid_len, dev, _I32, 1) and _fits(block_table, dev, _I32, 2),
-           query=(query, _BF16, 3), cache=(cache, _BF16, 2), valid_len=(valid_len, _I32, 1),
-           block_table=(block_table, _I32, 2))
+    try:
+        dev = query.get_device()
+        requests, pages = block_table.shape
+        stride, t1 = block_table.stride()
+        fine = (valid_len.get_device() == block_table.get_device() == dev
+                and valid_len.dtype is block_table.dtype is _I32 and valid_len.dim() == 1
+                and valid_len.is_contiguous() and (t1 == 1 or pages <= 1))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2), valid_len=(valid_len, _I32, 1),
+                block_table=(block_table, _I32, 2))
     page_size, rows_per_request = int(page_size), int(rows_per_request)
     if page_size < 1 or page_size & (page_size - 1) or rows_per_request < 1:
         raise ValueError("page_size must be a power of two and rows_per_request at least 1")
-    tokens, (requests, pages) = query.shape[0], block_table.shape
+    tokens = query.shape[0]
     if valid_len.shape[0] != tokens or requests < -(-tokens // rows_per_request):
         raise ValueError("valid_len must have one entry per token, block_table one row per request")
     width = pages * page_size if width is None else int(width)
     if not 0 <= width <= pages * page_size:
         raise ValueError("width exceeds the block table")
-    return _attend(load().latent_bf16_attend_paged, dev, query, cache, scale, latent, out, lse, workspace, stream,
+    return _attend(1, dev, query, cache, scale, latent, out, lse, workspace, stream,
                    (None, 0, valid_len.data_ptr(), block_table.data_ptr()),
-                   (0, width, block_table.stride(0) if requests > 1 else pages, page_size,
+                   (0, width, stride if requests > 1 else pages, page_size,
                     page_size if block_rows is None else int(block_rows), rows_per_request))
 
 
 def latent_workspace(device=None):
-    """Scratch for one attention call at a time on a device (uint8)."""
+    """Scratch that is enough for any one attention call at a time on a device (uint8)."""
     dev = torch.cuda.current_device() if device is None else torch.empty(0, device=device).get_device()
-    return torch.empty(_scratch(dev), dtype=_U8, device=torch.device("cuda", dev))
+    with torch.cuda.device(dev):
+        n = load().latent_bf16_workspace_bytes()
+    if n <= 0:
+        raise RuntimeError("no usable CUDA device")
+    return torch.empty(n, dtype=_U8, device=torch.device("cuda", dev))
 
 
-def _scratch(dev: int) -> int:
-    n = _workspace_bytes.get(dev)
-    if n is None:
-        with torch.cuda.device(dev):
-            n = load().latent_bf16_workspace_bytes()
-        if n <= 0:
-            raise RuntimeError("no usable CUDA device")
-        _workspace_bytes[dev] = n
-    return n
-
-
-def _attend(function, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes):
-    tokens, heads, dim = query.shape
-    rows, cache_dim = cache.shape
+def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes):
+    try:
+        tokens, heads, dim = query.shape
+        rows, cache_dim = cache.shape
+        cache_stride, c1 = cache.stride()
+        fine = (dev >= 0 and cache.get_device() == dev and query.dtype is cache.dtype is _BF16
+                and query.stride(2) == 1 and c1 == 1)
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2))
     if latent not in LATENTS or dim != latent + ROPE or cache_dim != dim:
         raise ValueError(f"latent must be one of {LATENTS}, query and cache rows latent + {ROPE} values")
     if not 1 <= heads <= MAX_HEADS:
         raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
-    if stream is None:
-        out, lse, workspace = _outputs(out, lse, workspace, query.device, tokens, heads, latent)
-    else:
-        with torch.cuda.stream(stream):     # allocated on the stream that uses them
-            out, lse, workspace = _outputs(out, lse, workspace, query.device, tokens, heads, latent)
-    if tokens:
-        args = Attend(query.data_ptr(), *_head_strides(query), cache.data_ptr(), _row_stride(cache), *pointers,
-                      out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                      workspace.numel(), rows, tokens, heads, latent, *sizes, scale)
-        _launch(function, args, dev, stream)
-    return out, lse
-
-
-def _outputs(out, lse, workspace, device, tokens, heads, latent):
-    """The caller's tensors, checked, or new ones."""
+    if _raw_device() != dev:
+        with torch.cuda.device(dev):
+            return _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes)
+    if stream is not None and stream != torch.cuda.current_stream(dev):
+        with torch.cuda.stream(stream):     # new tensors belong to the stream that uses them
+            return _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, None, pointers, sizes)
+    device = query.device
     if out is None:
         out = torch.empty((tokens, heads, latent), dtype=_BF16, device=device)
     elif not (out.dtype is _BF16 and out.device == device and out.shape == (tokens, heads, latent)
               and out.is_contiguous()):
         raise ValueError("out must be a contiguous bfloat16 [tokens, heads, latent] on the query's device")
+    lse_ptr = None
     if lse is True:
         lse = torch.empty((tokens, heads), dtype=_F32, device=device)
+        lse_ptr = lse.data_ptr()
     elif not isinstance(lse, torch.Tensor):
         lse = None
-    elif not (lse.dtype is _F32 and lse.device == device and lse.shape == (tokens, heads) and lse.is_contiguous()):
+    elif lse.dtype is _F32 and lse.device == device and lse.shape == (tokens, heads) and lse.is_contiguous():
+        lse_ptr = lse.data_ptr()
+    else:
         raise ValueError("lse must be a contiguous float32 [tokens, heads] on the query's device")
-    if workspace is None:
-        workspace = torch.empty(_scratch(device.index), dtype=_U8, device=device)
-    elif not (workspace.dtype is _U8 and workspace.device == device and workspace.is_contiguous()):
+    if workspace is not None and not (workspace.dtype is _U8 and workspace.device == device
+                                      and workspace.is_contiguous()):
         raise ValueError("workspace must be a uint8 tensor from latent_workspace() on the query's device")
-    return out, lse, workspace
+    if tokens:
+        args = Attend(query.data_ptr(), *_head_strides(query), cache.data_ptr(),
+                      _row_stride(rows, dim, cache_stride), *pointers, out.data_ptr(), lse_ptr, None, 0, rows, tokens, heads, latent, *sizes, scale)
+        lib = _package._lib or load()
+        if workspace is None:
+            n = lib.latent_bf16_attend_workspace(args, paged)
+            if n > 0:
+                workspace = torch.empty(n, dtype=_U8, device=device)
+        if workspace is not None:
+            args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        status = (lib.latent_bf16_attend_paged if paged else lib.latent_bf16_attend_selected)(args, _raw_stream(dev))
+        if status:
+            raise TopkError(status)
+    return out, lse

@@ -106,8 +106,10 @@ topk_status_t latent_bf16_append(const latent_bf16_append_t *args, void *stream)
  *                aligned, fully written.
  * lse            NULL, or device float [tokens, heads]: lse as above (natural
  *                logarithm), for joining parts of one softmax.
- * workspace      device scratch of latent_bf16_workspace_bytes() bytes, 16-byte
- *                aligned, used by this call alone until it completes.
+ * workspace      device scratch, 16-byte aligned, of latent_bf16_attend_workspace()
+ *                bytes for this call (0 for many: NULL will do) or of
+ *                latent_bf16_workspace_bytes(), which is enough for any; used by
+ *                this call alone until it completes.
  *
  * latent_bf16_attend_selected: token t sees the cache rows selected[t *
  * selected_stride + i], i < k, that lie in [0, cache_rows); other entries (the
@@ -148,8 +150,13 @@ typedef struct {
 topk_status_t latent_bf16_attend_selected(const latent_bf16_attend_t *args, void *stream);
 topk_status_t latent_bf16_attend_paged(const latent_bf16_attend_t *args, void *stream);
 
-/* Bytes of scratch an attention call needs on the current device (the same for
-   all sizes); 0 if the device cannot be asked. */
+/* Bytes of scratch that a call with these arguments needs on the current device
+   (paged: which form; `workspace` is not looked at); -1 for arguments that the
+   call would refuse, or if the device cannot be asked. */
+int64_t latent_bf16_attend_workspace(const latent_bf16_attend_t *args, int32_t paged);
+
+/* Bytes of scratch that are enough for any attention call on the current device;
+   0 if the device cannot be asked. */
 int64_t latent_bf16_workspace_bytes(void);
 
 #ifdef __cplusplus

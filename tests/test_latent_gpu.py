@@ -428,7 +428,8 @@ def test_refusals():
                  lambda: selected(torch.empty(1, 257, 576, dtype=torch.bfloat16, device="cuda"), s=sel[:1])):
         with pytest.raises(ValueError):
             call()
-    for call, status in ((lambda: selected(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")), 1),
+    pages = torch.zeros(2, 4000, dtype=torch.int32, device="cuda")     # long enough to need scratch
+    for call, status in ((lambda: paged(t=pages, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")), 1),
                          (lambda: paged(block_rows=32), 1),
                          (lambda: tk.latent_attend_selected(query, cache, sel, float("nan")), 1),
                          (lambda: selected(c=cache.flatten()[4:4 + 299 * 576].view(299, 576)), 2),
