@@ -1005,24 +1005,43 @@ __device__ __forceinline__ float4 ld_peer4(const void *p, uint32_t rank) {
 }
 
 // Joins a cluster's parts of its tile out of its CTAs' shared memory: each CTA
-// takes every cluster-th row, the parts are added in the CTAs' order.
-__device__ void join_cluster(const AttendParams &p, const Ctrl &c, const char *sums) {
+// takes every cluster-th row, the parts are added in the CTAs' order. First the
+// parts' weights, a lane per part, then the sums with all parts' loads in flight.
+constexpr int MAX_CLUSTER = 16;
+
+__device__ void join_cluster(const AttendParams &p, Ctrl &c, const char *sums) {
     const Tile t = tile_at(p, c.first_tile);
+    const int rank = static_cast<int>(cluster_rank()), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    static_assert(sizeof(c.rows) >= ROWS * MAX_CLUSTER * sizeof(float));
+    float(*weight)[MAX_CLUSTER] = reinterpret_cast<float(*)[MAX_CLUSTER]>(c.rows);   // (row numbers: used up)
+    for (int row = rank + p.cluster * warp; row < t.rows; row += p.cluster * (NT / 32)) {
+        const bool on = lane < c.ranks;
+        const float m = on ? ld_peer_f(&c.ref[row], lane) : -INFINITY;
+        float l = on ? ld_peer_f(&c.l[row], lane) : 0.0f, top = m;
+#pragma unroll
+        for (int o = MAX_CLUSTER / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const float f = part_weight(m, top);
+        l *= f;
+#pragma unroll
+        for (int o = MAX_CLUSTER / 2; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane < MAX_CLUSTER) weight[row][lane] = f;
+        if (lane == 0) {
+            c.factor[row] = l;
+            if (p.lse) p.lse[t.base + row] = finished_lse(top, l);
+        }
+    }
+    __syncthreads();
     const int vecs = p.latent / 4, groups = NT / vecs, g = threadIdx.x / vecs, v = threadIdx.x - g * vecs;
-    const int rank = static_cast<int>(cluster_rank());
     if (g >= groups) return;
     for (int row = rank + p.cluster * g; row < t.rows; row += p.cluster * groups) {
-        float top = -INFINITY, l = 0.0f;
-        for (int i = 0; i < c.ranks; ++i) top = fmaxf(top, ld_peer_f(&c.ref[row], i));
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int i = 0; i < c.ranks; ++i) {
-            const float f = part_weight(ld_peer_f(&c.ref[row], i), top);
-            l += f * ld_peer_f(&c.l[row], i);
-            add4(acc, f, ld_peer4(sums + (row * p.latent + v * 4) * 4, i));
-        }
-        write4(p, static_cast<int64_t>(t.base) + row, v, acc, l);
-        if (v == 0 && p.lse) p.lse[t.base + row] = finished_lse(top, l);
+        float4 x[MAX_CLUSTER], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < MAX_CLUSTER; ++i)
+            if (i < c.ranks) x[i] = ld_peer4(sums + (row * p.latent + v * 4) * 4, i);
+#pragma unroll
+        for (int i = 0; i < MAX_CLUSTER; ++i)
+            if (i < c.ranks) add4(acc, weight[row][i], x[i]);
+        write4(p, static_cast<int64_t>(t.base) + row, v, acc, c.factor[row]);
     }
 }
 
@@ -1268,7 +1287,8 @@ struct Deal {
 };
 
 constexpr int MIN_SHARE = 2;                   // blocks of a CTA in equal shares
-constexpr int JOIN_BLOCKS = 5;                 // blocks that cost what the second kernel does
+constexpr int JOIN_BLOCKS = 5;                 // blocks that cost what parts and the second kernel do
+constexpr int SHORT = 4;                       // blocks of a CTA in a cluster of several
 
 Deal deal(const AttendParams &p, const Device &d) {
     Deal r = {};
@@ -1283,11 +1303,17 @@ Deal deal(const AttendParams &p, const Device &d) {
     if (r.blocks < 1) r.blocks = 1;
     const int64_t even = (r.tiles * r.blocks + d.sms - 1) / d.sms;
     const int64_t share = even > MIN_SHARE ? even : MIN_SHARE;
-    // The largest cluster whose CTAs do not get more blocks than equal shares and
-    // the second kernel cost. (Measured: @DEAL@)
+    // Short work goes to the largest cluster that leaves each CTA a few blocks: one
+    // launch instead of two, and no scratch (1 token x 512 rows: 9.9 us against 10.8
+    // in a graph, 14.6 against 20 called one by one; 4096 tokens of pages: 14.7
+    // against 13.3, and 16 against 21). Longer work goes to equal shares (37 tokens x
+    // 128 heads x 2048 rows: 46 us against 50 as clusters of two), except tiles that
+    // a single CTA each finishes about as soon as equal shares would (128 tokens x 16
+    // heads x 2048 rows: 57 us against 65).
     for (int i = 4; i >= 0 && !r.cluster; --i) {
-        const int64_t size = 1 << i;
-        if (size <= r.blocks && r.tiles <= d.clusters[i] && (r.blocks + size - 1) / size <= share + JOIN_BLOCKS)
+        const int64_t size = 1 << i, run = (r.blocks + size - 1) / size;
+        if (size <= r.blocks && r.tiles <= d.clusters[i] &&
+            (size == 1 ? run <= share + JOIN_BLOCKS : run <= SHORT && run <= share + 2))
             r.cluster = static_cast<int32_t>(size);
     }
     const int64_t want = r.cluster ? r.tiles * r.cluster : (r.tiles * r.blocks + MIN_SHARE - 1) / MIN_SHARE;
