@@ -20,7 +20,8 @@ topk_status_t check_append(const latent_bf16_append_t *a) {
     if (!a || a->tokens < 0 || a->tokens > (1 << 27) || a->cache_rows < 0) return TOPK_ERR_ARG;
     if (bad_latent(a->latent)) return TOPK_ERR_WIDTH;
     if (a->tokens == 0) return TOPK_OK;
-    if ((!a->cache && a->cache_rows > 0) || !a->latents || !a->key_rope || !a->positions || !a->cos_sin || !a->slots) return TOPK_ERR_ARG;
+    if ((!a->cache && a->cache_rows > 0) || !a->latents || !a->key_rope || !a->positions || !a->cos_sin || !a->slots)
+        return TOPK_ERR_ARG;
     if (a->max_positions < 1) return TOPK_ERR_ARG;
     const int64_t dim = a->latent + LATENT_ROPE;
     if (a->cache_stride < dim || a->latents_stride < a->latent || a->key_stride < LATENT_ROPE) return TOPK_ERR_WIDTH;

@@ -1,5 +1,22 @@
 // Attention over latent cache rows on the tensor cores: one persistent kernel
 // for both forms, and the kernel that joins the parts of split tiles.
+//
+// A tile is up to 64 (token, head) rows that read the same cache rows; blocks of
+// 64 cache rows pass through shared memory once for scores and sums:
+//     scores (64 tokens x rows) = K Q^T,  weights = 2^(scores - reference),
+//     sums (values x rows) += V^T weights,   V the latent part of K.
+// Both products have the cache as the left operand: the sums of 512 values x 64
+// rows are 256 columns of tensor memory (as rows x values they would fill all of
+// it), and 16 rows cost little more than their share. Warps have one job each
+// (softmax, copies, issue of either product) and meet at mbarriers only.
+//
+// What bounds it. Few heads: DRAM (32 requests x 16 heads x up to 16384 tokens: 84
+// us, 5.2 TB/s). 64 rows a tile: shared memory. A block's operands leave it 36 x 4
+// KB (scores) and 16 x 6 KB (sums) at 128 bytes a cycle and its rows come in once:
+// 2560 cycles a block, what a chunk of 509 tokens x 128 heads over 9000 takes (1.27
+// ms, 0.97 PFLOP/s; tensor pipes 62 % active). More rows a tile would halve that but
+// neither their queries (74 KB for 64) nor their sums have room. Listed rows (no
+// TMA boxes) add the copies' latency: 3800 cycles a block at two blocks in flight.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -28,7 +45,7 @@ constexpr int BLOCKS = 16;                   // blocks that have row numbers and
                                              // than the rings hold
 constexpr int SMEM = 232448;                 // all of a CTA's shared memory
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
-constexpr float LAZY = 60.0f;                // the reference may lag the maximum by this much (log2)
+constexpr float LAZY = 16.0f;                // the reference may lag the maximum by this much (log2)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 using u64 = unsigned long long;
 
@@ -204,8 +221,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
 // 64 rows of 64 values from column x and row y, completing on `bar`.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, u64 *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
@@ -410,7 +427,8 @@ struct RowList {
 // are: every row is apart in scores, weights and sums, and nothing is written
 // for those.
 template <int NR, int THREADS>
-__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, uint32_t query, int chunks, int tid) {
+__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, uint32_t query, int chunks,
+                                           int tid) {
     const int piece = tid & 7;
     for (int r = tid >> 3; r < tile.rows; r += THREADS / 8) {
         const int32_t flat = tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
@@ -420,6 +438,17 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
     }
 }
 
+// After a wait that gave up: no copy may be in flight into shared memory when the
+// CTA ends, so wait (with its own limit) for the last ones into each slot. Copy q
+// went into slot q % slots for the q / slots-th time, q = last, last - step, ..
+__device__ __forceinline__ void settle(u64 *full, int32_t last, int step, int slots) {
+    const uint64_t t0 = global_timer_ns();
+    for (int32_t q = last; q >= 0 && q > last - slots; q -= step)
+        while (!mbar_try_wait(&full[q % slots], static_cast<uint32_t>(q / slots) & 1u) &&
+               global_timer_ns() - t0 < WAIT_LIMIT_NS) {
+        }
+}
+
 // Query and cache rows into shared memory. Each warp has one pair of every
 // block (and with few pairs only some of its rows), so that it waits for one
 // slot a block and the pairs of a block are copied side by side as their slots
@@ -427,9 +456,12 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
 // whole blocks come by TMA, 64 rows of 64 values a copy; their rows past the
 // context's end then hold whatever the page does, and are masked. A tile's query is
 // copied when its first block is on its way (the first tile's by the softmax
-// warps, which have nothing else to do yet). (Measured: the same cache
-// rows gathered four at a time by TMA come at 12 bytes a nanosecond per SM;
-// copies of 16 bytes reach 100 from L2 with four warps.)
+// warps, which have nothing else to do yet).
+// Measured: listed rows gathered four at a time by TMA came at 12 bytes a
+// nanosecond per SM, against up to 100 from L2 by four warps' 16-byte copies;
+// boxes in place of those copies took a chunk of 509 tokens x 128 heads over 9000
+// from 1647 to 1364 us. Eight copying warps, or prefetching rows into L2 ahead of
+// the copies, changed nothing.
 template <int NR>
 __device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &c, const Plan &plan, uint32_t query,
                            uint32_t pairs) {
@@ -465,8 +497,8 @@ __device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &
                 if (lane == 0) {
                     mbar_expect_tx(&c.pair_full[ps], 2 * CHUNK);
                     for (int k = 0; k < 2; ++k)
-                        copy_box(pairs + (2 * ps + k) * CHUNK, map, (2 * unit + k) * 64, first < 0 ? p.cache_rows : first,
-                                 &c.pair_full[ps]);
+                        copy_box(pairs + (2 * ps + k) * CHUNK, map, (2 * unit + k) * 64,
+                                 first < 0 ? p.cache_rows : first, &c.pair_full[ps]);
                 }
                 __syncwarp();
             } else {
@@ -500,6 +532,8 @@ __device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &
         ++piece_no;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (p.tiled && !idle && c.abort)
+        settle(c.pair_full, static_cast<int32_t>(pu * plan.pair_slots + ps) - plan.pairs, plan.pairs, plan.pair_slots);
 }
 
 __device__ void load_ropes(const AttendParams &p, const CUtensorMap *map, Ctrl &c, const Plan &plan, uint32_t ropes) {
@@ -548,6 +582,8 @@ __device__ void load_ropes(const AttendParams &p, const CUtensorMap *map, Ctrl &
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (p.tiled && c.abort)
+        settle(c.rope_full, static_cast<int32_t>(ru * plan.rope_slots + rs) - 1, 1, plan.rope_slots);
 }
 
 // The products, both with the cache as the left operand and the query rows as
@@ -582,8 +618,8 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, const Plan &plan
                     const uint64_t k = matrix(pairs + ps * 2 * CHUNK, 16), qu = q + u * (2 * QCHUNK >> 4);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        tc_mma(d, k + (e >> 2) * (CHUNK >> 4) + (e & 3) * 2, qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2,
-                               KIND, u > 0 || e > 0);
+                        tc_mma(d, k + (e >> 2) * (CHUNK >> 4) + (e & 3) * 2,
+                               qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2, KIND, u > 0 || e > 0);
                     if (++ps == static_cast<uint32_t>(plan.pair_slots)) {
                         ps = 0;
                         ++pu;
@@ -686,10 +722,11 @@ __device__ __forceinline__ int across_index() {
 // Scores to weights, the running reference and sums, and the outputs. Each group
 // of four warps has half of the query rows. Thread t of a group's warp w holds
 // tokens 16 w + t / 4 and 8 further of a block, against the rows 8 j + 2 (t % 4)
-// and the next of its half: their references and sums stay in its registers. The weights' reference is the maximum of the row's first
-// block; weights may grow to 2^60 before it moves (FP32 sums and BF16 weights
-// lose nothing by that), which is seen from the packed weights and almost never
-// happens.
+// and the next of its half: their references and sums stay in its registers.
+// The weights' reference is the maximum of the row's first block; weights may grow
+// to 2^16 before it moves (FP32 sums and BF16 weights lose nothing by that), which
+// is seen from the packed weights and rarely happens. Bound by latency: scores to
+// weights take about 1100 cycles at 64 rows, of which the exponentials are 130.
 template <int NR>
 __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, char *pairs, char *ropes,
                        uint32_t tmem) {
@@ -799,9 +836,10 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                         }
                         const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
                         top = __hmax2(top, v);
-                        *reinterpret_cast<__nv_bfloat162 *>(weights + h * 1024 + (((group * (N / 2) + j) ^ (t0 & 7)) << 4)) = v;
+                        const int at_row = (group * (N / 2) + j) ^ (t0 & 7);
+                        *reinterpret_cast<__nv_bfloat162 *>(weights + h * 1024 + (at_row << 4)) = v;
                     }
-                return fmaxf(__low2float(top), __high2float(top)) > 1.152921504606846976e18f;   // 2^60
+                return fmaxf(__low2float(top), __high2float(top)) > 65536.0f;   // 2^LAZY
             };
             mbar_wait(&c.s_full[i & 1], (i >> 1) & 1u, &c.abort);
             __syncwarp();
@@ -818,7 +856,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                 moved = soft_any(weigh(std::false_type{}));
             }
             if (moved) {
-                // New references: the rows' largest scores of this block where they are 2^60
+                // New references: the rows' largest scores of this block where they are 2^16
                 // above the old ones (or the first the row sees).
                 if (b > at.b0) take();
                 float top[N];
@@ -992,7 +1030,9 @@ __device__ __forceinline__ void write4(const AttendParams &p, int64_t row, int v
     reinterpret_cast<uint2 *>(p.out + row * p.latent)[v] = o;
 }
 
-__device__ __forceinline__ float ld_peer_f(const void *p, uint32_t rank) { return __uint_as_float(ld_peer(peer_addr(p, rank))); }
+__device__ __forceinline__ float ld_peer_f(const void *p, uint32_t rank) {
+    return __uint_as_float(ld_peer(peer_addr(p, rank)));
+}
 
 __device__ __forceinline__ float4 ld_peer4(const void *p, uint32_t rank) {
     float4 v;
@@ -1090,7 +1130,8 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     if (warp < SOFT / 32) soften<NR>(p, c, plan, smem_addr(smem), pairs, ropes, tmem);
     else if (warp < (SOFT + LOAD) / 32) load_pairs<NR>(p, &map, c, plan, smem_addr(smem), smem_addr(pairs));
     else if (warp < (SOFT + LOAD + ROPE_LOAD) / 32) load_ropes(p, &map, c, plan, smem_addr(ropes));
-    else if (warp < NT / 32 - 1) multiply_scores<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
+    else if (warp < NT / 32 - 1)
+        multiply_scores<NR>(p, c, plan, smem_addr(smem), smem_addr(pairs), smem_addr(ropes), tmem);
     else multiply_sums<NR>(p, c, plan, smem_addr(pairs), smem_addr(ropes), tmem);
     __syncwarp();
     tc_fence_before();
@@ -1360,12 +1401,13 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     CUtensorMap map = {};
     p.tiled = p.paged && (1 << p.page_shift) % KEYS == 0 && p.cache_rows >= KEYS ? 1 : 0;
     if (p.tiled) {
-        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.latent + LATENT_ROPE), static_cast<cuuint64_t>(p.cache_rows)};
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.latent + LATENT_ROPE),
+                                    static_cast<cuuint64_t>(p.cache_rows)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.cache_stride) * 2};
         const cuuint32_t box[2] = {64, KEYS}, steps[2] = {1, 1};
         if (d->encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(p.cache), dims, strides, box,
-                      steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                      steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
 
@@ -1397,7 +1439,9 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     cfg.blockDim = dim3(big ? 1024 : 256, 1, 1);
     cfg.dynamicSmemBytes = 0;
     void *join_args[] = {&p, &wide};
-    return cudaLaunchKernelExC(&cfg, big ? reinterpret_cast<const void *>(&join_kernel<1024>) : reinterpret_cast<const void *>(&join_kernel<256>),
+    return cudaLaunchKernelExC(&cfg,
+                               big ? reinterpret_cast<const void *>(&join_kernel<1024>)
+                                   : reinterpret_cast<const void *>(&join_kernel<256>),
                                join_args);
 }
 

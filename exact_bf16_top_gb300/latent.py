@@ -256,7 +256,8 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
         raise ValueError("workspace must be a uint8 tensor from latent_workspace() on the query's device")
     if tokens:
         args = Attend(query.data_ptr(), *_head_strides(query), cache.data_ptr(),
-                      _row_stride(rows, dim, cache_stride), *pointers, out.data_ptr(), lse_ptr, None, 0, rows, tokens, heads, latent, *sizes, scale)
+                      _row_stride(rows, dim, cache_stride), *pointers, out.data_ptr(), lse_ptr, None, 0, rows,
+                      tokens, heads, latent, *sizes, scale)
         lib = _package._lib or load()
         if workspace is None:
             n = lib.latent_bf16_attend_workspace(args, paged)

@@ -445,3 +445,56 @@ def test_refusals():
             tk.latent_append(**{**args, **kw})
     with pytest.raises(TypeError):
         tk.latent_append(cache, x.float(), key, pos, angles(4), pos)
+
+
+def test_the_example_decode_step():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_step.py")
+    spec = importlib.util.spec_from_file_location("decode_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    s = example.make(3, 5000, seed=3)
+    s["lens"][1] = 700                   # fewer than k: the selection is the whole context
+    s["slots"][1] = s["table"][1, 699 // 64] * 64 + 699 % 64
+    out, lse, rows = example.step(s)
+    ref, rl, tol, tl = R.attend(s["query"], s["cache"], R.visible_selected(rows, s["cache"].shape[0]), s["scale"], 512)
+    R.assert_close(out, ref, tol, "out")
+    R.assert_close(lse, rl, tl, "lse")
+    assert int(s["slots"][1]) in rows[1].tolist() and (rows[1] >= 0).sum().item() == 700
+    whole, wl = tk.latent_attend_paged(s["query"], s["cache"], s["lens"], s["table"], s["scale"], lse=True)
+    R.assert_close(whole[1:2], ref[1:2], tol[1:2], "out of a whole context")
+    assert (lse <= wl + 1e-3).all()
+
+
+def test_a_scaled_down_cluster_and_shares_agree():
+    # The same rows through every way of dealing the work: one token's list (a cluster), the same list for many
+    # tokens (equal shares), and as pages of one token each.
+    query, cache, sel = selected_case(1, 16, 256, 900, 4000, 40, empty=0.0)
+    one, l1 = check_selected(query, cache, sel, 256)
+    many, lm = tk.latent_attend_selected(query.expand(400, 16, 320), cache, sel.expand(400, 900).contiguous(), SCALE,
+                                         latent=256, lse=True)
+    paged, lp = tk.latent_attend_paged(query, cache, torch.tensor([900], dtype=torch.int32, device="cuda"), sel, SCALE,
+                                       page_size=1, latent=256, lse=True)
+    ref, rl, tol, tl = R.attend(query, cache, R.visible_selected(sel, 4000), SCALE, 256)
+    for got, lse in ((many, lm), (paged, lp)):
+        R.assert_close(got, ref.expand(got.shape), tol.expand(got.shape), "out")
+        R.assert_close(lse, rl.expand(lse.shape), tl.expand(lse.shape), "lse")
+
+
+@pytest.mark.parametrize("k", [128, 250, 700, 1024, 1100])
+@pytest.mark.parametrize("tokens,heads", [(1, 16), (2, 128), (9, 33)])
+def test_selected_short_work_in_clusters(tokens, heads, k):
+    check_selected(*selected_case(tokens, heads, 384, k, 3000, k + tokens), 384)
+
+
+def test_large_values_survive_a_late_maximum():
+    # The largest score comes last: the weights before it are rescaled, not overflowed.
+    query, cache, sel = selected_case(2, 16, 512, 300, 300, 41, empty=0.0)
+    sel[:] = torch.arange(300, device="cuda").int()
+    cache[:, 1:512] = (cache[:, 1:512].float() * 1e18).to(torch.bfloat16)
+    query[:, :, 1:512] = 0.0
+    cache[:, 0], query[:, :, 0] = 0.0, 1.0
+    cache[150:, 0] = 10.0
+    cache[299, 0] = 100.0
+    check_selected(query, cache, sel, 512, scale=1.0)
