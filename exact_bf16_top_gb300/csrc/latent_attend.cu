@@ -76,7 +76,6 @@ struct Ctrl {
 // each), a ring of pairs of latent chunks, a ring of rotary chunks (where a
 // block's weights go once its scores are out), the control block.
 struct Plan {
-    int parts;                                 // warps that load one pair of a block
     int pairs, pair_slots, rope_slots;         // pairs per block; slots: two blocks' at least
     uint32_t query_bytes;
 };
@@ -85,7 +84,6 @@ template <int NR>
 __host__ __device__ constexpr Plan make_plan(int latent) {
     Plan r = {};
     r.pairs = latent / 128;
-    r.parts = r.pairs == 1 ? 4 : r.pairs == 2 ? 2 : 1;
     r.query_bytes = static_cast<uint32_t>((2 * r.pairs + 1) * NR * 128);
     const int units = static_cast<int>((SMEM - 1024 - sizeof(Ctrl) - r.query_bytes) / CHUNK);
     r.rope_slots = units / (2 * r.pairs + 1);
@@ -465,64 +463,64 @@ __device__ __forceinline__ void settle(u64 *full, int32_t last, int step, int sl
 template <int NR>
 __device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &c, const Plan &plan, uint32_t query,
                            uint32_t pairs) {
+    constexpr int SHARE = KEYS / (LOAD / 32);  // rows of a warp
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - SOFT) >> 5;
-    const int unit = warp % plan.pairs, part = warp / plan.pairs;
-    // (Three pairs: one warp only helps with the query; by TMA, one warp a pair.)
-    const bool idle = part >= (p.tiled ? 1 : plan.parts);
     const int64_t pitch = p.cache_stride * 2;
-    const int rows = KEYS / plan.parts, half = lane >> 4, piece = lane & 15;
-    const char *cache = reinterpret_cast<const char *>(p.cache) + unit * 256 + piece * 16;
-    const int r0 = part * rows + half;         // this lane copies rows r0, r0 + 2, ..
+    const int half = lane >> 4, piece = lane & 15;
+    const char *cache = reinterpret_cast<const char *>(p.cache) + piece * 16;
+    const int r0 = warp * SHARE + half;        // by copies this lane has rows r0, r0 + 2, .. of every pair
     const uint32_t dst = pairs + (piece >> 3) * CHUNK + r0 * 128;
+    const int mine = p.tiled ? 0 : warp * SHARE + (lane & (SHARE - 1));
     Cursor at(c);
-    uint32_t ps = unit, pu = 0, piece_no = 0;  // slot and its use
+    uint32_t ps = 0, pu = 0, piece_no = 0;     // the block's first slot and its use
     while (at.next(p, lane)) {
         const RowList list(p, at);
-        const int mine = part * rows + (lane & (rows - 1));
-        int32_t now[2], then[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) now[h] = list.fetch(p, at.b0 * KEYS + mine + 32 * h);
+        int32_t now = list.fetch(p, at.b0 * KEYS + mine);
         for (int32_t b = at.b0; b < at.b1; ++b) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) then[h] = list.fetch(p, (b + 1) * KEYS + mine + 32 * h);
+            const int32_t then = list.fetch(p, (b + 1) * KEYS + mine);
             if (piece_no && b == at.b0 + 1) {
                 wait(&c.q_empty, piece_no + 1, c);
                 load_query<NR, LOAD>(p, at.tile, query, 2 * plan.pairs + 1, threadIdx.x - SOFT);
                 copies_arrive(&c.q_full);
             }
-            if (idle) continue;
-            wait(&c.pair_empty[ps], pu + 1, c);
-            if (p.tiled) {
-                const int32_t first = list.row(p, now[0], b * KEYS);
-                if (lane == 0) {
-                    mbar_expect_tx(&c.pair_full[ps], 2 * CHUNK);
-                    for (int k = 0; k < 2; ++k)
-                        copy_box(pairs + (2 * ps + k) * CHUNK, map, (2 * unit + k) * 64,
-                                 first < 0 ? p.cache_rows : first, &c.pair_full[ps]);
-                }
-                __syncwarp();
-            } else {
-                const uint32_t to = dst + ps * 2 * CHUNK;
+            const int32_t here = list.row(p, now, b * KEYS + mine);
+            const char *src[SHARE / 2];
+            bool on[SHARE / 2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (32 * h >= rows) break;
-                    const int32_t here = list.row(p, now[h], b * KEYS + mine + 32 * h);
-#pragma unroll 8
-                    for (int k = 0; k < min(rows, 32) / 2; ++k) {
-                        const int32_t v = __shfl_sync(0xFFFFFFFFu, here, 2 * k + half);
-                        copy16(to + h * 32 * 128 + k * 256 + (((piece ^ (r0 + 2 * k)) & 7) << 4),
-                               cache + (v >= 0 ? v * pitch : 0), v >= 0);
-                    }
+            for (int k = 0; k < SHARE / 2; ++k) {
+                const int32_t v = __shfl_sync(0xFFFFFFFFu, here, 2 * k + half);
+                on[k] = v >= 0;
+                src[k] = cache + (on[k] ? v * pitch : 0);
+            }
+            for (int u = p.tiled ? warp : 0; u < plan.pairs; u += p.tiled ? LOAD / 32 : 1) {
+                uint32_t slot = ps + u, used = pu;
+                if (slot >= static_cast<uint32_t>(plan.pair_slots)) {
+                    slot -= plan.pair_slots;
+                    ++used;
                 }
-                copies_arrive(&c.pair_full[ps]);
+                wait(&c.pair_empty[slot], used + 1, c);
+                if (p.tiled) {
+                    if (lane == 0) {
+                        mbar_expect_tx(&c.pair_full[slot], 2 * CHUNK);
+                        for (int k = 0; k < 2; ++k)
+                            copy_box(pairs + (2 * slot + k) * CHUNK, map, (2 * u + k) * 64,
+                                     here < 0 ? p.cache_rows : here, &c.pair_full[slot]);
+                    }
+                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < SHARE / 2; ++k)
+                        copy16(dst + slot * 2 * CHUNK + k * 256 + (((piece ^ (r0 + 2 * k)) & 7) << 4), src[k] + u * 256,
+                               on[k]);
+                    copies_arrive(&c.pair_full[slot]);
+                }
             }
             ps += plan.pairs;
             if (ps >= static_cast<uint32_t>(plan.pair_slots)) {
                 ps -= plan.pair_slots;
                 ++pu;
             }
-            now[0] = then[0];
-            now[1] = then[1];
+            now = then;
         }
         if (piece_no && at.b1 == at.b0 + 1) {
             wait(&c.q_empty, piece_no + 1, c);
@@ -532,8 +530,9 @@ __device__ void load_pairs(const AttendParams &p, const CUtensorMap *map, Ctrl &
         ++piece_no;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (p.tiled && !idle && c.abort)
-        settle(c.pair_full, static_cast<int32_t>(pu * plan.pair_slots + ps) - plan.pairs, plan.pairs, plan.pair_slots);
+    if (p.tiled && warp < plan.pairs && c.abort)
+        settle(c.pair_full, static_cast<int32_t>(pu * plan.pair_slots + ps) - plan.pairs + warp, plan.pairs,
+               plan.pair_slots);
 }
 
 __device__ void load_ropes(const AttendParams &p, const CUtensorMap *map, Ctrl &c, const Plan &plan, uint32_t ropes) {
@@ -1095,7 +1094,7 @@ __global__ void __launch_bounds__(NT, 1) attend_kernel(const __grid_constant__ A
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_SLOTS; ++s) {
-            mbar_init(&c.pair_full[s], p.tiled ? 1 : 32 * plan.parts);
+            mbar_init(&c.pair_full[s], p.tiled ? 1 : LOAD);
             mbar_init(&c.rope_full[s], p.tiled ? 2 : ROPE_LOAD + 1);
             mbar_init(&c.pair_empty[s], 1);
             mbar_init(&c.rope_empty[s], 1);

@@ -7,11 +7,14 @@ selection.
 Scores are random here (a model's indexer writes them); sizes are those of the
 library's benchmark: 64-token pages, k = 2048, a 512-value latent, 16 heads.
 """
+import os
 import sys
 
 import torch
 
-import exact_bf16_top_gb300 as tk
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import exact_bf16_top_gb300 as tk  # noqa: E402
 
 PAGE, K, HEADS, LATENT, ROPE = 64, 2048, 16, 512, 64
 
