@@ -33,7 +33,7 @@ struct AttendParams {
 
 cudaError_t launch_append(const latent_bf16_append_t &a, int sms, cudaStream_t stream);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
-int64_t attend_workspace(const AttendParams &p);   // bytes this call needs, -1 if the device cannot be asked
+int64_t attend_workspace(AttendParams p);   // bytes this call needs, -1 if the device cannot be asked
 int64_t workspace_bytes();   // 0 if the device cannot be asked
 
 }  // namespace topk::latent

@@ -236,6 +236,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// Whether either of two BF16 values is NaN or infinite.
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SOFT) : "memory"); }
 
 __device__ __forceinline__ bool soft_any(bool v) {
@@ -778,12 +783,12 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             const uint32_t scores = lanes + S_COL + (i & 1) * NR + group * (NR / 2);
             char *weights = ropes + rs * CHUNK + t0 * 128 + quad * 4;
             float x[2 * N];                    // x[4 j + 2 h + e]: token h, the thread's row 2 j + e
-            bool bad[2] = {false, false};
+            bool odd_token[2] = {false, false};
             // Scores in log2 units; where masked, -inf. A cache row that some or all of the
-            // tile's rows may not see must not reach them through 0 x inf: where a score that
-            // is masked here is not finite (a cache row's NaN and infinities show in the
-            // scores of all rows), the cache row is zeroed and the weights of the rows that
-            // do see it are NaN.
+            // tile's rows may not see must not reach them through 0 x inf: a masked score
+            // that is not finite marks the token, and what is not finite among the token's
+            // values is zeroed below (rows that do see it have a NaN or infinite score of
+            // their own; a query's own NaN marks tokens too, whose values then are fine).
             auto take = [&]() {
                 tc_load_groups<NR / 16>(scores, x);
                 tc_fence_before();
@@ -806,13 +811,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                         }
                         odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, 1);
                         odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, 2);
-                        bad[h] = odd;
-                        if (odd) {
-#pragma unroll
-                            for (int n = 0; n < N; ++n)
-                                if (there[h] && token + 8 * h < c.lim[row_of(n)])
-                                    x[4 * (n >> 1) + 2 * h + (n & 1)] = __uint_as_float(0x7FC00000u);
-                        }
+                        odd_token[h] = odd;
                     }
                 }
             };
@@ -900,12 +899,16 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (bad[h]) {
+                if (odd_token[h]) {
                     uint32_t s = ps;
                     for (int u = 0; u < plan.pairs; ++u) {
-                        for (int k = quad; k < 16; k += 4)
-                            *reinterpret_cast<uint4 *>(pairs + s * 2 * CHUNK + (k >> 3) * CHUNK + (t0 + 8 * h) * 128 +
-                                                       (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int k = quad; k < 16; k += 4) {
+                            uint4 *at16 = reinterpret_cast<uint4 *>(pairs + s * 2 * CHUNK + (k >> 3) * CHUNK +
+                                                                    (t0 + 8 * h) * 128 + (k & 7) * 16);
+                            const uint4 v = *at16;
+                            if (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w))
+                                *at16 = make_uint4(0, 0, 0, 0);
+                        }
                         if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
                     }
                 }
@@ -1377,9 +1380,10 @@ Deal deal(const AttendParams &p, const Device &d) {
 
 }  // namespace
 
-int64_t attend_workspace(const AttendParams &p) {
+int64_t attend_workspace(AttendParams p) {
     Device *d = nullptr;
     if (device(d) != cudaSuccess) return -1;
+    if (p.rows_per_request > p.tokens) p.rows_per_request = p.tokens;
     return deal(p, *d).cluster ? 0 : workspace_bytes();
 }
 
@@ -1387,6 +1391,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     Device *d = nullptr;
     cudaError_t e = device(d);
     if (e != cudaSuccess) return e;
+    if (p.rows_per_request > p.tokens) p.rows_per_request = p.tokens;   // (one request)
     const Deal plan = deal(p, *d);
     p.tiles_per_request = plan.tiles_per_request;
     p.tiles = static_cast<int32_t>(plan.tiles);

@@ -18,6 +18,7 @@ from ._latent_abi import Append, Attend
 ROPE = 64
 LATENTS = (128, 256, 384, 512)
 MAX_HEADS = 256
+MAX_ROWS = 2 ** 31 - 1
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 # (Plain integers: a step's smallest calls take a few microseconds on the host.)
@@ -88,6 +89,8 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
     if not fine:
         _refuse(cache=(cache, _BF16, 2), latent=(latent, _BF16, 2), key_rope=(key_rope, _BF16, 2),
                 positions=(positions, _I32, 1), cos_sin=(cos_sin, _F32, 2), slots=(slots, _I32, 1))
+    if rows > MAX_ROWS or tokens > MAX_ROWS:
+        raise ValueError(f"at most {MAX_ROWS} cache rows and tokens")
     if width not in LATENTS or dim != width + ROPE:
         raise ValueError(f"latent must have one of {LATENTS} columns and cache {ROPE} more")
     if key_rope.shape != (tokens, ROPE) or positions.shape[0] != tokens or slots.shape[0] != tokens:
@@ -198,6 +201,8 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     width = pages * page_size if width is None else int(width)
     if not 0 <= width <= pages * page_size:
         raise ValueError("width exceeds the block table")
+    if max(width, stride, rows_per_request, page_size) > MAX_ROWS:
+        raise ValueError("a length, stride or count passes 31 bits")
     return _attend(1, dev, query, cache, scale, latent, out, lse, workspace, stream,
                    (None, 0, valid_len.data_ptr(), block_table.data_ptr()),
                    (0, width, stride if requests > 1 else pages, page_size,
@@ -225,6 +230,8 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
         fine = False
     if not fine:
         _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2))
+    if rows > MAX_ROWS:
+        raise ValueError(f"cache must have at most {MAX_ROWS} rows")
     if latent not in LATENTS or dim != latent + ROPE or cache_dim != dim:
         raise ValueError(f"latent must be one of {LATENTS}, query and cache rows latent + {ROPE} values")
     if not 1 <= heads <= MAX_HEADS:

@@ -338,6 +338,29 @@ def test_paged_what_a_token_may_not_see_does_not_reach_it(heads, bad):
         R.assert_close(lse[s], rl[s], tl[s], "lse")
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heads", [4, 16])
+def test_paged_a_bad_query_row_stays_alone(heads, bad):
+    # One (token, head) row of the chunk holds NaN or infinity: only its own output may.
+    query, cache, valid, table, kw = paged_case([130, 71], 5, heads, 256, 64, 18)
+    clean, cl = check_paged(query, cache, valid, table, kw, 256)
+    query[1, 2] = bad
+    query[8, 0, 300] = bad
+    out, lse = tk.latent_attend_paged(query, cache, valid, table, SCALE, latent=256, lse=True, **kw)
+    touched = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    touched[1, 2] = touched[8, 0] = True
+    assert torch.equal(out[~touched], clean[~touched]) and torch.equal(lse[~touched], cl[~touched])
+    assert not torch.isfinite(out[1, 2]).any()
+
+
+def test_paged_rows_per_request_past_the_tokens():
+    query, cache, valid, table, kw = paged_case([90], 3, 16, 128, 64, 19)
+    want, _ = check_paged(query, cache, valid, table, kw, 128)
+    got, _ = tk.latent_attend_paged(query, cache, valid, table, SCALE, latent=128,
+                                    **dict(kw, rows_per_request=2 ** 31 - 1))
+    assert torch.equal(got, want)
+
+
 def test_paged_one_long_context():
     check_paged(*paged_case([50_001], 2, 16, 512, 64, 17), 512)
 
