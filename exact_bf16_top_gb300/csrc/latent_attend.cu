@@ -199,6 +199,19 @@ __device__ __forceinline__ void tc_load16(uint32_t addr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Sixteen of a shared array's floats, 16 bytes a load (as single loads they
+// outweighed all else of an output: 5.5 us a tile of 64 x 512 values).
+__device__ __forceinline__ void shared16(const float *from, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(from + i);
+        v[i] = x.x;
+        v[i + 1] = x.y;
+        v[i + 2] = x.z;
+        v[i + 3] = x.w;
+    }
+}
+
 __device__ __forceinline__ void tc_store16(uint32_t addr, const float (&v)[16]) {
     uint32_t r[16];
 #pragma unroll
@@ -770,8 +783,10 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
         }
         low = __reduce_min_sync(0xFFFFFFFFu, low);
         float l[N], ref[N];
+        int32_t lim[N];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
+            lim[n] = c.lim[row_of(n)];
             l[n] = 0.0f;
             ref[n] = c.ref[row_of(n)];
         }
@@ -805,7 +820,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                         for (int n = 0; n < N; ++n) {
                             float &v = x[4 * (n >> 1) + 2 * h + (n & 1)];
                             const int r = row_of(n);
-                            const bool seen = there[h] && token + 8 * h < c.lim[r];
+                            const bool seen = there[h] && token + 8 * h < lim[n];
                             odd |= !seen && r < at.tile.rows && !(fabsf(v) < INFINITY);
                             v = seen ? v : -INFINITY;
                         }
@@ -887,10 +902,11 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
 #pragma unroll
                         for (int v = 0; v < NR; v += 16) {
                             if (((h * (NR / 16) + v / 16) & 1) != group) continue;
-                            float o[16];
+                            float o[16], f[16];
+                            shared16(&c.factor[v], f);
                             tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= c.factor[v + e];
+                            for (int e = 0; e < 16; ++e) o[e] *= f[e];
                             tc_store16(lanes + O_COL + h * NR + v, o);
                         }
                     tc_wait_st();
@@ -938,7 +954,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             const bool sees = c.lim[tid] > start;
             const float sum = c.across[0][tid] + c.across[1][tid] + c.across[2][tid] + c.across[3][tid];
             c.l[tid] = sees ? sum : 0.0f;
-            c.factor[tid] = 1.0f / sum;
+            c.factor[tid] = sees && sum != 0.0f ? 1.0f / sum : 0.0f;   // (0: an empty row, whatever its sums)
             if (!sees) c.ref[tid] = -INFINITY;
         }
         soft_sync();
@@ -952,13 +968,14 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
 #pragma unroll
                 for (int v = 0; v < NR; v += 16) {
                     if (((h * (NR / 16) + v / 16) & 1) != group) continue;
-                    float o[16];
+                    float o[16], f[16];
+                    shared16(&c.factor[v], f);
                     tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         // Even lanes take the pair's values of one row, odd lanes of the next.
-                        const float a = c.l[v + e] == 0.0f ? 0.0f : o[e] * c.factor[v + e];
-                        const float a1 = c.l[v + e + 1] == 0.0f ? 0.0f : o[e + 1] * c.factor[v + e + 1];
+                        const float a = f[e] == 0.0f ? 0.0f : o[e] * f[e];
+                        const float a1 = f[e + 1] == 0.0f ? 0.0f : o[e + 1] * f[e + 1];
                         const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : a1, 1);
                         const int row = v + e + (lane & 1);
                         const __nv_bfloat162 two = lane & 1 ? __floats2bfloat162_rn(other, a1)
@@ -975,11 +992,12 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
 #pragma unroll
                 for (int v = 0; v < NR; v += 16) {
                     if (((h * (NR / 16) + v / 16) & 1) != group) continue;
-                    float o[16];
+                    float o[16], f[16];
+                    shared16(&c.factor[v], f);
                     tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        sums[(v + e) * p.latent + h * 128 + w * 32 + lane] = c.l[v + e] == 0.0f ? 0.0f : o[e];
+                        sums[(v + e) * p.latent + h * 128 + w * 32 + lane] = f[e] == 0.0f ? 0.0f : o[e];
                 }
         } else {
             Part &part = parts[2 * blockIdx.x + (at.b0 == 0 ? 1 : 0)];
@@ -991,11 +1009,12 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
 #pragma unroll
                 for (int v = 0; v < NR; v += 16) {
                     if (((h * (NR / 16) + v / 16) & 1) != group) continue;
-                    float o[16];
+                    float o[16], f[16];
+                    shared16(&c.factor[v], f);
                     tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        part.sum[(v + e) * p.latent + h * 128 + w * 32 + lane] = c.l[v + e] == 0.0f ? 0.0f : o[e];
+                        part.sum[(v + e) * p.latent + h * 128 + w * 32 + lane] = f[e] == 0.0f ? 0.0f : o[e];
                 }
         }
         if (!p.cluster && at.b0 == 0 && tid == 0 && (by_tile || !direct)) {
