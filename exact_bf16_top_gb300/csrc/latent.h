@@ -28,7 +28,7 @@ struct AttendParams {
     int32_t width, table_stride, page_shift, block_rows, rows_per_request;
     float scale;
     void *workspace;
-    int32_t tiles, tiles_per_request, min_share, sms, tiled, cluster;   // filled in by launch_attend
+    int32_t tiles, tiles_per_request, min_share, sms, tiled, cluster, tile_cost;   // filled in by launch_attend
 };
 
 cudaError_t launch_append(const latent_bf16_append_t &a, int sms, cudaStream_t stream);

@@ -59,7 +59,7 @@ struct Ctrl {
     u64 q_first, q_full, q_empty;              // the first query tile, a later one is in / it is used up
     u64 drain[2];
     long long sums[NT / 32];
-    int32_t first_tile, first_block;
+    int32_t first_tile, first_unit;
     int32_t ranks;                             // CTAs of the cluster that have blocks
     long long begin, share, total;
     uint32_t tmem;
@@ -319,27 +319,34 @@ __device__ __forceinline__ int32_t tile_len_warp(const AttendParams &p, const Ti
 }
 
 // All blocks of all tiles in order are cut into equal shares, one per CTA: a
-// CTA's share is a run of pieces, each part or all of one tile's blocks. (Or,
+// CTA's share is a run of pieces, each part or all of one tile's blocks. Where a
+// CTA has several tiles, a tile counts TILE_COST blocks more than it has: its
+// query, first reference and outputs (854 tiles
+// of 1 to 4 blocks: 118 us counted as none, 87 as five). (Or,
 // where the host chose so, a cluster's CTAs share one tile.)
 struct Cursor {
-    int32_t next_tile, next_block;
+    int32_t next_tile, next_unit;
     long long left;
     Tile tile;
     int32_t b0, b1, blocks, len, low;   // the piece: blocks [b0, b1) of `blocks`
+    int32_t u0, u1, units;              // the same with the tile's own cost in front
     __device__ Cursor(const Ctrl &c)
-        : next_tile(c.first_tile), next_block(c.first_block),
+        : next_tile(c.first_tile), next_unit(c.first_unit),
           left(min(c.begin + c.share, c.total) - c.begin) {}
     __device__ bool next(const AttendParams &p, int lane) {
         if (left <= 0) return false;
         tile = tile_at(p, next_tile);
         len = tile_len_warp(p, tile, lane, low);
         blocks = blocks_of(len);
-        b0 = next_block;
-        b1 = static_cast<int32_t>(min(static_cast<long long>(blocks), b0 + left));
-        left -= b1 - b0;
+        units = blocks + p.tile_cost;
+        u0 = next_unit;
+        u1 = static_cast<int32_t>(min(static_cast<long long>(units), u0 + left));
+        b0 = max(0, u0 - p.tile_cost);
+        b1 = max(0, u1 - p.tile_cost);
+        left -= u1 - u0;
         ++next_tile;
-        next_block = 0;
-        return true;
+        next_unit = 0;
+        return b1 > b0;                 // (a share that ends in a tile's cost leaves it to the next CTA)
     }
 };
 
@@ -354,7 +361,7 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
             const int32_t per = (n + p.cluster - 1) / p.cluster;
             if (lane == 0) {
                 c.first_tile = tile;
-                c.first_block = rank * per;
+                c.first_unit = rank * per;
                 c.begin = 0;
                 c.share = c.total = max(0, min(per, n - rank * per));
                 c.ranks = (n + per - 1) / per;
@@ -365,12 +372,12 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
     }
     if (!p.paged) {
         if (tid == 0) {
-            const long long n = blocks_of(p.k);
+            const long long n = blocks_of(p.k) + p.tile_cost;
             c.total = n * p.tiles;
             c.share = max(static_cast<long long>(p.min_share), (c.total + gridDim.x - 1) / gridDim.x);
             c.begin = min(c.total, c.share * blockIdx.x);
             c.first_tile = static_cast<int32_t>(c.begin / n);
-            c.first_block = static_cast<int32_t>(c.begin % n);
+            c.first_unit = static_cast<int32_t>(c.begin % n);
         }
         __syncthreads();
         return;
@@ -378,7 +385,7 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
     const int32_t per = (p.tiles + NT - 1) / NT;
     const int32_t t0 = min(p.tiles, tid * per), t1 = min(p.tiles, t0 + per);
     long long sum = 0;
-    for (int32_t t = t0; t < t1; ++t) sum += blocks_of(tile_len(p, tile_at(p, t)));
+    for (int32_t t = t0; t < t1; ++t) sum += blocks_of(tile_len(p, tile_at(p, t))) + p.tile_cost;
     long long pre = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -404,10 +411,10 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
     if (begin >= before && begin < before + sum) {
         long long at = before;
         for (int32_t t = t0; t < t1; ++t) {
-            const int32_t n = blocks_of(tile_len(p, tile_at(p, t)));
+            const int32_t n = blocks_of(tile_len(p, tile_at(p, t))) + p.tile_cost;
             if (begin < at + n) {
                 c.first_tile = t;
-                c.first_block = static_cast<int32_t>(begin - at);
+                c.first_unit = static_cast<int32_t>(begin - at);
                 break;
             }
             at += n;
@@ -1021,12 +1028,12 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             Joint j;
             j.tile = at.next_tile - 1;
             j.cta = static_cast<int32_t>(blockIdx.x);
-            j.parts = static_cast<int32_t>((done + at.blocks - 1) / c.share) - j.cta + 1;
+            j.parts = static_cast<int32_t>((done - at.u0 + at.units - 1) / c.share) - j.cta + 1;
             j.unused = 0;
             joints[by_tile ? j.tile : j.cta] = j;
         }
         split_here |= at.b0 == 0 && !direct;
-        done += at.b1 - at.b0;
+        done += at.u1 - at.u0;
         tc_fence_before();
         soft_sync();
     }
@@ -1363,6 +1370,7 @@ struct Deal {
 };
 
 constexpr int MIN_SHARE = 2;                   // blocks of a CTA in equal shares
+constexpr int TILE_COST = 5;                   // what a tile costs besides its blocks, in blocks
 constexpr int JOIN_BLOCKS = 5;                 // blocks that cost what parts and the second kernel do
 constexpr int SHORT = 4;                       // blocks of a CTA in a cluster of several
 
@@ -1415,6 +1423,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
     p.tiles_per_request = plan.tiles_per_request;
     p.tiles = static_cast<int32_t>(plan.tiles);
     p.cluster = plan.cluster;
+    p.tile_cost = plan.tiles > d->sms ? TILE_COST : 0;
     p.min_share = MIN_SHARE;
     p.sms = d->sms;
     const unsigned grid = plan.grid;
