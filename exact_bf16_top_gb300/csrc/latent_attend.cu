@@ -16,7 +16,7 @@
 // 2560 cycles a block, what a chunk of 509 tokens x 128 heads over 9000 takes (1.27
 // ms, 0.97 PFLOP/s; tensor pipes 62 % active). More rows a tile would halve that but
 // neither their queries (74 KB for 64) nor their sums have room. Listed rows (no
-// TMA boxes) add the copies' latency: 3800 cycles a block at two blocks in flight.
+// TMA boxes) add the copies' latency: 3300 cycles a block at two blocks in flight.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -321,9 +321,9 @@ __device__ __forceinline__ int32_t tile_len_warp(const AttendParams &p, const Ti
 // All blocks of all tiles in order are cut into equal shares, one per CTA: a
 // CTA's share is a run of pieces, each part or all of one tile's blocks. Where a
 // CTA has several tiles, a tile counts TILE_COST blocks more than it has: its
-// query, first reference and outputs (854 tiles
-// of 1 to 4 blocks: 118 us counted as none, 87 as five). (Or,
-// where the host chose so, a cluster's CTAs share one tile.)
+// query, first reference and outputs (854 tiles of 1 to 4 blocks: 118 us counted
+// as none, 87 as five). (Or, where the host chose so, a cluster's CTAs share one
+// tile.)
 struct Cursor {
     int32_t next_tile, next_unit;
     long long left;
@@ -970,28 +970,35 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
         const bool direct = at.b0 == 0 && at.b1 == at.blocks;
         if (direct) {
             if (p.lse && tid < at.tile.rows) p.lse[at.tile.base + tid] = finished_lse(c.ref[tid], c.l[tid]);
-            uint16_t *out = p.out + static_cast<int64_t>(at.tile.base) * p.latent + w * 32 + (lane & ~1);
-            for (int h = 0; h < plan.pairs; ++h)
+            // A lane has one value of 16 rows; two lanes trade theirs for pairs of one row
+            // each. (Tiles of all rows store without a test a row: 1144 tokens x 128 heads x
+            // 175 rows 194 us with it, 169 without; four lanes' 8-byte stores: 209.)
+            const bool odd = (lane & 1) != 0;
+            uint16_t *out = p.out + (static_cast<int64_t>(at.tile.base) + (lane & 1)) * p.latent + w * 32 + (lane & ~1);
+            auto write = [&](auto all) {
+                for (int h = 0; h < plan.pairs; ++h)
 #pragma unroll
-                for (int v = 0; v < NR; v += 16) {
-                    if (((h * (NR / 16) + v / 16) & 1) != group) continue;
-                    float o[16], f[16];
-                    shared16(&c.factor[v], f);
-                    tc_load16(lanes + O_COL + h * NR + v, o);
+                    for (int v = 0; v < NR; v += 16) {
+                        if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                        float o[16], f[16];
+                        shared16(&c.factor[v], f);
+                        tc_load16(lanes + O_COL + h * NR + v, o);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        // Even lanes take the pair's values of one row, odd lanes of the next.
-                        const float a = f[e] == 0.0f ? 0.0f : o[e] * f[e];
-                        const float a1 = f[e + 1] == 0.0f ? 0.0f : o[e + 1] * f[e + 1];
-                        const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : a1, 1);
-                        const int row = v + e + (lane & 1);
-                        const __nv_bfloat162 two = lane & 1 ? __floats2bfloat162_rn(other, a1)
-                                                            : __floats2bfloat162_rn(a, other);
-                        if (row < at.tile.rows)
-                            *reinterpret_cast<__nv_bfloat162 *>(out + static_cast<int64_t>(row) * p.latent + h * 128) =
-                                two;
+                        for (int e = 0; e < 16; e += 2) {
+                            const float x = f[e] == 0.0f ? 0.0f : o[e] * f[e];
+                            const float y = f[e + 1] == 0.0f ? 0.0f : o[e + 1] * f[e + 1];
+                            const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? x : y, 1);
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(odd ? other : x, odd ? y : other);
+                            if (decltype(all)::value || v + e + (lane & 1) < at.tile.rows)
+                                *reinterpret_cast<__nv_bfloat162 *>(
+                                    out + static_cast<uint32_t>((v + e) * p.latent + h * 128)) = two;
+                        }
                     }
-                }
+            };
+            if (at.tile.rows == NR)
+                write(std::true_type{});
+            else
+                write(std::false_type{});
         } else if (p.cluster) {
             // The rings are used up: this CTA's part stays there for the cluster to join.
             float *sums = reinterpret_cast<float *>(pairs);
