@@ -22,6 +22,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <mutex>
 #include <type_traits>
 #include <utility>
@@ -46,6 +47,8 @@ constexpr int BLOCKS = 16;                   // blocks that have row numbers and
 constexpr int SMEM = 232448;                 // all of a CTA's shared memory
 constexpr uint32_t O_COL = 0, S_COL = 256;   // tensor memory columns: sums (4 x NR), scores (2 x NR)
 constexpr float LAZY = 16.0f;                // the reference may lag the maximum by this much (log2)
+constexpr float LOWEST = -FLT_MAX;           // the reference of a row that has seen no score above -inf: finite, so
+                                             // that 2^(-inf - reference) is 0 in every block
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 using u64 = unsigned long long;
 
@@ -64,7 +67,8 @@ struct Ctrl {
     long long begin, share, total;
     uint32_t tmem;
     volatile uint32_t abort;
-    alignas(16) float ref[ROWS];               // reference maximum (log2); +inf: a row that sees nothing here
+    alignas(16) float ref[ROWS];               // reference maximum (log2), LOWEST at first; +inf: a row that sees
+                                               // nothing here
     alignas(16) float factor[ROWS];
     float l[ROWS];
     int32_t lim[ROWS];                         // tokens a row may see
@@ -779,7 +783,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             int32_t lim = 0;
             if (tid < at.tile.rows) lim = p.paged ? token_len(p, (at.tile.base + tid) / p.heads) : INT32_MAX;
             c.lim[tid] = lim;
-            c.ref[tid] = lim > start ? -INFINITY : INFINITY;
+            c.ref[tid] = lim > start ? LOWEST : INFINITY;
         }
         soft_sync();
         int32_t low = INT32_MAX;
@@ -850,9 +854,8 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                             a = exp2_fast(fmaf(a, scale, -ref[2 * j]));
                             d = exp2_fast(fmaf(d, scale, -ref[2 * j + 1]));
                         } else {
-                            const float ea = exp2_fast(a - ref[2 * j]), ed = exp2_fast(d - ref[2 * j + 1]);
-                            a = a == -INFINITY ? 0.0f : ea;      // (masked: the reference may be -inf too)
-                            d = d == -INFINITY ? 0.0f : ed;
+                            a = exp2_fast(a - ref[2 * j]);
+                            d = exp2_fast(d - ref[2 * j + 1]);
                         }
                         const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
                         top = __hmax2(top, v);
@@ -891,8 +894,8 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                     const float t = fmaxf(fmaxf(c.across[0][tid], c.across[1][tid]),
                                           fmaxf(c.across[2][tid], c.across[3][tid]));
                     const float old = c.ref[tid];
-                    const bool move = t > old + LAZY || (old == -INFINITY && t > old);
-                    c.factor[tid] = !move ? 1.0f : old == -INFINITY ? 0.0f : exp2_fast(old - t);
+                    const bool move = t > old + LAZY;  // (of LOWEST: t > old)
+                    c.factor[tid] = move ? exp2_fast(old - t) : 1.0f;
                     if (move) c.ref[tid] = t;
                 }
                 soft_sync();

@@ -22,7 +22,8 @@
  *     s_j   = scale * <query[t, h], row_j>          over the rows j it may see
  *     p_j   = exp(s_j - lse),   lse = log sum_j exp(s_j)
  *     out   = sum_j p_j c_j                          (latent values)
- * A query row that sees nothing gets out = 0 and lse = -inf. A cache row that
+ * A query row that sees nothing, or whose scores are all -inf, gets out = 0 and
+ * lse = -inf; a score of -inf among others weighs nothing. A cache row that
  * no query row of the call may see is never part of a result, whatever it holds.
  * If a row that query row (t, h) sees makes its s_j NaN or +inf, out[t, h] is NaN.
  */
