@@ -253,6 +253,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// The largest of |a|, |b| and m, NaN if one of them is.
+__device__ __forceinline__ float largest(float m, float a, float b) {
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(m), "f"(a), "f"(b));
+    return y;
+}
+
 // Whether either of two BF16 values is NaN or infinite.
 __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
@@ -450,18 +457,19 @@ struct RowList {
 };
 
 // A tile's query rows into shared memory, swizzled as the products read them, a
-// row's eighth of every chunk per thread. Rows past the tile's are left as they
-// are: every row is apart in scores, weights and sums, and nothing is written
-// for those.
+// row's eighth of every chunk per thread. Rows past the tile's are zeros: nothing
+// is written for them, but an infinity that lay there would have every block's
+// tokens looked over.
 template <int NR, int THREADS>
 __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, uint32_t query, int chunks,
                                            int tid) {
     const int piece = tid & 7;
-    for (int r = tid >> 3; r < tile.rows; r += THREADS / 8) {
-        const int32_t flat = tile.base + r, token = flat / p.heads, head = flat - token * p.heads;
+    for (int r = tid >> 3; r < NR; r += THREADS / 8) {
+        const bool on = r < tile.rows;
+        const int32_t flat = tile.base + (on ? r : 0), token = flat / p.heads, head = flat - token * p.heads;
         const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
         const uint32_t dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
-        for (int k = 0; k < chunks; ++k) copy16(dst + k * NR * 128, src + k * 64, true);
+        for (int k = 0; k < chunks; ++k) copy16(dst + k * NR * 128, src + k * 64, on);
     }
 }
 
@@ -809,36 +817,23 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             const uint32_t scores = lanes + S_COL + (i & 1) * NR + group * (NR / 2);
             char *weights = ropes + rs * CHUNK + t0 * 128 + quad * 4;
             float x[2 * N];                    // x[4 j + 2 h + e]: token h, the thread's row 2 j + e
-            bool odd_token[2] = {false, false};
-            // Scores in log2 units; where masked, -inf. A cache row that some or all of the
-            // tile's rows may not see must not reach them through 0 x inf: a masked score
-            // that is not finite marks the token, and what is not finite among the token's
-            // values is zeroed below (rows that do see it have a NaN or infinite score of
-            // their own; a query's own NaN marks tokens too, whose values then are fine).
+            float most = 0.0f;                 // the block's largest score (by size): infinity and NaN are rare
+            // Scores in log2 units; where masked, -inf.
             auto take = [&]() {
                 tc_load_groups<NR / 16>(scores, x);
                 tc_fence_before();
 #pragma unroll
+                for (int e = 0; e < 2 * N; e += 2) most = largest(most, x[e], x[e + 1]);
+#pragma unroll
                 for (int e = 0; e < 2 * N; ++e) x[e] *= scale;
-                if (!whole && !p.paged) {      // a place that holds no cache row is masked for every row
+                if (!whole) {
 #pragma unroll
-                    for (int e = 0; e < 2 * N; ++e) x[e] = there[(e >> 1) & 1] ? x[e] : -INFINITY;
-                } else if (!whole) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        bool odd = false;
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int n = 0; n < N; ++n) {
                             float &v = x[4 * (n >> 1) + 2 * h + (n & 1)];
-                            const int r = row_of(n);
-                            const bool seen = there[h] && token + 8 * h < lim[n];
-                            odd |= !seen && r < at.tile.rows && !(fabsf(v) < INFINITY);
-                            v = seen ? v : -INFINITY;
+                            v = there[h] && token + 8 * h < lim[n] ? v : -INFINITY;
                         }
-                        odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, 1);
-                        odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, 2);
-                        odd_token[h] = odd;
-                    }
                 }
             };
             // Weights from scores (or from the unscaled scores of a whole block), rounded once
@@ -851,6 +846,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                     for (int h = 0; h < 2; ++h) {
                         float &a = x[4 * j + 2 * h], &d = x[4 * j + 2 * h + 1];
                         if constexpr (decltype(unscaled)::value) {
+                            most = largest(most, a, d);
                             a = exp2_fast(fmaf(a, scale, -ref[2 * j]));
                             d = exp2_fast(fmaf(d, scale, -ref[2 * j + 1]));
                         } else {
@@ -923,21 +919,46 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
                     tc_fence_before();
                 }
             }
+            // What is not finite among a token's values must not reach a row that gives the token
+            // no weight through 0 x inf: neither one that may not see it nor one whose score of it
+            // is -inf. Such a row's score of it is not finite, which marks the token, and what is
+            // not finite among its values is zeroed (a row that does weigh it has a score of NaN or
+            // +inf, so NaN weights; a query's own NaN marks tokens too, whose values then are fine).
+            // Scores are read again for it, here and in small code: marks made in take(), which is
+            // inlined three times, cost 10 % of 512 x 128 heads x 2048 (412 us against 375).
+            if (__any_sync(0xFFFFFFFFu, !(most < INFINITY))) {
+                bool odd[2] = {false, false};
+#pragma unroll 1
+                for (int j = 0; j < N / 2; ++j) {
+                    float v[4];
+                    tc_load_groups<1>(scores + 8 * j, v);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (odd_token[h]) {
-                    uint32_t s = ps;
+                    for (int e = 0; e < 4; ++e) {
+                        const int h = e >> 1, r = row_of(2 * j + (e & 1));
+                        const bool seen = there[h] && token + 8 * h < c.lim[r];
+                        odd[h] |= r < at.tile.rows && (seen ? v[e] * scale == -INFINITY : !(fabsf(v[e]) < INFINITY));
+                    }
+                }
+                tc_fence_before();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    odd[h] |= __shfl_xor_sync(0xFFFFFFFFu, odd[h], 1);
+                    odd[h] |= __shfl_xor_sync(0xFFFFFFFFu, odd[h], 2);
+                    if (!odd[h]) continue;
+                    uint32_t slot = ps;
+#pragma unroll 1
                     for (int u = 0; u < plan.pairs; ++u) {
                         for (int k = quad; k < 16; k += 4) {
-                            uint4 *at16 = reinterpret_cast<uint4 *>(pairs + s * 2 * CHUNK + (k >> 3) * CHUNK +
+                            uint4 *at16 = reinterpret_cast<uint4 *>(pairs + slot * 2 * CHUNK + (k >> 3) * CHUNK +
                                                                     (t0 + 8 * h) * 128 + (k & 7) * 16);
                             const uint4 v = *at16;
                             if (not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w))
                                 *at16 = make_uint4(0, 0, 0, 0);
                         }
-                        if (++s == static_cast<uint32_t>(plan.pair_slots)) s = 0;
+                        if (++slot == static_cast<uint32_t>(plan.pair_slots)) slot = 0;
                     }
                 }
+            }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {

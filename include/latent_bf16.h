@@ -23,8 +23,9 @@
  *     p_j   = exp(s_j - lse),   lse = log sum_j exp(s_j)
  *     out   = sum_j p_j c_j                          (latent values)
  * A query row that sees nothing, or whose scores are all -inf, gets out = 0 and
- * lse = -inf; a score of -inf among others weighs nothing. A cache row that
- * no query row of the call may see is never part of a result, whatever it holds.
+ * lse = -inf. A cache row that query row (t, h) may not see, or whose score is
+ * -inf there, is no part of out[t, h] and lse[t, h], whatever it holds and whatever
+ * other query rows see of it.
  * If a row that query row (t, h) sees makes its s_j NaN or +inf, out[t, h] is NaN.
  */
 #ifndef LATENT_BF16_H

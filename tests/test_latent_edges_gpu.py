@@ -61,3 +61,65 @@ def test_scores_of_minus_infinity_weigh_nothing(form, tokens, length, first, blo
     ref, rl, tol, tl = R.attend(query, cache, [order[~gone]] * tokens, SCALE, latent)
     R.assert_close(out, ref, tol, "out")
     R.assert_close(lse, rl, tl, "lse")
+
+
+@pytest.mark.parametrize("heads", [4, 16])
+@pytest.mark.parametrize("blocks", [1, 3])
+@pytest.mark.parametrize("scale", [SCALE, -SCALE])
+def test_a_score_of_minus_infinity_masks_whatever_its_row_holds(heads, blocks, scale):
+    # A row whose latent part holds an infinity, at -inf for half of the heads (which give what they give without it)
+    # and at +inf for the others: in a block that all rows see whole, in one that they do not, and at a place that only
+    # the chunk's later tokens see.
+    q, latent = 3, 256
+    n = 64 * blocks
+    query, cache, valid, table, kw = paged_case([n, n], q, heads, latent, 64, 51)
+    row = table.long()[:, :, None] * 64 + torch.arange(64, device="cuda")
+    row = row.flatten(1)
+    low = heads // 2
+    query[:, :low, 3], query[:, low:, 3] = 1.0, -1.0
+    early = 10 if blocks == 1 else 74
+    for r, at in ((0, early), (1, n - 2)):
+        cache[row[r, at], 3] = float("-inf") * scale
+        cache[row[r, at], 200] = 5.0
+    out, lse = tk.latent_attend_paged(query, cache, valid, table, scale, latent=latent, lse=True, **kw)
+    visible = R.visible_paged(valid, table, n, 64, 64, q, cache.shape[0])
+    clean, sees = cache.clone(), []
+    for t, rows in enumerate(visible):
+        bad = row[t // q, early if t // q == 0 else n - 2]
+        sees.append(bool((rows == bad).any()))
+        visible[t] = rows[rows != bad]
+        clean[bad, 3] = 0.0
+    assert sees == [True] * q + [False, True, True]
+    ref, rl, tol, tl = R.attend(query, clean, visible, scale, latent)
+    for t in range(2 * q):
+        R.assert_close(out[t, :low], ref[t, :low], tol[t, :low], f"out of token {t}")
+        R.assert_close(lse[t, :low], rl[t, :low], tl[t, :low], f"lse of token {t}")
+        if sees[t]:
+            assert torch.isnan(out[t, low:]).all()
+        else:
+            R.assert_close(out[t, low:], ref[t, low:], tol[t, low:], f"out of token {t}")
+
+
+def test_a_listed_score_of_minus_infinity_masks_whatever_its_row_holds():
+    query, cache, sel = selected_case(3, 16, 512, 200, 1000, 52)
+    query[:, :, 0] = 1.0
+    sel[sel == 999] = -1
+    rest = sel.clone()
+    for t, i in ((0, 199), (1, 20), (2, 100)):
+        sel[t, i], rest[t, i] = 999, -1
+    ref, rl, tol, tl = R.attend(query, cache, R.visible_selected(rest, 1000), SCALE, 512)
+    cache[999, 0] = float("-inf")
+    out, lse = tk.latent_attend_selected(query, cache, sel, SCALE, lse=True)
+    R.assert_close(out, ref, tol, "out")
+    R.assert_close(lse, rl, tl, "lse")
+    # Lists without empty places: whole blocks.
+    sel = torch.randint(0, 999, (3, 192), generator=gen(53), device="cuda").int()
+    rest = sel.clone()
+    for t, i in ((0, 5), (1, 70), (2, 191)):
+        sel[t, i], rest[t, i] = 999, -1
+    cache[999, 0] = 0.0
+    ref, rl, tol, tl = R.attend(query, cache, R.visible_selected(rest, 1000), SCALE, 512)
+    cache[999, 0] = float("-inf")
+    out, lse = tk.latent_attend_selected(query, cache, sel, SCALE, lse=True)
+    R.assert_close(out, ref, tol, "out")
+    R.assert_close(lse, rl, tl, "lse")
