@@ -163,6 +163,8 @@ def latent_attend_selected(query, cache, selected, scale: float, *, latent: int 
         _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2), selected=(selected, _I32, 2))
     if lists != query.shape[0]:
         raise ValueError("selected must have one row per query token")
+    if k > MAX_ROWS:
+        raise ValueError(f"selected must have at most {MAX_ROWS} entries per row")
     return _attend(0, dev, query, cache, scale, latent, out, lse, workspace, stream,
                    (selected.data_ptr() if k else None, stride if lists > 1 else k, None, None),
                    (k, 0, 0, 1, 1, 1))
@@ -201,12 +203,12 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     width = pages * page_size if width is None else int(width)
     if not 0 <= width <= pages * page_size:
         raise ValueError("width exceeds the block table")
-    if max(width, stride, rows_per_request, page_size) > MAX_ROWS:
+    block_rows = page_size if block_rows is None else int(block_rows)
+    if max(width, stride, rows_per_request, page_size, abs(block_rows)) > MAX_ROWS:
         raise ValueError("a length, stride or count passes 31 bits")
     return _attend(1, dev, query, cache, scale, latent, out, lse, workspace, stream,
                    (None, 0, valid_len.data_ptr(), block_table.data_ptr()),
-                   (0, width, stride if requests > 1 else pages, page_size,
-                    page_size if block_rows is None else int(block_rows), rows_per_request))
+                   (0, width, stride if requests > 1 else pages, page_size, block_rows, rows_per_request))
 
 
 def latent_workspace(device=None):

@@ -123,3 +123,20 @@ def test_a_listed_score_of_minus_infinity_masks_whatever_its_row_holds():
     out, lse = tk.latent_attend_selected(query, cache, sel, SCALE, lse=True)
     R.assert_close(out, ref, tol, "out")
     R.assert_close(lse, rl, tl, "lse")
+
+
+# ------------------------------------------------------------------ arguments
+
+def test_counts_past_31_bits_are_refused():
+    query, cache, valid, table, kw = paged_case([100], 1, 16, 128, 64, 60)
+    for rows in (2 ** 31, 2 ** 32 + 64, 64 - 2 ** 32):
+        with pytest.raises(ValueError):
+            tk.latent_attend_paged(query, cache, valid, table, SCALE, latent=128, block_rows=rows)
+    lists = torch.empty((1, 2 ** 32 + 100), dtype=torch.int32, device="cuda")      # 17 GB, never read
+    lists[:, :100] = -1
+    try:
+        with pytest.raises(ValueError):
+            tk.latent_attend_selected(query, cache, lists, SCALE, latent=128)
+    finally:
+        del lists
+        torch.cuda.empty_cache()
