@@ -41,6 +41,11 @@ def _refuse(**tensors):
     raise ValueError("tensors do not fit the call")
 
 
+def _check_stream(stream, dev: int):
+    if stream.device_index != dev:
+        raise ValueError(f"stream must be one of cuda:{dev}, where the tensors are")
+
+
 def _row_stride(rows: int, width: int, stride: int) -> int:
     """Row stride of a 2-D tensor; a single row's is immaterial, its width rounded up is given."""
     return stride if rows > 1 else -(-width // 8) * 8
@@ -128,6 +133,8 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
                   _row_stride(tokens, ROPE, key_stride), positions.data_ptr(), cos_sin.data_ptr(),
                   slots.data_ptr(), weight_ptr, *r, *q, rows, tokens, width, heads, positions_known,
                   1 if interleaved else 0, eps)
+    if stream is not None:
+        _check_stream(stream, dev)
     function = (_package._lib or load()).latent_bf16_append
     handle = _raw_stream(dev) if stream is None else stream.cuda_stream
     if _raw_device() == dev:
@@ -238,6 +245,8 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
         raise ValueError(f"latent must be one of {LATENTS}, query and cache rows latent + {ROPE} values")
     if not 1 <= heads <= MAX_HEADS:
         raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
+    if stream is not None:
+        _check_stream(stream, dev)
     if _raw_device() != dev:
         with torch.cuda.device(dev):
             return _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes)

@@ -140,3 +140,24 @@ def test_counts_past_31_bits_are_refused():
     finally:
         del lists
         torch.cuda.empty_cache()
+
+
+class OtherStream:
+    """Stands for a stream of another device (a test machine has one)."""
+    device = torch.device("cuda", 1)
+    device_index = 1
+    cuda_stream = 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    query, cache, sel = selected_case(2, 16, 512, 100, 300, 61)
+    valid = torch.ones(2, dtype=torch.int32, device="cuda")
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    x, key = normal(gen(1), 2, 512), normal(gen(2), 2, ROPE)
+    slots = torch.arange(2, device="cuda", dtype=torch.int32)
+    for call in (lambda s: tk.latent_attend_selected(query, cache, sel, SCALE, stream=s),
+                 lambda s: tk.latent_attend_paged(query, cache, valid, table, SCALE, stream=s),
+                 lambda s: tk.latent_append(cache, x, key, valid, angles(4), slots, stream=s)):
+        with pytest.raises(ValueError):
+            call(OtherStream())
+    assert torch.cuda.current_device() == 0
