@@ -5,6 +5,8 @@ A cache row holds one token for all heads: ``latent`` values that are key and
 value, then 64 rotated values that are key only. ``latent_append`` writes new
 tokens' rows; ``latent_attend_selected`` attends over the rows the top-k
 selected; ``latent_attend_paged`` over the first tokens of a request's pages.
+They have no gradient: where gradients are recorded, tensors that require one
+are refused.
 """
 from __future__ import annotations
 
@@ -39,6 +41,12 @@ def _refuse(**tensors):
         if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
             raise ValueError(f"{name} must have {dim} dimension(s) with unit inner stride")
     raise ValueError("tensors do not fit the call")
+
+
+def _check_no_grad(*tensors):
+    if any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("the latent-cache operators have no gradient: call them under torch.no_grad(), or with "
+                         "tensors that do not require one")
 
 
 def _check_stream(stream, dev: int):
@@ -133,6 +141,8 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
                   _row_stride(tokens, ROPE, key_stride), positions.data_ptr(), cos_sin.data_ptr(),
                   slots.data_ptr(), weight_ptr, *r, *q, rows, tokens, width, heads, positions_known,
                   1 if interleaved else 0, eps)
+    if torch.is_grad_enabled():
+        _check_no_grad(cache, latent, key_rope, cos_sin, weight, query_rope, query)
     if stream is not None:
         _check_stream(stream, dev)
     function = (_package._lib or load()).latent_bf16_append
@@ -245,6 +255,8 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
         raise ValueError(f"latent must be one of {LATENTS}, query and cache rows latent + {ROPE} values")
     if not 1 <= heads <= MAX_HEADS:
         raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
+    if torch.is_grad_enabled() and (query.requires_grad or cache.requires_grad):
+        _check_no_grad(query, cache)
     if stream is not None:
         _check_stream(stream, dev)
     if _raw_device() != dev:

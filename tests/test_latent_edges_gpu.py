@@ -161,3 +161,28 @@ def test_a_stream_of_another_device_is_refused():
         with pytest.raises(ValueError):
             call(OtherStream())
     assert torch.cuda.current_device() == 0
+
+
+def test_what_wants_a_gradient_is_refused():
+    query, cache, sel = selected_case(2, 16, 512, 100, 300, 62)
+    valid = torch.ones(2, dtype=torch.int32, device="cuda")
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    x, key = normal(gen(1), 2, 512), normal(gen(2), 2, ROPE)
+    w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    args = dict(cache=cache, latent=x, key_rope=key, positions=valid, cos_sin=angles(4),
+                slots=torch.tensor([3, 4], dtype=torch.int32, device="cuda"), weight=w,
+                query_rope=normal(gen(3), 2, 16, ROPE), query=query)
+
+    want = {n: t.clone().requires_grad_() for n, t in args.items() if t.is_floating_point()}
+    assert len(want) == 7
+    calls = [lambda: tk.latent_attend_selected(want["query"], cache, sel, SCALE),
+             lambda: tk.latent_attend_selected(query, want["cache"], sel, SCALE),
+             lambda: tk.latent_attend_paged(want["query"], cache, valid, table, SCALE),
+             lambda: tk.latent_attend_paged(query, want["cache"], valid, table, SCALE)]
+    calls += [lambda n=n: tk.latent_append(**{**args, n: want[n]}) for n in want]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        for mode in (torch.no_grad(), torch.inference_mode()):
+            with mode:
+                call()
