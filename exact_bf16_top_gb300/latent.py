@@ -164,7 +164,7 @@ def latent_attend_selected(query, cache, selected, scale: float, *, latent: int 
     query: CUDA bfloat16 [tokens, heads, latent + 64]; cache: bfloat16 [rows,
     latent + 64]; selected: int32 [tokens, k], physical rows as the top-k writes
     them (entries outside the cache, e.g. -1, are empty places). out: bfloat16
-    [tokens, heads, latent], zero where a token sees nothing; lse: True for the
+    [tokens, heads, latent], zero where a token sees nothing; lse: true for the
     float32 [tokens, heads] logarithm of the softmax sum (-inf where a token
     sees nothing), else None is returned for it. workspace: None, or scratch
     from latent_workspace() that no other call uses at the same time.
@@ -271,19 +271,14 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
     elif not (out.dtype is _BF16 and out.device == device and out.shape == (tokens, heads, latent)
               and out.is_contiguous()):
         raise ValueError("out must be a contiguous bfloat16 [tokens, heads, latent] on the query's device")
-    lse_ptr = None
-    if lse is True:
-        lse = torch.empty((tokens, heads), dtype=_F32, device=device)
-        lse_ptr = lse.data_ptr()
-    elif not isinstance(lse, torch.Tensor):
-        lse = None
-    elif lse.dtype is _F32 and lse.device == device and lse.shape == (tokens, heads) and lse.is_contiguous():
-        lse_ptr = lse.data_ptr()
-    else:
+    if not isinstance(lse, torch.Tensor):
+        lse = torch.empty((tokens, heads), dtype=_F32, device=device) if lse else None
+    elif not (lse.dtype is _F32 and lse.device == device and lse.shape == (tokens, heads) and lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [tokens, heads] on the query's device")
     if workspace is not None and not (workspace.dtype is _U8 and workspace.device == device
                                       and workspace.is_contiguous()):
         raise ValueError("workspace must be a uint8 tensor from latent_workspace() on the query's device")
+    lse_ptr = None if lse is None else lse.data_ptr()
     if tokens:
         args = Attend(query.data_ptr(), *_head_strides(query), cache.data_ptr(),
                       _row_stride(rows, dim, cache_stride), *pointers, out.data_ptr(), lse_ptr, None, 0, rows,

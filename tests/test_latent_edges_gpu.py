@@ -186,3 +186,12 @@ def test_what_wants_a_gradient_is_refused():
         for mode in (torch.no_grad(), torch.inference_mode()):
             with mode:
                 call()
+
+
+def test_lse_by_any_truth_value():
+    query, cache, sel = selected_case(2, 16, 128, 100, 300, 63)
+    out, want = check_selected(query, cache, sel, 128)
+    for yes in (True, 1, torch.ones(1).bool().numpy()[0]):
+        assert torch.equal(tk.latent_attend_selected(query, cache, sel, SCALE, latent=128, lse=yes)[1], want)
+    for no in (False, None, 0):
+        assert tk.latent_attend_selected(query, cache, sel, SCALE, latent=128, lse=no)[1] is None
