@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(NT) append_kernel(const latent_bf16_append_t a
             for (int i = 0; i < HEADS / 4; ++i)
                 v[i] = h0 + 4 * i >= a.heads
                            ? make_uint4(0, 0, 0, 0)
-                           : __ldg(reinterpret_cast<const uint4 *>(from + (h0 + 4 * i) * a.query_rope_head_stride) +
-                                   part);
+                           // (an ordinary load: it may be where the unit's result goes)
+                           : reinterpret_cast<const uint4 *>(from + (h0 + 4 * i) * a.query_rope_head_stride)[part];
             pos = pos < 0 ? 0 : pos >= a.max_positions ? a.max_positions - 1 : pos;
             const Turn turn(a.cos_sin + static_cast<int64_t>(pos) * ROPE, part, interleaved);
             uint16_t *to = a.query + t * a.query_token_stride + a.latent;

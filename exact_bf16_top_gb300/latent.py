@@ -81,7 +81,8 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
     interleaved: rotated pairs are (2 i, 2 i + 1), else (i, i + 32).
     query_rope (bfloat16 [tokens, heads, 64]) and query (bfloat16 [tokens,
     heads, latent + 64]): the same tokens' rotated query parts are written to
-    query[..., latent:]; the rest of query is left alone.
+    query[..., latent:], which query_rope may be itself; the rest of query is left
+    alone. Other overlaps of what is written with what is read are not allowed.
     Rows may be strided: strides multiples of 8, 16-byte aligned.
     """
     try:

@@ -69,7 +69,8 @@ extern "C" {
  * query          device BF16 [tokens, heads, latent + 64] with the strides given;
  *                only its last 64 values are written. NULL with query_rope NULL.
  * All BF16 pointers are 16-byte aligned and all strides multiples of 8 elements.
- * Outputs must not overlap inputs.
+ * Outputs must not overlap inputs, except that query_rope may be query's own last
+ * 64 values (query + latent, with query's strides): they are then rotated in place.
  *
  * Errors: TOPK_ERR_ARG (null pointer, negative count, more than 2^27 tokens, heads
  * outside [1, LATENT_MAX_HEADS] with query_rope, max_positions < 1, query_rope without

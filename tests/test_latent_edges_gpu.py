@@ -195,3 +195,19 @@ def test_lse_by_any_truth_value():
         assert torch.equal(tk.latent_attend_selected(query, cache, sel, SCALE, latent=128, lse=yes)[1], want)
     for no in (False, None, 0):
         assert tk.latent_attend_selected(query, cache, sel, SCALE, latent=128, lse=no)[1] is None
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("tokens,heads", [(1, 3), (5, 16), (700, 33)])
+def test_append_rotates_queries_in_place(interleaved, tokens, heads):
+    g, latent = gen(64), 128
+    query = normal(g, tokens, heads, latent + ROPE)
+    x, key, table = normal(g, tokens, latent), normal(g, tokens, ROPE), angles(900)
+    slots = torch.arange(tokens, device="cuda", dtype=torch.int32)
+    caches = [torch.zeros(tokens, latent + ROPE, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    apart, together = query.clone(), query.clone()
+    tk.latent_append(caches[0], x, key, slots, table, slots, interleaved=interleaved,
+                     query_rope=query[..., latent:].clone(), query=apart)
+    tk.latent_append(caches[1], x, key, slots, table, slots, interleaved=interleaved,
+                     query_rope=together[..., latent:], query=together)
+    assert torch.equal(apart, together) and torch.equal(*caches)
