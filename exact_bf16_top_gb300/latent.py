@@ -23,8 +23,10 @@ MAX_HEADS = 256
 MAX_ROWS = 2 ** 31 - 1
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
-# (Plain integers: a step's smallest calls take a few microseconds on the host.)
-_raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (Plain integers: a step's smallest calls take a few microseconds on the host. A torch without CUDA
+# has neither, nor a tensor that gets as far as their use.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _refuse(**tensors):
