@@ -62,6 +62,7 @@ struct Ctrl {
     u64 q_first, q_full, q_empty;              // the first query tile, a later one is in / it is used up
     u64 drain[2];
     long long sums[NT / 32];
+    int32_t longest[NT / 32];
     int32_t first_tile, first_unit;
     int32_t ranks;                             // CTAs of the cluster that have blocks
     long long begin, share, total;
@@ -313,6 +314,11 @@ __device__ __forceinline__ int32_t tile_len(const AttendParams &p, const Tile &t
     return n;
 }
 
+// What split tiles cost besides their blocks, in blocks / 48 (SPLIT_UNIT): a part
+// and a tile to join.
+constexpr int SPLIT_UNIT = 48;
+__host__ __device__ __forceinline__ int64_t split_cost(int64_t parts, int64_t tiles) { return parts + 3 * tiles; }
+
 __device__ __forceinline__ int32_t blocks_of(int32_t len) { return max(1, (len + KEYS - 1) / KEYS); }
 
 // As tile_len, by a whole warp; low: the tile's smallest length.
@@ -333,8 +339,9 @@ __device__ __forceinline__ int32_t tile_len_warp(const AttendParams &p, const Ti
 // CTA's share is a run of pieces, each part or all of one tile's blocks. Where a
 // CTA has several tiles, a tile counts TILE_COST blocks more than it has: its
 // query, first reference and outputs (854 tiles of 1 to 4 blocks: 118 us counted
-// as none, 87 as five). (Or, where the host chose so, a cluster's CTAs share one
-// tile.)
+// as none, 87 as five). Or each CTA has one tile: a cluster's CTAs share one where
+// the host chose so, and pages whose tiles are about as many as the CTAs and about
+// as long as each other are not split, which only the lengths here can tell.
 struct Cursor {
     int32_t next_tile, next_unit;
     long long left;
@@ -396,14 +403,23 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
     const int32_t per = (p.tiles + NT - 1) / NT;
     const int32_t t0 = min(p.tiles, tid * per), t1 = min(p.tiles, t0 + per);
     long long sum = 0;
-    for (int32_t t = t0; t < t1; ++t) sum += blocks_of(tile_len(p, tile_at(p, t))) + p.tile_cost;
+    int32_t longest = 0;
+    for (int32_t t = t0; t < t1; ++t) {
+        const int32_t n = blocks_of(tile_len(p, tile_at(p, t)));
+        sum += n + p.tile_cost;
+        longest = max(longest, n);
+    }
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     long long pre = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xFFFFFFFFu, pre, o);
         if (lane >= o) pre += v;
     }
-    if (lane == 31) c.sums[warp] = pre;
+    if (lane == 31) {
+        c.sums[warp] = pre;
+        c.longest[warp] = longest;
+    }
     __syncthreads();
     long long before = pre - sum, total = 0;
 #pragma unroll
@@ -411,9 +427,26 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Ctrl &c) {
         const long long v = c.sums[w];
         before += w < warp ? v : 0;
         total += v;
+        longest = max(longest, c.longest[w]);
     }
     const long long share = max(static_cast<long long>(p.min_share), (total + gridDim.x - 1) / gridDim.x);
     const long long begin = min(total, share * static_cast<long long>(blockIdx.x));
+    const int32_t ctas = static_cast<int32_t>(gridDim.x);
+    if (p.tiles <= ctas && longest <= share + split_cost(ctas, p.tiles) / SPLIT_UNIT) {
+        if (warp == 0) {                       // every tile to a CTA of its own
+            const int32_t tile = blockIdx.x;
+            int32_t n = 0, low;
+            if (tile < p.tiles) n = blocks_of(tile_len_warp(p, tile_at(p, tile), lane, low));
+            if (lane == 0) {
+                c.first_tile = tile;
+                c.first_unit = 0;
+                c.begin = 0;
+                c.share = c.total = n;
+            }
+        }
+        __syncthreads();
+        return;
+    }
     if (tid == 0) {
         c.total = total;
         c.share = share;
@@ -1059,7 +1092,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             Joint j;
             j.tile = at.next_tile - 1;
             j.cta = static_cast<int32_t>(blockIdx.x);
-            j.parts = static_cast<int32_t>((done - at.u0 + at.units - 1) / c.share) - j.cta + 1;
+            j.parts = direct ? 1 : static_cast<int32_t>((done - at.u0 + at.units - 1) / c.share) - j.cta + 1;
             j.unused = 0;
             joints[by_tile ? j.tile : j.cta] = j;
         }
@@ -1417,7 +1450,9 @@ Deal deal(const AttendParams &p, const Device &d) {
     r.blocks = (static_cast<int64_t>(p.paged ? p.width : p.k) + KEYS - 1) / KEYS;
     if (r.blocks < 1) r.blocks = 1;
     const int64_t even = (r.tiles * r.blocks + d.sms - 1) / d.sms;
-    const int64_t share = even > MIN_SHARE ? even : MIN_SHARE;
+    // (How long requests really are is not known here: of pages, shares may come to as little
+    // as MIN_SHARE, and a tile is kept whole only where that is as fast even then.)
+    const int64_t share = p.paged || even < MIN_SHARE ? MIN_SHARE : even;
     // Short work goes to the largest cluster that leaves each CTA a few blocks: one
     // launch instead of two, and no scratch (1 token x 512 rows: 9.9 us against 10.8
     // in a graph, 14.6 against 20 called one by one; 4096 tokens of pages: 14.7

@@ -211,3 +211,30 @@ def test_append_rotates_queries_in_place(interleaved, tokens, heads):
     tk.latent_append(caches[1], x, key, slots, table, slots, interleaved=interleaved,
                      query_rope=together[..., latent:], query=together)
     assert torch.equal(apart, together) and torch.equal(*caches)
+
+
+# ------------------------------------------------------------------ the dealing of work
+
+@pytest.mark.parametrize("short_of_sms", [0, 1, 8])
+def test_ragged_pages_are_dealt_in_shares(short_of_sms):
+    # As many tiles as SMs, one of them long: lengths are on the device, so the table's width must not keep a tile
+    # to one CTA. Shares need scratch, whole tiles do not.
+    n = torch.cuda.get_device_properties(0).multi_processor_count - short_of_sms
+    lib = tk.load()
+    for width in (2048, 16384, 131072):
+        args = Attend(query=4096, query_token_stride=16 * 192, query_head_stride=192, cache=4096, cache_stride=192,
+                      valid_len=4096, block_table=4096, out=4096, cache_rows=64, tokens=n, heads=16, latent=128,
+                      width=width, table_stride=width // 64, page_size=64, block_rows=64, rows_per_request=1,
+                      scale=0.1)
+        assert lib.latent_bf16_attend_workspace(args, 1) > 0, width
+    lens = [20000] + [70 + i for i in range(n - 1)]
+    check_paged(*paged_case(lens, 1, 16, 128, 64, 70), 128)
+
+
+@pytest.mark.parametrize("lens", [[1500] * 140, [1500 - 9 * i for i in range(60)] + [1500] * 80, [1500] * 100 + [1] * 40,
+                                  [2000 + i for i in range(152)]])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_pages_of_about_as_many_tiles_as_sms(lens, heads):
+    query, cache, valid, table, kw = paged_case(lens, 1, heads, 128, 64, 76)
+    valid[7] = 0
+    check_paged(query, cache, valid, table, kw, 128)
