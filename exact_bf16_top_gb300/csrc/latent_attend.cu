@@ -315,7 +315,7 @@ __device__ __forceinline__ int32_t tile_len(const AttendParams &p, const Tile &t
 }
 
 // What split tiles cost besides their blocks, in blocks / 48 (SPLIT_UNIT): a part
-// and a tile to join.
+// and a tile to join. (Fitted with deal()'s costs.)
 constexpr int SPLIT_UNIT = 48;
 __host__ __device__ __forceinline__ int64_t split_cost(int64_t parts, int64_t tiles) { return parts + 3 * tiles; }
 
@@ -1435,8 +1435,9 @@ struct Deal {
 
 constexpr int MIN_SHARE = 2;                   // blocks of a CTA in equal shares
 constexpr int TILE_COST = 5;                   // what a tile costs besides its blocks, in blocks
-constexpr int JOIN_BLOCKS = 5;                 // blocks that cost what parts and the second kernel do
-constexpr int SHORT = 4;                       // blocks of a CTA in a cluster of several
+constexpr int CLUSTER_COST = 4;                // what a cluster of several costs a tile, in blocks
+constexpr int SHARES_COST = 3;                 // what parts and the second kernel cost at least
+constexpr int LENGTHS_COST = 2;                // what the shares of pages cost besides: every CTA adds up all lengths
 
 Deal deal(const AttendParams &p, const Device &d) {
     Deal r = {};
@@ -1449,24 +1450,31 @@ Deal deal(const AttendParams &p, const Device &d) {
     r.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     r.blocks = (static_cast<int64_t>(p.paged ? p.width : p.k) + KEYS - 1) / KEYS;
     if (r.blocks < 1) r.blocks = 1;
+    // The least of the expected times, in blocks of a CTA / 48: equal shares against every
+    // cluster size that runs at once. Costs fitted to both sides' times in graphs at 230 sizes
+    // of listed rows (1 to 152 tiles of 16, 32 and 64 rows, 4 to 64 blocks): the choice is 0.4 %
+    // slower than the best on average, 13 % at most. Some of them, shares against the cluster:
+    // 1 tile of 16 rows x 32 blocks 12.1 / 11.8 us (16 CTAs), x 64 12.8 / 14.3; 64 rows x 8 14.0
+    // / 13.6 (8), x 16 14.3 / 14.8 (8); 36 tiles of 16 rows x 64 39.5 / 36.1 (4); unsplit, 72 x
+    // 16 28.8 / 26.8, 96 x 32 52.3 / 48.6, 64 x 32 40.2 / 46.2. A cluster of 16 joins tiles of
+    // 64 rows slower than one of 8 (1 x 16 blocks: 16.5, 14.8).
+    // How long requests really are is not known here: of pages, shares may come to as little as
+    // MIN_SHARE, and a tile goes to a cluster or to one CTA only where that is as fast even then
+    // (1 request x 64 blocks: 14.5 us in shares, 15.0 as a cluster; 2: 16.0, 14.9). Beyond,
+    // make_schedule looks at the lengths.
+    const int64_t parts = (r.tiles * r.blocks + MIN_SHARE - 1) / MIN_SHARE;
     const int64_t even = (r.tiles * r.blocks + d.sms - 1) / d.sms;
-    // (How long requests really are is not known here: of pages, shares may come to as little
-    // as MIN_SHARE, and a tile is kept whole only where that is as fast even then.)
     const int64_t share = p.paged || even < MIN_SHARE ? MIN_SHARE : even;
-    // Short work goes to the largest cluster that leaves each CTA a few blocks: one
-    // launch instead of two, and no scratch (1 token x 512 rows: 9.9 us against 10.8
-    // in a graph, 14.6 against 20 called one by one; 4096 tokens of pages: 14.7
-    // against 13.3, and 16 against 21). Longer work goes to equal shares (37 tokens x
-    // 128 heads x 2048 rows: 46 us against 50 as clusters of two), except tiles that
-    // a single CTA each finishes about as soon as equal shares would (128 tokens x 16
-    // heads x 2048 rows: 57 us against 65).
-    for (int i = 4; i >= 0 && !r.cluster; --i) {
+    int64_t least = (share + SHARES_COST + (p.paged ? LENGTHS_COST : 0)) * SPLIT_UNIT +
+                    split_cost(parts < d.sms ? parts : d.sms, r.tiles);
+    for (int i = r.nr > 32 ? 3 : 4; i >= 0; --i) {
         const int64_t size = 1 << i, run = (r.blocks + size - 1) / size;
-        if (size <= r.blocks && r.tiles <= d.clusters[i] &&
-            (size == 1 ? run <= share + JOIN_BLOCKS : run <= SHORT && run <= share + 2))
-            r.cluster = static_cast<int32_t>(size);
+        const int64_t cost = (run + (size > 1 ? CLUSTER_COST : 0)) * SPLIT_UNIT;
+        if (size > r.blocks || r.tiles > d.clusters[i] || cost > least) continue;
+        r.cluster = static_cast<int32_t>(size);
+        least = cost;
     }
-    const int64_t want = r.cluster ? r.tiles * r.cluster : (r.tiles * r.blocks + MIN_SHARE - 1) / MIN_SHARE;
+    const int64_t want = r.cluster ? r.tiles * r.cluster : parts;
     r.grid = static_cast<unsigned>(r.cluster || want < d.sms ? want : d.sms);
     return r;
 }
