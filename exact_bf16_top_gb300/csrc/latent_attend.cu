@@ -1453,19 +1453,21 @@ Deal deal(const AttendParams &p, const Device &d) {
     // The least of the expected times, in blocks of a CTA / 48: equal shares against every
     // cluster size that runs at once. Costs fitted to both sides' times in graphs at 230 sizes
     // of listed rows (1 to 152 tiles of 16, 32 and 64 rows, 4 to 64 blocks): the choice is 0.4 %
-    // slower than the best on average, 13 % at most. Some of them, shares against the cluster:
+    // slower than the best on average, 11 % at most. Shares count half a block more than
+    // that: called one by one they cost the host a second launch and scratch (1 request of 16
+    // heads x 64 blocks of pages: 24.8 us a call against 19.5). Some of them, shares against the cluster:
     // 1 tile of 16 rows x 32 blocks 12.1 / 11.8 us (16 CTAs), x 64 12.8 / 14.3; 64 rows x 8 14.0
     // / 13.6 (8), x 16 14.3 / 14.8 (8); 36 tiles of 16 rows x 64 39.5 / 36.1 (4); unsplit, 72 x
     // 16 28.8 / 26.8, 96 x 32 52.3 / 48.6, 64 x 32 40.2 / 46.2. A cluster of 16 joins tiles of
     // 64 rows slower than one of 8 (1 x 16 blocks: 16.5, 14.8).
     // How long requests really are is not known here: of pages, shares may come to as little as
     // MIN_SHARE, and a tile goes to a cluster or to one CTA only where that is as fast even then
-    // (1 request x 64 blocks: 14.5 us in shares, 15.0 as a cluster; 2: 16.0, 14.9). Beyond,
-    // make_schedule looks at the lengths.
+    // (16 heads x 64 blocks: 1 request 14.5 us in shares, 15.0 as a cluster; 2: 16.0, 14.9).
+    // Beyond, make_schedule looks at the lengths.
     const int64_t parts = (r.tiles * r.blocks + MIN_SHARE - 1) / MIN_SHARE;
     const int64_t even = (r.tiles * r.blocks + d.sms - 1) / d.sms;
     const int64_t share = p.paged || even < MIN_SHARE ? MIN_SHARE : even;
-    int64_t least = (share + SHARES_COST + (p.paged ? LENGTHS_COST : 0)) * SPLIT_UNIT +
+    int64_t least = (share + SHARES_COST + (p.paged ? LENGTHS_COST : 0)) * SPLIT_UNIT + SPLIT_UNIT / 2 +
                     split_cost(parts < d.sms ? parts : d.sms, r.tiles);
     for (int i = r.nr > 32 ? 3 : 4; i >= 0; --i) {
         const int64_t size = 1 << i, run = (r.blocks + size - 1) / size;

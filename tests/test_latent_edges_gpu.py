@@ -238,3 +238,83 @@ def test_pages_of_about_as_many_tiles_as_sms(lens, heads):
     query, cache, valid, table, kw = paged_case(lens, 1, heads, 128, 64, 76)
     valid[7] = 0
     check_paged(query, cache, valid, table, kw, 128)
+
+
+def test_a_long_tile_among_many_short_ones():
+    # Rows enough for a warp per row in the joining kernel, and a tile of more parts than a warp has lanes.
+    check_paged(*paged_case([40000] + [500] * 99, 1, 16, 256, 64, 71), 256)
+    check_paged(*paged_case([300] * 60 + [30001] + [77] * 30, 1, 64, 128, 64, 72), 128)
+
+
+def test_many_tiles_of_64_rows_of_the_widest_latent():
+    # More tiles than SMs: several pieces a CTA, tiles split between CTAs, a last tile of few rows.
+    check_selected(*selected_case(230, 70, 512, 333, 3000, 73), 512)
+    lens = [200 + (i * 37) % 190 for i in range(90)]
+    query, cache, valid, table, kw = paged_case(lens, 3, 67, 512, 64, 74)
+    check_paged(query[:268], cache, valid[:268], table, kw, 512)
+
+
+def test_whole_tiles_of_ragged_listed_rows():
+    # About as many tokens as SMs, each its own tile, lists between empty and full.
+    query, cache, sel = selected_case(128, 16, 512, 640, 5000, 75)
+    for t in range(128):
+        sel[t, (t * 53) % 641:] = -1
+    check_selected(query, cache, sel, 512)
+
+
+# ------------------------------------------------------------------ layouts of pages
+
+def test_paged_strided_cache_and_given_outputs():
+    query, cache, valid, table, kw = paged_case([333, 200, 64], 4, 20, 256, 64, 80)
+    want, wl = check_paged(query, cache, valid, table, kw, 256)
+    wide = normal(gen(81), cache.shape[0], 320 + 40)[:, :320]
+    wide.copy_(cache)
+    q = normal(gen(82), 20, 12, 320 + 24)[:, :, 8:328].transpose(0, 1)
+    q.copy_(query)
+    t = torch.full((3, table.shape[1] + 5), 2 ** 30, dtype=torch.int32, device="cuda")[:, 2:2 + table.shape[1]]
+    t.copy_(table)
+    out = torch.empty(12, 20, 256, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(12, 20, device="cuda")
+    got = tk.latent_attend_paged(q, wide, valid, t, SCALE, latent=256, out=out, lse=lse,
+                                 workspace=tk.latent_workspace(), **kw)
+    assert got[0] is out and got[1] is lse
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("rows", [150, 190, 63, 65])
+def test_paged_last_page_ends_with_the_cache(rows):
+    # Pages lead past the cache's last row in their middle: those tokens are left out.
+    query, cache, valid, table, kw = paged_case([256, 100], 2, 16, 256, 64, 83)
+    table[0], table[1] = torch.tensor([2, 0, 1, 3]), torch.tensor([1, 2, 0, 3])
+    check_paged(query, cache[:rows], valid, table, kw, 256)
+
+
+def test_paged_rows_past_32_bit_offsets():
+    pages, dim = 86_000, 576                    # 6.3 GB of cache
+    cache = torch.empty(pages * 64, dim, dtype=torch.bfloat16, device="cuda")
+    g = gen(84)
+    cache[-640:], cache[:640] = normal(g, 640, dim), normal(g, 640, dim)
+    table = torch.tensor([[pages - 1, 3, pages - 7, 0, pages - 10], [1, pages - 2, 9, pages - 3, 5]],
+                         dtype=torch.int32, device="cuda")
+    valid = torch.tensor([317, 318, 200, 201], dtype=torch.int32, device="cuda")
+    check_paged(normal(g, 4, 16, dim), cache, valid, table,
+                dict(page_size=64, block_rows=64, rows_per_request=2), 512)
+
+
+# ------------------------------------------------------------------ the size of the errors
+
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("length", [100, 2048])
+def test_errors_are_of_two_roundings(heads, length):
+    # Of independent values of zero mean the weights' rounding (relative, at most 2^-8, so at most 2^-8 / sqrt 3 in the
+    # mean square) leaves the same share of the output's mean square, and the output's own rounding as much again:
+    # together sqrt(2 / 3) 2^-8 = 0.0032, with a tenth for the sample.
+    query, cache, sel = selected_case(40, heads, 512, length, 9000, 90)
+    out, _ = tk.latent_attend_selected(query, cache, sel, SCALE)
+    ref = R.attend(query, cache, R.visible_selected(sel, 9000), SCALE, 512)[0]
+    assert ((out.double() - ref).pow(2).mean() / ref.pow(2).mean()).sqrt().item() < 1.1 * (2 / 3) ** 0.5 * 2.0 ** -8
+    query, cache, valid, table, kw = paged_case([length, length // 2], 20, heads, 512, 64, 91)
+    out, _ = tk.latent_attend_paged(query, cache, valid, table, SCALE, **kw)
+    ref = R.attend(query, cache, R.visible_paged(valid, table, table.shape[1] * 64, 64, 64, 20, cache.shape[0]), SCALE,
+                   512)[0]
+    assert ((out.double() - ref).pow(2).mean() / ref.pow(2).mean()).sqrt().item() < 1.1 * (2 / 3) ** 0.5 * 2.0 ** -8
