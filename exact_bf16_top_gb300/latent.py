@@ -45,8 +45,8 @@ def _refuse(**tensors):
     raise ValueError("tensors do not fit the call")
 
 
-def _check_no_grad(*tensors):
-    if any(t is not None and t.requires_grad for t in tensors):
+def _check_no_grad():
+    if torch.is_grad_enabled():
         raise ValueError("the latent-cache operators have no gradient: call them under torch.no_grad(), or with "
                          "tensors that do not require one")
 
@@ -144,8 +144,10 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
                   _row_stride(tokens, ROPE, key_stride), positions.data_ptr(), cos_sin.data_ptr(),
                   slots.data_ptr(), weight_ptr, *r, *q, rows, tokens, width, heads, positions_known,
                   1 if interleaved else 0, eps)
-    if torch.is_grad_enabled():
-        _check_no_grad(cache, latent, key_rope, cos_sin, weight, query_rope, query)
+    if (cache.requires_grad or latent.requires_grad or key_rope.requires_grad or cos_sin.requires_grad
+            or (weight is not None and weight.requires_grad)
+            or (query is not None and (query.requires_grad or query_rope.requires_grad))):
+        _check_no_grad()
     if stream is not None:
         _check_stream(stream, dev)
     function = (_package._lib or load()).latent_bf16_append
@@ -258,8 +260,8 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
         raise ValueError(f"latent must be one of {LATENTS}, query and cache rows latent + {ROPE} values")
     if not 1 <= heads <= MAX_HEADS:
         raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
-    if torch.is_grad_enabled() and (query.requires_grad or cache.requires_grad):
-        _check_no_grad(query, cache)
+    if query.requires_grad or cache.requires_grad:
+        _check_no_grad()
     if stream is not None:
         _check_stream(stream, dev)
     if _raw_device() != dev:
