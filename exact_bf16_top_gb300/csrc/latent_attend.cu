@@ -10,13 +10,14 @@
 // it), and 16 rows cost little more than their share. Warps have one job each
 // (softmax, copies, issue of either product) and meet at mbarriers only.
 //
-// What bounds it. Few heads: DRAM (32 requests x 16 heads x up to 16384 tokens: 86
-// us, 5.1 TB/s). 64 rows a tile: shared memory. A block's operands leave it 36 x 4
+// What bounds it. Few heads: DRAM (32 requests x 16 heads x up to 16384 tokens: 85
+// us, 5.2 TB/s). 64 rows a tile: shared memory. A block's operands leave it 36 x 4
 // KB (scores) and 16 x 6 KB (sums) at 128 bytes a cycle and its rows come in once:
-// 2560 cycles a block, what a chunk of 509 tokens x 128 heads over 9000 takes (1.23
-// ms, 1.0 PFLOP/s; tensor pipes 62 % active). More rows a tile would halve that but
-// neither their queries (74 KB for 64) nor their sums have room. Listed rows (no
-// TMA boxes) add the copies' latency: 3300 cycles a block at two blocks in flight.
+// about 2500 cycles a block, what a chunk of 509 tokens x 128 heads over 9000 takes
+// (1.22 ms, 1.0 PFLOP/s; tensor pipes 66 % active). More rows a tile would halve
+// that but neither their queries (74 KB for 64) nor their sums have room. Listed
+// rows (no TMA boxes) add the copies' latency: 3200 cycles a block at two blocks in
+// flight, tile ends included (512 tokens x 128 heads x 2048: 356 us).
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -338,8 +339,8 @@ __device__ __forceinline__ int32_t tile_len_warp(const AttendParams &p, const Ti
 // All blocks of all tiles in order are cut into equal shares, one per CTA: a
 // CTA's share is a run of pieces, each part or all of one tile's blocks. Where a
 // CTA has several tiles, a tile counts TILE_COST blocks more than it has: its
-// query, first reference and outputs (854 tiles of 1 to 4 blocks: 118 us counted
-// as none, 87 as five). Or each CTA has one tile: a cluster's CTAs share one where
+// query, first reference and outputs (854 tiles of 1 to 4 blocks: 97 us counted
+// as none, 72 as five). Or each CTA has one tile: a cluster's CTAs share one where
 // the host chose so, and pages whose tiles are about as many as the CTAs and about
 // as long as each other are not split, which only the lengths here can tell.
 struct Cursor {
@@ -794,8 +795,8 @@ __device__ __forceinline__ int across_index() {
 // and the next of its half: their references and sums stay in its registers.
 // The weights' reference is the maximum of the row's first block; weights may grow
 // to 2^16 before it moves (FP32 sums and BF16 weights lose nothing by that), which
-// is seen from the packed weights and rarely happens. Bound by latency: scores to
-// weights take about 1100 cycles at 64 rows, of which the exponentials are 130.
+// is seen from the packed weights and rarely happens. Bound by latency, not by the
+// exponentials (16 a thread and block at 64 rows).
 template <int NR>
 __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_t query, char *pairs, char *ropes,
                        uint32_t tmem) {
@@ -1029,7 +1030,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, const Plan &plan, uint32_
             if (p.lse && tid < at.tile.rows) p.lse[at.tile.base + tid] = finished_lse(c.ref[tid], c.l[tid]);
             // A lane has one value of 16 rows; two lanes trade theirs for pairs of one row
             // each. (Tiles of all rows store without a test a row: 1144 tokens x 128 heads x
-            // 175 rows 194 us with it, 169 without; four lanes' 8-byte stores: 209.)
+            // 175 rows 193 us with it, 160 without; 512 x 128 x 2048 398 and 357.)
             const bool odd = (lane & 1) != 0;
             uint16_t *out = p.out + (static_cast<int64_t>(at.tile.base) + (lane & 1)) * p.latent + w * 32 + (lane & ~1);
             auto write = [&](auto all) {
@@ -1455,11 +1456,11 @@ Deal deal(const AttendParams &p, const Device &d) {
     // of listed rows (1 to 152 tiles of 16, 32 and 64 rows, 4 to 64 blocks): the choice is 0.4 %
     // slower than the best on average, 11 % at most. Shares count half a block more than
     // that: called one by one they cost the host a second launch and scratch (1 request of 16
-    // heads x 64 blocks of pages: 24.8 us a call against 19.5). Some of them, shares against the cluster:
-    // 1 tile of 16 rows x 32 blocks 12.1 / 11.8 us (16 CTAs), x 64 12.8 / 14.3; 64 rows x 8 14.0
-    // / 13.6 (8), x 16 14.3 / 14.8 (8); 36 tiles of 16 rows x 64 39.5 / 36.1 (4); unsplit, 72 x
-    // 16 28.8 / 26.8, 96 x 32 52.3 / 48.6, 64 x 32 40.2 / 46.2. A cluster of 16 joins tiles of
-    // 64 rows slower than one of 8 (1 x 16 blocks: 16.5, 14.8).
+    // heads x 64 blocks of pages: 22.8 us a call against 16.5). Some of both sides, shares
+    // against the cluster: 1 tile of 16 rows x 32 blocks 12.1 / 11.8 us (16 CTAs), x 64 12.8 /
+    // 14.3; 64 rows x 8 14.0 / 13.6 (8), x 16 14.3 / 14.8 (8); 36 tiles of 16 rows x 64 39.5 /
+    // 36.1 (4); unsplit, 72 x 16 28.8 / 26.8, 96 x 32 52.3 / 48.6, 64 x 32 40.2 / 46.2. A
+    // cluster of 16 joins tiles of 64 rows slower than one of 8 (1 x 16 blocks: 16.5, 14.8).
     // How long requests really are is not known here: of pages, shares may come to as little as
     // MIN_SHARE, and a tile goes to a cluster or to one CTA only where that is as fast even then
     // (16 heads x 64 blocks: 1 request 14.5 us in shares, 15.0 as a cluster; 2: 16.0, 14.9).

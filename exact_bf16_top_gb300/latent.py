@@ -168,7 +168,8 @@ def latent_attend_selected(query, cache, selected, scale: float, *, latent: int 
 
     query: CUDA bfloat16 [tokens, heads, latent + 64]; cache: bfloat16 [rows,
     latent + 64]; selected: int32 [tokens, k], physical rows as the top-k writes
-    them (entries outside the cache, e.g. -1, are empty places). out: bfloat16
+    them in token mode, in any order (entries outside the cache, e.g. -1, are
+    empty places; a block-mode selection's blocks are not rows). out: bfloat16
     [tokens, heads, latent], zero where a token sees nothing; lse: true for the
     float32 [tokens, heads] logarithm of the softmax sum (-inf where a token
     sees nothing), else None is returned for it. workspace: None, or scratch

@@ -27,6 +27,8 @@
  * -inf there, is no part of out[t, h] and lse[t, h], whatever it holds and whatever
  * other query rows see of it.
  * If a row that query row (t, h) sees makes its s_j NaN or +inf, out[t, h] is NaN.
+ * The sums are held in 32 bits, in units of a weight that may lag the largest by
+ * 2^16: latent values past 2^96 may overflow them.
  */
 #ifndef LATENT_BF16_H
 #define LATENT_BF16_H
@@ -116,7 +118,9 @@ topk_status_t latent_bf16_append(const latent_bf16_append_t *args, void *stream)
  *
  * latent_bf16_attend_selected: token t sees the cache rows selected[t *
  * selected_stride + i], i < k, that lie in [0, cache_rows); other entries (the
- * top-k's -1) are empty places. A row listed twice counts twice.
+ * top-k's -1) are empty places, in any order. A row listed twice counts twice. A
+ * block-mode selection (TOPK_BLOCK8) names 8-token blocks, not rows: it has to be
+ * expanded to its tokens' rows first.
  *
  * latent_bf16_attend_paged: token t belongs to request t / rows_per_request and
  * sees that request's first valid_len[t] tokens (clamped to [0, width]); token
