@@ -26,10 +26,13 @@ from ._build import LIB_PATH, build
 def __getattr__(name: str):
     # The latent-cache operators import torch when first used, as the functions below do.
     if name in ("latent_append", "latent_attend_selected", "latent_attend_paged", "latent_workspace"):
-        from . import latent
-        value = globals()[name] = getattr(latent, name)
-        return value
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        from . import latent as module
+    elif name == "page_step":
+        from . import pages as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(module, name)
+    return value
 
 TOKEN = 0
 BLOCK8 = 1

@@ -14,7 +14,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 HEADER = os.path.join(ROOT, "include", "topk_bf16.h")
-LATENT_HEADER = os.path.join(ROOT, "include", "latent_bf16.h")
 LIB_PATH = os.path.join(PKG, "libtopk_bf16.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -27,7 +26,7 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return [*sources(), *glob.glob(os.path.join(CSRC, "*.cuh")), *glob.glob(os.path.join(CSRC, "*.h")),
-            HEADER, LATENT_HEADER, __file__]
+            *glob.glob(os.path.join(os.path.dirname(HEADER), "*.h")), __file__]
 
 
 def _nvcc() -> str:

@@ -1,4 +1,4 @@
-"""ctypes mirror of include/latent_bf16.h."""
+"""ctypes mirror of include/latent_bf16.h and page_step.h."""
 from __future__ import annotations
 
 import ctypes
@@ -24,14 +24,20 @@ class Attend(ctypes.Structure):
                 ("rows_per_request", _I), ("scale", _F)]
 
 
+class PageStep(ctypes.Structure):
+    _fields_ = [("block_table", _P), ("table_stride", _L), ("lengths", _P), ("new_tokens", _P), ("free_pages", _P),
+                ("free_count", _P), ("next_lengths", _P), ("next_free_count", _P), ("granted", _P),
+                ("positions", _P), ("slots", _P), ("valid_len", _P), ("requests", _I), ("pages", _I),
+                ("free_size", _I), ("page_size", _I), ("block_rows", _I), ("rows_per_request", _I)]
+
+
 def declare(lib) -> None:
-    """Argument types of the latent entry points of a loaded library."""
-    lib.latent_bf16_append.argtypes = [ctypes.POINTER(Append), _P]
-    lib.latent_bf16_attend_selected.argtypes = [ctypes.POINTER(Attend), _P]
-    lib.latent_bf16_attend_paged.argtypes = [ctypes.POINTER(Attend), _P]
-    for f in (lib.latent_bf16_append, lib.latent_bf16_attend_selected, lib.latent_bf16_attend_paged):
+    """Argument types of the entry points of those headers in a loaded library."""
+    for f, args in ((lib.latent_bf16_append, Append), (lib.latent_bf16_attend_selected, Attend),
+                    (lib.latent_bf16_attend_paged, Attend), (lib.page_step, PageStep)):
+        f.argtypes = [ctypes.POINTER(args), _P]
         f.restype = ctypes.c_int
-    lib.latent_bf16_attend_workspace.argtypes = [ctypes.POINTER(Attend), ctypes.c_int32]
+    lib.latent_bf16_attend_workspace.argtypes = [ctypes.POINTER(Attend), _I]
     lib.latent_bf16_attend_workspace.restype = ctypes.c_int64
     lib.latent_bf16_workspace_bytes.argtypes = []
     lib.latent_bf16_workspace_bytes.restype = ctypes.c_int64

@@ -1,0 +1,207 @@
+// One step of a batch's page tables (page_step.h): pages from prefix sums over the
+// requests, then every row's position, slot and valid length, in one launch.
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "page_step.h"
+
+namespace topk::pages {
+
+namespace {
+
+constexpr int NT = 512;
+constexpr int MAX_CLUSTER = 8;
+constexpr int ROWS = 4096;                   // rows (or requests) a CTA has before another joins the cluster
+constexpr uint32_t FULL = 0xFFFFFFFFu;
+
+struct Params {
+    page_step_t a;
+    int32_t page_shift, slice;               // slice: requests of a CTA
+};
+
+struct Request {
+    int32_t length, add, owned, need, back;  // tokens it has and asks for; pages it holds, needs, gives back
+};
+
+__device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t shift) {
+    return static_cast<int32_t>((static_cast<uint32_t>(tokens) + (1u << shift) - 1u) >> shift);
+}
+
+__device__ __forceinline__ Request request_at(const Params &p, int32_t r) {
+    const int32_t width = p.a.pages << p.page_shift, ask = p.a.new_tokens[r];
+    Request x;
+    x.length = min(max(p.a.lengths[r], 0), width);
+    x.owned = pages_of(x.length, p.page_shift);
+    x.add = min(max(ask, 0), p.a.rows_per_request);
+    if (x.add > width - x.length) x.add = 0;
+    x.need = pages_of(x.length + x.add, p.page_shift) - x.owned;
+    x.back = ask < 0 ? x.owned : 0;
+    return x;
+}
+
+// Every CTA of the (one) cluster goes over all requests, NT at a time: a prefix
+// sum of the pages they need, of which its own rows take theirs; so no CTA waits for
+// another's sums. What other CTAs still read (lengths, the count, the stack's top)
+// is written after the cluster's barrier, which is what makes the call work in
+// place without scratch of its own.
+// Bound by latency: two rounds of loads, a scan and the launch.
+__global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ Params p) {
+    extern __shared__ int32_t own[];         // the CTA's requests: next length, first page given back
+    __shared__ uint32_t s_first[NT];
+    __shared__ int32_t s_length[NT], s_add[NT], s_need[NT / 32], s_back[NT / 32], s_taken;
+    const page_step_t &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t ctas = static_cast<int32_t>(gridDim.x), rank = static_cast<int32_t>(blockIdx.x);
+    const int32_t q = a.rows_per_request, n = a.requests;
+    const int32_t r0 = min(n, rank * p.slice), r1 = min(n, r0 + p.slice);
+    const int32_t rows = n * q, per = (rows + ctas - 1) / ctas;
+    const int32_t t0 = static_cast<int32_t>(min(static_cast<long long>(rows), static_cast<long long>(rank) * per));
+    const int32_t t1 = t0 + min(rows - t0, per);
+    if (tid == 0) s_taken = 0;
+    grid_dependents_release();
+    grid_dependency_wait();
+    const int32_t count = min(max(a.free_count[0], 0), a.free_size);
+    int32_t need_before = 0, back_before = 0;
+    for (int32_t base = 0; base < n; base += NT) {
+        const int32_t r = base + tid;
+        Request x = {};
+        if (r < n) x = request_at(p, r);
+        int32_t need = x.need, back = x.back;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(FULL, need, o), v = __shfl_up_sync(FULL, back, o);
+            if (lane >= o) need += u, back += v;
+        }
+        __syncthreads();                     // (the last chunk's rows are written)
+        if (lane == 31) s_need[warp] = need, s_back[warp] = back;
+        __syncthreads();
+        int32_t need_all = 0, back_all = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            const int32_t u = s_need[w], v = s_back[w];
+            if (w < warp) need += u, back += v;
+            need_all += u, back_all += v;
+        }
+        need += need_before, back += back_before;
+        const bool fits = x.need == 0 || need <= count;
+        if (x.need != 0 && fits) atomicMax(&s_taken, need);
+        const int32_t add = fits ? x.add : 0;
+        // Page i >= owned of the request is free_pages[first - i] (modulo 2^32).
+        s_first[tid] = static_cast<uint32_t>(count) - 1u - static_cast<uint32_t>(need - x.need) +
+                       static_cast<uint32_t>(x.owned);
+        s_length[tid] = x.length;
+        s_add[tid] = add;
+        if (r >= r0 && r < r1) {
+            a.granted[r] = add;
+            own[r - r0] = x.back != 0 || a.new_tokens[r] < 0 ? 0 : x.length + add;
+            own[p.slice + r - r0] = back - x.back;
+        }
+        __syncthreads();
+        const long long from = static_cast<long long>(base) * q;
+        const long long to = min(from + static_cast<long long>(NT) * q, static_cast<long long>(t1));
+        for (long long t = max(from, static_cast<long long>(t0)) + tid; t < to; t += NT) {
+            const uint32_t in = static_cast<uint32_t>(t - from);
+            const int32_t i = static_cast<int32_t>(in / static_cast<uint32_t>(q)), j = static_cast<int32_t>(in - i * q);
+            int32_t pos = 0, slot = -1, valid = 0;
+            if (j < s_add[i]) {
+                const int32_t length = s_length[i], owned = pages_of(length, p.page_shift);
+                pos = length + j;
+                valid = pos + 1;
+                const int32_t at = pos >> p.page_shift, offset = pos & ((1 << p.page_shift) - 1);
+                int32_t *entry = a.block_table + (base + i) * a.table_stride + at;
+                const int32_t page = at < owned ? *entry : a.free_pages[s_first[i] - static_cast<uint32_t>(at)];
+                if (at >= owned && offset == 0) *entry = page;   // (a new page's first token is one of the call's)
+                const long long row = static_cast<long long>(page) * a.block_rows + offset;
+                slot = page >= 0 && row <= INT32_MAX ? static_cast<int32_t>(row) : -1;
+            }
+            a.positions[t] = pos;
+            a.slots[t] = slot;
+            a.valid_len[t] = valid;
+        }
+        need_before += need_all;
+        back_before += back_all;
+    }
+    __syncthreads();
+    if (ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    const long long left = count - s_taken;
+    for (int32_t r = r0 + warp; r < r1; r += NT / 32) {
+        const int32_t next = own[r - r0];
+        const long long first = left + own[p.slice + r - r0];
+        int32_t back = 0;
+        if (lane == 0 && next == 0 && a.new_tokens[r] < 0) {
+            const int32_t width = a.pages << p.page_shift;
+            back = pages_of(min(max(a.lengths[r], 0), width), p.page_shift);
+        }
+        back = __shfl_sync(FULL, back, 0);
+        for (int32_t i = lane; i < back; i += 32)
+            if (first + i < a.free_size) a.free_pages[first + i] = a.block_table[r * a.table_stride + i];
+        __syncwarp();
+        if (lane == 0) a.next_lengths[r] = next;
+    }
+    if (rank == 0 && tid == 0)
+        a.next_free_count[0] = static_cast<int32_t>(min(left + back_before, static_cast<long long>(a.free_size)));
+}
+
+topk_status_t check(const page_step_t *a) {
+    if (!a || a->requests < 0 || a->requests > PAGE_STEP_MAX_REQUESTS || a->pages < 0 || a->free_size < 0)
+        return TOPK_ERR_ARG;
+    if (a->page_size < 1 || (a->page_size & (a->page_size - 1)) || a->block_rows < a->page_size ||
+        a->rows_per_request < 1 || a->table_stride < a->pages)
+        return TOPK_ERR_ARG;
+    if (static_cast<int64_t>(a->requests) * a->pages > INT32_MAX ||
+        static_cast<int64_t>(a->requests) * a->rows_per_request > INT32_MAX)
+        return TOPK_ERR_ARG;
+    if (static_cast<int64_t>(a->pages) * a->page_size > PAGE_STEP_MAX_WIDTH) return TOPK_ERR_WIDTH;
+    if (!a->free_count || !a->next_free_count || (!a->free_pages && a->free_size > 0)) return TOPK_ERR_ARG;
+    if (a->requests > 0 && ((!a->block_table && a->pages > 0) || !a->lengths || !a->new_tokens || !a->next_lengths ||
+                            !a->granted || !a->positions || !a->slots || !a->valid_len))
+        return TOPK_ERR_ARG;
+    for (const void *v : {static_cast<const void *>(a->block_table), static_cast<const void *>(a->lengths),
+                          static_cast<const void *>(a->new_tokens), static_cast<const void *>(a->free_pages),
+                          static_cast<const void *>(a->free_count), static_cast<const void *>(a->next_lengths),
+                          static_cast<const void *>(a->next_free_count), static_cast<const void *>(a->granted),
+                          static_cast<const void *>(a->positions), static_cast<const void *>(a->slots),
+                          static_cast<const void *>(a->valid_len)})
+        if (reinterpret_cast<uintptr_t>(v) & 3u) return TOPK_ERR_ALIGN;
+    return TOPK_OK;
+}
+
+}  // namespace
+
+}  // namespace topk::pages
+
+extern "C" topk_status_t page_step(const page_step_t *args, void *stream) {
+    using namespace topk::pages;
+    const topk_status_t st = check(args);
+    if (st != TOPK_OK) return st;
+    Params p = {};
+    p.a = *args;
+    while ((1 << p.page_shift) < args->page_size) ++p.page_shift;
+    const int64_t rows = static_cast<int64_t>(args->requests) * args->rows_per_request;
+    int ctas = 1;
+    while (ctas < MAX_CLUSTER && rows > static_cast<int64_t>(ctas) * ROWS) ctas *= 2;
+    p.slice = (args->requests + ctas - 1) / ctas;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.slice) * 8;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    void *kargs[] = {&p};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&page_step_kernel), kargs) == cudaSuccess
+               ? TOPK_OK
+               : TOPK_ERR_CUDA;
+}
