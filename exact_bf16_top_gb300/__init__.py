@@ -27,6 +27,9 @@ def __getattr__(name: str):
     # The latent-cache operators import torch when first used, as the functions below do.
     if name in ("latent_append", "latent_attend_selected", "latent_attend_paged", "latent_workspace"):
         from . import latent as module
+    elif name in ("latent4_append", "latent4_rows", "latent4_attend_selected", "latent4_attend_paged",
+                  "latent4_row_bytes", "latent4_workspace"):
+        from . import latent4 as module
     elif name == "page_step":
         from . import pages as module
     else:

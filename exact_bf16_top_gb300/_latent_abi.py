@@ -1,9 +1,9 @@
-"""ctypes mirror of include/latent_bf16.h and page_step.h."""
+"""ctypes mirror of include/latent_bf16.h, latent4.h and page_step.h."""
 from __future__ import annotations
 
 import ctypes
 
-_P, _L, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+_P, _L, _I, _F, _D = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_double
 
 
 class Append(ctypes.Structure):
@@ -24,6 +24,13 @@ class Attend(ctypes.Structure):
                 ("rows_per_request", _I), ("scale", _F)]
 
 
+class Append4(ctypes.Structure):
+    _fields_ = [*Append._fields_[:-1], ("eps", _D)]
+
+
+# latent4_attend_t has latent_bf16_attend_t's fields.
+
+
 class PageStep(ctypes.Structure):
     _fields_ = [("block_table", _P), ("table_stride", _L), ("lengths", _P), ("new_tokens", _P), ("free_pages", _P),
                 ("free_count", _P), ("next_lengths", _P), ("next_free_count", _P), ("granted", _P),
@@ -34,10 +41,16 @@ class PageStep(ctypes.Structure):
 def declare(lib) -> None:
     """Argument types of the entry points of those headers in a loaded library."""
     for f, args in ((lib.latent_bf16_append, Append), (lib.latent_bf16_attend_selected, Attend),
-                    (lib.latent_bf16_attend_paged, Attend), (lib.page_step, PageStep)):
+                    (lib.latent_bf16_attend_paged, Attend), (lib.latent4_append, Append4),
+                    (lib.latent4_attend_selected, Attend), (lib.latent4_attend_paged, Attend),
+                    (lib.page_step, PageStep)):
         f.argtypes = [ctypes.POINTER(args), _P]
         f.restype = ctypes.c_int
-    lib.latent_bf16_attend_workspace.argtypes = [ctypes.POINTER(Attend), _I]
-    lib.latent_bf16_attend_workspace.restype = ctypes.c_int64
-    lib.latent_bf16_workspace_bytes.argtypes = []
-    lib.latent_bf16_workspace_bytes.restype = ctypes.c_int64
+    lib.latent4_rows.argtypes = [_P, _L, _I, _I, _P, _I, _P, _L, _P]
+    lib.latent4_rows.restype = ctypes.c_int
+    for f in (lib.latent_bf16_attend_workspace, lib.latent4_attend_workspace):
+        f.argtypes = [ctypes.POINTER(Attend), _I]
+        f.restype = ctypes.c_int64
+    for f in (lib.latent_bf16_workspace_bytes, lib.latent4_workspace_bytes):
+        f.argtypes = []
+        f.restype = ctypes.c_int64

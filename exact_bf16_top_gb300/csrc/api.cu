@@ -505,7 +505,7 @@ topk_status_t topk_bf16_device_status(uint32_t *flags, int32_t clear) {
     if (cudaDeviceSynchronize() != cudaSuccess) return TOPK_ERR_CUDA;
     uint32_t v = 0;
     for (auto f : {topk::status_stream, topk::status_direct, topk::status_one, topk::status_ordered,
-                   topk::latent::status_attend}) {
+                   topk::latent::status_attend, topk::latent::status_attend4}) {
         uint32_t u = 0;
         if (f(&u, clear != 0) != cudaSuccess) return TOPK_ERR_CUDA;
         v |= u;

@@ -1,0 +1,262 @@
+// Appending tokens to the 4-bit latent cache (norm, rounding to 4 bits, rotation,
+// the write to the token's slot, and the rotation of the token's query parts, in one
+// launch), and reading rows back as BF16.
+
+#include <cuda_fp16.h>
+
+#include <cfloat>
+
+#include "latent_rotate.cuh"
+
+namespace topk::latent {
+
+namespace {
+
+constexpr int NT = 256;
+constexpr uint32_t FULL = 0xFFFFFFFFu;
+
+// A number as the sum of two floats, the second at most half a unit of the first.
+struct Two {
+    float hi, lo;
+};
+
+// a + b of two such numbers; exact but for the last product of errors (2^-48).
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const float s = __fadd_rn(a.hi, b.hi), d = __fadd_rn(s, -a.hi);
+    const float e = __fadd_rn(__fadd_rn(a.hi, -__fadd_rn(s, -d)), __fadd_rn(b.hi, -d));
+    return {s, __fadd_rn(__fadd_rn(a.lo, b.lo), e)};
+}
+
+__device__ __forceinline__ Two times(Two a, Two b) {
+    const float h = __fmul_rn(a.hi, b.hi);
+    return {h, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -h)))};
+}
+
+// 1 / sqrt(x): Newton's step in pairs of floats on the hardware's estimate, whose
+// error of 2^-22 becomes 2^-44 (and stays none where there was none: rows whose mean
+// square is a power of four give values that lie on the borders).
+__device__ __forceinline__ Two over_sqrt(Two x) {
+    const float y = rsqrtf(x.hi);
+    const float p = __fmul_rn(y, y), pe = __fmaf_rn(y, y, -p);
+    const float q = __fmul_rn(x.hi, p), qe = __fmaf_rn(x.hi, p, -q);
+    const float e = __fadd_rn(1.0f, -q) - qe - x.hi * pe - x.lo * p;   // 1 - x y^2
+    const float d = y * __fmaf_rn(0.375f * e, e, 0.5f * e), r = __fadd_rn(y, d);   // (NaN of an infinite x)
+    return {r, __fadd_rn(d, -__fadd_rn(r, -y))};
+}
+
+// xw * r, rounded to odd: what is not a float becomes the neighbour whose last bit is
+// 1. Rounded further to any format of two bits less it gives what the exact product
+// would, ties included.
+__device__ __forceinline__ float times_odd(float xw, Two r) {
+    const float v = __fmul_rn(xw, r.hi);
+    const float e = __fmaf_rn(xw, r.lo, __fmaf_rn(xw, r.hi, -v));
+    uint32_t b = __float_as_uint(v);
+    if (e != 0.0f && !(b & 1u)) b += (__float_as_uint(e) ^ b) >> 31 ? FULL : 1u;   // (towards e; NaN stays NaN)
+    return __uint_as_float(b);
+}
+
+// The larger of m and |v|, NaN if one of them is.
+__device__ __forceinline__ float largest(float m, float v) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(fabsf(v)));
+    return y;
+}
+
+// A block's 16 values to its scale's e4m3 byte and 16 codes. Both quotients are rounded
+// to nearest, which no float near a border can be moved onto it by: a border is the
+// quotient of a float of few bits, its neighbours' quotients are floats of their own.
+__device__ __forceinline__ uint32_t to_codes(const float (&v)[16], uint32_t (&code)[2]) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = largest(most, v[i]);
+    uint32_t s8 = 0x7Fu;                     // NaN: one of the values is not finite
+    float s = 1.0f;
+    if (most <= FLT_MAX) {
+        uint16_t two;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(__fdiv_rn(most, 6.0f)));
+        s8 = max(static_cast<uint32_t>(two) & 0xFFu, 1u);
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(s8)));
+        s = __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = s8 == 0x7Fu ? 0.0f : __fdiv_rn(v[8 * w + i], s);
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+            "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+            : "=r"(code[w])
+            : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    }
+    return s8;
+}
+
+struct Norm {
+    Two share, eps;                          // 1 / latent, eps
+};
+
+// One warp per unit of work, as in the BF16 form: a token's cache row (a block of 16
+// values that share a scale per lane, so that none of the rounding crosses lanes), or
+// up to 16 of a token's query heads. The sum of squares and the norm are pairs of
+// floats: a value next to a border of 4 bits takes the side that exact arithmetic
+// gives it, whatever the order of the sums.
+__global__ void __launch_bounds__(NT) append4_kernel(const latent4_append_t a, uint32_t units, uint32_t groups,
+                                                     const Norm norm) {
+    grid_dependents_release();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, part = lane & 7;
+    const bool interleaved = a.interleaved != 0;
+    const uint32_t step = gridDim.x * (NT / 32);
+    for (uint32_t u = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); u < units; u += step) {
+        const bool key = u < static_cast<uint32_t>(a.tokens);
+        const uint32_t q = u - a.tokens;
+        const int32_t t = static_cast<int32_t>(key ? u : q / groups);
+        int32_t pos = __ldg(a.positions + t);
+        if (!key) {
+            turn_heads(a, t, static_cast<int32_t>(q - t * groups) * APPEND_HEADS, pos, lane);
+            continue;
+        }
+        pos = pos < 0 ? 0 : pos >= a.max_positions ? a.max_positions - 1 : pos;
+        const float *cs = a.cos_sin + static_cast<int64_t>(pos) * ROPE;
+        const int32_t slot = a.slots[t];
+        const bool mine = lane < a.latent / 16;
+        uint4 x[2] = {}, w[2] = {};
+        if (mine) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.latents + t * a.latents_stride) + 2 * lane;
+            x[0] = __ldg(src);
+            x[1] = __ldg(src + 1);
+            if (a.weight) {
+                w[0] = __ldg(reinterpret_cast<const uint4 *>(a.weight) + 2 * lane);
+                w[1] = __ldg(reinterpret_cast<const uint4 *>(a.weight) + 2 * lane + 1);
+            }
+        }
+        const uint4 k = __ldg(reinterpret_cast<const uint4 *>(a.key_rope + t * a.key_stride) + part);
+        if (slot < 0 || slot >= a.cache_rows) continue;
+        uint8_t *row = a.cache + static_cast<int64_t>(slot) * a.cache_stride;
+        const uint32_t *b = &x[0].x, *g = &w[0].x;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] = lo_f(b[i]);
+            v[2 * i + 1] = hi_f(b[i]);
+        }
+        if (a.weight) {
+            Two sum = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum = add(sum, {__fmul_rn(v[i], v[i]), 0.0f});   // (squares of BF16 are exact)
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                sum = add(sum, {__shfl_xor_sync(FULL, sum.hi, o), __shfl_xor_sync(FULL, sum.lo, o)});
+            const Two r = over_sqrt(add(times(sum, norm.share), norm.eps));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[2 * i] = times_odd(__fmul_rn(v[2 * i], lo_f(g[i])), r);
+                v[2 * i + 1] = times_odd(__fmul_rn(v[2 * i + 1], hi_f(g[i])), r);
+            }
+        }
+        uint32_t code[2];
+        const uint32_t s8 = to_codes(v, code);
+        if (mine) {
+            reinterpret_cast<uint2 *>(row)[lane] = make_uint2(code[0], code[1]);
+            row[a.latent / 2 + 2 * ROPE + lane] = static_cast<uint8_t>(s8);
+        }
+        const uint4 turned = Turn(cs, part, interleaved)(k, part, interleaved);
+        if (lane < 8) reinterpret_cast<uint4 *>(row + a.latent / 2)[part] = turned;
+    }
+}
+
+// Eight codes and their scale as eight BF16 values.
+__device__ __forceinline__ uint4 from_codes(uint32_t w, __half2 scale) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&h[i]), scale));
+        r[i] = pack(f.x, f.y);               // (at most six significant bits: nothing is rounded)
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// A warp per row: 16 values of one scale per lane, the key part by eight lanes.
+__global__ void __launch_bounds__(NT) rows4_kernel(const uint8_t *__restrict__ cache, int64_t cache_stride,
+                                                   int32_t cache_rows, int32_t latent, const int32_t *__restrict__ rows,
+                                                   int32_t count, uint16_t *__restrict__ out, int64_t out_stride) {
+    grid_dependents_release();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const bool mine = lane < latent / 16;
+    const int32_t step = static_cast<int32_t>(gridDim.x) * (NT / 32);
+    for (int64_t i = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); i < count; i += step) {
+        const int32_t r = __ldg(rows + i);
+        uint2 code = make_uint2(0, 0);
+        uint32_t s8 = 0;
+        uint4 key = make_uint4(0, 0, 0, 0);
+        if (r >= 0 && r < cache_rows) {
+            const uint8_t *row = cache + r * cache_stride;
+            if (mine) {
+                code = __ldg(reinterpret_cast<const uint2 *>(row) + lane);
+                s8 = __ldg(row + latent / 2 + 2 * ROPE + lane);
+            }
+            if (lane < 8) key = __ldg(reinterpret_cast<const uint4 *>(row + latent / 2) + lane);
+        }
+        uint32_t s;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(s8 | s8 << 8)));
+        const __half2 scale = *reinterpret_cast<const __half2 *>(&s);
+        uint4 *to = reinterpret_cast<uint4 *>(out + i * out_stride);
+        if (mine) {
+            to[2 * lane] = from_codes(code.x, scale);
+            to[2 * lane + 1] = from_codes(code.y, scale);
+        }
+        if (lane < 8) to[latent / 8 + lane] = key;
+    }
+}
+
+cudaLaunchConfig_t config(int64_t units, int sms, cudaStream_t stream, cudaLaunchAttribute *attr) {
+    const int64_t want = (units + NT / 32 - 1) / (NT / 32), most = static_cast<int64_t>(sms) * (2048 / NT);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most), 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+Two two(double v) {
+    const float hi = static_cast<float>(v);
+    return {hi, static_cast<float>(v - hi)};
+}
+
+}  // namespace
+
+cudaError_t launch_append4(const latent4_append_t &a, int sms, cudaStream_t stream) {
+    uint32_t groups = a.query_rope ? static_cast<uint32_t>((a.heads + APPEND_HEADS - 1) / APPEND_HEADS) : 0u;
+    uint32_t units = static_cast<uint32_t>(a.tokens) * (1u + groups);   // (at most 2^27 tokens: checked)
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(units, sms, stream, &attr);
+    latent4_append_t arg = a;
+    Norm norm = {two(1.0 / a.latent), two(a.eps)};
+    void *args[] = {&arg, &units, &groups, &norm};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&append4_kernel), args);
+}
+
+cudaError_t launch_rows4(const uint8_t *cache, int64_t cache_stride, int32_t cache_rows, int32_t latent,
+                         const int32_t *rows, int32_t count, uint16_t *out, int64_t out_stride, int sms,
+                         cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(count, sms, stream, &attr);
+    void *args[] = {&cache, &cache_stride, &cache_rows, &latent, &rows, &count, &out, &out_stride};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&rows4_kernel), args);
+}
+
+}  // namespace topk::latent

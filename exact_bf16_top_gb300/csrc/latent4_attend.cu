@@ -1,0 +1,853 @@
+// Attention over latent cache rows in 4 bits on the tensor cores: one persistent
+// kernel for both forms, dealt and joined as the BF16 rows' (latent_attend.cuh).
+//
+// A tile is up to 64 (token, head) rows that read the same cache rows; blocks of 128
+// cache rows become FP16 on their way, once for both products:
+//     scores (128 tokens x rows) = K Q^T,  weights = 2^(scores - reference),
+//     sums (values x rows)      += V^T weights,   V the latent part of K.
+// A thread takes 128 values of a row from memory to registers, makes FP16 of them (the
+// conversion and one product are exact) and writes them twice: into tensor memory,
+// where they are the scores' left operand, and into shared memory, where, read across
+// rows, they are the sums'. So shared memory, which bounds the BF16 kernel, gives
+// each block away once instead of twice, and the scores run at 128 rows a step.
+// The key part stays BF16 and only goes to tensor memory. Warps have one job each
+// (softmax, rows, issue of either product) and meet at mbarriers only.
+
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "latent_attend.cuh"
+
+namespace topk::latent {
+
+namespace {
+
+constexpr int SOFT = 256;                    // warps 0 to 7: query rows, softmax and outputs, in two groups
+constexpr int LOAD = 256;                    // warps 8 to 15: cache rows, in two groups
+constexpr int NT = SOFT + LOAD + 64;         // warps 16 and 17: the tensor cores (scores, sums)
+constexpr int KEYS = 128;                    // cache rows of a block
+constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
+constexpr int BLOCKS = 8;                    // blocks that have marks and barriers of their own: more than are
+                                             // under way
+constexpr int KEY_SLOTS = 2;                 // blocks' key parts in tensor memory
+constexpr uint32_t FULL = 0xFFFFFFFFu;
+// Weights are FP16: the reference is set this far below the maximum and moves when a
+// weight passes 2^MOST, so that the largest weight of a row is 2^11 at least and what
+// FP16 rounds away below 2^-25 is less than 2^-36 of it.
+constexpr float BELOW = 11.0f, MOST = 15.0f;
+
+// How a tile of NR rows uses the memories: pairs of 64-value chunks in shared memory
+// (sums) and tensor memory (scores), blocks of weights and of scores.
+template <int NR>
+struct Shape {
+    static constexpr int PAIRS = NR == 64 ? 4 : 5, A_PAIRS = NR == 64 ? 2 : 4;
+    static constexpr int WEIGHTS = NR == 16 ? 2 : 1, SCORES = NR == 64 ? 1 : 2;
+    static constexpr uint32_t O_COL = 0, S_COL = 4 * NR, A_COL = S_COL + SCORES * NR, K_COL = A_COL + A_PAIRS * 64;
+    static_assert(K_COL + KEY_SLOTS * 32 <= 512);
+};
+
+struct Ctrl : Schedule<NT> {
+    u64 pair_full[5], pair_empty[5];           // a pair of chunks is in / its sums are added
+    u64 a_empty[4];                            // a pair's scores are added
+    u64 key_full[KEY_SLOTS], key_empty[KEY_SLOTS];
+    u64 s_full[2], s_empty[2];                 // scores written / read
+    u64 row_full[BLOCKS];                      // a block's marks are in
+    u64 p_full[BLOCKS], o_done[BLOCKS];        // a block's weights are in / its sums are added
+    u64 q_full;                                // a tile's query rows are in
+    u64 drain[2];
+    uint32_t tmem;
+    volatile uint32_t abort;
+    alignas(16) float ref[ROWS];               // reference (log2), LOWEST at first; +inf: a row that sees nothing here
+    alignas(16) float factor[ROWS];
+    alignas(16) float unit[ROWS];              // scores in log2 units: times this
+    float l[ROWS];
+    int32_t lim[ROWS];                         // tokens a row may see
+    float across[4][ROWS];
+    uint32_t marks[BLOCKS][KEYS / 32];         // which rows of a block there are
+};
+
+using Cursor = CursorOf<KEYS>;
+using RowList = RowListOf<KEYS>;
+
+template <int NR>
+__host__ __device__ constexpr uint32_t query_bytes(int latent) {
+    return static_cast<uint32_t>((latent / 64 + 1) * NR * 128);
+}
+template <int NR>
+constexpr bool fits() {
+    return 1024 + query_bytes<NR>(LATENT_MAX) + (2 * Shape<NR>::PAIRS + Shape<NR>::WEIGHTS) * CHUNK + sizeof(Ctrl) <=
+           SMEM;
+}
+static_assert(fits<16>() && fits<32>() && fits<64>());
+
+__device__ __forceinline__ void tc_mma_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+            r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SOFT) : "memory"); }
+
+__device__ __forceinline__ bool soft_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u), "n"(SOFT)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ bool half_not_finite(uint32_t w) {
+    return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
+}
+
+// Eight codes as FP16, times their scale: exact.
+__device__ __forceinline__ void from_codes(uint32_t w, __half2 scale, uint32_t *to) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[i]), scale);
+        to[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+__device__ __forceinline__ void load32(const uint8_t *from, uint32_t *v) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(from));
+}
+
+// ------------------------------------------------------------------ the warps' parts
+
+// A tile's query rows into shared memory, eight threads a row: the latent part as
+// FP16, all of it times the power of two that brings the row's largest finite value to
+// [2^8, 2^9). Both are exact for values down to 2^-22 of it.
+template <int NR>
+__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, Ctrl &c, char *query, int tid) {
+    const int piece = tid & 7, pairs = p.latent / 128;
+    for (int r = tid >> 3; r < NR; r += SOFT / 8) {
+        const bool on = r < tile.rows;
+        const int32_t flat = tile.base + (on ? r : 0), token = flat / p.heads, head = flat - token * p.heads;
+        const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
+        uint4 v[LATENT_MAX / 64 + 1];
+#pragma unroll
+        for (int k = 0; k <= LATENT_MAX / 64; ++k)
+            v[k] = on && k <= 2 * pairs ? __ldg(reinterpret_cast<const uint4 *>(src + k * 64)) : make_uint4(0, 0, 0, 0);
+        uint32_t most = 0;
+#pragma unroll
+        for (int k = 0; k <= LATENT_MAX / 64; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = w[i] & 0x7F80u, hi = w[i] >> 16 & 0x7F80u;
+                most = max(most, max(lo == 0x7F80u ? 0u : lo, hi == 0x7F80u ? 0u : hi));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(FULL, most, o));
+        const uint32_t up = min(262u - (most >> 7), 253u);       // exponent field of the factor: 2^(8 - exponent)
+        const float by = __uint_as_float(up << 23);
+        if (piece == 0) {
+            const float u = p.scale * LOG2E * __uint_as_float((254u - up) << 23);
+            c.unit[r] = fminf(fmaxf(u, -FLT_MAX), FLT_MAX);
+        }
+        char *dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
+#pragma unroll
+        for (int k = 0; k <= LATENT_MAX / 64; ++k) {
+            if (k > 2 * pairs) break;
+            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(w[i] << 16) * by, b = __uint_as_float(w[i] & 0xFFFF0000u) * by;
+                if (k < 2 * pairs) {
+                    const __half2 h = __floats2half2_rn(a, b);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst + k * NR * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if ((tid & 31) == 0) arrive(&c.q_full);
+}
+
+// A unit of a block's rows: 64 bytes of each, that is 128 values with their eight
+// scales, or one half of the key part.
+struct Raw {
+    uint32_t v[16];
+    uint2 scales;
+    bool there;
+};
+
+// The units of all blocks in order; a group of four warps takes every other one, and a
+// lane always the same row of a block (as tensor memory wants it). Row numbers are
+// read one unit before the rows, rows two units before they are converted.
+struct Feed {
+    Cursor at;
+    const int32_t *list = nullptr;
+    int32_t len = 0, b = 0, j = 0, fetched = -1;
+    int u, of;                                 // unit and units of a block
+    bool live;
+    __device__ __forceinline__ Feed(const AttendParams &p, const Ctrl &c, int first, int units, int lane, int row)
+        : at(c), u(first), of(units) {
+        live = piece(p, lane);
+        if (live) fetch(p, row);
+    }
+    __device__ __forceinline__ bool piece(const AttendParams &p, int lane) {
+        if (!at.next(p, lane)) return false;
+        const RowList l(p, at);
+        list = l.list;
+        len = l.len;
+        b = at.b0;
+        return true;
+    }
+    __device__ __forceinline__ void fetch(const AttendParams &p, int row) {
+        j = b * KEYS + row;
+        fetched = j < len ? __ldg(list + (p.paged ? j >> p.page_shift : j)) : -1;
+    }
+    // Loads the unit whose row number was fetched, and fetches the next one's.
+    __device__ __forceinline__ bool load(const AttendParams &p, Raw &r, int lane, int row) {
+        if (!live) return false;
+        const int64_t v = p.paged ? static_cast<int64_t>(fetched) * p.block_rows + (j & ((1 << p.page_shift) - 1))
+                                  : fetched;
+        r.there = fetched >= 0 && v < p.cache_rows;
+        if (r.there) {
+            const uint8_t *from = static_cast<const uint8_t *>(p.cache) + v * p.cache_stride;
+            load32(from + u * 64, r.v);
+            load32(from + u * 64 + 32, r.v + 8);
+            if (u < of - 2) r.scales = __ldg(reinterpret_cast<const uint2 *>(from + p.latent / 2 + 2 * LATENT_ROPE) + u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r.v[i] = 0;
+            r.scales = make_uint2(0, 0);
+        }
+        u += 2;
+        while (u >= of && live) {
+            u -= of;
+            if (++b == at.b1) live = piece(p, lane);
+        }
+        if (live) fetch(p, row);
+        return true;
+    }
+};
+
+template <int NR>
+__device__ void load_rows(const AttendParams &p, Ctrl &c, char *pairs_at, uint32_t tmem) {
+    using S = Shape<NR>;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x - SOFT) >> 5, quarter = warp & 3, group = warp >> 2;
+    const int row = quarter * 32 + lane, pairs = p.latent / 128, units = pairs + 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t i = 0;                            // the block and the unit that are converted next
+    int u = group;
+    Feed feed(p, c, group, units, lane, row);
+    auto convert = [&](const Raw &r) {
+        if (u < pairs) {
+            const uint32_t n = i * pairs + u, slot = n % S::PAIRS, a = n % S::A_PAIRS;
+            char *to = pairs_at + slot * 2 * CHUNK + row * 128;
+            wait(&c.a_empty[a], n / S::A_PAIRS + 1, c);
+            wait(&c.pair_empty[slot], n / S::PAIRS + 1, c);
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {      // 32 values with two scales
+                const uint32_t two = (q < 2 ? r.scales.x : r.scales.y) >> (16 * (q & 1));
+                uint32_t s, w[16];
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
+                const __half2 scales = *reinterpret_cast<const __half2 *>(&s);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    from_codes(r.v[4 * q + k], k < 2 ? __low2half2(scales) : __high2half2(scales), w + 4 * k);
+                tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4 *>(to + (q >> 1) * CHUNK + ((((q & 1) * 4 + k) ^ (row & 7)) << 4)) =
+                        make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) arrive(&c.pair_full[slot]);
+        } else {
+            const uint32_t slot = i % KEY_SLOTS;
+            wait(&c.key_empty[slot], i / KEY_SLOTS + 1, c);
+            if (u == pairs) {
+                const uint32_t mask = __ballot_sync(FULL, r.there);
+                if (lane == 0) {
+                    c.marks[i % BLOCKS][quarter] = mask;
+                    arrive(&c.row_full[i % BLOCKS]);
+                }
+            }
+            tc_fence_after();
+            tc_store16(lanes + S::K_COL + slot * 32 + (u - pairs) * 16, r.v);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&c.key_full[slot]);
+        }
+        u += 2;
+        while (u >= units) {
+            u -= units;
+            ++i;
+        }
+    };
+    Raw x, y;
+    bool on_x = feed.load(p, x, lane, row), on_y = feed.load(p, y, lane, row);
+    while (on_x) {
+        convert(x);
+        on_x = feed.load(p, x, lane, row);
+        if (!on_y) break;
+        convert(y);
+        on_y = feed.load(p, y, lane, row);
+    }
+}
+
+// Instruction descriptor as instruction(), FP16 operands.
+__host__ __device__ constexpr uint32_t half_instruction(int m, int n, bool along) {
+    return instruction(m, n, along) & ~((1u << 7) | (1u << 10));
+}
+
+// The products, both with the cache as the left operand and the query rows as columns
+// (128 x NR x 16 a step): scores out of tensor memory, sums out of shared memory. Each
+// has a warp of its own, of which one lane issues.
+template <int NR>
+__device__ void multiply_scores(const AttendParams &p, Ctrl &c, uint32_t query, uint32_t tmem) {
+    using S = Shape<NR>;
+    const int lane = threadIdx.x & 31, pairs = p.latent / 128;
+    const bool one = elected();
+    constexpr uint32_t LATENT_KIND = half_instruction(KEYS, NR, false), KEY_KIND = instruction(KEYS, NR, false);
+    constexpr int QCHUNK = NR * 128;
+    Cursor at(c);
+    uint32_t i = 0, n = 0, piece = 0;
+    const uint64_t q = matrix(query, 16);
+    while (at.next(p, lane)) {
+        if (one) {
+            for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+                const uint32_t s = i % S::SCORES, d = tmem + S::S_COL + s * NR, key = i % KEY_SLOTS;
+                mbar_wait(&c.s_empty[s], (i / S::SCORES + 1) & 1u, &c.abort);
+                if (b == at.b0) {
+                    mbar_wait(&c.q_full, piece & 1u, &c.abort);
+                    fence_proxy_async();
+                }
+                for (int u = 0; u < pairs; ++u, ++n) {
+                    mbar_wait(&c.pair_full[n % S::PAIRS], (n / S::PAIRS) & 1u, &c.abort);
+                    tc_fence_after();
+                    const uint32_t k = tmem + S::A_COL + n % S::A_PAIRS * 64;
+                    const uint64_t qu = q + u * (2 * QCHUNK >> 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        tc_mma_a(d, k + e * 8, qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2, LATENT_KIND,
+                                 u > 0 || e > 0);
+                    tc_commit(&c.a_empty[n % S::A_PAIRS]);
+                }
+                mbar_wait(&c.key_full[key], (i / KEY_SLOTS) & 1u, &c.abort);
+                tc_fence_after();
+                const uint64_t qk = q + pairs * (2 * QCHUNK >> 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    tc_mma_a(d, tmem + S::K_COL + key * 32 + e * 8, qk + e * 2, KEY_KIND, true);
+                tc_commit(&c.key_empty[key]);
+                tc_commit(&c.s_full[s]);
+            }
+        }
+        __syncwarp();
+        ++piece;
+    }
+    drain(&c.drain[0], one);
+}
+
+template <int NR>
+__device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at, uint32_t weights, uint32_t tmem) {
+    using S = Shape<NR>;
+    const int lane = threadIdx.x & 31, pairs = p.latent / 128;
+    const bool one = elected();
+    constexpr uint32_t KIND = half_instruction(128, NR, true);
+    Cursor at(c);
+    uint32_t i = 0, n = 0;
+    while (at.next(p, lane)) {
+        if (one) {
+            for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+                mbar_wait(&c.p_full[i % BLOCKS], (i / BLOCKS) & 1u, &c.abort);
+                const uint64_t w = matrix(weights + i % S::WEIGHTS * CHUNK, 16);
+                for (int h = 0; h < pairs; ++h, ++n) {
+                    const uint32_t slot = n % S::PAIRS;
+                    mbar_wait(&c.pair_full[slot], (n / S::PAIRS) & 1u, &c.abort);   // (it is: for its writes' sake)
+                    fence_proxy_async();
+                    tc_fence_after();
+                    const uint64_t v = matrix(pairs_at + slot * 2 * CHUNK, CHUNK);
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k)
+                        tc_mma(tmem + S::O_COL + h * NR, v + k * 128, w + k * 128, KIND, b > at.b0 || k > 0);
+                    tc_commit(&c.pair_empty[slot]);
+                }
+                tc_commit(&c.o_done[i % BLOCKS]);
+            }
+        }
+        __syncwarp();
+    }
+    drain(&c.drain[1], one);
+}
+
+// Scores to weights, the running reference and sums, and the outputs. Each group of
+// four warps has half of the query rows. Thread t of a group's warp w holds tokens
+// 32 w + t / 4 + 8 h, h < 4, of a block, against the rows 8 j + 2 (t % 4) and the next
+// of its half: their references and sums stay in its registers.
+template <int NR>
+__device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_at, char *weights_at, uint32_t tmem) {
+    using S = Shape<NR>;
+    constexpr int N = NR / 8;                  // query rows of a thread
+    const int tid = threadIdx.x, lane = tid & 31, w = (tid >> 5) & 3, group = tid >> 7, quad = lane & 3;
+    const int t0 = w * 32 + lane / 4, pairs = p.latent / 128;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
+    Part *parts = reinterpret_cast<Part *>(p.workspace);
+    Joint *joints = reinterpret_cast<Joint *>(parts + 2 * p.sms);
+    const bool by_tile = p.tiles <= static_cast<int32_t>(gridDim.x);
+    auto row_of = [&](int n) { return group * (NR / 2) + 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
+    bool split_here = false;
+    Cursor at(c);
+    uint32_t i = 0;
+    long long done = c.begin;
+    bool more = at.next(p, lane);
+    if (more) load_query<NR>(p, at.tile, c, query, tid);
+    while (more) {
+        const int32_t start = at.b0 * KEYS;
+        // A row that sees nothing of this piece has an infinite reference: whatever its
+        // scores, its weights never move it, and its results are written as empty.
+        if (tid < ROWS) {
+            int32_t lim = 0;
+            if (tid < at.tile.rows) lim = p.paged ? token_len(p, (at.tile.base + tid) / p.heads) : INT32_MAX;
+            c.lim[tid] = lim;
+            c.ref[tid] = lim > start ? LOWEST : INFINITY;
+        }
+        soft_sync();
+        int32_t low = INT32_MAX;
+#pragma unroll
+        for (int r = 0; r < ROWS; r += 32) {
+            const int32_t lim = c.lim[r + lane];
+            low = min(low, lim > start ? lim : INT32_MAX);
+        }
+        low = __reduce_min_sync(FULL, low);
+        float l[N], ref[N], unit[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            l[n] = 0.0f;
+            ref[n] = c.ref[row_of(n)];
+            unit[n] = c.unit[row_of(n)];
+        }
+        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+            const uint32_t s = i % S::SCORES;
+            const int32_t token = b * KEYS + t0;
+            wait(&c.row_full[i % BLOCKS], i / BLOCKS, c);
+            const uint32_t marks = c.marks[i % BLOCKS][w] >> (lane / 4);   // bit 8 h: token h is there
+            const bool whole = __all_sync(FULL, (marks & 0x01010101u) == 0x01010101u) && (b + 1) * KEYS <= low;
+            const uint32_t scores = lanes + S::S_COL + s * NR + group * (NR / 2);
+            char *weights = weights_at + i % S::WEIGHTS * CHUNK + t0 * 128 + quad * 4;
+            float x[2][2 * N];                 // x[g][4 j + 2 h + e]: token 2 g + h, the thread's row 2 j + e
+            float most = 0.0f;                 // the block's largest score (by size): infinity and NaN are rare
+            auto load = [&]() {
+                tc_load_groups<NR / 16>(scores, x[0]);
+                tc_load_groups<NR / 16>(scores + (16u << 16), x[1]);
+                tc_fence_before();
+            };
+            // Scores in log2 units; where masked, -inf.
+            auto take = [&]() {
+                load();
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int e = 0; e < 2 * N; ++e) {
+                        float &v = x[g][e];
+                        const int n = 2 * (e >> 2) + (e & 1), h = 2 * g + ((e >> 1) & 1);
+                        most = largest(most, v, v);
+                        v *= unit[n];
+                        if (!whole) v = (marks >> 8 * h & 1u) && token + 8 * h < c.lim[row_of(n)] ? v : -INFINITY;
+                    }
+            };
+            // Weights from scores (or from the unscaled scores of a whole block), rounded once
+            // to FP16 for the tensor cores; true if one outgrew the reference.
+            auto weigh = [&](auto unscaled) -> bool {
+                __half2 top = __floats2half2_rn(0.0f, 0.0f);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int j = 0; j < N / 2; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float &a = x[g][4 * j + 2 * h], &d = x[g][4 * j + 2 * h + 1];
+                            if constexpr (decltype(unscaled)::value) {
+                                most = largest(most, a, d);
+                                a = exp2_fast(fmaf(a, unit[2 * j], -ref[2 * j]));
+                                d = exp2_fast(fmaf(d, unit[2 * j + 1], -ref[2 * j + 1]));
+                            } else {
+                                a = exp2_fast(a - ref[2 * j]);
+                                d = exp2_fast(d - ref[2 * j + 1]);
+                            }
+                            const __half2 v = __floats2half2_rn(a, d);
+                            top = __hmax2(top, v);
+                            const int at_row = (group * (N / 2) + j) ^ (t0 & 7);
+                            *reinterpret_cast<__half2 *>(weights + (2 * g + h) * 1024 + (at_row << 4)) = v;
+                        }
+                return fmaxf(__low2float(top), __high2float(top)) > 32768.0f;   // 2^MOST
+            };
+            mbar_wait(&c.s_full[s], (i / S::SCORES) & 1u, &c.abort);
+            __syncwarp();
+            if (i >= S::WEIGHTS) {             // (the weights' place is free)
+                const uint32_t last = i - S::WEIGHTS;
+                wait(&c.o_done[last % BLOCKS], last / BLOCKS, c);
+            }
+            tc_fence_after();
+            bool moved = true;
+            if (b == at.b0) {
+                take();
+            } else if (whole) {
+                load();
+                moved = soft_any(weigh(std::true_type{}));
+            } else {
+                take();
+                moved = soft_any(weigh(std::false_type{}));
+            }
+            if (moved) {
+                // New references where the rows' largest scores of this block are 2^MOST above
+                // the old ones (or the first the row sees).
+                if (b > at.b0) take();
+                float top[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const int e = 4 * (n >> 1) + (n & 1);
+                    top[n] = fmaxf(fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2]));
+                }
+                across_lanes<N>(top, [](float a, float d) { return fmaxf(a, d); });
+                const int mine = across_index<N>();
+#pragma unroll
+                for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = top[j];
+                soft_sync();
+                if (tid < NR) {
+                    const float t = fmaxf(fmaxf(c.across[0][tid], c.across[1][tid]),
+                                          fmaxf(c.across[2][tid], c.across[3][tid]));
+                    const float old = c.ref[tid];
+                    const bool move = t > old + MOST;  // (of LOWEST: t > old)
+                    c.factor[tid] = move ? exp2_fast(old - (t - BELOW)) : 1.0f;
+                    if (move) c.ref[tid] = t - BELOW;
+                }
+                soft_sync();
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    ref[n] = c.ref[row_of(n)];
+                    l[n] *= c.factor[row_of(n)];
+                }
+                weigh(std::false_type{});
+                if (b > at.b0) {
+                    wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
+                    tc_fence_after();
+                    for (int h = 0; h < pairs; ++h)
+#pragma unroll
+                        for (int v = 0; v < NR; v += 16) {
+                            if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                            float o[16], f[16];
+                            shared16(&c.factor[v], f);
+                            tc_load16(lanes + S::O_COL + h * NR + v, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f[e];
+                            latent::tc_store16(lanes + S::O_COL + h * NR + v, o);
+                        }
+                    tc_wait_st();
+                    tc_fence_before();
+                }
+            }
+            // What is NaN among a token's values (scales can be) must not reach a row that gives
+            // the token no weight through 0 x NaN: neither one that may not see it nor one whose
+            // score of it is -inf. Such a row's score of it is not finite, which marks the token,
+            // and what is not finite among its values is zeroed (a row that does weigh it has a
+            // score of NaN, so NaN weights).
+            if (__any_sync(FULL, !(most < INFINITY))) {
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    bool odd[2] = {false, false};
+#pragma unroll 1
+                    for (int j = 0; j < N / 2; ++j) {
+                        float v[4];
+                        tc_load_groups<1>(scores + (static_cast<uint32_t>(g) << 20) + 8 * j, v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int h = 2 * g + (e >> 1), r = row_of(2 * j + (e & 1));
+                            const bool seen = (marks >> 8 * h & 1u) && token + 8 * h < c.lim[r];
+                            odd[e >> 1] |= r < at.tile.rows &&
+                                           (seen ? v[e] * c.unit[r] == -INFINITY : !(fabsf(v[e]) < INFINITY));
+                        }
+                    }
+                    tc_fence_before();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        odd[h] |= __shfl_xor_sync(FULL, odd[h], 1);
+                        odd[h] |= __shfl_xor_sync(FULL, odd[h], 2);
+                        if (!odd[h]) continue;
+#pragma unroll 1
+                        for (int u = 0; u < pairs; ++u) {
+                            const uint32_t slot = (i * pairs + u) % S::PAIRS;
+                            for (int k = quad; k < 16; k += 4) {
+                                uint4 *at16 = reinterpret_cast<uint4 *>(pairs_at + slot * 2 * CHUNK + (k >> 3) * CHUNK +
+                                                                        (t0 + 8 * (2 * g + h)) * 128 + (k & 7) * 16);
+                                const uint4 v = *at16;
+                                if (half_not_finite(v.x) || half_not_finite(v.y) || half_not_finite(v.z) ||
+                                    half_not_finite(v.w))
+                                    *at16 = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                    }
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                arrive(&c.s_empty[s]);
+                arrive(&c.p_full[i % BLOCKS]);
+            }
+            // The sums are of the unrounded weights, in 32 bits.
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int e = 4 * (n >> 1) + (n & 1);
+                l[n] += (x[0][e] + x[0][e + 2]) + (x[1][e] + x[1][e + 2]);
+            }
+        }
+        // The piece is done: the next one's query rows (the last scores are read), then this
+        // one's rows, or its part of them.
+        Cursor then = at;
+        const bool again = then.next(p, lane);
+        across_lanes<N>(l, [](float a, float d) { return a + d; });
+        const int mine = across_index<N>();
+#pragma unroll
+        for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = l[j];
+        soft_sync();
+        if (again) load_query<NR>(p, then.tile, c, query, tid);
+        if (tid < NR) {
+            const bool sees = c.lim[tid] > start;
+            const float sum = c.across[0][tid] + c.across[1][tid] + c.across[2][tid] + c.across[3][tid];
+            c.l[tid] = sees ? sum : 0.0f;
+            c.factor[tid] = sees && sum != 0.0f ? 1.0f / sum : 0.0f;   // (0: an empty row, whatever its sums)
+            if (!sees) c.ref[tid] = -INFINITY;
+        }
+        soft_sync();
+        wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
+        tc_fence_after();
+        const bool direct = at.b0 == 0 && at.b1 == at.blocks;
+        if (direct) {
+            if (p.lse && tid < at.tile.rows) p.lse[at.tile.base + tid] = finished_lse(c.ref[tid], c.l[tid]);
+            // A lane has one value of 16 rows; two lanes trade theirs for pairs of one row each.
+            const bool odd = (lane & 1) != 0;
+            uint16_t *out = p.out + (static_cast<int64_t>(at.tile.base) + (lane & 1)) * p.latent + w * 32 + (lane & ~1);
+            auto write = [&](auto all) {
+                for (int h = 0; h < pairs; ++h)
+#pragma unroll
+                    for (int v = 0; v < NR; v += 16) {
+                        if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                        float o[16], f[16];
+                        shared16(&c.factor[v], f);
+                        tc_load16(lanes + S::O_COL + h * NR + v, o);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float x = f[e] == 0.0f ? 0.0f : o[e] * f[e];
+                            const float y = f[e + 1] == 0.0f ? 0.0f : o[e + 1] * f[e + 1];
+                            const float other = __shfl_xor_sync(FULL, odd ? x : y, 1);
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(odd ? other : x, odd ? y : other);
+                            if (decltype(all)::value || v + e + (lane & 1) < at.tile.rows)
+                                *reinterpret_cast<__nv_bfloat162 *>(
+                                    out + static_cast<uint32_t>((v + e) * p.latent + h * 128)) = two;
+                        }
+                    }
+            };
+            if (at.tile.rows == NR)
+                write(std::true_type{});
+            else
+                write(std::false_type{});
+        } else {
+            // In a cluster the ring is used up: this CTA's part stays there for the others to join.
+            Part &part = parts[2 * blockIdx.x + (at.b0 == 0 ? 1 : 0)];
+            float *sums = p.cluster ? reinterpret_cast<float *>(pairs_at) : part.sum;
+            if (!p.cluster && tid < NR) {
+                part.m[tid] = c.ref[tid];
+                part.l[tid] = c.l[tid];
+            }
+            for (int h = 0; h < pairs; ++h)
+#pragma unroll
+                for (int v = 0; v < NR; v += 16) {
+                    if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                    float o[16], f[16];
+                    shared16(&c.factor[v], f);
+                    tc_load16(lanes + S::O_COL + h * NR + v, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        sums[(v + e) * p.latent + h * 128 + w * 32 + lane] = f[e] == 0.0f ? 0.0f : o[e];
+                }
+        }
+        if (!p.cluster && at.b0 == 0 && tid == 0 && (by_tile || !direct)) {
+            Joint j;
+            j.tile = at.next_tile - 1;
+            j.cta = static_cast<int32_t>(blockIdx.x);
+            j.parts = direct ? 1 : static_cast<int32_t>((done - at.u0 + at.units - 1) / c.share) - j.cta + 1;
+            j.unused = 0;
+            joints[by_tile ? j.tile : j.cta] = j;
+        }
+        split_here |= at.b0 == 0 && !direct;
+        done += at.u1 - at.u0;
+        tc_fence_before();
+        soft_sync();
+        at = then;
+        more = again;
+    }
+    if (!p.cluster && !by_tile && !split_here && tid == 0) joints[blockIdx.x] = Joint{0, 0, 0, 0};
+}
+
+template <int NR>
+__global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ AttendParams p) {
+    using S = Shape<NR>;
+    extern __shared__ char raw[];
+    char *query = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    char *pairs = query + query_bytes<NR>(p.latent), *weights = pairs + S::PAIRS * 2 * CHUNK;
+    Ctrl &c = *reinterpret_cast<Ctrl *>(weights + S::WEIGHTS * CHUNK);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::PAIRS; ++s) {
+            mbar_init(&c.pair_full[s], 4);
+            mbar_init(&c.pair_empty[s], 1);
+        }
+        for (int s = 0; s < S::A_PAIRS; ++s) mbar_init(&c.a_empty[s], 1);
+        for (int s = 0; s < KEY_SLOTS; ++s) {
+            mbar_init(&c.key_full[s], 8);
+            mbar_init(&c.key_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&c.s_full[s], 1);
+            mbar_init(&c.s_empty[s], SOFT / 32);
+            mbar_init(&c.drain[s], 1);
+        }
+        for (int s = 0; s < BLOCKS; ++s) {
+            mbar_init(&c.row_full[s], 4);
+            mbar_init(&c.p_full[s], SOFT / 32);
+            mbar_init(&c.o_done[s], 1);
+        }
+        mbar_init(&c.q_full, SOFT / 32);
+        c.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == NT / 32 - 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&c.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    grid_dependents_release();
+    grid_dependency_wait();
+    make_schedule<KEYS, NT>(p, c);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    if (warp < SOFT / 32) soften<NR>(p, c, query, pairs, weights, tmem);
+    else if (warp < (SOFT + LOAD) / 32) load_rows<NR>(p, c, pairs, tmem);
+    else if (warp < NT / 32 - 1) multiply_scores<NR>(p, c, smem_addr(query), tmem);
+    else multiply_sums<NR>(p, c, smem_addr(pairs), smem_addr(weights), tmem);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == NT / 32 - 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+    if (p.cluster > 1) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        static_assert(CHUNK >= ROWS * MAX_CLUSTER * sizeof(float));
+        if (c.ranks > 1) join_cluster<NT>(p, c, pairs, reinterpret_cast<float(*)[MAX_CLUSTER]>(weights));
+        __syncwarp();
+        cluster_arrive();                      // no CTA leaves while others read its part
+        cluster_wait();
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+constexpr Costs COSTS = {1, 3, 3, 2, 1};
+
+Device g_device[64];
+
+template <int NR>
+const void *attend_fn() {
+    return reinterpret_cast<const void *>(&attend4_kernel<NR>);
+}
+
+cudaError_t device(Device *&out) {
+    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, NT, out,
+                  [](Device &) { return cudaSuccess; });
+}
+
+}  // namespace
+
+int64_t workspace4_bytes() {
+    Device *d = nullptr;
+    if (device(d) != cudaSuccess) return 0;
+    return static_cast<int64_t>(d->sms) * static_cast<int64_t>(2 * sizeof(Part) + sizeof(Joint));
+}
+
+cudaError_t status_attend4(uint32_t *v, bool clear) { return unit_status(v, clear); }
+
+int64_t attend4_workspace(AttendParams p) {
+    Device *d = nullptr;
+    if (device(d) != cudaSuccess) return -1;
+    if (p.rows_per_request > p.tokens) p.rows_per_request = p.tokens;
+    return deal<KEYS>(p, *d, COSTS).cluster ? 0 : workspace4_bytes();
+}
+
+cudaError_t launch_attend4(AttendParams p, cudaStream_t stream) {
+    Device *d = nullptr;
+    cudaError_t e = device(d);
+    if (e != cudaSuccess) return e;
+    if (p.rows_per_request > p.tokens) p.rows_per_request = p.tokens;   // (one request)
+    const Deal plan = deal<KEYS>(p, *d, COSTS);
+    p.tiles_per_request = plan.tiles_per_request;
+    p.tiles = static_cast<int32_t>(plan.tiles);
+    p.cluster = plan.cluster;
+    p.tile_cost = plan.tiles > d->sms ? COSTS.tile : 0;
+    p.min_share = COSTS.min_share;
+    p.sms = d->sms;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan.grid, 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    void *args[] = {&p};
+    e = cudaLaunchKernelExC(&cfg, plan.nr == 16 ? attend_fn<16>() : plan.nr == 32 ? attend_fn<32>() : attend_fn<64>(),
+                            args);
+    if (e != cudaSuccess || p.cluster || plan.blocks <= 1) return e;   // tiles of one block are never split
+    return launch_join(p, plan.grid, plan.nr, stream);
+}
+
+}  // namespace topk::latent

@@ -88,6 +88,7 @@ cudaError_t status_one(uint32_t *v, bool clear);
 cudaError_t status_ordered(uint32_t *v, bool clear);
 namespace latent {
 cudaError_t status_attend(uint32_t *v, bool clear);   // latent_attend.cu
+cudaError_t status_attend4(uint32_t *v, bool clear);  // latent4_attend.cu
 }
 
 }  // namespace topk

@@ -10,6 +10,8 @@ are refused.
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 
 import exact_bf16_top_gb300 as _package
@@ -27,6 +29,21 @@ _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 # has neither, nor a tensor that gets as far as their use.)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+class Form(NamedTuple):
+    """How a cache holds its rows, and the entry points that take it."""
+    dtype: torch.dtype
+    granule: int            # a row's stride is a multiple of this many elements
+    columns: dict           # elements of a row by latent
+    arguments: type
+    append: str
+    attend: tuple           # over selected rows, over pages
+    workspace: str
+
+
+BF16 = Form(_BF16, 8, {n: n + ROPE for n in LATENTS}, Append, "latent_bf16_append",
+            ("latent_bf16_attend_selected", "latent_bf16_attend_paged"), "latent_bf16_attend_workspace")
 
 
 def _refuse(**tensors):
@@ -56,9 +73,9 @@ def _check_stream(stream, dev: int):
         raise ValueError(f"stream must be one of cuda:{dev}, where the tensors are")
 
 
-def _row_stride(rows: int, width: int, stride: int) -> int:
+def _row_stride(rows: int, width: int, stride: int, granule: int = 8) -> int:
     """Row stride of a 2-D tensor; a single row's is immaterial, its width rounded up is given."""
-    return stride if rows > 1 else -(-width // 8) * 8
+    return stride if rows > 1 else -(-width // granule) * granule
 
 
 def _head_strides(t) -> tuple[int, int]:
@@ -87,79 +104,8 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
     alone. Other overlaps of what is written with what is read are not allowed.
     Rows may be strided: strides multiples of 8, 16-byte aligned.
     """
-    try:
-        dev = cache.get_device()
-        rows, dim = cache.shape
-        cache_stride, c1 = cache.stride()
-        tokens, width = latent.shape
-        latent_stride, l1 = latent.stride()
-        key_stride, k1 = key_rope.stride()
-        fine = (dev >= 0 and latent.get_device() == key_rope.get_device() == positions.get_device() == dev
-                and cos_sin.get_device() == slots.get_device() == dev
-                and cache.dtype is latent.dtype is key_rope.dtype is _BF16
-                and positions.dtype is slots.dtype is _I32 and cos_sin.dtype is _F32
-                and c1 == l1 == k1 == 1 and positions.is_contiguous() and slots.is_contiguous()
-                and positions.dim() == slots.dim() == 1 and cos_sin.dim() == 2)
-    except (AttributeError, ValueError):
-        fine = False
-    if not fine:
-        _refuse(cache=(cache, _BF16, 2), latent=(latent, _BF16, 2), key_rope=(key_rope, _BF16, 2),
-                positions=(positions, _I32, 1), cos_sin=(cos_sin, _F32, 2), slots=(slots, _I32, 1))
-    if rows > MAX_ROWS or tokens > MAX_ROWS:
-        raise ValueError(f"at most {MAX_ROWS} cache rows and tokens")
-    if width not in LATENTS or dim != width + ROPE:
-        raise ValueError(f"latent must have one of {LATENTS} columns and cache {ROPE} more")
-    if key_rope.shape != (tokens, ROPE) or positions.shape[0] != tokens or slots.shape[0] != tokens:
-        raise ValueError("key_rope, positions and slots must have one row per token (key_rope of 64)")
-    positions_known, angles = cos_sin.shape
-    if angles != ROPE or positions_known < 1 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be contiguous [positions, 64]")
-    weight_ptr = None
-    if weight is not None:
-        if not (isinstance(weight, torch.Tensor) and weight.get_device() == dev and weight.dtype is _BF16
-                and weight.dim() == 1 and weight.is_contiguous()):
-            _refuse(cache=(cache, _BF16, 2), weight=(weight, _BF16, 1))
-        if weight.shape[0] != width:
-            raise ValueError("weight must have one entry per latent column")
-        weight_ptr = weight.data_ptr()
-    if (query is None) != (query_rope is None):
-        raise ValueError("query and query_rope come together")
-    if query is None:
-        heads, r, q = 0, (None, 0, 0), (None, 0, 0)
-    else:
-        if not (isinstance(query, torch.Tensor) and isinstance(query_rope, torch.Tensor)
-                and query.get_device() == query_rope.get_device() == dev
-                and query.dtype is query_rope.dtype is _BF16 and query.dim() == query_rope.dim() == 3
-                and query.stride(2) == query_rope.stride(2) == 1):
-            _refuse(cache=(cache, _BF16, 2), query=(query, _BF16, 3), query_rope=(query_rope, _BF16, 3))
-        heads = query.shape[1]
-        if query.shape != (tokens, heads, dim) or query_rope.shape != (tokens, heads, ROPE):
-            raise ValueError("query must be [tokens, heads, latent + 64] and query_rope [tokens, heads, 64]")
-        if not 1 <= heads <= MAX_HEADS:
-            raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
-        r = (query_rope.data_ptr(), *_head_strides(query_rope))
-        q = (query.data_ptr(), *_head_strides(query))
-    args = Append(cache.data_ptr(), _row_stride(rows, dim, cache_stride), latent.data_ptr(),
-                  _row_stride(tokens, width, latent_stride), key_rope.data_ptr(),
-                  _row_stride(tokens, ROPE, key_stride), positions.data_ptr(), cos_sin.data_ptr(),
-                  slots.data_ptr(), weight_ptr, *r, *q, rows, tokens, width, heads, positions_known,
-                  1 if interleaved else 0, eps)
-    if (cache.requires_grad or latent.requires_grad or key_rope.requires_grad or cos_sin.requires_grad
-            or (weight is not None and weight.requires_grad)
-            or (query is not None and (query.requires_grad or query_rope.requires_grad))):
-        _check_no_grad()
-    if stream is not None:
-        _check_stream(stream, dev)
-    function = (_package._lib or load()).latent_bf16_append
-    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if _raw_device() == dev:
-        status = function(args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = function(args, handle)
-    if status:
-        raise TopkError(status)
-    return cache
+    return _append(BF16, cache, latent, key_rope, positions, cos_sin, slots, weight, eps, interleaved, query_rope, query,
+                   stream)
 
 
 def latent_attend_selected(query, cache, selected, scale: float, *, latent: int = 512, out=None, lse=False,
@@ -175,22 +121,7 @@ def latent_attend_selected(query, cache, selected, scale: float, *, latent: int 
     sees nothing), else None is returned for it. workspace: None, or scratch
     from latent_workspace() that no other call uses at the same time.
     """
-    try:
-        dev = query.get_device()
-        lists, k = selected.shape
-        stride, s1 = selected.stride()
-        fine = (selected.get_device() == dev and selected.dtype is _I32 and (s1 == 1 or k <= 1))
-    except (AttributeError, ValueError):
-        fine = False
-    if not fine:
-        _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2), selected=(selected, _I32, 2))
-    if lists != query.shape[0]:
-        raise ValueError("selected must have one row per query token")
-    if k > MAX_ROWS:
-        raise ValueError(f"selected must have at most {MAX_ROWS} entries per row")
-    return _attend(0, dev, query, cache, scale, latent, out, lse, workspace, stream,
-                   (selected.data_ptr() if k else None, stride if lists > 1 else k, None, None),
-                   (k, 0, 0, 1, 1, 1))
+    return _selected(BF16, query, cache, selected, scale, latent, out, lse, workspace, stream)
 
 
 def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, page_size: int = 64,
@@ -205,6 +136,45 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     chunk of new tokens after n others has valid_len n + 1, n + 2, ...; a padded
     token has 0. Other arguments and results as latent_attend_selected.
     """
+    return _paged(BF16, query, cache, valid_len, block_table, scale, page_size, block_rows, rows_per_request, width,
+                  latent, out, lse, workspace, stream)
+
+
+def latent_workspace(device=None):
+    """Scratch that is enough for any one attention call at a time on a device (uint8)."""
+    return _workspace(device, "latent_bf16_workspace_bytes")
+
+
+def _workspace(device, function):
+    dev = torch.cuda.current_device() if device is None else torch.empty(0, device=device).get_device()
+    with torch.cuda.device(dev):
+        n = getattr(load(), function)()
+    if n <= 0:
+        raise RuntimeError("no usable CUDA device")
+    return torch.empty(n, dtype=_U8, device=torch.device("cuda", dev))
+
+
+def _selected(form, query, cache, selected, scale, latent, out, lse, workspace, stream):
+    try:
+        dev = query.get_device()
+        lists, k = selected.shape
+        stride, s1 = selected.stride()
+        fine = (selected.get_device() == dev and selected.dtype is _I32 and (s1 == 1 or k <= 1))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse(query=(query, _BF16, 3), cache=(cache, form.dtype, 2), selected=(selected, _I32, 2))
+    if lists != query.shape[0]:
+        raise ValueError("selected must have one row per query token")
+    if k > MAX_ROWS:
+        raise ValueError(f"selected must have at most {MAX_ROWS} entries per row")
+    return _attend(form, 0, dev, query, cache, scale, latent, out, lse, workspace, stream,
+                   (selected.data_ptr() if k else None, stride if lists > 1 else k, None, None),
+                   (k, 0, 0, 1, 1, 1))
+
+
+def _paged(form, query, cache, valid_len, block_table, scale, page_size, block_rows, rows_per_request, width, latent, out,
+           lse, workspace, stream):
     try:
         dev = query.get_device()
         requests, pages = block_table.shape
@@ -215,7 +185,7 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     except (AttributeError, ValueError):
         fine = False
     if not fine:
-        _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2), valid_len=(valid_len, _I32, 1),
+        _refuse(query=(query, _BF16, 3), cache=(cache, form.dtype, 2), valid_len=(valid_len, _I32, 1),
                 block_table=(block_table, _I32, 2))
     page_size, rows_per_request = int(page_size), int(rows_per_request)
     if page_size < 1 or page_size & (page_size - 1) or rows_per_request < 1:
@@ -229,36 +199,27 @@ def latent_attend_paged(query, cache, valid_len, block_table, scale: float, *, p
     block_rows = page_size if block_rows is None else int(block_rows)
     if max(width, stride, rows_per_request, page_size, abs(block_rows)) > MAX_ROWS:
         raise ValueError("a length, stride or count passes 31 bits")
-    return _attend(1, dev, query, cache, scale, latent, out, lse, workspace, stream,
+    return _attend(form, 1, dev, query, cache, scale, latent, out, lse, workspace, stream,
                    (None, 0, valid_len.data_ptr(), block_table.data_ptr()),
                    (0, width, stride if requests > 1 else pages, page_size, block_rows, rows_per_request))
 
 
-def latent_workspace(device=None):
-    """Scratch that is enough for any one attention call at a time on a device (uint8)."""
-    dev = torch.cuda.current_device() if device is None else torch.empty(0, device=device).get_device()
-    with torch.cuda.device(dev):
-        n = load().latent_bf16_workspace_bytes()
-    if n <= 0:
-        raise RuntimeError("no usable CUDA device")
-    return torch.empty(n, dtype=_U8, device=torch.device("cuda", dev))
-
-
-def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes):
+def _attend(form, paged, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes):
     try:
         tokens, heads, dim = query.shape
-        rows, cache_dim = cache.shape
+        rows, columns = cache.shape
         cache_stride, c1 = cache.stride()
-        fine = (dev >= 0 and cache.get_device() == dev and query.dtype is cache.dtype is _BF16
+        fine = (dev >= 0 and cache.get_device() == dev and query.dtype is _BF16 and cache.dtype is form.dtype
                 and query.stride(2) == 1 and c1 == 1)
     except (AttributeError, ValueError):
         fine = False
     if not fine:
-        _refuse(query=(query, _BF16, 3), cache=(cache, _BF16, 2))
+        _refuse(query=(query, _BF16, 3), cache=(cache, form.dtype, 2))
     if rows > MAX_ROWS:
         raise ValueError(f"cache must have at most {MAX_ROWS} rows")
-    if latent not in LATENTS or dim != latent + ROPE or cache_dim != dim:
-        raise ValueError(f"latent must be one of {LATENTS}, query and cache rows latent + {ROPE} values")
+    if form.columns.get(latent) != columns or dim != latent + ROPE:
+        raise ValueError(f"latent must be one of {LATENTS}, query rows latent + {ROPE} values, cache rows one of "
+                         f"{[*form.columns.values()]} columns")
     if not 1 <= heads <= MAX_HEADS:
         raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
     if query.requires_grad or cache.requires_grad:
@@ -267,10 +228,11 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
         _check_stream(stream, dev)
     if _raw_device() != dev:
         with torch.cuda.device(dev):
-            return _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers, sizes)
+            return _attend(form, paged, dev, query, cache, scale, latent, out, lse, workspace, stream, pointers,
+                           sizes)
     if stream is not None and stream != torch.cuda.current_stream(dev):
         with torch.cuda.stream(stream):     # new tensors belong to the stream that uses them
-            return _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, None, pointers, sizes)
+            return _attend(form, paged, dev, query, cache, scale, latent, out, lse, workspace, None, pointers, sizes)
     device = query.device
     if out is None:
         out = torch.empty((tokens, heads, latent), dtype=_BF16, device=device)
@@ -287,16 +249,94 @@ def _attend(paged, dev, query, cache, scale, latent, out, lse, workspace, stream
     lse_ptr = None if lse is None else lse.data_ptr()
     if tokens:
         args = Attend(query.data_ptr(), *_head_strides(query), cache.data_ptr(),
-                      _row_stride(rows, dim, cache_stride), *pointers, out.data_ptr(), lse_ptr, None, 0, rows,
+                      _row_stride(rows, columns, cache_stride, form.granule), *pointers, out.data_ptr(), lse_ptr, None, 0, rows,
                       tokens, heads, latent, *sizes, scale)
         lib = _package._lib or load()
         if workspace is None:
-            n = lib.latent_bf16_attend_workspace(args, paged)
+            n = getattr(lib, form.workspace)(args, paged)
             if n > 0:
                 workspace = torch.empty(n, dtype=_U8, device=device)
         if workspace is not None:
             args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
-        status = (lib.latent_bf16_attend_paged if paged else lib.latent_bf16_attend_selected)(args, _raw_stream(dev))
+        status = getattr(lib, form.attend[paged])(args, _raw_stream(dev))
         if status:
             raise TopkError(status)
     return out, lse
+
+
+def _append(form, cache, latent, key_rope, positions, cos_sin, slots, weight, eps, interleaved, query_rope, query,
+            stream):
+    try:
+        dev = cache.get_device()
+        rows, columns = cache.shape
+        cache_stride, c1 = cache.stride()
+        tokens, width = latent.shape
+        latent_stride, l1 = latent.stride()
+        key_stride, k1 = key_rope.stride()
+        fine = (dev >= 0 and latent.get_device() == key_rope.get_device() == positions.get_device() == dev
+                and cos_sin.get_device() == slots.get_device() == dev
+                and cache.dtype is form.dtype and latent.dtype is key_rope.dtype is _BF16
+                and positions.dtype is slots.dtype is _I32 and cos_sin.dtype is _F32
+                and c1 == l1 == k1 == 1 and positions.is_contiguous() and slots.is_contiguous()
+                and positions.dim() == slots.dim() == 1 and cos_sin.dim() == 2)
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse(cache=(cache, form.dtype, 2), latent=(latent, _BF16, 2), key_rope=(key_rope, _BF16, 2),
+                positions=(positions, _I32, 1), cos_sin=(cos_sin, _F32, 2), slots=(slots, _I32, 1))
+    if rows > MAX_ROWS or tokens > MAX_ROWS:
+        raise ValueError(f"at most {MAX_ROWS} cache rows and tokens")
+    if form.columns.get(width) != columns:
+        raise ValueError(f"latent must have one of {LATENTS} columns and cache {[*form.columns.values()]}")
+    dim = width + ROPE
+    if key_rope.shape != (tokens, ROPE) or positions.shape[0] != tokens or slots.shape[0] != tokens:
+        raise ValueError("key_rope, positions and slots must have one row per token (key_rope of 64)")
+    positions_known, angles = cos_sin.shape
+    if angles != ROPE or positions_known < 1 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous [positions, 64]")
+    weight_ptr = None
+    if weight is not None:
+        if not (isinstance(weight, torch.Tensor) and weight.get_device() == dev and weight.dtype is _BF16
+                and weight.dim() == 1 and weight.is_contiguous()):
+            _refuse(cache=(cache, form.dtype, 2), weight=(weight, _BF16, 1))
+        if weight.shape[0] != width:
+            raise ValueError("weight must have one entry per latent column")
+        weight_ptr = weight.data_ptr()
+    if (query is None) != (query_rope is None):
+        raise ValueError("query and query_rope come together")
+    if query is None:
+        heads, r, q = 0, (None, 0, 0), (None, 0, 0)
+    else:
+        if not (isinstance(query, torch.Tensor) and isinstance(query_rope, torch.Tensor)
+                and query.get_device() == query_rope.get_device() == dev
+                and query.dtype is query_rope.dtype is _BF16 and query.dim() == query_rope.dim() == 3
+                and query.stride(2) == query_rope.stride(2) == 1):
+            _refuse(cache=(cache, form.dtype, 2), query=(query, _BF16, 3), query_rope=(query_rope, _BF16, 3))
+        heads = query.shape[1]
+        if query.shape != (tokens, heads, dim) or query_rope.shape != (tokens, heads, ROPE):
+            raise ValueError("query must be [tokens, heads, latent + 64] and query_rope [tokens, heads, 64]")
+        if not 1 <= heads <= MAX_HEADS:
+            raise ValueError(f"heads must be in [1, {MAX_HEADS}]")
+        r = (query_rope.data_ptr(), *_head_strides(query_rope))
+        q = (query.data_ptr(), *_head_strides(query))
+    args = form.arguments(cache.data_ptr(), _row_stride(rows, columns, cache_stride, form.granule), latent.data_ptr(),
+                          _row_stride(tokens, width, latent_stride), key_rope.data_ptr(),
+                          _row_stride(tokens, ROPE, key_stride), positions.data_ptr(), cos_sin.data_ptr(),
+                          slots.data_ptr(), weight_ptr, *r, *q, rows, tokens, width, heads, positions_known,
+                          1 if interleaved else 0, eps)
+    if (cache.requires_grad or latent.requires_grad or key_rope.requires_grad or cos_sin.requires_grad
+            or (weight is not None and weight.requires_grad)
+            or (query is not None and (query.requires_grad or query_rope.requires_grad))):
+        _check_no_grad()
+    if stream is not None:
+        _check_stream(stream, dev)
+    function = getattr(_package._lib or load(), form.append)
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if _raw_device() == dev:
+        status = function(args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = function(args, handle)
+    if status:
+        raise TopkError(status)
+    return cache
