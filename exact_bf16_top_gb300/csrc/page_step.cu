@@ -24,6 +24,7 @@ struct Params {
 
 struct Request {
     int32_t length, add, owned, need, back;  // tokens it has and asks for; pages it holds, needs, gives back
+    bool done;
 };
 
 __device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t shift) {
@@ -38,7 +39,8 @@ __device__ __forceinline__ Request request_at(const Params &p, int32_t r) {
     x.add = min(max(ask, 0), p.a.rows_per_request);
     if (x.add > width - x.length) x.add = 0;
     x.need = pages_of(x.length + x.add, p.page_shift) - x.owned;
-    x.back = ask < 0 ? x.owned : 0;
+    x.done = ask < 0;
+    x.back = x.done ? x.owned : 0;
     return x;
 }
 
@@ -49,7 +51,7 @@ __device__ __forceinline__ Request request_at(const Params &p, int32_t r) {
 // place without scratch of its own.
 // Bound by latency: two rounds of loads, a scan and the launch.
 __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ Params p) {
-    extern __shared__ int32_t own[];         // the CTA's requests: next length, first page given back
+    extern __shared__ int32_t own[];         // the CTA's requests: next length, or ~ the place of the first page back
     __shared__ uint32_t s_first[NT];
     __shared__ int32_t s_length[NT], s_add[NT], s_need[NT / 32], s_back[NT / 32], s_taken;
     const page_step_t &a = p.a;
@@ -96,8 +98,7 @@ __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ P
         s_add[tid] = add;
         if (r >= r0 && r < r1) {
             a.granted[r] = add;
-            own[r - r0] = x.back != 0 || a.new_tokens[r] < 0 ? 0 : x.length + add;
-            own[p.slice + r - r0] = back - x.back;
+            own[r - r0] = x.done ? ~(back - x.back) : x.length + add;
         }
         __syncthreads();
         const long long from = static_cast<long long>(base) * q;
@@ -130,19 +131,28 @@ __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ P
         cluster_wait();
     }
     const long long left = count - s_taken;
-    for (int32_t r = r0 + warp; r < r1; r += NT / 32) {
-        const int32_t next = own[r - r0];
-        const long long first = left + own[p.slice + r - r0];
-        int32_t back = 0;
-        if (lane == 0 && next == 0 && a.new_tokens[r] < 0) {
-            const int32_t width = a.pages << p.page_shift;
-            back = pages_of(min(max(a.lengths[r], 0), width), p.page_shift);
+    // Lengths, a request per thread; then a warp's finished requests one by one.
+    for (int32_t base = r0 + warp * 32; base < r1; base += NT) {
+        const int32_t r = base + lane;
+        int32_t back = 0, first = 0;
+        if (r < r1) {
+            const int32_t next = own[r - r0];
+            if (next < 0) {
+                const int32_t width = a.pages << p.page_shift;
+                back = pages_of(min(max(a.lengths[r], 0), width), p.page_shift);
+                first = ~next;
+            }
+            a.next_lengths[r] = max(next, 0);
         }
-        back = __shfl_sync(FULL, back, 0);
-        for (int32_t i = lane; i < back; i += 32)
-            if (first + i < a.free_size) a.free_pages[first + i] = a.block_table[r * a.table_stride + i];
-        __syncwarp();
-        if (lane == 0) a.next_lengths[r] = next;
+        for (uint32_t m = __ballot_sync(FULL, back > 0); m; m &= m - 1) {
+            const int from = __ffs(m) - 1;
+            const int32_t n = __shfl_sync(FULL, back, from);
+            const long long to = left + __shfl_sync(FULL, first, from);
+            const int32_t *row = a.block_table + (base + from) * a.table_stride;
+#pragma unroll 4
+            for (int32_t i = lane; i < n; i += 32)
+                if (to + i < a.free_size) a.free_pages[to + i] = row[i];
+        }
     }
     if (rank == 0 && tid == 0)
         a.next_free_count[0] = static_cast<int32_t>(min(left + back_before, static_cast<long long>(a.free_size)));
@@ -196,7 +206,7 @@ extern "C" topk_status_t page_step(const page_step_t *args, void *stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(NT, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.slice) * 8;
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.slice) * 4;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
