@@ -5,11 +5,11 @@
 // cache rows become FP16 on their way, once for both products:
 //     scores (128 tokens x rows) = K Q^T,  weights = 2^(scores - reference),
 //     sums (values x rows)      += V^T weights,   V the latent part of K.
-// A thread takes 128 values of a row from memory to registers, makes FP16 of them (the
-// conversion and one product are exact) and writes them twice: into tensor memory,
-// where they are the scores' left operand, and into shared memory, where, read across
-// rows, they are the sums'. So shared memory, which bounds the BF16 kernel, gives
-// each block away once instead of twice, and the scores run at 128 rows a step.
+// A thread makes FP16 of 128 values of a row (the conversion and one product are exact)
+// and writes them into tensor memory, where they are the scores' left operand; others
+// copy them from there into shared memory, where, read across rows, they are the
+// sums'. So shared memory, which bounds the BF16 kernel, gives each block away once
+// instead of twice, and the scores run at 128 rows a step, ahead of the sums.
 // The key part stays BF16 and only goes to tensor memory. Warps have one job each
 // (softmax, rows, issue of either product) and meet at mbarriers only.
 
@@ -24,8 +24,9 @@ namespace topk::latent {
 namespace {
 
 constexpr int SOFT = 256;                    // warps 0 to 7: query rows, softmax and outputs, in two groups
-constexpr int LOAD = 256;                    // warps 8 to 15: cache rows, in two groups
-constexpr int NT = SOFT + LOAD + 64;         // warps 16 and 17: the tensor cores (scores, sums)
+constexpr int LOAD = 128;                    // warps 8 to 11: cache rows, as FP16 into tensor memory
+constexpr int COPY = 128;                    // warps 12 to 15: their values from there into shared memory
+constexpr int NT = SOFT + LOAD + COPY + 64;  // warps 16 and 17: the tensor cores (scores, sums)
 constexpr int KEYS = 128;                    // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
 constexpr int BLOCKS = 8;                    // blocks that have marks and barriers of their own: more than are
@@ -37,19 +38,26 @@ constexpr uint32_t FULL = 0xFFFFFFFFu;
 // FP16 rounds away below 2^-25 is less than 2^-36 of it.
 constexpr float BELOW = 11.0f, MOST = 15.0f;
 
+constexpr int UNIT = 32 * 64;                // bytes of a unit as it comes: 64 bytes of a warp's 32 rows
+constexpr int SCALES = 32 * 32;              // bytes of a warp's rows' scales
+
 // How a tile of NR rows uses the memories: pairs of 64-value chunks in shared memory
-// (sums) and tensor memory (scores), blocks of weights and of scores.
+// (sums) and tensor memory (scores), blocks of weights and of scores, units on their way.
 template <int NR>
 struct Shape {
-    static constexpr int PAIRS = NR == 64 ? 4 : 5, A_PAIRS = NR == 64 ? 2 : 4;
-    static constexpr int WEIGHTS = NR == 16 ? 2 : 1, SCORES = NR == 64 ? 1 : 2;
+    static constexpr int PAIRS = NR == 64 ? 3 : 4, A_PAIRS = NR == 64 ? 2 : 4;
+    static constexpr int WEIGHTS = NR == 16 ? 2 : 1, SCORES = NR == 64 ? 1 : 2, UNITS = NR == 64 ? 3 : 4;
     static constexpr uint32_t O_COL = 0, S_COL = 4 * NR, A_COL = S_COL + SCORES * NR, K_COL = A_COL + A_PAIRS * 64;
+    static constexpr uint32_t RAW = LOAD / 32 * (UNITS * UNIT + 2 * SCALES);
+    static constexpr uint32_t RINGS = (2 * PAIRS + WEIGHTS) * CHUNK + RAW;
     static_assert(K_COL + KEY_SLOTS * 32 <= 512);
+    // A cluster's parts lie where the rings were, and what weighs them behind.
+    static_assert(RINGS >= NR * LATENT_MAX * sizeof(float) + ROWS * MAX_CLUSTER * sizeof(float));
 };
 
 struct Ctrl : Schedule<NT> {
-    u64 pair_full[5], pair_empty[5];           // a pair of chunks is in / its sums are added
-    u64 a_empty[4];                            // a pair's scores are added
+    u64 pair_full[4], pair_empty[4];           // a pair of chunks is in / its sums are added
+    u64 a_full[4], a_empty[4];                 // a pair is in tensor memory / its scores are added and it is copied
     u64 key_full[KEY_SLOTS], key_empty[KEY_SLOTS];
     u64 s_full[2], s_empty[2];                 // scores written / read
     u64 row_full[BLOCKS];                      // a block's marks are in
@@ -65,6 +73,7 @@ struct Ctrl : Schedule<NT> {
     int32_t lim[ROWS];                         // tokens a row may see
     float across[4][ROWS];
     uint32_t marks[BLOCKS][KEYS / 32];         // which rows of a block there are
+    uint32_t bad[4][KEYS / 32];                // which rows of a pair in tensor memory have a scale of NaN
 };
 
 using Cursor = CursorOf<KEYS>;
@@ -76,8 +85,7 @@ __host__ __device__ constexpr uint32_t query_bytes(int latent) {
 }
 template <int NR>
 constexpr bool fits() {
-    return 1024 + query_bytes<NR>(LATENT_MAX) + (2 * Shape<NR>::PAIRS + Shape<NR>::WEIGHTS) * CHUNK + sizeof(Ctrl) <=
-           SMEM;
+    return 1024 + query_bytes<NR>(LATENT_MAX) + Shape<NR>::RINGS + sizeof(Ctrl) <= SMEM;
 }
 static_assert(fits<16>() && fits<32>() && fits<64>());
 
@@ -110,8 +118,9 @@ __device__ __forceinline__ bool soft_any(bool v) {
     return r != 0;
 }
 
-__device__ __forceinline__ bool half_not_finite(uint32_t w) {
-    return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
+// A pair of FP16 values, zero where not finite.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+    return w & ((w & 0x7C00u) == 0x7C00u ? 0xFFFF0000u : FULL) & ((w & 0x7C000000u) == 0x7C000000u ? 0xFFFFu : FULL);
 }
 
 // Eight codes as FP16, times their scale: exact.
@@ -129,10 +138,23 @@ __device__ __forceinline__ void from_codes(uint32_t w, __half2 scale, uint32_t *
     }
 }
 
-__device__ __forceinline__ void load32(const uint8_t *from, uint32_t *v) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(from));
+__device__ __forceinline__ uint4 shared_vec(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// 64 columns of this warp's 32 lanes, one lane per thread.
+__device__ __forceinline__ void tc_load64(uint32_t addr, uint32_t (&r)[64]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[16 * q]), "=r"(r[16 * q + 1]), "=r"(r[16 * q + 2]), "=r"(r[16 * q + 3]), "=r"(r[16 * q + 4]),
+              "=r"(r[16 * q + 5]), "=r"(r[16 * q + 6]), "=r"(r[16 * q + 7]), "=r"(r[16 * q + 8]),
+              "=r"(r[16 * q + 9]), "=r"(r[16 * q + 10]), "=r"(r[16 * q + 11]), "=r"(r[16 * q + 12]),
+              "=r"(r[16 * q + 13]), "=r"(r[16 * q + 14]), "=r"(r[16 * q + 15])
+            : "r"(addr + 16 * q));
 }
 
 // ------------------------------------------------------------------ the warps' parts
@@ -193,25 +215,24 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
     if ((tid & 31) == 0) arrive(&c.q_full);
 }
 
-// A unit of a block's rows: 64 bytes of each, that is 128 values with their eight
-// scales, or one half of the key part.
-struct Raw {
-    uint32_t v[16];
-    uint2 scales;
-    bool there;
-};
-
-// The units of all blocks in order; a group of four warps takes every other one, and a
-// lane always the same row of a block (as tensor memory wants it). Row numbers are
-// read one unit before the rows, rows two units before they are converted.
+// Cache rows on their way to the tensor cores: a warp has a quarter of every block's
+// rows, as tensor memory wants it, and a ring of its own for what comes: units of 64
+// bytes of each row (128 values, or half of the key part) one after another, a few of
+// them on their way while one is converted, a lane its own row of it. (Rows read
+// straight into registers, a row a lane, were held up at 7 KB on their way per SM: the
+// first-level cache, small beside this much shared memory, keeps a line of 128 bytes
+// for each 32 that come. 32 requests x 16 heads x 16384: 118 us.)
 struct Feed {
     Cursor at;
     const int32_t *list = nullptr;
-    int32_t len = 0, b = 0, j = 0, fetched = -1;
-    int u, of;                                 // unit and units of a block
+    int32_t len = 0, b = 0, fetched = -1;
+    int u = 0, units;                          // the unit that is sent for next, and units of a block
+    uint32_t i = 0, slot = 0;                  // its block and its place
     bool live;
-    __device__ __forceinline__ Feed(const AttendParams &p, const Ctrl &c, int first, int units, int lane, int row)
-        : at(c), u(first), of(units) {
+    const uint8_t *src[4];                     // where this lane's copies come from: rows 8 m + lane / 4
+    bool on[4];
+    __device__ __forceinline__ Feed(const AttendParams &p, const Ctrl &c, int lane, int row)
+        : at(c), units(p.latent / 128 + 2) {
         live = piece(p, lane);
         if (live) fetch(p, row);
     }
@@ -224,103 +245,173 @@ struct Feed {
         return true;
     }
     __device__ __forceinline__ void fetch(const AttendParams &p, int row) {
-        j = b * KEYS + row;
+        const int32_t j = b * KEYS + row;
         fetched = j < len ? __ldg(list + (p.paged ? j >> p.page_shift : j)) : -1;
     }
-    // Loads the unit whose row number was fetched, and fetches the next one's.
-    __device__ __forceinline__ bool load(const AttendParams &p, Raw &r, int lane, int row) {
-        if (!live) return false;
-        const int64_t v = p.paged ? static_cast<int64_t>(fetched) * p.block_rows + (j & ((1 << p.page_shift) - 1))
-                                  : fetched;
-        r.there = fetched >= 0 && v < p.cache_rows;
-        if (r.there) {
-            const uint8_t *from = static_cast<const uint8_t *>(p.cache) + v * p.cache_stride;
-            load32(from + u * 64, r.v);
-            load32(from + u * 64 + 32, r.v + 8);
-            if (u < of - 2) r.scales = __ldg(reinterpret_cast<const uint2 *>(from + p.latent / 2 + 2 * LATENT_ROPE) + u);
-        } else {
+    // Sends for the next unit (a group of copies, empty behind the last one).
+    template <int SLOTS>
+    __device__ __forceinline__ void send(const AttendParams &p, Ctrl &c, uint32_t ring, int lane, int quarter) {
+        const int row = quarter * 32 + lane;
+        if (live) {
+            if (u == 0) {
+                // A new block: its rows' places, and their scales; the next block's row numbers.
+                const int64_t v = p.paged ? static_cast<int64_t>(fetched) * p.block_rows +
+                                                ((b * KEYS + row) & ((1 << p.page_shift) - 1))
+                                          : fetched;
+                const bool there = fetched >= 0 && v < p.cache_rows;
+                const long long offset = there ? v * p.cache_stride : 0;
+                const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
+                const uint32_t mask = __ballot_sync(FULL, there);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r.v[i] = 0;
-            r.scales = make_uint2(0, 0);
-        }
-        u += 2;
-        while (u >= of && live) {
-            u -= of;
-            if (++b == at.b1) live = piece(p, lane);
-        }
-        if (live) fetch(p, row);
-        return true;
-    }
-};
-
-template <int NR>
-__device__ void load_rows(const AttendParams &p, Ctrl &c, char *pairs_at, uint32_t tmem) {
-    using S = Shape<NR>;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x - SOFT) >> 5, quarter = warp & 3, group = warp >> 2;
-    const int row = quarter * 32 + lane, pairs = p.latent / 128, units = pairs + 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint32_t i = 0;                            // the block and the unit that are converted next
-    int u = group;
-    Feed feed(p, c, group, units, lane, row);
-    auto convert = [&](const Raw &r) {
-        if (u < pairs) {
-            const uint32_t n = i * pairs + u, slot = n % S::PAIRS, a = n % S::A_PAIRS;
-            char *to = pairs_at + slot * 2 * CHUNK + row * 128;
-            wait(&c.a_empty[a], n / S::A_PAIRS + 1, c);
-            wait(&c.pair_empty[slot], n / S::PAIRS + 1, c);
-            tc_fence_after();
+                for (int m = 0; m < 4; ++m) {
+                    const int r = 8 * m + (lane >> 2);
+                    src[m] = cache + __shfl_sync(FULL, offset, r) + (lane & 3) * 16;
+                    on[m] = mask >> r & 1u;
+                }
+                const uint32_t to = ring + SLOTS * UNIT + (i & 1) * SCALES;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {      // 32 values with two scales
-                const uint32_t two = (q < 2 ? r.scales.x : r.scales.y) >> (16 * (q & 1));
-                uint32_t s, w[16];
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
-                const __half2 scales = *reinterpret_cast<const __half2 *>(&s);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    from_codes(r.v[4 * q + k], k < 2 ? __low2half2(scales) : __high2half2(scales), w + 4 * k);
-                tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    *reinterpret_cast<uint4 *>(to + (q >> 1) * CHUNK + ((((q & 1) * 4 + k) ^ (row & 7)) << 4)) =
-                        make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            }
-            tc_wait_st();
-            tc_fence_before();
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) arrive(&c.pair_full[slot]);
-        } else {
-            const uint32_t slot = i % KEY_SLOTS;
-            wait(&c.key_empty[slot], i / KEY_SLOTS + 1, c);
-            if (u == pairs) {
-                const uint32_t mask = __ballot_sync(FULL, r.there);
+                for (int m = 0; m < 2; ++m) {
+                    const int r = 16 * m + (lane >> 1);
+                    copy16(to + r * 32 + (lane & 1) * 16,
+                           cache + __shfl_sync(FULL, offset, r) + units * 64 + (lane & 1) * 16, mask >> r & 1u);
+                }
                 if (lane == 0) {
                     c.marks[i % BLOCKS][quarter] = mask;
                     arrive(&c.row_full[i % BLOCKS]);
                 }
             }
-            tc_fence_after();
-            tc_store16(lanes + S::K_COL + slot * 32 + (u - pairs) * 16, r.v);
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&c.key_full[slot]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int r = 8 * m + (lane >> 2);
+                copy16(ring + slot * UNIT + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4), src[m] + u * 64, on[m]);
+            }
+            if (++slot == SLOTS) slot = 0;
+            if (++u == units) {
+                u = 0;
+                ++i;
+                if (++b == at.b1) live = piece(p, lane);
+                if (live) fetch(p, row);
+            }
         }
-        u += 2;
-        while (u >= units) {
-            u -= units;
-            ++i;
-        }
-    };
-    Raw x, y;
-    bool on_x = feed.load(p, x, lane, row), on_y = feed.load(p, y, lane, row);
-    while (on_x) {
-        convert(x);
-        on_x = feed.load(p, x, lane, row);
-        if (!on_y) break;
-        convert(y);
-        on_y = feed.load(p, y, lane, row);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
+};
+
+template <int NR>
+__device__ void load_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint32_t tmem) {
+    using S = Shape<NR>;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, pairs = p.latent / 128;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t ring = raw + quarter * (S::UNITS * UNIT + 2 * SCALES);
+    const uint32_t mine = ring + lane * 64, turn = (lane >> 1 & 3) << 4;
+    Feed feed(p, c, lane, quarter * 32 + lane);
+    if (!feed.live) return;
+#pragma unroll
+    for (int k = 0; k < S::UNITS - 1; ++k) feed.send<S::UNITS>(p, c, ring, lane, quarter);
+    uint32_t n = 0, slot = 0;                  // the pair and the place that are converted next
+    for (uint32_t i = 0; feed.live || i < feed.i; ++i) {
+        uint4 scales[2];
+        for (int u = 0; u < pairs + 2; ++u) {
+            __syncwarp();                      // (the place that is sent for next has been read)
+            feed.send<S::UNITS>(p, c, ring, lane, quarter);
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::UNITS - 1) : "memory");
+            __syncwarp();
+            uint32_t v[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 x = shared_vec(mine + slot * UNIT + ((q << 4) ^ turn));
+                v[4 * q] = x.x;
+                v[4 * q + 1] = x.y;
+                v[4 * q + 2] = x.z;
+                v[4 * q + 3] = x.w;
+            }
+            if (++slot == S::UNITS) slot = 0;
+            if (u < pairs) {
+                if (u == 0) {
+                    scales[0] = shared_vec(ring + S::UNITS * UNIT + (i & 1) * SCALES + lane * 32);
+                    scales[1] = shared_vec(ring + S::UNITS * UNIT + (i & 1) * SCALES + lane * 32 + 16);
+                }
+                const uint2 s8 = u == 0   ? make_uint2(scales[0].x, scales[0].y)
+                                 : u == 1 ? make_uint2(scales[0].z, scales[0].w)
+                                 : u == 2 ? make_uint2(scales[1].x, scales[1].y)
+                                          : make_uint2(scales[1].z, scales[1].w);
+                const uint32_t a = n % S::A_PAIRS;
+                wait(&c.a_empty[a], n / S::A_PAIRS + 1, c);
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // 32 values with two scales
+                    const uint32_t two = (q < 2 ? s8.x : s8.y) >> (16 * (q & 1));
+                    uint32_t s, w[16];
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
+                    const __half2 both = *reinterpret_cast<const __half2 *>(&s);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        from_codes(v[4 * q + k], k < 2 ? __low2half2(both) : __high2half2(both), w + 4 * k);
+                    tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
+                }
+                const uint32_t bad = __ballot_sync(
+                    FULL, ((((s8.x & 0x7F7F7F7Fu) + 0x01010101u) | ((s8.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u));
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    c.bad[a][quarter] = bad;
+                    arrive(&c.a_full[a]);
+                }
+                ++n;
+            } else {
+                const uint32_t key = i % KEY_SLOTS;
+                wait(&c.key_empty[key], i / KEY_SLOTS + 1, c);
+                tc_fence_after();
+                tc_store16(lanes + S::K_COL + key * 32 + (u - pairs) * 16, v);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&c.key_full[key]);
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The sums' left operand: pairs out of tensor memory into shared memory, a chunk's rows
+// of 128 bytes swizzled as the products read them. What waits for its place waits in
+// registers, so that tensor memory is free for the pairs behind it. A scale of NaN makes
+// every score of its row NaN, and with it the weights of all that see the row; the
+// values become zeros here, so that 0 x NaN does not reach those that may not see it.
+template <int NR>
+__device__ void copy_values(const AttendParams &p, Ctrl &c, char *pairs_at, uint32_t tmem) {
+    using S = Shape<NR>;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, pairs = p.latent / 128;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    Cursor at(c);
+    uint32_t n = 0;
+    while (at.next(p, lane))
+        for (const uint32_t end = n + (at.b1 - at.b0) * pairs; n < end; ++n) {
+            const uint32_t a = n % S::A_PAIRS, slot = n % S::PAIRS;
+            char *to = pairs_at + slot * 2 * CHUNK + row * 128;
+            uint32_t w[64];
+            wait(&c.a_full[a], n / S::A_PAIRS, c);
+            tc_fence_after();
+            tc_load64(lanes + S::A_COL + a * 64, w);
+            tc_wait_ld();
+            tc_fence_before();
+            if (c.bad[a][quarter] >> lane & 1u) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k) w[k] = finite_halves(w[k]);
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&c.a_empty[a]);
+            wait(&c.pair_empty[slot], n / S::PAIRS + 1, c);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                *reinterpret_cast<uint4 *>(to + (k >> 3) * CHUNK + (((k & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) arrive(&c.pair_full[slot]);
+        }
 }
 
 // Instruction descriptor as instruction(), FP16 operands.
@@ -351,7 +442,7 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, uint32_t query, 
                     fence_proxy_async();
                 }
                 for (int u = 0; u < pairs; ++u, ++n) {
-                    mbar_wait(&c.pair_full[n % S::PAIRS], (n / S::PAIRS) & 1u, &c.abort);
+                    mbar_wait(&c.a_full[n % S::A_PAIRS], (n / S::A_PAIRS) & 1u, &c.abort);
                     tc_fence_after();
                     const uint32_t k = tmem + S::A_COL + n % S::A_PAIRS * 64;
                     const uint64_t qu = q + u * (2 * QCHUNK >> 4);
@@ -392,7 +483,7 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
                 const uint64_t w = matrix(weights + i % S::WEIGHTS * CHUNK, 16);
                 for (int h = 0; h < pairs; ++h, ++n) {
                     const uint32_t slot = n % S::PAIRS;
-                    mbar_wait(&c.pair_full[slot], (n / S::PAIRS) & 1u, &c.abort);   // (it is: for its writes' sake)
+                    mbar_wait(&c.pair_full[slot], (n / S::PAIRS) & 1u, &c.abort);
                     fence_proxy_async();
                     tc_fence_after();
                     const uint64_t v = matrix(pairs_at + slot * 2 * CHUNK, CHUNK);
@@ -464,7 +555,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             const uint32_t scores = lanes + S::S_COL + s * NR + group * (NR / 2);
             char *weights = weights_at + i % S::WEIGHTS * CHUNK + t0 * 128 + quad * 4;
             float x[2][2 * N];                 // x[g][4 j + 2 h + e]: token 2 g + h, the thread's row 2 j + e
-            float most = 0.0f;                 // the block's largest score (by size): infinity and NaN are rare
             auto load = [&]() {
                 tc_load_groups<NR / 16>(scores, x[0]);
                 tc_load_groups<NR / 16>(scores + (16u << 16), x[1]);
@@ -479,7 +569,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                     for (int e = 0; e < 2 * N; ++e) {
                         float &v = x[g][e];
                         const int n = 2 * (e >> 2) + (e & 1), h = 2 * g + ((e >> 1) & 1);
-                        most = largest(most, v, v);
                         v *= unit[n];
                         if (!whole) v = (marks >> 8 * h & 1u) && token + 8 * h < c.lim[row_of(n)] ? v : -INFINITY;
                     }
@@ -496,7 +585,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                         for (int h = 0; h < 2; ++h) {
                             float &a = x[g][4 * j + 2 * h], &d = x[g][4 * j + 2 * h + 1];
                             if constexpr (decltype(unscaled)::value) {
-                                most = largest(most, a, d);
                                 a = exp2_fast(fmaf(a, unit[2 * j], -ref[2 * j]));
                                 d = exp2_fast(fmaf(d, unit[2 * j + 1], -ref[2 * j + 1]));
                             } else {
@@ -573,48 +661,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                         }
                     tc_wait_st();
                     tc_fence_before();
-                }
-            }
-            // What is NaN among a token's values (scales can be) must not reach a row that gives
-            // the token no weight through 0 x NaN: neither one that may not see it nor one whose
-            // score of it is -inf. Such a row's score of it is not finite, which marks the token,
-            // and what is not finite among its values is zeroed (a row that does weigh it has a
-            // score of NaN, so NaN weights).
-            if (__any_sync(FULL, !(most < INFINITY))) {
-#pragma unroll 1
-                for (int g = 0; g < 2; ++g) {
-                    bool odd[2] = {false, false};
-#pragma unroll 1
-                    for (int j = 0; j < N / 2; ++j) {
-                        float v[4];
-                        tc_load_groups<1>(scores + (static_cast<uint32_t>(g) << 20) + 8 * j, v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int h = 2 * g + (e >> 1), r = row_of(2 * j + (e & 1));
-                            const bool seen = (marks >> 8 * h & 1u) && token + 8 * h < c.lim[r];
-                            odd[e >> 1] |= r < at.tile.rows &&
-                                           (seen ? v[e] * c.unit[r] == -INFINITY : !(fabsf(v[e]) < INFINITY));
-                        }
-                    }
-                    tc_fence_before();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        odd[h] |= __shfl_xor_sync(FULL, odd[h], 1);
-                        odd[h] |= __shfl_xor_sync(FULL, odd[h], 2);
-                        if (!odd[h]) continue;
-#pragma unroll 1
-                        for (int u = 0; u < pairs; ++u) {
-                            const uint32_t slot = (i * pairs + u) % S::PAIRS;
-                            for (int k = quad; k < 16; k += 4) {
-                                uint4 *at16 = reinterpret_cast<uint4 *>(pairs_at + slot * 2 * CHUNK + (k >> 3) * CHUNK +
-                                                                        (t0 + 8 * (2 * g + h)) * 128 + (k & 7) * 16);
-                                const uint4 v = *at16;
-                                if (half_not_finite(v.x) || half_not_finite(v.y) || half_not_finite(v.z) ||
-                                    half_not_finite(v.w))
-                                    *at16 = make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                    }
                 }
             }
             fence_proxy_async();
@@ -724,14 +770,17 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
     extern __shared__ char raw[];
     char *query = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     char *pairs = query + query_bytes<NR>(p.latent), *weights = pairs + S::PAIRS * 2 * CHUNK;
-    Ctrl &c = *reinterpret_cast<Ctrl *>(weights + S::WEIGHTS * CHUNK);
+    Ctrl &c = *reinterpret_cast<Ctrl *>(pairs + S::RINGS);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::PAIRS; ++s) {
             mbar_init(&c.pair_full[s], 4);
             mbar_init(&c.pair_empty[s], 1);
         }
-        for (int s = 0; s < S::A_PAIRS; ++s) mbar_init(&c.a_empty[s], 1);
+        for (int s = 0; s < S::A_PAIRS; ++s) {
+            mbar_init(&c.a_full[s], 4);
+            mbar_init(&c.a_empty[s], 5);
+        }
         for (int s = 0; s < KEY_SLOTS; ++s) {
             mbar_init(&c.key_full[s], 8);
             mbar_init(&c.key_empty[s], 1);
@@ -763,7 +812,8 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     if (warp < SOFT / 32) soften<NR>(p, c, query, pairs, weights, tmem);
-    else if (warp < (SOFT + LOAD) / 32) load_rows<NR>(p, c, pairs, tmem);
+    else if (warp < (SOFT + LOAD) / 32) load_rows<NR>(p, c, smem_addr(weights + S::WEIGHTS * CHUNK), tmem);
+    else if (warp < (SOFT + LOAD + COPY) / 32) copy_values<NR>(p, c, pairs, tmem);
     else if (warp < NT / 32 - 1) multiply_scores<NR>(p, c, smem_addr(query), tmem);
     else multiply_sums<NR>(p, c, smem_addr(pairs), smem_addr(weights), tmem);
     __syncwarp();
@@ -777,8 +827,9 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        static_assert(CHUNK >= ROWS * MAX_CLUSTER * sizeof(float));
-        if (c.ranks > 1) join_cluster<NT>(p, c, pairs, reinterpret_cast<float(*)[MAX_CLUSTER]>(weights));
+        if (c.ranks > 1)
+            join_cluster<NT>(p, c, pairs,
+                             reinterpret_cast<float(*)[MAX_CLUSTER]>(pairs + NR * LATENT_MAX * sizeof(float)));
         __syncwarp();
         cluster_arrive();                      // no CTA leaves while others read its part
         cluster_wait();
