@@ -23,10 +23,12 @@ namespace topk::latent {
 
 namespace {
 
-constexpr int SOFT = 256;                    // warps 0 to 7: query rows, softmax and outputs, in two groups
-constexpr int LOAD = 128;                    // warps 8 to 11: cache rows, as FP16 into tensor memory
-constexpr int COPY = 128;                    // warps 12 to 15: their values from there into shared memory
-constexpr int NT = SOFT + LOAD + COPY + 64;  // warps 16 and 17: the tensor cores (scores, sums)
+// Warps, each with one job: softmax, query rows and outputs (4 where query rows are
+// few, else 8); cache rows from 4 bits into tensor memory (8, else 4); 12 to 15: values
+// from there into shared memory; 16 and 17: copies of cache rows as they are; 18 and
+// 19: the tensor cores (scores, sums).
+constexpr int NT = 640;
+constexpr int COPY_WARP = 12, SEND_WARP = 16, SCORES_WARP = 18, SUMS_WARP = 19;
 constexpr int KEYS = 128;                    // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
 constexpr int BLOCKS = 8;                    // blocks that have marks and barriers of their own: more than are
@@ -38,17 +40,20 @@ constexpr uint32_t FULL = 0xFFFFFFFFu;
 // FP16 rounds away below 2^-25 is less than 2^-36 of it.
 constexpr float BELOW = 11.0f, MOST = 15.0f;
 
-constexpr int UNIT = 32 * 64;                // bytes of a unit as it comes: 64 bytes of a warp's 32 rows
-constexpr int SCALES = 32 * 32;              // bytes of a warp's rows' scales
+constexpr int HALF = 64;                     // rows of a block that are sent for together
+constexpr int UNIT = HALF * 128;             // bytes of a unit as it comes: 128 bytes of each row of a half
+constexpr int SCALES = HALF * 32;            // bytes of a half's scales
 
 // How a tile of NR rows uses the memories: pairs of 64-value chunks in shared memory
 // (sums) and tensor memory (scores), blocks of weights and of scores, units on their way.
 template <int NR>
 struct Shape {
-    static constexpr int PAIRS = NR == 64 ? 3 : 4, A_PAIRS = NR == 64 ? 2 : 4;
-    static constexpr int WEIGHTS = NR == 16 ? 2 : 1, SCORES = NR == 64 ? 1 : 2, UNITS = NR == 64 ? 3 : 4;
+    static constexpr int SOFT = NR == 64 ? 256 : 128, GROUPS = SOFT / 128, CONVERT = 3 - GROUPS;   // groups of 4 warps
+    static constexpr int PAIRS = 3, A_PAIRS = NR == 64 ? 2 : 4;
+    static constexpr int WEIGHTS = NR == 64 ? 1 : 2, SCORES = NR == 64 ? 1 : 2;
+    static constexpr int UNITS = NR == 64 ? 2 : 3, SCALE_SLOTS = NR == 64 ? 1 : 2;
     static constexpr uint32_t O_COL = 0, S_COL = 4 * NR, A_COL = S_COL + SCORES * NR, K_COL = A_COL + A_PAIRS * 64;
-    static constexpr uint32_t RAW = LOAD / 32 * (UNITS * UNIT + 2 * SCALES);
+    static constexpr uint32_t RING = UNITS * UNIT + SCALE_SLOTS * SCALES, RAW = KEYS / HALF * RING;
     static constexpr uint32_t RINGS = (2 * PAIRS + WEIGHTS) * CHUNK + RAW;
     static_assert(K_COL + KEY_SLOTS * 32 <= 512);
     // A cluster's parts lie where the rings were, and what weighs them behind.
@@ -58,6 +63,8 @@ struct Shape {
 struct Ctrl : Schedule<NT> {
     u64 pair_full[4], pair_empty[4];           // a pair of chunks is in / its sums are added
     u64 a_full[4], a_empty[4];                 // a pair is in tensor memory / its scores are added and it is copied
+    u64 unit_full[2][3], unit_empty[2][3];     // a half's unit is in / read
+    u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in / read
     u64 key_full[KEY_SLOTS], key_empty[KEY_SLOTS];
     u64 s_full[2], s_empty[2];                 // scores written / read
     u64 row_full[BLOCKS];                      // a block's marks are in
@@ -106,8 +113,12 @@ __device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t (&r)[16
         : "memory");
 }
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SOFT) : "memory"); }
+template <int SOFT>
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(SOFT) : "memory");
+}
 
+template <int SOFT>
 __device__ __forceinline__ bool soft_any(bool v) {
     uint32_t r;
     asm volatile(
@@ -165,7 +176,7 @@ __device__ __forceinline__ void tc_load64(uint32_t addr, uint32_t (&r)[64]) {
 template <int NR>
 __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, Ctrl &c, char *query, int tid) {
     const int piece = tid & 7, pairs = p.latent / 128;
-    for (int r = tid >> 3; r < NR; r += SOFT / 8) {
+    for (int r = tid >> 3; r < NR; r += Shape<NR>::SOFT / 8) {
         const bool on = r < tile.rows;
         const int32_t flat = tile.base + (on ? r : 0), token = flat / p.heads, head = flat - token * p.heads;
         const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
@@ -215,173 +226,217 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
     if ((tid & 31) == 0) arrive(&c.q_full);
 }
 
-// Cache rows on their way to the tensor cores: a warp has a quarter of every block's
-// rows, as tensor memory wants it, and a ring of its own for what comes: units of 64
-// bytes of each row (128 values, or half of the key part) one after another, a few of
-// them on their way while one is converted, a lane its own row of it. (Rows read
-// straight into registers, a row a lane, were held up at 7 KB on their way per SM: the
-// first-level cache, small beside this much shared memory, keeps a line of 128 bytes
-// for each 32 that come. 32 requests x 16 heads x 16384: 118 us.)
-struct Feed {
-    Cursor at;
-    const int32_t *list = nullptr;
-    int32_t len = 0, b = 0, fetched = -1;
-    int u = 0, units;                          // the unit that is sent for next, and units of a block
-    uint32_t i = 0, slot = 0;                  // its block and its place
-    bool live;
-    const uint8_t *src[4];                     // where this lane's copies come from: rows 8 m + lane / 4
-    bool on[4];
-    __device__ __forceinline__ Feed(const AttendParams &p, const Ctrl &c, int lane, int row)
-        : at(c), units(p.latent / 128 + 2) {
-        live = piece(p, lane);
-        if (live) fetch(p, row);
-    }
-    __device__ __forceinline__ bool piece(const AttendParams &p, int lane) {
-        if (!at.next(p, lane)) return false;
-        const RowList l(p, at);
-        list = l.list;
-        len = l.len;
-        b = at.b0;
-        return true;
-    }
-    __device__ __forceinline__ void fetch(const AttendParams &p, int row) {
-        const int32_t j = b * KEYS + row;
-        fetched = j < len ? __ldg(list + (p.paged ? j >> p.page_shift : j)) : -1;
-    }
-    // Sends for the next unit (a group of copies, empty behind the last one).
-    template <int SLOTS>
-    __device__ __forceinline__ void send(const AttendParams &p, Ctrl &c, uint32_t ring, int lane, int quarter) {
-        const int row = quarter * 32 + lane;
-        if (live) {
-            if (u == 0) {
-                // A new block: its rows' places, and their scales; the next block's row numbers.
-                const int64_t v = p.paged ? static_cast<int64_t>(fetched) * p.block_rows +
-                                                ((b * KEYS + row) & ((1 << p.page_shift) - 1))
-                                          : fetched;
-                const bool there = fetched >= 0 && v < p.cache_rows;
-                const long long offset = there ? v * p.cache_stride : 0;
-                const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
-                const uint32_t mask = __ballot_sync(FULL, there);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int r = 8 * m + (lane >> 2);
-                    src[m] = cache + __shfl_sync(FULL, offset, r) + (lane & 3) * 16;
-                    on[m] = mask >> r & 1u;
-                }
-                const uint32_t to = ring + SLOTS * UNIT + (i & 1) * SCALES;
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int r = 16 * m + (lane >> 1);
-                    copy16(to + r * 32 + (lane & 1) * 16,
-                           cache + __shfl_sync(FULL, offset, r) + units * 64 + (lane & 1) * 16, mask >> r & 1u);
-                }
-                if (lane == 0) {
-                    c.marks[i % BLOCKS][quarter] = mask;
-                    arrive(&c.row_full[i % BLOCKS]);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int r = 8 * m + (lane >> 2);
-                copy16(ring + slot * UNIT + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4), src[m] + u * 64, on[m]);
-            }
-            if (++slot == SLOTS) slot = 0;
-            if (++u == units) {
-                u = 0;
-                ++i;
-                if (++b == at.b1) live = piece(p, lane);
-                if (live) fetch(p, row);
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-};
-
+// Cache rows as they are, into a ring for each half of a block's rows, a warp a half:
+// units of 128 bytes of each row, the key part, then 256 values after 256 (behind the
+// last of an odd number of pairs lies something else, which nobody reads), swizzled so
+// that lanes reading a row each meet no conflict; and a block's scales. Pages of 32 rows
+// and more come by TMA, a box a unit (two of pages of 32 rows); listed rows by 16-byte
+// copies. (Rows read straight into registers, a row a lane, were held up at 7 KB on
+// their way per SM: the first-level cache, small beside this much shared memory, keeps a
+// line of 128 bytes for each 32 that come. 32 requests x 16 heads x 16384: 118 us. With
+// units a quarter of this size the sender was what all others waited for: a box or a
+// group of copies costs it 200 to 300 cycles.)
 template <int NR>
-__device__ void load_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint32_t tmem) {
+__device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, const CUtensorMap *scales_map, Ctrl &c,
+                          uint32_t raw) {
     using S = Shape<NR>;
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, pairs = p.latent / 128;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t ring = raw + quarter * (S::UNITS * UNIT + 2 * SCALES);
-    const uint32_t mine = ring + lane * 64, turn = (lane >> 1 & 3) << 4;
-    Feed feed(p, c, lane, quarter * 32 + lane);
-    if (!feed.live) return;
+    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - SEND_WARP, pairs = p.latent / 128;
+    const int units = 1 + (pairs + 1) / 2;
+    const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
+    const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT;
+    Cursor at(c);
+    uint32_t i = 0, slot = 0, use = 0;         // the block; the place of the next unit, and its use
+    while (at.next(p, lane)) {
+        const RowList list(p, at);
+        int32_t now[2];
 #pragma unroll
-    for (int k = 0; k < S::UNITS - 1; ++k) feed.send<S::UNITS>(p, c, ring, lane, quarter);
-    uint32_t n = 0, slot = 0;                  // the pair and the place that are converted next
-    for (uint32_t i = 0; feed.live || i < feed.i; ++i) {
-        uint4 scales[2];
-        for (int u = 0; u < pairs + 2; ++u) {
-            __syncwarp();                      // (the place that is sent for next has been read)
-            feed.send<S::UNITS>(p, c, ring, lane, quarter);
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::UNITS - 1) : "memory");
-            __syncwarp();
-            uint32_t v[16];
+        for (int h = 0; h < 2; ++h) now[h] = list.fetch(p, at.b0 * KEYS + half * HALF + h * 32 + lane);
+        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+            const uint32_t s = i % S::SCALE_SLOTS;
+            int32_t row[2];
+            uint32_t mask[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 x = shared_vec(mine + slot * UNIT + ((q << 4) ^ turn));
-                v[4 * q] = x.x;
-                v[4 * q + 1] = x.y;
-                v[4 * q + 2] = x.z;
-                v[4 * q + 3] = x.w;
+            for (int h = 0; h < 2; ++h) {
+                const int32_t j = b * KEYS + half * HALF + h * 32 + lane;
+                row[h] = list.row(p, now[h], j);
+                now[h] = list.fetch(p, j + KEYS);
+                mask[h] = __ballot_sync(FULL, row[h] >= 0);
             }
-            if (++slot == S::UNITS) slot = 0;
-            if (u < pairs) {
-                if (u == 0) {
-                    scales[0] = shared_vec(ring + S::UNITS * UNIT + (i & 1) * SCALES + lane * 32);
-                    scales[1] = shared_vec(ring + S::UNITS * UNIT + (i & 1) * SCALES + lane * 32 + 16);
-                }
-                const uint2 s8 = u == 0   ? make_uint2(scales[0].x, scales[0].y)
-                                 : u == 1 ? make_uint2(scales[0].z, scales[0].w)
-                                 : u == 2 ? make_uint2(scales[1].x, scales[1].y)
-                                          : make_uint2(scales[1].z, scales[1].w);
-                const uint32_t a = n % S::A_PAIRS;
-                wait(&c.a_empty[a], n / S::A_PAIRS + 1, c);
-                tc_fence_after();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {  // 32 values with two scales
-                    const uint32_t two = (q < 2 ? s8.x : s8.y) >> (16 * (q & 1));
-                    uint32_t s, w[16];
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
-                    const __half2 both = *reinterpret_cast<const __half2 *>(&s);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        from_codes(v[4 * q + k], k < 2 ? __low2half2(both) : __high2half2(both), w + 4 * k);
-                    tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
-                }
-                const uint32_t bad = __ballot_sync(
-                    FULL, ((((s8.x & 0x7F7F7F7Fu) + 0x01010101u) | ((s8.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u));
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
+            if (p.tiled) {
                 if (lane == 0) {
-                    c.bad[a][quarter] = bad;
-                    arrive(&c.a_full[a]);
+                    // (rows of which there are none, and rows past the cache, come as zeros)
+                    const int32_t y0 = row[0] >= 0 ? row[0] : p.cache_rows, y1 = row[1] >= 0 ? row[1] : p.cache_rows;
+                    for (int u = 0; u < units; ++u) {
+                        u64 *full = &c.unit_full[half][slot];
+                        const uint32_t to = ring + slot * UNIT;
+                        const int x = u ? (u - 1) * 128 : p.latent / 2;
+                        mbar_wait(&c.unit_empty[half][slot], (use + 1) & 1u, &c.abort);
+                        mbar_expect_tx(full, UNIT);
+                        copy_box(to, units_map, x, y0, full);
+                        if (p.tiled == 1) copy_box(to + UNIT / 2, units_map, x, y1, full);
+                        if (++slot == S::UNITS) {
+                            slot = 0;
+                            ++use;
+                        }
+                        if (u == 0) {
+                            full = &c.scales_full[half][s];
+                            mbar_wait(&c.scales_empty[half][s], (i / S::SCALE_SLOTS + 1) & 1u, &c.abort);
+                            mbar_expect_tx(full, SCALES);
+                            copy_box(scales + s * SCALES, scales_map, p.latent / 2 + 128, y0, full);
+                            if (p.tiled == 1) copy_box(scales + s * SCALES + SCALES / 2, scales_map, p.latent / 2 + 128, y1, full);
+                            c.marks[i % BLOCKS][2 * half] = mask[0];
+                            c.marks[i % BLOCKS][2 * half + 1] = mask[1];
+                            arrive(&c.row_full[i % BLOCKS]);
+                        }
+                    }
                 }
-                ++n;
-            } else {
-                const uint32_t key = i % KEY_SLOTS;
-                wait(&c.key_empty[key], i / KEY_SLOTS + 1, c);
-                tc_fence_after();
-                tc_store16(lanes + S::K_COL + key * 32 + (u - pairs) * 16, v);
-                tc_wait_st();
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(&c.key_full[key]);
+                slot = __shfl_sync(FULL, slot, 0);
+                use = __shfl_sync(FULL, use, 0);
+                continue;
+            }
+            const uint64_t all = mask[0] | static_cast<uint64_t>(mask[1]) << 32;
+            const long long offset[2] = {row[0] >= 0 ? row[0] * p.cache_stride : 0,
+                                         row[1] >= 0 ? row[1] * p.cache_stride : 0};
+            for (int u = 0; u < units; ++u) {
+                const uint32_t to = ring + slot * UNIT;
+                const int x = u ? (u - 1) * 128 : p.latent / 2;
+                // Eight lanes a row, four rows a copy.
+                wait(&c.unit_empty[half][slot], use + 1, c);
+#pragma unroll
+                for (int m = 0; m < HALF / 4; ++m) {
+                    const int r = 4 * m + (lane >> 3);
+                    copy16(to + r * 128 + (((lane ^ r) & 7) << 4),
+                           cache + __shfl_sync(FULL, offset[m / 8], r & 31) + x + (lane & 7) * 16, all >> r & 1u);
+                }
+                copies_arrive(&c.unit_full[half][slot]);
+                if (++slot == S::UNITS) {
+                    slot = 0;
+                    ++use;
+                }
+                if (u == 0) {
+                    wait(&c.scales_empty[half][s], i / S::SCALE_SLOTS + 1, c);
+#pragma unroll
+                    for (int m = 0; m < HALF / 16; ++m) {
+                        const int r = 16 * m + (lane >> 1);
+                        copy16(scales + s * SCALES + r * 32 + (lane & 1) * 16,
+                               cache + __shfl_sync(FULL, offset[m / 2], r & 31) + p.latent / 2 + 128 + (lane & 1) * 16,
+                               all >> r & 1u);
+                    }
+                    copies_arrive(&c.scales_full[half][s]);
+                    if (lane == 0) {
+                        c.marks[i % BLOCKS][2 * half] = mask[0];
+                        c.marks[i % BLOCKS][2 * half + 1] = mask[1];
+                        arrive(&c.row_full[i % BLOCKS]);
+                    }
+                }
             }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (p.tiled && c.abort) {
+        settle(c.unit_full[half], static_cast<int32_t>(use * S::UNITS + slot) - 1, 1, S::UNITS);
+        settle(c.scales_full[half], static_cast<int32_t>(i) - 1, 1, S::SCALE_SLOTS);
+    }
+}
+
+// Units into tensor memory, a row a lane, each warp the rows of its own lanes there;
+// where two groups of warps do it each has 64 bytes of every unit, else the one group
+// has them in turn. 128 values become FP16, the scores' left operand; the key part
+// goes there as it is.
+template <int NR>
+__device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint32_t tmem) {
+    using S = Shape<NR>;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x - S::SOFT) >> 5, quarter = warp & 3, half = quarter >> 1;
+    const int pairs = p.latent / 128, row = (quarter & 1) * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT + row * 32;
+    const uint32_t mine = ring + row * 128, turn = (row & 7) << 4;
+    Cursor at(c);
+    uint32_t i = 0, slot = 0, use = 0;         // the block; the place of the next unit, and its use
+    while (at.next(p, lane))
+        for (const uint32_t end = i + (at.b1 - at.b0); i < end; ++i) {
+            const uint32_t s = i % S::SCALE_SLOTS;
+            for (int u = 0; u < 1 + (pairs + 1) / 2; ++u) {
+                wait(&c.unit_full[half][slot], use, c);
+                if (u == 1) wait(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
+#pragma unroll 1
+                for (int e = S::CONVERT == 2 ? warp >> 2 : 0; e < 2; e += S::CONVERT) {
+                    const int pair = 2 * (u - 1) + e;
+                    uint32_t v[16];
+                    uint2 s8 = make_uint2(0, 0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 x = shared_vec(mine + slot * UNIT + ((e * 64 + q * 16) ^ turn));
+                        v[4 * q] = x.x;
+                        v[4 * q + 1] = x.y;
+                        v[4 * q + 2] = x.z;
+                        v[4 * q + 3] = x.w;
+                    }
+                    if (u)
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                     : "=r"(s8.x), "=r"(s8.y)
+                                     : "r"(scales + s * SCALES + (pair & 3) * 8));
+                    if (e + S::CONVERT >= 2) {
+                        __syncwarp();
+                        if (lane == 0) arrive(&c.unit_empty[half][slot]);
+                    }
+                    if (u == 0) {
+                        const uint32_t key = i % KEY_SLOTS;
+                        wait(&c.key_empty[key], i / KEY_SLOTS + 1, c);
+                        tc_fence_after();
+                        tc_store16(lanes + S::K_COL + key * 32 + e * 16, v);
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive(&c.key_full[key]);
+                    } else if (pair < pairs) {
+                        const uint32_t n = i * pairs + pair, a = n % S::A_PAIRS;
+                        wait(&c.a_empty[a], n / S::A_PAIRS + 1, c);
+                        tc_fence_after();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // 32 values with two scales
+                            const uint32_t two = (q < 2 ? s8.x : s8.y) >> (16 * (q & 1));
+                            uint32_t both, w[16];
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(both) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
+                            const __half2 h = *reinterpret_cast<const __half2 *>(&both);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                from_codes(v[4 * q + k], k < 2 ? __low2half2(h) : __high2half2(h), w + 4 * k);
+                            tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
+                        }
+                        const uint32_t bad = __ballot_sync(FULL, ((((s8.x & 0x7F7F7F7Fu) + 0x01010101u) |
+                                                                   ((s8.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u));
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            c.bad[a][quarter] = bad;
+                            arrive(&c.a_full[a]);
+                        }
+                    }
+                }
+                if (++slot == S::UNITS) {
+                    slot = 0;
+                    ++use;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&c.scales_empty[half][s]);
+        }
 }
 
 // The sums' left operand: pairs out of tensor memory into shared memory, a chunk's rows
 // of 128 bytes swizzled as the products read them. What waits for its place waits in
-// registers, so that tensor memory is free for the pairs behind it. A scale of NaN makes
-// every score of its row NaN, and with it the weights of all that see the row; the
-// values become zeros here, so that 0 x NaN does not reach those that may not see it.
+// registers, so that tensor memory is free for the pairs behind it: three places, this
+// one and two in tensor memory hold more than a block, whose scores so never wait for
+// its own sums. A scale of NaN makes every score of its row NaN, and with it the weights
+// of all that see the row; the values become zeros here, so that 0 x NaN does not reach
+// those that may not see it.
 template <int NR>
 __device__ void copy_values(const AttendParams &p, Ctrl &c, char *pairs_at, uint32_t tmem) {
     using S = Shape<NR>;
+    static_assert(S::PAIRS + 1 + S::A_PAIRS >= LATENT_MAX / 128);
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, pairs = p.latent / 128;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -395,14 +450,15 @@ __device__ void copy_values(const AttendParams &p, Ctrl &c, char *pairs_at, uint
             wait(&c.a_full[a], n / S::A_PAIRS, c);
             tc_fence_after();
             tc_load64(lanes + S::A_COL + a * 64, w);
+            const bool bad = c.bad[a][quarter] >> lane & 1u;
             tc_wait_ld();
             tc_fence_before();
-            if (c.bad[a][quarter] >> lane & 1u) {
+            __syncwarp();
+            if (lane == 0) arrive(&c.a_empty[a]);
+            if (bad) {
 #pragma unroll
                 for (int k = 0; k < 64; ++k) w[k] = finite_halves(w[k]);
             }
-            __syncwarp();
-            if (lane == 0) arrive(&c.a_empty[a]);
             wait(&c.pair_empty[slot], n / S::PAIRS + 1, c);
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -501,20 +557,20 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
 }
 
 // Scores to weights, the running reference and sums, and the outputs. Each group of
-// four warps has half of the query rows. Thread t of a group's warp w holds tokens
+// four warps has its share of the query rows. Thread t of a group's warp w holds tokens
 // 32 w + t / 4 + 8 h, h < 4, of a block, against the rows 8 j + 2 (t % 4) and the next
-// of its half: their references and sums stay in its registers.
+// of its share: their references and sums stay in its registers.
 template <int NR>
 __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_at, char *weights_at, uint32_t tmem) {
     using S = Shape<NR>;
-    constexpr int N = NR / 8;                  // query rows of a thread
+    constexpr int SOFT = S::SOFT, SHARE = NR / S::GROUPS, N = SHARE / 4;   // query rows of a group, a thread
     const int tid = threadIdx.x, lane = tid & 31, w = (tid >> 5) & 3, group = tid >> 7, quad = lane & 3;
     const int t0 = w * 32 + lane / 4, pairs = p.latent / 128;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
     Part *parts = reinterpret_cast<Part *>(p.workspace);
     Joint *joints = reinterpret_cast<Joint *>(parts + 2 * p.sms);
     const bool by_tile = p.tiles <= static_cast<int32_t>(gridDim.x);
-    auto row_of = [&](int n) { return group * (NR / 2) + 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
+    auto row_of = [&](int n) { return group * SHARE + 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
     bool split_here = false;
     Cursor at(c);
     uint32_t i = 0;
@@ -531,7 +587,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             c.lim[tid] = lim;
             c.ref[tid] = lim > start ? LOWEST : INFINITY;
         }
-        soft_sync();
+        soft_sync<SOFT>();
         int32_t low = INT32_MAX;
 #pragma unroll
         for (int r = 0; r < ROWS; r += 32) {
@@ -552,12 +608,12 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             wait(&c.row_full[i % BLOCKS], i / BLOCKS, c);
             const uint32_t marks = c.marks[i % BLOCKS][w] >> (lane / 4);   // bit 8 h: token h is there
             const bool whole = __all_sync(FULL, (marks & 0x01010101u) == 0x01010101u) && (b + 1) * KEYS <= low;
-            const uint32_t scores = lanes + S::S_COL + s * NR + group * (NR / 2);
+            const uint32_t scores = lanes + S::S_COL + s * NR + group * SHARE;
             char *weights = weights_at + i % S::WEIGHTS * CHUNK + t0 * 128 + quad * 4;
             float x[2][2 * N];                 // x[g][4 j + 2 h + e]: token 2 g + h, the thread's row 2 j + e
             auto load = [&]() {
-                tc_load_groups<NR / 16>(scores, x[0]);
-                tc_load_groups<NR / 16>(scores + (16u << 16), x[1]);
+                tc_load_groups<SHARE / 8>(scores, x[0]);
+                tc_load_groups<SHARE / 8>(scores + (16u << 16), x[1]);
                 tc_fence_before();
             };
             // Scores in log2 units; where masked, -inf.
@@ -593,7 +649,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                             }
                             const __half2 v = __floats2half2_rn(a, d);
                             top = __hmax2(top, v);
-                            const int at_row = (group * (N / 2) + j) ^ (t0 & 7);
+                            const int at_row = (group * (SHARE / 8) + j) ^ (t0 & 7);
                             *reinterpret_cast<__half2 *>(weights + (2 * g + h) * 1024 + (at_row << 4)) = v;
                         }
                 return fmaxf(__low2float(top), __high2float(top)) > 32768.0f;   // 2^MOST
@@ -610,10 +666,10 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                 take();
             } else if (whole) {
                 load();
-                moved = soft_any(weigh(std::true_type{}));
+                moved = soft_any<SOFT>(weigh(std::true_type{}));
             } else {
                 take();
-                moved = soft_any(weigh(std::false_type{}));
+                moved = soft_any<SOFT>(weigh(std::false_type{}));
             }
             if (moved) {
                 // New references where the rows' largest scores of this block are 2^MOST above
@@ -629,7 +685,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                 const int mine = across_index<N>();
 #pragma unroll
                 for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = top[j];
-                soft_sync();
+                soft_sync<SOFT>();
                 if (tid < NR) {
                     const float t = fmaxf(fmaxf(c.across[0][tid], c.across[1][tid]),
                                           fmaxf(c.across[2][tid], c.across[3][tid]));
@@ -638,7 +694,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                     c.factor[tid] = move ? exp2_fast(old - (t - BELOW)) : 1.0f;
                     if (move) c.ref[tid] = t - BELOW;
                 }
-                soft_sync();
+                soft_sync<SOFT>();
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     ref[n] = c.ref[row_of(n)];
@@ -651,7 +707,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                     for (int h = 0; h < pairs; ++h)
 #pragma unroll
                         for (int v = 0; v < NR; v += 16) {
-                            if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                            if (((h * (NR / 16) + v / 16) & (S::GROUPS - 1)) != group) continue;
                             float o[16], f[16];
                             shared16(&c.factor[v], f);
                             tc_load16(lanes + S::O_COL + h * NR + v, o);
@@ -684,7 +740,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
         const int mine = across_index<N>();
 #pragma unroll
         for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = l[j];
-        soft_sync();
+        soft_sync<SOFT>();
         if (again) load_query<NR>(p, then.tile, c, query, tid);
         if (tid < NR) {
             const bool sees = c.lim[tid] > start;
@@ -693,7 +749,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             c.factor[tid] = sees && sum != 0.0f ? 1.0f / sum : 0.0f;   // (0: an empty row, whatever its sums)
             if (!sees) c.ref[tid] = -INFINITY;
         }
-        soft_sync();
+        soft_sync<SOFT>();
         wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
         tc_fence_after();
         const bool direct = at.b0 == 0 && at.b1 == at.blocks;
@@ -706,7 +762,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                 for (int h = 0; h < pairs; ++h)
 #pragma unroll
                     for (int v = 0; v < NR; v += 16) {
-                        if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                        if (((h * (NR / 16) + v / 16) & (S::GROUPS - 1)) != group) continue;
                         float o[16], f[16];
                         shared16(&c.factor[v], f);
                         tc_load16(lanes + S::O_COL + h * NR + v, o);
@@ -737,7 +793,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             for (int h = 0; h < pairs; ++h)
 #pragma unroll
                 for (int v = 0; v < NR; v += 16) {
-                    if (((h * (NR / 16) + v / 16) & 1) != group) continue;
+                    if (((h * (NR / 16) + v / 16) & (S::GROUPS - 1)) != group) continue;
                     float o[16], f[16];
                     shared16(&c.factor[v], f);
                     tc_load16(lanes + S::O_COL + h * NR + v, o);
@@ -757,7 +813,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
         split_here |= at.b0 == 0 && !direct;
         done += at.u1 - at.u0;
         tc_fence_before();
-        soft_sync();
+        soft_sync<SOFT>();
         at = then;
         more = again;
     }
@@ -765,7 +821,9 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
 }
 
 template <int NR>
-__global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ AttendParams p,
+                                                        const __grid_constant__ CUtensorMap units_map,
+                                                        const __grid_constant__ CUtensorMap scales_map) {
     using S = Shape<NR>;
     extern __shared__ char raw[];
     char *query = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -781,25 +839,35 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
             mbar_init(&c.a_full[s], 4);
             mbar_init(&c.a_empty[s], 5);
         }
+        for (int h = 0; h < 2; ++h) {
+            for (int s = 0; s < S::UNITS; ++s) {
+                mbar_init(&c.unit_full[h][s], p.tiled ? 1 : 32);
+                mbar_init(&c.unit_empty[h][s], 2 * S::CONVERT);
+            }
+            for (int s = 0; s < S::SCALE_SLOTS; ++s) {
+                mbar_init(&c.scales_full[h][s], p.tiled ? 1 : 32);
+                mbar_init(&c.scales_empty[h][s], 2 * S::CONVERT);
+            }
+        }
         for (int s = 0; s < KEY_SLOTS; ++s) {
             mbar_init(&c.key_full[s], 8);
             mbar_init(&c.key_empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&c.s_full[s], 1);
-            mbar_init(&c.s_empty[s], SOFT / 32);
+            mbar_init(&c.s_empty[s], S::SOFT / 32);
             mbar_init(&c.drain[s], 1);
         }
         for (int s = 0; s < BLOCKS; ++s) {
-            mbar_init(&c.row_full[s], 4);
-            mbar_init(&c.p_full[s], SOFT / 32);
+            mbar_init(&c.row_full[s], 2);
+            mbar_init(&c.p_full[s], S::SOFT / 32);
             mbar_init(&c.o_done[s], 1);
         }
-        mbar_init(&c.q_full, SOFT / 32);
+        mbar_init(&c.q_full, S::SOFT / 32);
         c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == NT / 32 - 1) {
+    if (warp == SUMS_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&c.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -811,15 +879,17 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
-    if (warp < SOFT / 32) soften<NR>(p, c, query, pairs, weights, tmem);
-    else if (warp < (SOFT + LOAD) / 32) load_rows<NR>(p, c, smem_addr(weights + S::WEIGHTS * CHUNK), tmem);
-    else if (warp < (SOFT + LOAD + COPY) / 32) copy_values<NR>(p, c, pairs, tmem);
-    else if (warp < NT / 32 - 1) multiply_scores<NR>(p, c, smem_addr(query), tmem);
+    const uint32_t ring = smem_addr(weights + S::WEIGHTS * CHUNK);
+    if (warp < S::SOFT / 32) soften<NR>(p, c, query, pairs, weights, tmem);
+    else if (warp < COPY_WARP) convert_rows<NR>(p, c, ring, tmem);
+    else if (warp < SEND_WARP) copy_values<NR>(p, c, pairs, tmem);
+    else if (warp < SCORES_WARP) send_rows<NR>(p, &units_map, &scales_map, c, ring);
+    else if (warp < SUMS_WARP) multiply_scores<NR>(p, c, smem_addr(query), tmem);
     else multiply_sums<NR>(p, c, smem_addr(pairs), smem_addr(weights), tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == NT / 32 - 1) {
+    if (warp == SUMS_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
@@ -848,8 +918,7 @@ const void *attend_fn() {
 }
 
 cudaError_t device(Device *&out) {
-    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, NT, out,
-                  [](Device &) { return cudaSuccess; });
+    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, NT, out);
 }
 
 }  // namespace
@@ -881,6 +950,24 @@ cudaError_t launch_attend4(AttendParams p, cudaStream_t stream) {
     p.tile_cost = plan.tiles > d->sms ? COSTS.tile : 0;
     p.min_share = COSTS.min_share;
     p.sms = d->sms;
+
+    // Pages of 32 rows (1) or 64 and more (2): as many rows of a half follow each other in the cache.
+    CUtensorMap units_map = {}, scales_map = {};
+    const int run = p.page_shift >= 6 ? 64 : 32;
+    p.tiled = p.paged && p.page_shift >= 5 && p.cache_rows >= run ? run / 32 : 0;
+    for (CUtensorMap *map : {&units_map, &scales_map}) {
+        if (!p.tiled) break;
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(LATENT4_ROW_BYTES(p.latent)),
+                                    static_cast<cuuint64_t>(p.cache_rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.cache_stride)};
+        const cuuint32_t box[2] = {map == &units_map ? 128u : 32u, static_cast<cuuint32_t>(run)}, steps[2] = {1, 1};
+        if (d->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p.cache), dims, strides, box, steps,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      map == &units_map ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -894,7 +981,7 @@ cudaError_t launch_attend4(AttendParams p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    void *args[] = {&p};
+    void *args[] = {&p, &units_map, &scales_map};
     e = cudaLaunchKernelExC(&cfg, plan.nr == 16 ? attend_fn<16>() : plan.nr == 32 ? attend_fn<32>() : attend_fn<64>(),
                             args);
     if (e != cudaSuccess || p.cluster || plan.blocks <= 1) return e;   // tiles of one block are never split

@@ -19,9 +19,6 @@
 // rows (no TMA boxes) add the copies' latency: 3200 cycles a block at two blocks in
 // flight, tile ends included (512 tokens x 128 heads x 2048: 356 us).
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <type_traits>
 
 #include "latent_attend.cuh"
@@ -89,15 +86,6 @@ __host__ __device__ constexpr Plan make_plan(int latent) {
 static_assert(make_plan<ROWS>(LATENT_MAX).pair_slots >= 2 * LATENT_MAX / 128 &&
               make_plan<ROWS>(LATENT_MAX).rope_slots >= 2);
 
-// 64 rows of 64 values from column x and row y, completing on `bar`.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, u64 *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-            "r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
-}
-
 // Whether either of two BF16 values is NaN or infinite.
 __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
@@ -132,17 +120,6 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
         const uint32_t dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
         for (int k = 0; k < chunks; ++k) copy16(dst + k * NR * 128, src + k * 64, on);
     }
-}
-
-// After a wait that gave up: no copy may be in flight into shared memory when the
-// CTA ends, so wait (with its own limit) for the last ones into each slot. Copy q
-// went into slot q % slots for the q / slots-th time, q = last, last - step, ..
-__device__ __forceinline__ void settle(u64 *full, int32_t last, int step, int slots) {
-    const uint64_t t0 = global_timer_ns();
-    for (int32_t q = last; q >= 0 && q > last - slots; q -= step)
-        while (!mbar_try_wait(&full[q % slots], static_cast<uint32_t>(q / slots) & 1u) &&
-               global_timer_ns() - t0 < WAIT_LIMIT_NS) {
-        }
 }
 
 // Query and cache rows into shared memory. Each warp has one pair of every
@@ -883,7 +860,6 @@ namespace {
 constexpr Costs COSTS = {2, 5, 4, 3, 2};
 
 Device g_device[64];
-PFN_cuTensorMapEncodeTiled_v12000 g_encode;
 
 template <int NR>
 const void *attend_fn() {
@@ -891,16 +867,7 @@ const void *attend_fn() {
 }
 
 cudaError_t device(Device *&out) {
-    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, NT, out, [](Device &) {
-        cudaDriverEntryPointQueryResult found;
-        void *f = nullptr;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                                               &found);
-        if (e != cudaSuccess) return e;
-        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-        return cudaSuccess;
-    });
+    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, NT, out);
 }
 
 }  // namespace
@@ -943,7 +910,7 @@ cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
                                     static_cast<cuuint64_t>(p.cache_rows)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.cache_stride) * 2};
         const cuuint32_t box[2] = {64, KEYS}, steps[2] = {1, 1};
-        if (g_encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p.cache), dims, strides, box,
+        if (d->encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p.cache), dims, strides, box,
                       steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;

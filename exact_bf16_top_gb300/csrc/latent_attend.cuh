@@ -3,6 +3,8 @@
 // split tiles' parts.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -157,9 +159,29 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
+// The map's box from column x and row y, completing on `bar`.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, u64 *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // An arrival on `bar` once this thread's copies so far are done.
 __device__ __forceinline__ void copies_arrive(u64 *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// After a wait that gave up: no copy may be in flight into shared memory when the
+// CTA ends, so wait (with its own limit) for the last ones into each slot. Copy q
+// went into slot q % slots for the q / slots-th time, q = last, last - step, ..
+__device__ __forceinline__ void settle(u64 *full, int32_t last, int step, int slots) {
+    const uint64_t t0 = global_timer_ns();
+    for (int32_t q = last; q >= 0 && q > last - slots; q -= step)
+        while (!mbar_try_wait(&full[q % slots], static_cast<uint32_t>(q / slots) & 1u) &&
+               global_timer_ns() - t0 < WAIT_LIMIT_NS) {
+        }
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -525,12 +547,12 @@ struct Device {
     cudaError_t err = cudaSuccess;
     int sms = 0;
     int clusters[5] = {};                      // of 1, 2, 4, 8, 16 CTAs that run at once
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
 // Looks at the current device once: `fns`, the kernel's forms by query rows, get their
-// attributes; `more` does what else the kernel wants.
-template <class More>
-cudaError_t device(Device (&devices)[64], const void *const (&fns)[3], int threads, Device *&out, More more) {
+// attributes.
+inline cudaError_t device(Device (&devices)[64], const void *const (&fns)[3], int threads, Device *&out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -559,7 +581,12 @@ cudaError_t device(Device (&devices)[64], const void *const (&fns)[3], int threa
                 d.clusters[i] = 0;             // (a size that the device does not take)
             }
         }
-        if (e == cudaSuccess) e = more(d);
+        cudaDriverEntryPointQueryResult found;
+        void *f = nullptr;
+        if (e == cudaSuccess)
+            e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !f)) e = cudaErrorNotSupported;
+        d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
         if (e == cudaSuccess && d.sms > 512) e = cudaErrorNotSupported;   // (join_kernel's weights)
         d.err = e;
     });
