@@ -24,15 +24,17 @@ namespace topk::latent {
 namespace {
 
 // Warps, each with one job: softmax, query rows and outputs (4 where query rows are
-// few, else 8); cache rows from 4 bits into tensor memory (8, else 4); 12 to 15: values
-// from there into shared memory; 16 and 17: copies of cache rows as they are; 18 and
-// 19: the tensor cores (scores, sums).
-constexpr int NT = 640;
-constexpr int COPY_WARP = 12, SEND_WARP = 16, SCORES_WARP = 18, SUMS_WARP = 19;
+// few, else 8); cache rows from 4 bits to FP16 (8, else 4); 12 to 19: values from tensor
+// memory to shared memory; 20 and 21: copies of cache rows as they are; 22 and 23: the
+// tensor cores (scores, sums).
+constexpr int NT = 768;
+constexpr int COPY_WARP = 12, SEND_WARP = 20, SCORES_WARP = 22, SUMS_WARP = 23;
+constexpr int COPIERS = 2;                   // groups of four copying warps
 constexpr int KEYS = 128;                    // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
-constexpr int BLOCKS = 8;                    // blocks that have marks and barriers of their own: more than are
-                                             // under way
+constexpr int BLOCKS = 8, TURNS = 16;        // blocks; pairs and units that have barriers of their own: more than are
+                                             // under way (who waits for one may find later ones done, or earlier ones
+                                             // not, and two phases of one barrier look like none)
 constexpr int KEY_SLOTS = 2;                 // blocks' key parts in tensor memory
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 // Weights are FP16: the reference is set this far below the maximum and moves when a
@@ -56,16 +58,18 @@ struct Shape {
     static constexpr uint32_t RING = UNITS * UNIT + SCALE_SLOTS * SCALES, RAW = KEYS / HALF * RING;
     static constexpr uint32_t RINGS = (2 * PAIRS + WEIGHTS) * CHUNK + RAW;
     static_assert(K_COL + KEY_SLOTS * 32 <= 512);
+    // Places, what waits in registers and tensor memory hold a block: its scores never wait for its own sums.
+    static_assert(PAIRS + COPIERS + A_PAIRS > LATENT_MAX / 128 && A_PAIRS % COPIERS == 0);
     // A cluster's parts lie where the rings were, and what weighs them behind.
     static_assert(RINGS >= NR * LATENT_MAX * sizeof(float) + ROWS * MAX_CLUSTER * sizeof(float));
 };
 
 struct Ctrl : Schedule<NT> {
-    u64 pair_full[4], pair_empty[4];           // a pair of chunks is in / its sums are added
-    u64 a_full[4], a_empty[4];                 // a pair is in tensor memory / its scores are added and it is copied
-    u64 unit_full[2][3], unit_empty[2][3];     // a half's unit is in / read
+    u64 unit_full[2][TURNS], unit_empty[2][3]; // a half's unit is in / read
     u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in / read
-    u64 key_full[KEY_SLOTS], key_empty[KEY_SLOTS];
+    u64 a_full[4], scored[TURNS], copied[TURNS];   // a pair is in tensor memory / its scores are added, it is read
+    u64 pair_full[3], summed[TURNS];           // a pair is in shared memory / its sums are added
+    u64 key_full[KEY_SLOTS], key_done[BLOCKS]; // a block's key part is in tensor memory / its scores are added
     u64 s_full[2], s_empty[2];                 // scores written / read
     u64 row_full[BLOCKS];                      // a block's marks are in
     u64 p_full[BLOCKS], o_done[BLOCKS];        // a block's weights are in / its sums are added
@@ -113,18 +117,15 @@ __device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t (&r)[16
         : "memory");
 }
 
-template <int SOFT>
-__device__ __forceinline__ void soft_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(SOFT) : "memory");
-}
+// Barriers of a softmax group.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 
-template <int SOFT>
-__device__ __forceinline__ bool soft_any(bool v) {
+__device__ __forceinline__ bool group_any(int group, bool v) {
     uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(v ? 1u : 0u), "n"(SOFT)
+        : "r"(v ? 1u : 0u), "r"(1 + group)
         : "memory");
     return r != 0;
 }
@@ -149,34 +150,32 @@ __device__ __forceinline__ void from_codes(uint32_t w, __half2 scale, uint32_t *
     }
 }
 
+// 16 columns of this warp's 32 lanes, one lane per thread, to be waited for.
+__device__ __forceinline__ void tc_issue16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
 __device__ __forceinline__ uint4 shared_vec(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
 
-// 64 columns of this warp's 32 lanes, one lane per thread.
-__device__ __forceinline__ void tc_load64(uint32_t addr, uint32_t (&r)[64]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(r[16 * q]), "=r"(r[16 * q + 1]), "=r"(r[16 * q + 2]), "=r"(r[16 * q + 3]), "=r"(r[16 * q + 4]),
-              "=r"(r[16 * q + 5]), "=r"(r[16 * q + 6]), "=r"(r[16 * q + 7]), "=r"(r[16 * q + 8]),
-              "=r"(r[16 * q + 9]), "=r"(r[16 * q + 10]), "=r"(r[16 * q + 11]), "=r"(r[16 * q + 12]),
-              "=r"(r[16 * q + 13]), "=r"(r[16 * q + 14]), "=r"(r[16 * q + 15])
-            : "r"(addr + 16 * q));
-}
-
 // ------------------------------------------------------------------ the warps' parts
 
-// A tile's query rows into shared memory, eight threads a row: the latent part as
-// FP16, all of it times the power of two that brings the row's largest finite value to
-// [2^8, 2^9). Both are exact for values down to 2^-22 of it.
+// A softmax group's query rows into shared memory, eight threads a row: the latent part
+// as FP16, all of it times the power of two that brings the row's largest finite value
+// to [2^8, 2^9). Both are exact for values down to 2^-22 of it.
 template <int NR>
-__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, Ctrl &c, char *query, int tid) {
+__device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, Ctrl &c, char *query, int group,
+                                           int tid) {
+    constexpr int SHARE = NR / Shape<NR>::GROUPS;
     const int piece = tid & 7, pairs = p.latent / 128;
-    for (int r = tid >> 3; r < NR; r += Shape<NR>::SOFT / 8) {
+    for (int r = group * SHARE + (tid >> 3); r < (group + 1) * SHARE; r += 16) {
         const bool on = r < tile.rows;
         const int32_t flat = tile.base + (on ? r : 0), token = flat / p.heads, head = flat - token * p.heads;
         const uint16_t *src = p.query + token * p.query_token_stride + head * p.query_head_stride + piece * 8;
@@ -245,7 +244,7 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
     const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
     const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT;
     Cursor at(c);
-    uint32_t i = 0, slot = 0, use = 0;         // the block; the place of the next unit, and its use
+    uint32_t i = 0, turn = 0, slot = 0, use = 0;   // the block; the next unit, its place and the place's use
     while (at.next(p, lane)) {
         const RowList list(p, at);
         int32_t now[2];
@@ -267,13 +266,14 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                     // (rows of which there are none, and rows past the cache, come as zeros)
                     const int32_t y0 = row[0] >= 0 ? row[0] : p.cache_rows, y1 = row[1] >= 0 ? row[1] : p.cache_rows;
                     for (int u = 0; u < units; ++u) {
-                        u64 *full = &c.unit_full[half][slot];
+                        u64 *full = &c.unit_full[half][turn % TURNS];
                         const uint32_t to = ring + slot * UNIT;
                         const int x = u ? (u - 1) * 128 : p.latent / 2;
                         mbar_wait(&c.unit_empty[half][slot], (use + 1) & 1u, &c.abort);
                         mbar_expect_tx(full, UNIT);
                         copy_box(to, units_map, x, y0, full);
                         if (p.tiled == 1) copy_box(to + UNIT / 2, units_map, x, y1, full);
+                        ++turn;
                         if (++slot == S::UNITS) {
                             slot = 0;
                             ++use;
@@ -293,6 +293,7 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                 __syncwarp();
                 slot = __shfl_sync(FULL, slot, 0);
                 use = __shfl_sync(FULL, use, 0);
+                turn = __shfl_sync(FULL, turn, 0);
                 continue;
             }
             const uint64_t all = mask[0] | static_cast<uint64_t>(mask[1]) << 32;
@@ -309,7 +310,8 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                     copy16(to + r * 128 + (((lane ^ r) & 7) << 4),
                            cache + __shfl_sync(FULL, offset[m / 8], r & 31) + x + (lane & 7) * 16, all >> r & 1u);
                 }
-                copies_arrive(&c.unit_full[half][slot]);
+                copies_arrive(&c.unit_full[half][turn % TURNS]);
+                ++turn;
                 if (++slot == S::UNITS) {
                     slot = 0;
                     ++use;
@@ -335,138 +337,141 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (p.tiled && c.abort) {
-        settle(c.unit_full[half], static_cast<int32_t>(use * S::UNITS + slot) - 1, 1, S::UNITS);
+        settle(c.unit_full[half], static_cast<int32_t>(turn) - 1, 1, TURNS);
         settle(c.scales_full[half], static_cast<int32_t>(i) - 1, 1, S::SCALE_SLOTS);
     }
 }
 
-// Units into tensor memory, a row a lane, each warp the rows of its own lanes there;
-// where two groups of warps do it each has 64 bytes of every unit, else the one group
-// has them in turn. 128 values become FP16, the scores' left operand; the key part
-// goes there as it is.
+// Halves of units, 64 bytes of each row, into tensor memory, a row a lane, each warp the
+// rows of its own lanes there; groups of four warps take turns. 128 values become FP16,
+// the scores' left operand; the key part goes there as it is.
 template <int NR>
 __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint32_t tmem) {
     using S = Shape<NR>;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x - S::SOFT) >> 5, quarter = warp & 3, half = quarter >> 1;
-    const int pairs = p.latent / 128, row = (quarter & 1) * 32 + lane;
+    const int pairs = p.latent / 128, parts = 2 + (pairs + 1) / 2 * 2, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT + row * 32;
-    const uint32_t mine = ring + row * 128, turn = (row & 7) << 4;
+    const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT + (row % HALF) * 32;
+    const uint32_t mine = ring + (row % HALF) * 128, turn = (row & 7) << 4;
     Cursor at(c);
-    uint32_t i = 0, slot = 0, use = 0;         // the block; the place of the next unit, and its use
+    uint32_t i = 0, t = warp >> 2;             // the block, and the half unit, that come next
+    int e = t;                                 // its number in the block
     while (at.next(p, lane))
         for (const uint32_t end = i + (at.b1 - at.b0); i < end; ++i) {
             const uint32_t s = i % S::SCALE_SLOTS;
-            for (int u = 0; u < 1 + (pairs + 1) / 2; ++u) {
-                wait(&c.unit_full[half][slot], use, c);
-                if (u == 1) wait(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
-#pragma unroll 1
-                for (int e = S::CONVERT == 2 ? warp >> 2 : 0; e < 2; e += S::CONVERT) {
-                    const int pair = 2 * (u - 1) + e;
-                    uint32_t v[16];
-                    uint2 s8 = make_uint2(0, 0);
+            for (; e < parts; e += S::CONVERT, t += S::CONVERT) {
+                const uint32_t unit = t >> 1, slot = unit % S::UNITS;
+                const int pair = e - 2;
+                uint32_t v[16];
+                uint2 s8 = make_uint2(0, 0);
+                wait(&c.unit_full[half][unit % TURNS], unit / TURNS, c);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 x = shared_vec(mine + slot * UNIT + ((e * 64 + q * 16) ^ turn));
-                        v[4 * q] = x.x;
-                        v[4 * q + 1] = x.y;
-                        v[4 * q + 2] = x.z;
-                        v[4 * q + 3] = x.w;
-                    }
-                    if (u)
-                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                     : "=r"(s8.x), "=r"(s8.y)
-                                     : "r"(scales + s * SCALES + (pair & 3) * 8));
-                    if (e + S::CONVERT >= 2) {
-                        __syncwarp();
-                        if (lane == 0) arrive(&c.unit_empty[half][slot]);
-                    }
-                    if (u == 0) {
-                        const uint32_t key = i % KEY_SLOTS;
-                        wait(&c.key_empty[key], i / KEY_SLOTS + 1, c);
-                        tc_fence_after();
-                        tc_store16(lanes + S::K_COL + key * 32 + e * 16, v);
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive(&c.key_full[key]);
-                    } else if (pair < pairs) {
-                        const uint32_t n = i * pairs + pair, a = n % S::A_PAIRS;
-                        wait(&c.a_empty[a], n / S::A_PAIRS + 1, c);
-                        tc_fence_after();
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {  // 32 values with two scales
-                            const uint32_t two = (q < 2 ? s8.x : s8.y) >> (16 * (q & 1));
-                            uint32_t both, w[16];
-                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(both) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
-                            const __half2 h = *reinterpret_cast<const __half2 *>(&both);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                from_codes(v[4 * q + k], k < 2 ? __low2half2(h) : __high2half2(h), w + 4 * k);
-                            tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
-                        }
-                        const uint32_t bad = __ballot_sync(FULL, ((((s8.x & 0x7F7F7F7Fu) + 0x01010101u) |
-                                                                   ((s8.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u));
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            c.bad[a][quarter] = bad;
-                            arrive(&c.a_full[a]);
-                        }
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 x = shared_vec(mine + slot * UNIT + (((t & 1) * 64 + q * 16) ^ turn));
+                    v[4 * q] = x.x;
+                    v[4 * q + 1] = x.y;
+                    v[4 * q + 2] = x.z;
+                    v[4 * q + 3] = x.w;
                 }
-                if (++slot == S::UNITS) {
-                    slot = 0;
-                    ++use;
+                if (pair >= 0) {
+                    wait(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                 : "=r"(s8.x), "=r"(s8.y)
+                                 : "r"(scales + s * SCALES + (pair & 3) * 8));
+                }
+                __syncwarp();
+                if (lane == 0) arrive(&c.unit_empty[half][slot]);
+                if (pair < 0) {
+                    const uint32_t key = i % KEY_SLOTS;
+                    if (i >= KEY_SLOTS) wait(&c.key_done[(i - KEY_SLOTS) % BLOCKS], (i - KEY_SLOTS) / BLOCKS, c);
+                    tc_fence_after();
+                    tc_store16(lanes + S::K_COL + key * 32 + e * 16, v);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&c.key_full[key]);
+                } else if (pair < pairs) {
+                    const uint32_t n = i * pairs + pair, a = n % S::A_PAIRS;
+                    if (n >= S::A_PAIRS) {
+                        const uint32_t last = n - S::A_PAIRS;
+                        wait(&c.scored[last % TURNS], last / TURNS, c);
+                        wait(&c.copied[last % TURNS], last / TURNS, c);
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {  // 32 values with two scales
+                        const uint32_t two = (q < 2 ? s8.x : s8.y) >> (16 * (q & 1));
+                        uint32_t both, w[16];
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(both) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
+                        const __half2 h = *reinterpret_cast<const __half2 *>(&both);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            from_codes(v[4 * q + k], k < 2 ? __low2half2(h) : __high2half2(h), w + 4 * k);
+                        tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
+                    }
+                    const uint32_t bad = __ballot_sync(FULL, ((((s8.x & 0x7F7F7F7Fu) + 0x01010101u) |
+                                                               ((s8.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u));
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        c.bad[a][quarter] = bad;
+                        arrive(&c.a_full[a]);
+                    }
                 }
             }
-            __syncwarp();
+            e -= parts;
+            // (Also by a warp that read none: its next arrival must not count for this block.)
+            wait(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
             if (lane == 0) arrive(&c.scales_empty[half][s]);
         }
 }
 
 // The sums' left operand: pairs out of tensor memory into shared memory, a chunk's rows
-// of 128 bytes swizzled as the products read them. What waits for its place waits in
-// registers, so that tensor memory is free for the pairs behind it: three places, this
-// one and two in tensor memory hold more than a block, whose scores so never wait for
-// its own sums. A scale of NaN makes every score of its row NaN, and with it the weights
-// of all that see the row; the values become zeros here, so that 0 x NaN does not reach
-// those that may not see it.
+// of 128 bytes swizzled as the products read them; two groups of four warps take turns.
+// What waits for its place waits in registers, so that tensor memory is free for the
+// pairs behind it. A scale of NaN makes every score of its row NaN, and with it the
+// weights of all that see the row; its values become zeros here, so that 0 x NaN does
+// not reach those that may not see it.
 template <int NR>
 __device__ void copy_values(const AttendParams &p, Ctrl &c, char *pairs_at, uint32_t tmem) {
     using S = Shape<NR>;
-    static_assert(S::PAIRS + 1 + S::A_PAIRS >= LATENT_MAX / 128);
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, pairs = p.latent / 128;
-    const int row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - COPY_WARP, quarter = warp & 3;
+    const int row = quarter * 32 + lane, pairs = p.latent / 128;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + S::A_COL;
     Cursor at(c);
-    uint32_t n = 0;
+    uint32_t n = warp >> 2, end = 0;
     while (at.next(p, lane))
-        for (const uint32_t end = n + (at.b1 - at.b0) * pairs; n < end; ++n) {
-            const uint32_t a = n % S::A_PAIRS, slot = n % S::PAIRS;
-            char *to = pairs_at + slot * 2 * CHUNK + row * 128;
-            uint32_t w[64];
+        for (end += (at.b1 - at.b0) * pairs; n < end; n += COPIERS) {
+            const uint32_t a = n % S::A_PAIRS, place = n % S::PAIRS;
+            char *to = pairs_at + place * 2 * CHUNK + row * 128;
+            uint32_t w[4][16];
             wait(&c.a_full[a], n / S::A_PAIRS, c);
             tc_fence_after();
-            tc_load64(lanes + S::A_COL + a * 64, w);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tc_issue16(lanes + a * 64 + q * 16, w[q]);
             const bool bad = c.bad[a][quarter] >> lane & 1u;
             tc_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive(&c.a_empty[a]);
-            if (bad) {
+            if (lane == 0) arrive(&c.copied[n % TURNS]);
+            if (n >= S::PAIRS) wait(&c.summed[(n - S::PAIRS) % TURNS], (n - S::PAIRS) / TURNS, c);
 #pragma unroll
-                for (int k = 0; k < 64; ++k) w[k] = finite_halves(w[k]);
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t *x = w[k / 4] + 4 * (k % 4);
+                *reinterpret_cast<uint4 *>(to + (k >> 3) * CHUNK + (((k ^ row) & 7) << 4)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
             }
-            wait(&c.pair_empty[slot], n / S::PAIRS + 1, c);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                *reinterpret_cast<uint4 *>(to + (k >> 3) * CHUNK + (((k & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            if (bad) {
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {
+                    uint4 *x = reinterpret_cast<uint4 *>(to + (k >> 3) * CHUNK + (k & 7) * 16);
+                    *x = make_uint4(finite_halves(x->x), finite_halves(x->y), finite_halves(x->z), finite_halves(x->w));
+                }
+            }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive(&c.pair_full[slot]);
+            if (lane == 0) arrive(&c.pair_full[place]);
         }
 }
 
@@ -506,7 +511,7 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, uint32_t query, 
                     for (int e = 0; e < 8; ++e)
                         tc_mma_a(d, k + e * 8, qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2, LATENT_KIND,
                                  u > 0 || e > 0);
-                    tc_commit(&c.a_empty[n % S::A_PAIRS]);
+                    tc_commit(&c.scored[n % TURNS]);
                 }
                 mbar_wait(&c.key_full[key], (i / KEY_SLOTS) & 1u, &c.abort);
                 tc_fence_after();
@@ -514,7 +519,7 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, uint32_t query, 
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     tc_mma_a(d, tmem + S::K_COL + key * 32 + e * 8, qk + e * 2, KEY_KIND, true);
-                tc_commit(&c.key_empty[key]);
+                tc_commit(&c.key_done[i % BLOCKS]);
                 tc_commit(&c.s_full[s]);
             }
         }
@@ -546,7 +551,7 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
 #pragma unroll
                     for (int k = 0; k < KEYS / 16; ++k)
                         tc_mma(tmem + S::O_COL + h * NR, v + k * 128, w + k * 128, KIND, b > at.b0 || k > 0);
-                    tc_commit(&c.pair_empty[slot]);
+                    tc_commit(&c.summed[n % TURNS]);
                 }
                 tc_commit(&c.o_done[i % BLOCKS]);
             }
@@ -557,41 +562,43 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
 }
 
 // Scores to weights, the running reference and sums, and the outputs. Each group of
-// four warps has its share of the query rows. Thread t of a group's warp w holds tokens
-// 32 w + t / 4 + 8 h, h < 4, of a block, against the rows 8 j + 2 (t % 4) and the next
-// of its share: their references and sums stay in its registers.
+// four warps has its share of the query rows and goes its own way. Thread t of a
+// group's warp w holds tokens 32 w + t / 4 + 8 h, h < 4, of a block, against the rows
+// 8 j + 2 (t % 4) and the next of its share: their references and sums stay in its
+// registers. Whether a score outgrows its reference is voted on before the exponentials:
+// the scores' place is free from then on.
 template <int NR>
 __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_at, char *weights_at, uint32_t tmem) {
     using S = Shape<NR>;
-    constexpr int SOFT = S::SOFT, SHARE = NR / S::GROUPS, N = SHARE / 4;   // query rows of a group, a thread
-    const int tid = threadIdx.x, lane = tid & 31, w = (tid >> 5) & 3, group = tid >> 7, quad = lane & 3;
+    constexpr int SHARE = NR / S::GROUPS, N = SHARE / 4;   // query rows of a group, of a thread
+    const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, lane = tid & 31, w = tid >> 5, quad = lane & 3;
+    const int r0 = group * SHARE, mine_row = r0 + tid;     // the group's first row; a row of a thread < SHARE
     const int t0 = w * 32 + lane / 4, pairs = p.latent / 128;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
     Part *parts = reinterpret_cast<Part *>(p.workspace);
     Joint *joints = reinterpret_cast<Joint *>(parts + 2 * p.sms);
     const bool by_tile = p.tiles <= static_cast<int32_t>(gridDim.x);
-    auto row_of = [&](int n) { return group * SHARE + 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
+    auto row_of = [&](int n) { return r0 + 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
     bool split_here = false;
     Cursor at(c);
     uint32_t i = 0;
     long long done = c.begin;
     bool more = at.next(p, lane);
-    if (more) load_query<NR>(p, at.tile, c, query, tid);
+    if (more) load_query<NR>(p, at.tile, c, query, group, tid);
     while (more) {
         const int32_t start = at.b0 * KEYS;
         // A row that sees nothing of this piece has an infinite reference: whatever its
         // scores, its weights never move it, and its results are written as empty.
-        if (tid < ROWS) {
+        if (tid < SHARE) {
             int32_t lim = 0;
-            if (tid < at.tile.rows) lim = p.paged ? token_len(p, (at.tile.base + tid) / p.heads) : INT32_MAX;
-            c.lim[tid] = lim;
-            c.ref[tid] = lim > start ? LOWEST : INFINITY;
+            if (mine_row < at.tile.rows) lim = p.paged ? token_len(p, (at.tile.base + mine_row) / p.heads) : INT32_MAX;
+            c.lim[mine_row] = lim;
+            c.ref[mine_row] = lim > start ? LOWEST : INFINITY;
         }
-        soft_sync<SOFT>();
+        group_sync(group);
         int32_t low = INT32_MAX;
-#pragma unroll
-        for (int r = 0; r < ROWS; r += 32) {
-            const int32_t lim = c.lim[r + lane];
+        for (int r = lane; r < SHARE; r += 32) {
+            const int32_t lim = c.lim[r0 + r];
             low = min(low, lim > start ? lim : INT32_MAX);
         }
         low = __reduce_min_sync(FULL, low);
@@ -608,129 +615,123 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             wait(&c.row_full[i % BLOCKS], i / BLOCKS, c);
             const uint32_t marks = c.marks[i % BLOCKS][w] >> (lane / 4);   // bit 8 h: token h is there
             const bool whole = __all_sync(FULL, (marks & 0x01010101u) == 0x01010101u) && (b + 1) * KEYS <= low;
-            const uint32_t scores = lanes + S::S_COL + s * NR + group * SHARE;
+            const uint32_t scores = lanes + S::S_COL + s * NR + r0;
             char *weights = weights_at + i % S::WEIGHTS * CHUNK + t0 * 128 + quad * 4;
             float x[2][2 * N];                 // x[g][4 j + 2 h + e]: token 2 g + h, the thread's row 2 j + e
-            auto load = [&]() {
-                tc_load_groups<SHARE / 8>(scores, x[0]);
-                tc_load_groups<SHARE / 8>(scores + (16u << 16), x[1]);
+            // Scores in log2 units less `less` (none, or the references); where masked, -inf.
+            auto take = [&](auto less) {
+                uint32_t u[2][2 * N];
+                tc_issue_groups<SHARE / 8>(scores, u[0]);
+                tc_issue_groups<SHARE / 8>(scores + (16u << 16), u[1]);
+                tc_wait_ld();
                 tc_fence_before();
-            };
-            // Scores in log2 units; where masked, -inf.
-            auto take = [&]() {
-                load();
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
-                    for (int e = 0; e < 2 * N; ++e) {
-                        float &v = x[g][e];
-                        const int n = 2 * (e >> 2) + (e & 1), h = 2 * g + ((e >> 1) & 1);
-                        v *= unit[n];
-                        if (!whole) v = (marks >> 8 * h & 1u) && token + 8 * h < c.lim[row_of(n)] ? v : -INFINITY;
+                    for (int k = 0; k < 2 * N; ++k) {
+                        const int n = 2 * (k >> 2) + (k & 1);
+                        const float v = __uint_as_float(u[g][k]);
+                        x[g][k] = decltype(less)::value ? fmaf(v, unit[n], -ref[n]) : v * unit[n];
                     }
-            };
-            // Weights from scores (or from the unscaled scores of a whole block), rounded once
-            // to FP16 for the tensor cores; true if one outgrew the reference.
-            auto weigh = [&](auto unscaled) -> bool {
-                __half2 top = __floats2half2_rn(0.0f, 0.0f);
+                if (whole) return;
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
-                    for (int j = 0; j < N / 2; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float &a = x[g][4 * j + 2 * h], &d = x[g][4 * j + 2 * h + 1];
-                            if constexpr (decltype(unscaled)::value) {
-                                a = exp2_fast(fmaf(a, unit[2 * j], -ref[2 * j]));
-                                d = exp2_fast(fmaf(d, unit[2 * j + 1], -ref[2 * j + 1]));
-                            } else {
-                                a = exp2_fast(a - ref[2 * j]);
-                                d = exp2_fast(d - ref[2 * j + 1]);
-                            }
-                            const __half2 v = __floats2half2_rn(a, d);
-                            top = __hmax2(top, v);
-                            const int at_row = (group * (SHARE / 8) + j) ^ (t0 & 7);
-                            *reinterpret_cast<__half2 *>(weights + (2 * g + h) * 1024 + (at_row << 4)) = v;
-                        }
-                return fmaxf(__low2float(top), __high2float(top)) > 32768.0f;   // 2^MOST
+                    for (int k = 0; k < 2 * N; ++k) {
+                        const int n = 2 * (k >> 2) + (k & 1), h = 2 * g + ((k >> 1) & 1);
+                        if (!((marks >> 8 * h & 1u) && token + 8 * h < c.lim[row_of(n)])) x[g][k] = -INFINITY;
+                    }
             };
             mbar_wait(&c.s_full[s], (i / S::SCORES) & 1u, &c.abort);
             __syncwarp();
-            if (i >= S::WEIGHTS) {             // (the weights' place is free)
-                const uint32_t last = i - S::WEIGHTS;
-                wait(&c.o_done[last % BLOCKS], last / BLOCKS, c);
-            }
             tc_fence_after();
             bool moved = true;
-            if (b == at.b0) {
-                take();
-            } else if (whole) {
-                load();
-                moved = soft_any<SOFT>(weigh(std::true_type{}));
-            } else {
-                take();
-                moved = soft_any<SOFT>(weigh(std::false_type{}));
+            if (b > at.b0) {
+                take(std::true_type{});
+                float top = x[0][0];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int k = 0; k < 2 * N; ++k) top = fmaxf(top, x[g][k]);
+                moved = group_any(group, top > MOST);
             }
             if (moved) {
                 // New references where the rows' largest scores of this block are 2^MOST above
                 // the old ones (or the first the row sees).
-                if (b > at.b0) take();
+                take(std::false_type{});
                 float top[N];
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const int e = 4 * (n >> 1) + (n & 1);
-                    top[n] = fmaxf(fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2]));
+                    const int k = 4 * (n >> 1) + (n & 1);
+                    top[n] = fmaxf(fmaxf(x[0][k], x[0][k + 2]), fmaxf(x[1][k], x[1][k + 2]));
                 }
                 across_lanes<N>(top, [](float a, float d) { return fmaxf(a, d); });
                 const int mine = across_index<N>();
 #pragma unroll
                 for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = top[j];
-                soft_sync<SOFT>();
-                if (tid < NR) {
-                    const float t = fmaxf(fmaxf(c.across[0][tid], c.across[1][tid]),
-                                          fmaxf(c.across[2][tid], c.across[3][tid]));
-                    const float old = c.ref[tid];
+                group_sync(group);
+                if (tid < SHARE) {
+                    const float t = fmaxf(fmaxf(c.across[0][mine_row], c.across[1][mine_row]),
+                                          fmaxf(c.across[2][mine_row], c.across[3][mine_row]));
+                    const float old = c.ref[mine_row];
                     const bool move = t > old + MOST;  // (of LOWEST: t > old)
-                    c.factor[tid] = move ? exp2_fast(old - (t - BELOW)) : 1.0f;
-                    if (move) c.ref[tid] = t - BELOW;
+                    c.factor[mine_row] = move ? exp2_fast(old - (t - BELOW)) : 1.0f;
+                    if (move) c.ref[mine_row] = t - BELOW;
                 }
-                soft_sync<SOFT>();
+                group_sync(group);
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     ref[n] = c.ref[row_of(n)];
                     l[n] *= c.factor[row_of(n)];
                 }
-                weigh(std::false_type{});
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int k = 0; k < 2 * N; ++k) x[g][k] -= ref[2 * (k >> 2) + (k & 1)];
                 if (b > at.b0) {
                     wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
                     tc_fence_after();
+#pragma unroll 1
                     for (int h = 0; h < pairs; ++h)
-#pragma unroll
-                        for (int v = 0; v < NR; v += 16) {
-                            if (((h * (NR / 16) + v / 16) & (S::GROUPS - 1)) != group) continue;
+#pragma unroll 1
+                        for (int v = r0; v < r0 + SHARE; v += 16) {
                             float o[16], f[16];
                             shared16(&c.factor[v], f);
                             tc_load16(lanes + S::O_COL + h * NR + v, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f[e];
+                            for (int k = 0; k < 16; ++k) o[k] *= f[k];
                             latent::tc_store16(lanes + S::O_COL + h * NR + v, o);
                         }
                     tc_wait_st();
                     tc_fence_before();
                 }
             }
+            __syncwarp();
+            if (lane == 0) arrive(&c.s_empty[s]);
+            if (i >= S::WEIGHTS) {             // (the weights' place is free)
+                const uint32_t last = i - S::WEIGHTS;
+                wait(&c.o_done[last % BLOCKS], last / BLOCKS, c);
+            }
+            // Weights, rounded once to FP16 for the tensor cores; their sums are of the unrounded
+            // ones, in 32 bits.
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const int at_row = (group * (SHARE / 8) + j) ^ (t0 & 7);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float a = exp2_fast(x[g][4 * j + 2 * h]), d = exp2_fast(x[g][4 * j + 2 * h + 1]);
+                        l[2 * j] += a;
+                        l[2 * j + 1] += d;
+                        *reinterpret_cast<__half2 *>(weights + (2 * g + h) * 1024 + (at_row << 4)) =
+                            __floats2half2_rn(a, d);
+                    }
+            }
+            tc_fence_before();
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) {
-                arrive(&c.s_empty[s]);
-                arrive(&c.p_full[i % BLOCKS]);
-            }
-            // The sums are of the unrounded weights, in 32 bits.
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int e = 4 * (n >> 1) + (n & 1);
-                l[n] += (x[0][e] + x[0][e + 2]) + (x[1][e] + x[1][e + 2]);
-            }
+            if (lane == 0) arrive(&c.p_full[i % BLOCKS]);
         }
         // The piece is done: the next one's query rows (the last scores are read), then this
         // one's rows, or its part of them.
@@ -740,69 +741,65 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
         const int mine = across_index<N>();
 #pragma unroll
         for (int j = 0; j < (N + 7) / 8; ++j) c.across[w][row_of(mine + j)] = l[j];
-        soft_sync<SOFT>();
-        if (again) load_query<NR>(p, then.tile, c, query, tid);
-        if (tid < NR) {
-            const bool sees = c.lim[tid] > start;
-            const float sum = c.across[0][tid] + c.across[1][tid] + c.across[2][tid] + c.across[3][tid];
-            c.l[tid] = sees ? sum : 0.0f;
-            c.factor[tid] = sees && sum != 0.0f ? 1.0f / sum : 0.0f;   // (0: an empty row, whatever its sums)
-            if (!sees) c.ref[tid] = -INFINITY;
+        group_sync(group);
+        if (again) load_query<NR>(p, then.tile, c, query, group, tid);
+        if (tid < SHARE) {
+            const bool sees = c.lim[mine_row] > start;
+            const float sum = c.across[0][mine_row] + c.across[1][mine_row] + c.across[2][mine_row] +
+                              c.across[3][mine_row];
+            c.l[mine_row] = sees ? sum : 0.0f;
+            c.factor[mine_row] = sees && sum != 0.0f ? 1.0f / sum : 0.0f;   // (0: an empty row, whatever its sums)
+            if (!sees) c.ref[mine_row] = -INFINITY;
         }
-        soft_sync<SOFT>();
+        group_sync(group);
         wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
         tc_fence_after();
         const bool direct = at.b0 == 0 && at.b1 == at.blocks;
         if (direct) {
-            if (p.lse && tid < at.tile.rows) p.lse[at.tile.base + tid] = finished_lse(c.ref[tid], c.l[tid]);
+            if (p.lse && tid < SHARE && mine_row < at.tile.rows)
+                p.lse[at.tile.base + mine_row] = finished_lse(c.ref[mine_row], c.l[mine_row]);
             // A lane has one value of 16 rows; two lanes trade theirs for pairs of one row each.
-            const bool odd = (lane & 1) != 0;
+            const bool odd = (lane & 1) != 0, all = at.tile.rows == NR;
             uint16_t *out = p.out + (static_cast<int64_t>(at.tile.base) + (lane & 1)) * p.latent + w * 32 + (lane & ~1);
-            auto write = [&](auto all) {
-                for (int h = 0; h < pairs; ++h)
-#pragma unroll
-                    for (int v = 0; v < NR; v += 16) {
-                        if (((h * (NR / 16) + v / 16) & (S::GROUPS - 1)) != group) continue;
-                        float o[16], f[16];
-                        shared16(&c.factor[v], f);
-                        tc_load16(lanes + S::O_COL + h * NR + v, o);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float x = f[e] == 0.0f ? 0.0f : o[e] * f[e];
-                            const float y = f[e + 1] == 0.0f ? 0.0f : o[e + 1] * f[e + 1];
-                            const float other = __shfl_xor_sync(FULL, odd ? x : y, 1);
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(odd ? other : x, odd ? y : other);
-                            if (decltype(all)::value || v + e + (lane & 1) < at.tile.rows)
-                                *reinterpret_cast<__nv_bfloat162 *>(
-                                    out + static_cast<uint32_t>((v + e) * p.latent + h * 128)) = two;
-                        }
-                    }
-            };
-            if (at.tile.rows == NR)
-                write(std::true_type{});
-            else
-                write(std::false_type{});
-        } else {
-            // In a cluster the ring is used up: this CTA's part stays there for the others to join.
-            Part &part = parts[2 * blockIdx.x + (at.b0 == 0 ? 1 : 0)];
-            float *sums = p.cluster ? reinterpret_cast<float *>(pairs_at) : part.sum;
-            if (!p.cluster && tid < NR) {
-                part.m[tid] = c.ref[tid];
-                part.l[tid] = c.l[tid];
-            }
+#pragma unroll 1
             for (int h = 0; h < pairs; ++h)
-#pragma unroll
-                for (int v = 0; v < NR; v += 16) {
-                    if (((h * (NR / 16) + v / 16) & (S::GROUPS - 1)) != group) continue;
+#pragma unroll 1
+                for (int v = r0; v < r0 + SHARE; v += 16) {
                     float o[16], f[16];
                     shared16(&c.factor[v], f);
                     tc_load16(lanes + S::O_COL + h * NR + v, o);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        sums[(v + e) * p.latent + h * 128 + w * 32 + lane] = f[e] == 0.0f ? 0.0f : o[e];
+                    for (int k = 0; k < 16; k += 2) {
+                        const float x = f[k] == 0.0f ? 0.0f : o[k] * f[k];
+                        const float y = f[k + 1] == 0.0f ? 0.0f : o[k + 1] * f[k + 1];
+                        const float other = __shfl_xor_sync(FULL, odd ? x : y, 1);
+                        const __nv_bfloat162 two = __floats2bfloat162_rn(odd ? other : x, odd ? y : other);
+                        if (all || v + k + (lane & 1) < at.tile.rows)
+                            *reinterpret_cast<__nv_bfloat162 *>(
+                                out + static_cast<uint32_t>((v + k) * p.latent + h * 128)) = two;
+                    }
+                }
+        } else {
+            // In a cluster the rings are used up: this CTA's part stays there for the others to join.
+            Part &part = parts[2 * blockIdx.x + (at.b0 == 0 ? 1 : 0)];
+            float *sums = p.cluster ? reinterpret_cast<float *>(pairs_at) : part.sum;
+            if (!p.cluster && tid < SHARE) {
+                part.m[mine_row] = c.ref[mine_row];
+                part.l[mine_row] = c.l[mine_row];
+            }
+#pragma unroll 1
+            for (int h = 0; h < pairs; ++h)
+#pragma unroll 1
+                for (int v = r0; v < r0 + SHARE; v += 16) {
+                    float o[16], f[16];
+                    shared16(&c.factor[v], f);
+                    tc_load16(lanes + S::O_COL + h * NR + v, o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        sums[(v + k) * p.latent + h * 128 + w * 32 + lane] = f[k] == 0.0f ? 0.0f : o[k];
                 }
         }
-        if (!p.cluster && at.b0 == 0 && tid == 0 && (by_tile || !direct)) {
+        if (!p.cluster && at.b0 == 0 && threadIdx.x == 0 && (by_tile || !direct)) {
             Joint j;
             j.tile = at.next_tile - 1;
             j.cta = static_cast<int32_t>(blockIdx.x);
@@ -813,11 +810,11 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
         split_here |= at.b0 == 0 && !direct;
         done += at.u1 - at.u0;
         tc_fence_before();
-        soft_sync<SOFT>();
+        group_sync(group);
         at = then;
         more = again;
     }
-    if (!p.cluster && !by_tile && !split_here && tid == 0) joints[blockIdx.x] = Joint{0, 0, 0, 0};
+    if (!p.cluster && !by_tile && !split_here && threadIdx.x == 0) joints[blockIdx.x] = Joint{0, 0, 0, 0};
 }
 
 template <int NR>
@@ -831,34 +828,29 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
     Ctrl &c = *reinterpret_cast<Ctrl *>(pairs + S::RINGS);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S::PAIRS; ++s) {
-            mbar_init(&c.pair_full[s], 4);
-            mbar_init(&c.pair_empty[s], 1);
-        }
-        for (int s = 0; s < S::A_PAIRS; ++s) {
-            mbar_init(&c.a_full[s], 4);
-            mbar_init(&c.a_empty[s], 5);
+        for (int s = 0; s < S::PAIRS; ++s) mbar_init(&c.pair_full[s], 4);
+        for (int s = 0; s < S::A_PAIRS; ++s) mbar_init(&c.a_full[s], 4);
+        for (int s = 0; s < TURNS; ++s) {
+            mbar_init(&c.scored[s], 1);
+            mbar_init(&c.copied[s], 4);
+            mbar_init(&c.summed[s], 1);
         }
         for (int h = 0; h < 2; ++h) {
-            for (int s = 0; s < S::UNITS; ++s) {
-                mbar_init(&c.unit_full[h][s], p.tiled ? 1 : 32);
-                mbar_init(&c.unit_empty[h][s], 2 * S::CONVERT);
-            }
+            for (int s = 0; s < TURNS; ++s) mbar_init(&c.unit_full[h][s], p.tiled ? 1 : 32);
+            for (int s = 0; s < S::UNITS; ++s) mbar_init(&c.unit_empty[h][s], 4);
             for (int s = 0; s < S::SCALE_SLOTS; ++s) {
                 mbar_init(&c.scales_full[h][s], p.tiled ? 1 : 32);
                 mbar_init(&c.scales_empty[h][s], 2 * S::CONVERT);
             }
         }
-        for (int s = 0; s < KEY_SLOTS; ++s) {
-            mbar_init(&c.key_full[s], 8);
-            mbar_init(&c.key_empty[s], 1);
-        }
+        for (int s = 0; s < KEY_SLOTS; ++s) mbar_init(&c.key_full[s], 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&c.s_full[s], 1);
             mbar_init(&c.s_empty[s], S::SOFT / 32);
             mbar_init(&c.drain[s], 1);
         }
         for (int s = 0; s < BLOCKS; ++s) {
+            mbar_init(&c.key_done[s], 1);
             mbar_init(&c.row_full[s], 2);
             mbar_init(&c.p_full[s], S::SOFT / 32);
             mbar_init(&c.o_done[s], 1);

@@ -94,9 +94,9 @@ __host__ __device__ constexpr uint32_t instruction(int m, int n, bool along) {
 // Eight columns of this warp's first 16 lanes, N groups of them: thread t gets
 // of group j the values of lane t / 4 (v[4 j], v[4 j + 1]) and of lane t / 4 + 8
 // (v[4 j + 2], v[4 j + 3]) at columns 8 j + 2 (t % 4) and the next.
+// (tc_issue_groups: to be waited for.)
 template <int N>
-__device__ __forceinline__ void tc_load_groups(uint32_t addr, float (&v)[4 * N]) {
-    uint32_t r[4 * N];
+__device__ __forceinline__ void tc_issue_groups(uint32_t addr, uint32_t (&r)[4 * N]) {
     if constexpr (N == 1)
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -111,6 +111,12 @@ __device__ __forceinline__ void tc_load_groups(uint32_t addr, float (&v)[4 * N])
             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
               "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
             : "r"(addr));
+}
+
+template <int N>
+__device__ __forceinline__ void tc_load_groups(uint32_t addr, float (&v)[4 * N]) {
+    uint32_t r[4 * N];
+    tc_issue_groups<N>(addr, r);
     tc_wait_ld();
 #pragma unroll
     for (int i = 0; i < 4 * N; ++i) v[i] = __uint_as_float(r[i]);
