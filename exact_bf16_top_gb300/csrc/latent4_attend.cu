@@ -67,7 +67,7 @@ struct Shape {
 struct Ctrl : Schedule<NT> {
     u64 unit_full[2][TURNS], unit_empty[2][3]; // a half's unit is in / read
     u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in / read
-    u64 a_full[4], scored[TURNS], copied[TURNS];   // a pair is in tensor memory / its scores are added, it is read
+    u64 a_full[4], a_done[TURNS];              // a pair is in tensor memory / its scores are added and it is copied
     u64 pair_full[3], summed[TURNS];           // a pair is in shared memory / its sums are added
     u64 key_full[KEY_SLOTS], key_done[BLOCKS]; // a block's key part is in tensor memory / its scores are added
     u64 s_full[2], s_empty[2];                 // scores written / read
@@ -99,6 +99,20 @@ constexpr bool fits() {
     return 1024 + query_bytes<NR>(LATENT_MAX) + Shape<NR>::RINGS + sizeof(Ctrl) <= SMEM;
 }
 static_assert(fits<16>() && fits<32>() && fits<64>());
+
+// As mbar_wait() and wait(), in fewer instructions where there is nothing to wait for.
+__device__ __forceinline__ void await(u64 *bar, uint32_t parity, Ctrl &c) {
+    if (!mbar_try_wait(bar, parity & 1u)) [[unlikely]] mbar_wait(bar, parity & 1u, &c.abort);
+}
+
+__device__ __forceinline__ void await_warp(u64 *bar, uint32_t parity, Ctrl &c) {
+    await(bar, parity, c);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void store_vec(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 
 __device__ __forceinline__ void tc_mma_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
@@ -269,7 +283,7 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                         u64 *full = &c.unit_full[half][turn % TURNS];
                         const uint32_t to = ring + slot * UNIT;
                         const int x = u ? (u - 1) * 128 : p.latent / 2;
-                        mbar_wait(&c.unit_empty[half][slot], (use + 1) & 1u, &c.abort);
+                        await(&c.unit_empty[half][slot], (use + 1) & 1u, c);
                         mbar_expect_tx(full, UNIT);
                         copy_box(to, units_map, x, y0, full);
                         if (p.tiled == 1) copy_box(to + UNIT / 2, units_map, x, y1, full);
@@ -280,7 +294,7 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                         }
                         if (u == 0) {
                             full = &c.scales_full[half][s];
-                            mbar_wait(&c.scales_empty[half][s], (i / S::SCALE_SLOTS + 1) & 1u, &c.abort);
+                            await(&c.scales_empty[half][s], (i / S::SCALE_SLOTS + 1) & 1u, c);
                             mbar_expect_tx(full, SCALES);
                             copy_box(scales + s * SCALES, scales_map, p.latent / 2 + 128, y0, full);
                             if (p.tiled == 1) copy_box(scales + s * SCALES + SCALES / 2, scales_map, p.latent / 2 + 128, y1, full);
@@ -303,7 +317,7 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                 const uint32_t to = ring + slot * UNIT;
                 const int x = u ? (u - 1) * 128 : p.latent / 2;
                 // Eight lanes a row, four rows a copy.
-                wait(&c.unit_empty[half][slot], use + 1, c);
+                await_warp(&c.unit_empty[half][slot], use + 1, c);
 #pragma unroll
                 for (int m = 0; m < HALF / 4; ++m) {
                     const int r = 4 * m + (lane >> 3);
@@ -317,7 +331,7 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                     ++use;
                 }
                 if (u == 0) {
-                    wait(&c.scales_empty[half][s], i / S::SCALE_SLOTS + 1, c);
+                    await_warp(&c.scales_empty[half][s], i / S::SCALE_SLOTS + 1, c);
 #pragma unroll
                     for (int m = 0; m < HALF / 16; ++m) {
                         const int r = 16 * m + (lane >> 1);
@@ -364,7 +378,7 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
                 const int pair = e - 2;
                 uint32_t v[16];
                 uint2 s8 = make_uint2(0, 0);
-                wait(&c.unit_full[half][unit % TURNS], unit / TURNS, c);
+                await_warp(&c.unit_full[half][unit % TURNS], unit / TURNS, c);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint4 x = shared_vec(mine + slot * UNIT + (((t & 1) * 64 + q * 16) ^ turn));
@@ -374,7 +388,7 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
                     v[4 * q + 3] = x.w;
                 }
                 if (pair >= 0) {
-                    wait(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
+                    await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
                     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
                                  : "=r"(s8.x), "=r"(s8.y)
                                  : "r"(scales + s * SCALES + (pair & 3) * 8));
@@ -383,7 +397,7 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
                 if (lane == 0) arrive(&c.unit_empty[half][slot]);
                 if (pair < 0) {
                     const uint32_t key = i % KEY_SLOTS;
-                    if (i >= KEY_SLOTS) wait(&c.key_done[(i - KEY_SLOTS) % BLOCKS], (i - KEY_SLOTS) / BLOCKS, c);
+                    if (i >= KEY_SLOTS) await_warp(&c.key_done[(i - KEY_SLOTS) % BLOCKS], (i - KEY_SLOTS) / BLOCKS, c);
                     tc_fence_after();
                     tc_store16(lanes + S::K_COL + key * 32 + e * 16, v);
                     tc_wait_st();
@@ -394,8 +408,7 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
                     const uint32_t n = i * pairs + pair, a = n % S::A_PAIRS;
                     if (n >= S::A_PAIRS) {
                         const uint32_t last = n - S::A_PAIRS;
-                        wait(&c.scored[last % TURNS], last / TURNS, c);
-                        wait(&c.copied[last % TURNS], last / TURNS, c);
+                        await_warp(&c.a_done[last % TURNS], last / TURNS, c);
                     }
                     tc_fence_after();
 #pragma unroll
@@ -422,7 +435,7 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
             }
             e -= parts;
             // (Also by a warp that read none: its next arrival must not count for this block.)
-            wait(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
+            await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
             if (lane == 0) arrive(&c.scales_empty[half][s]);
         }
 }
@@ -434,19 +447,20 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
 // weights of all that see the row; its values become zeros here, so that 0 x NaN does
 // not reach those that may not see it.
 template <int NR>
-__device__ void copy_values(const AttendParams &p, Ctrl &c, char *pairs_at, uint32_t tmem) {
+__device__ void copy_values(const AttendParams &p, Ctrl &c, uint32_t pairs_at, uint32_t tmem) {
     using S = Shape<NR>;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - COPY_WARP, quarter = warp & 3;
     const int row = quarter * 32 + lane, pairs = p.latent / 128;
+    const uint32_t mine = pairs_at + row * 128 + ((row & 7) << 4);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + S::A_COL;
     Cursor at(c);
     uint32_t n = warp >> 2, end = 0;
     while (at.next(p, lane))
         for (end += (at.b1 - at.b0) * pairs; n < end; n += COPIERS) {
             const uint32_t a = n % S::A_PAIRS, place = n % S::PAIRS;
-            char *to = pairs_at + place * 2 * CHUNK + row * 128;
+            const uint32_t to = mine + place * 2 * CHUNK;
             uint32_t w[4][16];
-            wait(&c.a_full[a], n / S::A_PAIRS, c);
+            await_warp(&c.a_full[a], n / S::A_PAIRS, c);
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < 4; ++q) tc_issue16(lanes + a * 64 + q * 16, w[q]);
@@ -454,19 +468,19 @@ __device__ void copy_values(const AttendParams &p, Ctrl &c, char *pairs_at, uint
             tc_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive(&c.copied[n % TURNS]);
-            if (n >= S::PAIRS) wait(&c.summed[(n - S::PAIRS) % TURNS], (n - S::PAIRS) / TURNS, c);
+            if (lane == 0) arrive(&c.a_done[n % TURNS]);
+            if (n >= S::PAIRS) await_warp(&c.summed[(n - S::PAIRS) % TURNS], (n - S::PAIRS) / TURNS, c);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const uint32_t *x = w[k / 4] + 4 * (k % 4);
-                *reinterpret_cast<uint4 *>(to + (k >> 3) * CHUNK + (((k ^ row) & 7) << 4)) =
-                    make_uint4(x[0], x[1], x[2], x[3]);
+                store_vec((to ^ ((k & 7) << 4)) + (k >> 3) * CHUNK, x[0], x[1], x[2], x[3]);
             }
-            if (bad) {
+            if (bad) [[unlikely]] {
 #pragma unroll 1
                 for (int k = 0; k < 16; ++k) {
-                    uint4 *x = reinterpret_cast<uint4 *>(to + (k >> 3) * CHUNK + (k & 7) * 16);
-                    *x = make_uint4(finite_halves(x->x), finite_halves(x->y), finite_halves(x->z), finite_halves(x->w));
+                    const uint32_t at16 = (to ^ ((k & 7) << 4)) + (k >> 3) * CHUNK;
+                    const uint4 x = shared_vec(at16);
+                    store_vec(at16, finite_halves(x.x), finite_halves(x.y), finite_halves(x.z), finite_halves(x.w));
                 }
             }
             fence_proxy_async();
@@ -497,13 +511,10 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, uint32_t query, 
         if (one) {
             for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
                 const uint32_t s = i % S::SCORES, d = tmem + S::S_COL + s * NR, key = i % KEY_SLOTS;
-                mbar_wait(&c.s_empty[s], (i / S::SCORES + 1) & 1u, &c.abort);
-                if (b == at.b0) {
-                    mbar_wait(&c.q_full, piece & 1u, &c.abort);
-                    fence_proxy_async();
-                }
+                await(&c.s_empty[s], (i / S::SCORES + 1) & 1u, c);
+                if (b == at.b0) await(&c.q_full, piece & 1u, c);
                 for (int u = 0; u < pairs; ++u, ++n) {
-                    mbar_wait(&c.a_full[n % S::A_PAIRS], (n / S::A_PAIRS) & 1u, &c.abort);
+                    await(&c.a_full[n % S::A_PAIRS], (n / S::A_PAIRS) & 1u, c);
                     tc_fence_after();
                     const uint32_t k = tmem + S::A_COL + n % S::A_PAIRS * 64;
                     const uint64_t qu = q + u * (2 * QCHUNK >> 4);
@@ -511,9 +522,9 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, uint32_t query, 
                     for (int e = 0; e < 8; ++e)
                         tc_mma_a(d, k + e * 8, qu + (e >> 2) * (QCHUNK >> 4) + (e & 3) * 2, LATENT_KIND,
                                  u > 0 || e > 0);
-                    tc_commit(&c.scored[n % TURNS]);
+                    tc_commit(&c.a_done[n % TURNS]);
                 }
-                mbar_wait(&c.key_full[key], (i / KEY_SLOTS) & 1u, &c.abort);
+                await(&c.key_full[key], (i / KEY_SLOTS) & 1u, c);
                 tc_fence_after();
                 const uint64_t qk = q + pairs * (2 * QCHUNK >> 4);
 #pragma unroll
@@ -540,12 +551,11 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
     while (at.next(p, lane)) {
         if (one) {
             for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
-                mbar_wait(&c.p_full[i % BLOCKS], (i / BLOCKS) & 1u, &c.abort);
+                await(&c.p_full[i % BLOCKS], (i / BLOCKS) & 1u, c);
                 const uint64_t w = matrix(weights + i % S::WEIGHTS * CHUNK, 16);
                 for (int h = 0; h < pairs; ++h, ++n) {
                     const uint32_t slot = n % S::PAIRS;
-                    mbar_wait(&c.pair_full[slot], (n / S::PAIRS) & 1u, &c.abort);
-                    fence_proxy_async();
+                    await(&c.pair_full[slot], (n / S::PAIRS) & 1u, c);
                     tc_fence_after();
                     const uint64_t v = matrix(pairs_at + slot * 2 * CHUNK, CHUNK);
 #pragma unroll
@@ -568,7 +578,7 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
 // registers. Whether a score outgrows its reference is voted on before the exponentials:
 // the scores' place is free from then on.
 template <int NR>
-__device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_at, char *weights_at, uint32_t tmem) {
+__device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_at, uint32_t weights_at, uint32_t tmem) {
     using S = Shape<NR>;
     constexpr int SHARE = NR / S::GROUPS, N = SHARE / 4;   // query rows of a group, of a thread
     const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, lane = tid & 31, w = tid >> 5, quad = lane & 3;
@@ -579,6 +589,8 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
     Joint *joints = reinterpret_cast<Joint *>(parts + 2 * p.sms);
     const bool by_tile = p.tiles <= static_cast<int32_t>(gridDim.x);
     auto row_of = [&](int n) { return r0 + 8 * (n >> 1) + 2 * quad + (n & 1); };   // of the thread's n-th
+    // Where the thread's weights go: of its first token, its first rows (the others' a constant away).
+    weights_at += t0 * 128 + quad * 4 + (((group * (SHARE / 8)) ^ (t0 & 7)) << 4);
     bool split_here = false;
     Cursor at(c);
     uint32_t i = 0;
@@ -612,11 +624,11 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
         for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
             const uint32_t s = i % S::SCORES;
             const int32_t token = b * KEYS + t0;
-            wait(&c.row_full[i % BLOCKS], i / BLOCKS, c);
+            await_warp(&c.row_full[i % BLOCKS], i / BLOCKS, c);
             const uint32_t marks = c.marks[i % BLOCKS][w] >> (lane / 4);   // bit 8 h: token h is there
             const bool whole = __all_sync(FULL, (marks & 0x01010101u) == 0x01010101u) && (b + 1) * KEYS <= low;
             const uint32_t scores = lanes + S::S_COL + s * NR + r0;
-            char *weights = weights_at + i % S::WEIGHTS * CHUNK + t0 * 128 + quad * 4;
+            const uint32_t weights = weights_at + i % S::WEIGHTS * CHUNK;
             float x[2][2 * N];                 // x[g][4 j + 2 h + e]: token 2 g + h, the thread's row 2 j + e
             // Scores in log2 units less `less` (none, or the references); where masked, -inf.
             auto take = [&](auto less) {
@@ -642,7 +654,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                         if (!((marks >> 8 * h & 1u) && token + 8 * h < c.lim[row_of(n)])) x[g][k] = -INFINITY;
                     }
             };
-            mbar_wait(&c.s_full[s], (i / S::SCORES) & 1u, &c.abort);
+            await(&c.s_full[s], (i / S::SCORES) & 1u, c);
             __syncwarp();
             tc_fence_after();
             bool moved = true;
@@ -689,7 +701,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
 #pragma unroll
                     for (int k = 0; k < 2 * N; ++k) x[g][k] -= ref[2 * (k >> 2) + (k & 1)];
                 if (b > at.b0) {
-                    wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
+                    await_warp(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
                     tc_fence_after();
 #pragma unroll 1
                     for (int h = 0; h < pairs; ++h)
@@ -710,22 +722,23 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             if (lane == 0) arrive(&c.s_empty[s]);
             if (i >= S::WEIGHTS) {             // (the weights' place is free)
                 const uint32_t last = i - S::WEIGHTS;
-                wait(&c.o_done[last % BLOCKS], last / BLOCKS, c);
+                await_warp(&c.o_done[last % BLOCKS], last / BLOCKS, c);
             }
             // Weights, rounded once to FP16 for the tensor cores; their sums are of the unrounded
             // ones, in 32 bits.
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
-                const int at_row = (group * (SHARE / 8) + j) ^ (t0 & 7);
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float a = exp2_fast(x[g][4 * j + 2 * h]), d = exp2_fast(x[g][4 * j + 2 * h + 1]);
+                        const __half2 v = __floats2half2_rn(a, d);
                         l[2 * j] += a;
                         l[2 * j + 1] += d;
-                        *reinterpret_cast<__half2 *>(weights + (2 * g + h) * 1024 + (at_row << 4)) =
-                            __floats2half2_rn(a, d);
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"((weights ^ (j << 4)) + (2 * g + h) * 1024),
+                                     "r"(*reinterpret_cast<const uint32_t *>(&v))
+                                     : "memory");
                     }
             }
             tc_fence_before();
@@ -752,7 +765,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             if (!sees) c.ref[mine_row] = -INFINITY;
         }
         group_sync(group);
-        wait(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
+        await_warp(&c.o_done[(i - 1) % BLOCKS], (i - 1) / BLOCKS, c);
         tc_fence_after();
         const bool direct = at.b0 == 0 && at.b1 == at.blocks;
         if (direct) {
@@ -831,8 +844,7 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
         for (int s = 0; s < S::PAIRS; ++s) mbar_init(&c.pair_full[s], 4);
         for (int s = 0; s < S::A_PAIRS; ++s) mbar_init(&c.a_full[s], 4);
         for (int s = 0; s < TURNS; ++s) {
-            mbar_init(&c.scored[s], 1);
-            mbar_init(&c.copied[s], 4);
+            mbar_init(&c.a_done[s], 5);
             mbar_init(&c.summed[s], 1);
         }
         for (int h = 0; h < 2; ++h) {
@@ -872,9 +884,9 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     const uint32_t ring = smem_addr(weights + S::WEIGHTS * CHUNK);
-    if (warp < S::SOFT / 32) soften<NR>(p, c, query, pairs, weights, tmem);
+    if (warp < S::SOFT / 32) soften<NR>(p, c, query, pairs, smem_addr(weights), tmem);
     else if (warp < COPY_WARP) convert_rows<NR>(p, c, ring, tmem);
-    else if (warp < SEND_WARP) copy_values<NR>(p, c, pairs, tmem);
+    else if (warp < SEND_WARP) copy_values<NR>(p, c, smem_addr(pairs), tmem);
     else if (warp < SCORES_WARP) send_rows<NR>(p, &units_map, &scales_map, c, ring);
     else if (warp < SUMS_WARP) multiply_scores<NR>(p, c, smem_addr(query), tmem);
     else multiply_sums<NR>(p, c, smem_addr(pairs), smem_addr(weights), tmem);
