@@ -23,13 +23,14 @@ namespace topk::latent {
 
 namespace {
 
-// Warps, each with one job: softmax, query rows and outputs (4 where query rows are
-// few, else 8); cache rows from 4 bits to FP16 (8, else 4); 12 to 19: values from tensor
-// memory to shared memory; 20 and 21: copies of cache rows as they are; 22 and 23: the
-// tensor cores (scores, sums).
-constexpr int NT = 768;
-constexpr int COPY_WARP = 12, SEND_WARP = 20, SCORES_WARP = 22, SUMS_WARP = 23;
-constexpr int COPIERS = 2;                   // groups of four copying warps
+// Warps, each with one job, in groups of four: softmax, query rows and outputs (one
+// group, two of 64 query rows); cache rows from 4 bits to FP16 in tensor memory; values
+// from there to shared memory; and two for copies of cache rows as they are, two for the
+// tensor cores (scores, sums). No more than that: registers kept out of memory count for
+// more than warps (24 of them, two groups for either job, had 80 each; what did not fit
+// lay in a first-level cache of 28 KB that 24 warps' share: 32 requests x 16 heads x
+// 16384 took 73 us).
+constexpr int MAX_NT = 640;
 constexpr int KEYS = 128;                    // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
 constexpr int BLOCKS = 8, TURNS = 16;        // blocks; pairs and units that have barriers of their own: more than are
@@ -50,7 +51,10 @@ constexpr int SCALES = HALF * 32;            // bytes of a half's scales
 // (sums) and tensor memory (scores), blocks of weights and of scores, units on their way.
 template <int NR>
 struct Shape {
-    static constexpr int SOFT = NR == 64 ? 256 : 128, GROUPS = SOFT / 128, CONVERT = 3 - GROUPS;   // groups of 4 warps
+    static constexpr int GROUPS = NR == 64 ? 2 : 1, SOFT = 128 * GROUPS, NT = SOFT + 384;
+    static constexpr int CONVERT_WARP = SOFT / 32, COPY_WARP = CONVERT_WARP + 4, SEND_WARP = COPY_WARP + 4,
+                         SCORES_WARP = SEND_WARP + 2, SUMS_WARP = SCORES_WARP + 1;
+    static_assert(NT <= MAX_NT);
     static constexpr int PAIRS = 3, A_PAIRS = NR == 64 ? 2 : 4;
     static constexpr int WEIGHTS = NR == 64 ? 1 : 2, SCORES = NR == 64 ? 1 : 2;
     static constexpr int UNITS = NR == 64 ? 2 : 3, SCALE_SLOTS = NR == 64 ? 1 : 2;
@@ -59,12 +63,12 @@ struct Shape {
     static constexpr uint32_t RINGS = (2 * PAIRS + WEIGHTS) * CHUNK + RAW;
     static_assert(K_COL + KEY_SLOTS * 32 <= 512);
     // Places, what waits in registers and tensor memory hold a block: its scores never wait for its own sums.
-    static_assert(PAIRS + COPIERS + A_PAIRS > LATENT_MAX / 128 && A_PAIRS % COPIERS == 0);
+    static_assert(PAIRS + 1 + A_PAIRS > LATENT_MAX / 128);
     // A cluster's parts lie where the rings were, and what weighs them behind.
     static_assert(RINGS >= NR * LATENT_MAX * sizeof(float) + ROWS * MAX_CLUSTER * sizeof(float));
 };
 
-struct Ctrl : Schedule<NT> {
+struct Ctrl : Schedule<MAX_NT> {
     u64 unit_full[2][TURNS], unit_empty[2][3]; // a half's unit is in / read
     u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in / read
     u64 a_full[4], a_done[TURNS];              // a pair is in tensor memory / its scores are added and it is copied
@@ -100,14 +104,31 @@ constexpr bool fits() {
 }
 static_assert(fits<16>() && fits<32>() && fits<64>());
 
-// As mbar_wait() and wait(), in fewer instructions where there is nothing to wait for.
+// As mbar_wait() and wait() where there is mostly nothing to wait for: few instructions
+// and branches that a warp takes as one (the time of a block goes to instructions and
+// not to what they do: without the conversions, or the exponentials, or either product,
+// it took a few percent less).
 __device__ __forceinline__ void await(u64 *bar, uint32_t parity, Ctrl &c) {
     if (!mbar_try_wait(bar, parity & 1u)) [[unlikely]] mbar_wait(bar, parity & 1u, &c.abort);
 }
 
 __device__ __forceinline__ void await_warp(u64 *bar, uint32_t parity, Ctrl &c) {
-    await(bar, parity, c);
-    __syncwarp();
+    if (__all_sync(FULL, mbar_try_wait(bar, parity & 1u))) [[likely]] return;
+    const uint64_t t0 = global_timer_ns();
+    while (!__all_sync(FULL, mbar_try_wait(bar, parity & 1u) || c.abort))
+        if (__any_sync(FULL, global_timer_ns() - t0 > WAIT_LIMIT_NS)) {
+            c.abort = 1u;
+            atomicOr(&g_device_status, ERR_WAIT);
+        }
+}
+
+// An arrival by a warp's first lane, without a branch.
+__device__ __forceinline__ void arrive_one(u64 *bar, int lane) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+            smem_addr(bar)),
+        "r"(lane)
+        : "memory");
 }
 
 __device__ __forceinline__ void store_vec(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -253,7 +274,7 @@ template <int NR>
 __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, const CUtensorMap *scales_map, Ctrl &c,
                           uint32_t raw) {
     using S = Shape<NR>;
-    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - SEND_WARP, pairs = p.latent / 128;
+    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - S::SEND_WARP, pairs = p.latent / 128;
     const int units = 1 + (pairs + 1) / 2;
     const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
     const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT;
@@ -357,106 +378,118 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
 }
 
 // Halves of units, 64 bytes of each row, into tensor memory, a row a lane, each warp the
-// rows of its own lanes there; groups of four warps take turns. 128 values become FP16,
-// the scores' left operand; the key part goes there as it is.
+// rows of its own lanes there. 128 values become FP16, the scores' left operand; the key
+// part goes there as it is.
 template <int NR>
 __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint32_t tmem) {
     using S = Shape<NR>;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x - S::SOFT) >> 5, quarter = warp & 3, half = quarter >> 1;
-    const int pairs = p.latent / 128, parts = 2 + (pairs + 1) / 2 * 2, row = quarter * 32 + lane;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = quarter >> 1;
+    const int pairs = p.latent / 128, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT + (row % HALF) * 32;
-    const uint32_t mine = ring + (row % HALF) * 128, turn = (row & 7) << 4;
+    const uint32_t mine = ring + (row % HALF) * 128, turned = (row & 7) << 4;
     Cursor at(c);
-    uint32_t i = 0, t = warp >> 2;             // the block, and the half unit, that come next
-    int e = t;                                 // its number in the block
+    uint32_t i = 0, n = 0, turn = 0, slot = 0; // the block, the pair, the unit and its place that come next
+    auto next_unit = [&]() {
+        await_warp(&c.unit_full[half][turn % TURNS], turn / TURNS, c);
+        ++turn;
+        return mine + slot * UNIT;
+    };
+    auto read = [&](uint32_t from, int e, uint32_t (&v)[16]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint4 x = shared_vec(from + ((e * 64 + q * 16) ^ turned));
+            v[4 * q] = x.x;
+            v[4 * q + 1] = x.y;
+            v[4 * q + 2] = x.z;
+            v[4 * q + 3] = x.w;
+        }
+    };
+    auto unit_read = [&]() {
+        __syncwarp();
+        arrive_one(&c.unit_empty[half][slot], lane);
+        if (++slot == S::UNITS) slot = 0;
+    };
     while (at.next(p, lane))
         for (const uint32_t end = i + (at.b1 - at.b0); i < end; ++i) {
-            const uint32_t s = i % S::SCALE_SLOTS;
-            for (; e < parts; e += S::CONVERT, t += S::CONVERT) {
-                const uint32_t unit = t >> 1, slot = unit % S::UNITS;
-                const int pair = e - 2;
-                uint32_t v[16];
-                uint2 s8 = make_uint2(0, 0);
-                await_warp(&c.unit_full[half][unit % TURNS], unit / TURNS, c);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 x = shared_vec(mine + slot * UNIT + (((t & 1) * 64 + q * 16) ^ turn));
-                    v[4 * q] = x.x;
-                    v[4 * q + 1] = x.y;
-                    v[4 * q + 2] = x.z;
-                    v[4 * q + 3] = x.w;
-                }
-                if (pair >= 0) {
-                    await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                 : "=r"(s8.x), "=r"(s8.y)
-                                 : "r"(scales + s * SCALES + (pair & 3) * 8));
-                }
+            const uint32_t s = i % S::SCALE_SLOTS, key = i % KEY_SLOTS;
+            {
+                const uint32_t from = next_unit();
+                uint32_t v[2][16];
+                read(from, 0, v[0]);
+                read(from, 1, v[1]);
+                if (i >= KEY_SLOTS) await_warp(&c.key_done[(i - KEY_SLOTS) % BLOCKS], (i - KEY_SLOTS) / BLOCKS, c);
+                tc_fence_after();
+                tc_store16(lanes + S::K_COL + key * 32, v[0]);
+                tc_store16(lanes + S::K_COL + key * 32 + 16, v[1]);
+                unit_read();
+                tc_wait_st();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(&c.unit_empty[half][slot]);
-                if (pair < 0) {
-                    const uint32_t key = i % KEY_SLOTS;
-                    if (i >= KEY_SLOTS) await_warp(&c.key_done[(i - KEY_SLOTS) % BLOCKS], (i - KEY_SLOTS) / BLOCKS, c);
+                arrive_one(&c.key_full[key], lane);
+            }
+            await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
+            uint4 scale[2];                    // the row's scales
+            scale[0] = shared_vec(scales + s * SCALES);
+            scale[1] = shared_vec(scales + s * SCALES + 16);
+            __syncwarp();
+            arrive_one(&c.scales_empty[half][s], lane);
+#pragma unroll 1
+            for (int left = pairs; left > 0;) {
+                const uint32_t from = next_unit();
+#pragma unroll 1
+                for (int e = 0; e < 2 && left > 0; ++e, --left, ++n) {
+                    const uint32_t a = n % S::A_PAIRS;
+                    uint32_t v[16];
+                    read(from, e, v);
+                    if (n >= S::A_PAIRS)
+                        await_warp(&c.a_done[(n - S::A_PAIRS) % TURNS], (n - S::A_PAIRS) / TURNS, c);
                     tc_fence_after();
-                    tc_store16(lanes + S::K_COL + key * 32 + e * 16, v);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(&c.key_full[key]);
-                } else if (pair < pairs) {
-                    const uint32_t n = i * pairs + pair, a = n % S::A_PAIRS;
-                    if (n >= S::A_PAIRS) {
-                        const uint32_t last = n - S::A_PAIRS;
-                        await_warp(&c.a_done[last % TURNS], last / TURNS, c);
-                    }
-                    tc_fence_after();
+                    const uint32_t s8[2] = {scale[0].x, scale[0].y};
+                    // (the next pair's scales move up)
+                    scale[0].x = scale[0].z, scale[0].y = scale[0].w, scale[0].z = scale[1].x, scale[0].w = scale[1].y;
+                    scale[1].x = scale[1].z, scale[1].y = scale[1].w;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // 32 values with two scales
-                        const uint32_t two = (q < 2 ? s8.x : s8.y) >> (16 * (q & 1));
                         uint32_t both, w[16];
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(both) : "h"(static_cast<uint16_t>(two & 0xFFFFu)));
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                            : "=r"(both)
+                            : "h"(static_cast<uint16_t>(s8[q >> 1] >> (16 * (q & 1)))));
                         const __half2 h = *reinterpret_cast<const __half2 *>(&both);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             from_codes(v[4 * q + k], k < 2 ? __low2half2(h) : __high2half2(h), w + 4 * k);
                         tc_store16(lanes + S::A_COL + a * 64 + q * 16, w);
                     }
-                    const uint32_t bad = __ballot_sync(FULL, ((((s8.x & 0x7F7F7F7Fu) + 0x01010101u) |
-                                                               ((s8.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u));
+                    const uint32_t bad = __ballot_sync(FULL, ((((s8[0] & 0x7F7F7F7Fu) + 0x01010101u) |
+                                                               ((s8[1] & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u));
+                    if (lane == 0) c.bad[a][quarter] = bad;
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        c.bad[a][quarter] = bad;
-                        arrive(&c.a_full[a]);
-                    }
+                    arrive_one(&c.a_full[a], lane);
                 }
+                unit_read();
             }
-            e -= parts;
-            // (Also by a warp that read none: its next arrival must not count for this block.)
-            await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
-            if (lane == 0) arrive(&c.scales_empty[half][s]);
         }
 }
 
 // The sums' left operand: pairs out of tensor memory into shared memory, a chunk's rows
-// of 128 bytes swizzled as the products read them; two groups of four warps take turns.
-// What waits for its place waits in registers, so that tensor memory is free for the
+// of 128 bytes swizzled as the products read them. What waits for its place waits in registers, so that tensor memory is free for the
 // pairs behind it. A scale of NaN makes every score of its row NaN, and with it the
 // weights of all that see the row; its values become zeros here, so that 0 x NaN does
 // not reach those that may not see it.
 template <int NR>
 __device__ void copy_values(const AttendParams &p, Ctrl &c, uint32_t pairs_at, uint32_t tmem) {
     using S = Shape<NR>;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - COPY_WARP, quarter = warp & 3;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int row = quarter * 32 + lane, pairs = p.latent / 128;
     const uint32_t mine = pairs_at + row * 128 + ((row & 7) << 4);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + S::A_COL;
     Cursor at(c);
-    uint32_t n = warp >> 2, end = 0;
+    uint32_t n = 0, end = 0;
     while (at.next(p, lane))
-        for (end += (at.b1 - at.b0) * pairs; n < end; n += COPIERS) {
+        for (end += (at.b1 - at.b0) * pairs; n < end; ++n) {
             const uint32_t a = n % S::A_PAIRS, place = n % S::PAIRS;
             const uint32_t to = mine + place * 2 * CHUNK;
             uint32_t w[4][16];
@@ -468,7 +501,7 @@ __device__ void copy_values(const AttendParams &p, Ctrl &c, uint32_t pairs_at, u
             tc_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive(&c.a_done[n % TURNS]);
+            arrive_one(&c.a_done[n % TURNS], lane);
             if (n >= S::PAIRS) await_warp(&c.summed[(n - S::PAIRS) % TURNS], (n - S::PAIRS) / TURNS, c);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -485,7 +518,7 @@ __device__ void copy_values(const AttendParams &p, Ctrl &c, uint32_t pairs_at, u
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive(&c.pair_full[place]);
+            arrive_one(&c.pair_full[place], lane);
         }
 }
 
@@ -719,7 +752,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                 }
             }
             __syncwarp();
-            if (lane == 0) arrive(&c.s_empty[s]);
+            arrive_one(&c.s_empty[s], lane);
             if (i >= S::WEIGHTS) {             // (the weights' place is free)
                 const uint32_t last = i - S::WEIGHTS;
                 await_warp(&c.o_done[last % BLOCKS], last / BLOCKS, c);
@@ -744,7 +777,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
             tc_fence_before();
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive(&c.p_full[i % BLOCKS]);
+            arrive_one(&c.p_full[i % BLOCKS], lane);
         }
         // The piece is done: the next one's query rows (the last scores are read), then this
         // one's rows, or its part of them.
@@ -831,7 +864,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
 }
 
 template <int NR>
-__global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ AttendParams p,
+__global__ void __launch_bounds__(Shape<NR>::NT, 1) attend4_kernel(const __grid_constant__ AttendParams p,
                                                         const __grid_constant__ CUtensorMap units_map,
                                                         const __grid_constant__ CUtensorMap scales_map) {
     using S = Shape<NR>;
@@ -849,13 +882,13 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
         }
         for (int h = 0; h < 2; ++h) {
             for (int s = 0; s < TURNS; ++s) mbar_init(&c.unit_full[h][s], p.tiled ? 1 : 32);
-            for (int s = 0; s < S::UNITS; ++s) mbar_init(&c.unit_empty[h][s], 4);
+            for (int s = 0; s < S::UNITS; ++s) mbar_init(&c.unit_empty[h][s], 2);
             for (int s = 0; s < S::SCALE_SLOTS; ++s) {
                 mbar_init(&c.scales_full[h][s], p.tiled ? 1 : 32);
-                mbar_init(&c.scales_empty[h][s], 2 * S::CONVERT);
+                mbar_init(&c.scales_empty[h][s], 2);
             }
         }
-        for (int s = 0; s < KEY_SLOTS; ++s) mbar_init(&c.key_full[s], 8);
+        for (int s = 0; s < KEY_SLOTS; ++s) mbar_init(&c.key_full[s], 4);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&c.s_full[s], 1);
             mbar_init(&c.s_empty[s], S::SOFT / 32);
@@ -871,29 +904,29 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
         c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == SUMS_WARP) {
+    if (warp == S::SUMS_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&c.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     grid_dependents_release();
     grid_dependency_wait();
-    make_schedule<KEYS, NT>(p, c);
+    make_schedule<KEYS, S::NT>(p, c);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     const uint32_t ring = smem_addr(weights + S::WEIGHTS * CHUNK);
     if (warp < S::SOFT / 32) soften<NR>(p, c, query, pairs, smem_addr(weights), tmem);
-    else if (warp < COPY_WARP) convert_rows<NR>(p, c, ring, tmem);
-    else if (warp < SEND_WARP) copy_values<NR>(p, c, smem_addr(pairs), tmem);
-    else if (warp < SCORES_WARP) send_rows<NR>(p, &units_map, &scales_map, c, ring);
-    else if (warp < SUMS_WARP) multiply_scores<NR>(p, c, smem_addr(query), tmem);
+    else if (warp < S::COPY_WARP) convert_rows<NR>(p, c, ring, tmem);
+    else if (warp < S::SEND_WARP) copy_values<NR>(p, c, smem_addr(pairs), tmem);
+    else if (warp < S::SCORES_WARP) send_rows<NR>(p, &units_map, &scales_map, c, ring);
+    else if (warp < S::SUMS_WARP) multiply_scores<NR>(p, c, smem_addr(query), tmem);
     else multiply_sums<NR>(p, c, smem_addr(pairs), smem_addr(weights), tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == SUMS_WARP) {
+    if (warp == S::SUMS_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
@@ -902,7 +935,7 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
         cluster_arrive();
         cluster_wait();
         if (c.ranks > 1)
-            join_cluster<NT>(p, c, pairs,
+            join_cluster<S::NT>(p, c, pairs,
                              reinterpret_cast<float(*)[MAX_CLUSTER]>(pairs + NR * LATENT_MAX * sizeof(float)));
         __syncwarp();
         cluster_arrive();                      // no CTA leaves while others read its part
@@ -922,7 +955,7 @@ const void *attend_fn() {
 }
 
 cudaError_t device(Device *&out) {
-    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, NT, out);
+    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, MAX_NT, out);
 }
 
 }  // namespace
@@ -980,7 +1013,7 @@ cudaError_t launch_attend4(AttendParams p, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.grid, 1, 1);
-    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(plan.nr == 64 ? Shape<64>::NT : Shape<16>::NT), 1, 1);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;

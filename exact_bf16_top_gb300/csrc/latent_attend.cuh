@@ -205,7 +205,7 @@ __device__ __forceinline__ float largest(float m, float a, float b) {
 
 // ------------------------------------------------------------------ the schedule
 
-// What a CTA knows of its share of the blocks (part of its control block).
+// What a CTA (of NT threads at most) knows of its share of the blocks: part of its control block.
 template <int NT>
 struct Schedule {
     long long sums[NT / 32];
@@ -307,8 +307,9 @@ struct CursorOf {
 };
 
 // The CTA's share, by all threads of the CTA.
-template <int KEYS, int NT>
-__device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<NT> &c) {
+template <int KEYS, int NT, int SIZE>
+__device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<SIZE> &c) {
+    static_assert(NT <= SIZE);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.cluster) {                           // a tile per cluster, its blocks in equal runs
         if (warp == 0) {
