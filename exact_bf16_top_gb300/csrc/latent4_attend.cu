@@ -51,10 +51,10 @@ constexpr int SCALES = HALF * 32;            // bytes of a half's scales
 // (sums) and tensor memory (scores), blocks of weights and of scores, units on their way.
 template <int NR>
 struct Shape {
-    static constexpr int GROUPS = NR == 64 ? 2 : 1, SOFT = 128 * GROUPS, NT = SOFT + 384;
-    static constexpr int CONVERT_WARP = SOFT / 32, COPY_WARP = CONVERT_WARP + 4, SEND_WARP = COPY_WARP + 4,
+    static constexpr int GROUPS = NR == 64 ? 2 : 1, CONVERT = 3 - GROUPS, SOFT = 128 * GROUPS, NT = 640;
+    static constexpr int CONVERT_WARP = SOFT / 32, COPY_WARP = CONVERT_WARP + 4 * CONVERT, SEND_WARP = COPY_WARP + 4,
                          SCORES_WARP = SEND_WARP + 2, SUMS_WARP = SCORES_WARP + 1;
-    static_assert(NT <= MAX_NT);
+    static_assert(NT <= MAX_NT && NT == 32 * (SUMS_WARP + 1));
     static constexpr int PAIRS = 3, A_PAIRS = NR == 64 ? 2 : 4;
     static constexpr int WEIGHTS = NR == 64 ? 1 : 2, SCORES = NR == 64 ? 1 : 2;
     static constexpr int UNITS = NR == 64 ? 2 : 3, SCALE_SLOTS = NR == 64 ? 1 : 2;
@@ -255,7 +255,6 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
             *reinterpret_cast<uint4 *>(dst + k * NR * 128) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    fence_proxy_async();
     __syncwarp();
     if ((tid & 31) == 0) arrive(&c.q_full);
 }
@@ -377,19 +376,21 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
     }
 }
 
-// Halves of units, 64 bytes of each row, into tensor memory, a row a lane, each warp the
-// rows of its own lanes there. 128 values become FP16, the scores' left operand; the key
-// part goes there as it is.
+// Units into tensor memory, a row a lane, each warp the rows of its own lanes there, 64
+// bytes of each row at a time (with two groups of warps each has the same half of every
+// unit). 128 values become FP16, the scores' left operand; the key part goes there as it
+// is.
 template <int NR>
 __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint32_t tmem) {
     using S = Shape<NR>;
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = quarter >> 1;
+    const int group = S::CONVERT == 2 ? (threadIdx.x - S::SOFT) >> 7 : 0;
     const int pairs = p.latent / 128, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT + (row % HALF) * 32;
     const uint32_t mine = ring + (row % HALF) * 128, turned = (row & 7) << 4;
     Cursor at(c);
-    uint32_t i = 0, n = 0, turn = 0, slot = 0; // the block, the pair, the unit and its place that come next
+    uint32_t i = 0, turn = 0, slot = 0;        // the block, the unit and its place that come next
     auto next_unit = [&]() {
         await_warp(&c.unit_full[half][turn % TURNS], turn / TURNS, c);
         ++turn;
@@ -416,12 +417,13 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
             {
                 const uint32_t from = next_unit();
                 uint32_t v[2][16];
-                read(from, 0, v[0]);
-                read(from, 1, v[1]);
+#pragma unroll
+                for (int e = 0; e < 2; e += S::CONVERT) read(from, group + e, v[e]);
                 if (i >= KEY_SLOTS) await_warp(&c.key_done[(i - KEY_SLOTS) % BLOCKS], (i - KEY_SLOTS) / BLOCKS, c);
                 tc_fence_after();
-                tc_store16(lanes + S::K_COL + key * 32, v[0]);
-                tc_store16(lanes + S::K_COL + key * 32 + 16, v[1]);
+#pragma unroll
+                for (int e = 0; e < 2; e += S::CONVERT)
+                    tc_store16(lanes + S::K_COL + key * 32 + (group + e) * 16, v[e]);
                 unit_read();
                 tc_wait_st();
                 tc_fence_before();
@@ -429,26 +431,20 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
                 arrive_one(&c.key_full[key], lane);
             }
             await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
-            uint4 scale[2];                    // the row's scales
-            scale[0] = shared_vec(scales + s * SCALES);
-            scale[1] = shared_vec(scales + s * SCALES + 16);
-            __syncwarp();
-            arrive_one(&c.scales_empty[half][s], lane);
 #pragma unroll 1
-            for (int left = pairs; left > 0;) {
+            for (int first = 0; first < pairs; first += 2) {
                 const uint32_t from = next_unit();
 #pragma unroll 1
-                for (int e = 0; e < 2 && left > 0; ++e, --left, ++n) {
-                    const uint32_t a = n % S::A_PAIRS;
-                    uint32_t v[16];
+                for (int e = group; e < 2 && first + e < pairs; e += S::CONVERT) {
+                    const uint32_t n = i * pairs + first + e, a = n % S::A_PAIRS;
+                    uint32_t v[16], s8[2];
                     read(from, e, v);
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                 : "=r"(s8[0]), "=r"(s8[1])
+                                 : "r"(scales + s * SCALES + (first + e) * 8));
                     if (n >= S::A_PAIRS)
                         await_warp(&c.a_done[(n - S::A_PAIRS) % TURNS], (n - S::A_PAIRS) / TURNS, c);
                     tc_fence_after();
-                    const uint32_t s8[2] = {scale[0].x, scale[0].y};
-                    // (the next pair's scales move up)
-                    scale[0].x = scale[0].z, scale[0].y = scale[0].w, scale[0].z = scale[1].x, scale[0].w = scale[1].y;
-                    scale[1].x = scale[1].z, scale[1].y = scale[1].w;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // 32 values with two scales
                         uint32_t both, w[16];
@@ -471,6 +467,7 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
                 }
                 unit_read();
             }
+            arrive_one(&c.scales_empty[half][s], lane);
         }
 }
 
@@ -516,7 +513,6 @@ __device__ void copy_values(const AttendParams &p, Ctrl &c, uint32_t pairs_at, u
                     store_vec(at16, finite_halves(x.x), finite_halves(x.y), finite_halves(x.z), finite_halves(x.w));
                 }
             }
-            fence_proxy_async();
             __syncwarp();
             arrive_one(&c.pair_full[place], lane);
         }
@@ -545,7 +541,10 @@ __device__ void multiply_scores(const AttendParams &p, Ctrl &c, uint32_t query, 
             for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
                 const uint32_t s = i % S::SCORES, d = tmem + S::S_COL + s * NR, key = i % KEY_SLOTS;
                 await(&c.s_empty[s], (i / S::SCORES + 1) & 1u, c);
-                if (b == at.b0) await(&c.q_full, piece & 1u, c);
+                if (b == at.b0) {
+                    await(&c.q_full, piece & 1u, c);
+                    fence_proxy_async();
+                }
                 for (int u = 0; u < pairs; ++u, ++n) {
                     await(&c.a_full[n % S::A_PAIRS], (n / S::A_PAIRS) & 1u, c);
                     tc_fence_after();
@@ -589,6 +588,7 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
                 for (int h = 0; h < pairs; ++h, ++n) {
                     const uint32_t slot = n % S::PAIRS;
                     await(&c.pair_full[slot], (n / S::PAIRS) & 1u, c);
+                    fence_proxy_async();           // (weights and values were written by ordinary stores)
                     tc_fence_after();
                     const uint64_t v = matrix(pairs_at + slot * 2 * CHUNK, CHUNK);
 #pragma unroll
@@ -775,7 +775,6 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                     }
             }
             tc_fence_before();
-            fence_proxy_async();
             __syncwarp();
             arrive_one(&c.p_full[i % BLOCKS], lane);
         }
@@ -882,13 +881,13 @@ __global__ void __launch_bounds__(Shape<NR>::NT, 1) attend4_kernel(const __grid_
         }
         for (int h = 0; h < 2; ++h) {
             for (int s = 0; s < TURNS; ++s) mbar_init(&c.unit_full[h][s], p.tiled ? 1 : 32);
-            for (int s = 0; s < S::UNITS; ++s) mbar_init(&c.unit_empty[h][s], 2);
+            for (int s = 0; s < S::UNITS; ++s) mbar_init(&c.unit_empty[h][s], 2 * S::CONVERT);
             for (int s = 0; s < S::SCALE_SLOTS; ++s) {
                 mbar_init(&c.scales_full[h][s], p.tiled ? 1 : 32);
-                mbar_init(&c.scales_empty[h][s], 2);
+                mbar_init(&c.scales_empty[h][s], 2 * S::CONVERT);
             }
         }
-        for (int s = 0; s < KEY_SLOTS; ++s) mbar_init(&c.key_full[s], 4);
+        for (int s = 0; s < KEY_SLOTS; ++s) mbar_init(&c.key_full[s], 4 * S::CONVERT);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&c.s_full[s], 1);
             mbar_init(&c.s_empty[s], S::SOFT / 32);
