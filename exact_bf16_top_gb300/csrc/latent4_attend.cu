@@ -330,20 +330,22 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                 turn = __shfl_sync(FULL, turn, 0);
                 continue;
             }
+            // Eight lanes a row, four rows a copy: where this lane's copies come from.
             const uint64_t all = mask[0] | static_cast<uint64_t>(mask[1]) << 32;
             const long long offset[2] = {row[0] >= 0 ? row[0] * p.cache_stride : 0,
                                          row[1] >= 0 ? row[1] * p.cache_stride : 0};
+            const uint8_t *src[HALF / 4];
+#pragma unroll
+            for (int m = 0; m < HALF / 4; ++m)
+                src[m] = cache + __shfl_sync(FULL, offset[m / 8], (4 * m + (lane >> 3)) & 31) + (lane & 7) * 16;
+            const uint64_t mine = all >> (lane >> 3);   // bit 4 m: there is something to copy
             for (int u = 0; u < units; ++u) {
-                const uint32_t to = ring + slot * UNIT;
+                const uint32_t to = ring + slot * UNIT + (lane >> 3) * 128;
                 const int x = u ? (u - 1) * 128 : p.latent / 2;
-                // Eight lanes a row, four rows a copy.
                 await_warp(&c.unit_empty[half][slot], use + 1, c);
 #pragma unroll
-                for (int m = 0; m < HALF / 4; ++m) {
-                    const int r = 4 * m + (lane >> 3);
-                    copy16(to + r * 128 + (((lane ^ r) & 7) << 4),
-                           cache + __shfl_sync(FULL, offset[m / 8], r & 31) + x + (lane & 7) * 16, all >> r & 1u);
-                }
+                for (int m = 0; m < HALF / 4; ++m)
+                    copy16(to + m * 512 + (((lane ^ (4 * m + (lane >> 3))) & 7) << 4), src[m] + x, mine >> 4 * m & 1u);
                 copies_arrive(&c.unit_full[half][turn % TURNS]);
                 ++turn;
                 if (++slot == S::UNITS) {
