@@ -62,6 +62,13 @@ __device__ __forceinline__ float largest(float m, float v) {
     return y;
 }
 
+// v / s rounded to nearest, by Markstein's correction of a quotient from the rounded
+// reciprocal: the remainder is exact, and its share of s is added with one rounding.
+__device__ __forceinline__ float quotient(float v, float s, float over_s) {
+    const float q = __fmul_rn(v, over_s);
+    return __fmaf_rn(__fmaf_rn(-q, s, v), over_s, q);
+}
+
 // A block's 16 values to its scale's e4m3 byte and 16 codes. Both quotients are rounded
 // to nearest, which no float near a border can be moved onto it by: a border is the
 // quotient of a float of few bits, its neighbours' quotients are floats of their own.
@@ -79,11 +86,12 @@ __device__ __forceinline__ uint32_t to_codes(const float (&v)[16], uint32_t (&co
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(s8)));
         s = __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
     }
+    const float over_s = __frcp_rn(s);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         float q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = s8 == 0x7Fu ? 0.0f : __fdiv_rn(v[8 * w + i], s);
+        for (int i = 0; i < 8; ++i) q[i] = s8 == 0x7Fu ? 0.0f : quotient(v[8 * w + i], s, over_s);
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
@@ -144,9 +152,13 @@ __global__ void __launch_bounds__(NT) append4_kernel(const latent4_append_t a, u
             v[2 * i + 1] = hi_f(b[i]);
         }
         if (a.weight) {
-            Two sum = {0.0f, 0.0f};
+            Two sums[4];                     // (squares of BF16 are exact; four sums side by side)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum = add(sum, {__fmul_rn(v[i], v[i]), 0.0f});   // (squares of BF16 are exact)
+            for (int i = 0; i < 16; ++i) {
+                const Two square = {__fmul_rn(v[i], v[i]), 0.0f};
+                sums[i % 4] = i < 4 ? square : add(sums[i % 4], square);
+            }
+            Two sum = add(add(sums[0], sums[1]), add(sums[2], sums[3]));
 #pragma unroll
             for (int o = 16; o; o >>= 1)
                 sum = add(sum, {__shfl_xor_sync(FULL, sum.hi, o), __shfl_xor_sync(FULL, sum.lo, o)});
@@ -185,7 +197,10 @@ __device__ __forceinline__ uint4 from_codes(uint32_t w, __half2 scale) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// A warp per row: 16 values of one scale per lane, the key part by eight lanes.
+// R rows of a warp at a time, all their loads together: 16 values of one scale per lane,
+// the key part by eight lanes. Bound by DRAM where rows are many (131071: see
+// launch_rows4), by the launch and two rounds of loads else.
+template <int R>
 __global__ void __launch_bounds__(NT) rows4_kernel(const uint8_t *__restrict__ cache, int64_t cache_stride,
                                                    int32_t cache_rows, int32_t latent, const int32_t *__restrict__ rows,
                                                    int32_t count, uint16_t *__restrict__ out, int64_t out_stride) {
@@ -193,29 +208,41 @@ __global__ void __launch_bounds__(NT) rows4_kernel(const uint8_t *__restrict__ c
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const bool mine = lane < latent / 16;
-    const int32_t step = static_cast<int32_t>(gridDim.x) * (NT / 32);
-    for (int64_t i = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); i < count; i += step) {
-        const int32_t r = __ldg(rows + i);
-        uint2 code = make_uint2(0, 0);
-        uint32_t s8 = 0;
-        uint4 key = make_uint4(0, 0, 0, 0);
-        if (r >= 0 && r < cache_rows) {
-            const uint8_t *row = cache + r * cache_stride;
-            if (mine) {
-                code = __ldg(reinterpret_cast<const uint2 *>(row) + lane);
-                s8 = __ldg(row + latent / 2 + 2 * ROPE + lane);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (NT / 32) * R;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * (NT / 32) + (threadIdx.x >> 5)) * R; i < count; i += step) {
+        int32_t r[R];
+        uint2 code[R];
+        uint32_t s8[R];
+        uint4 key[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) r[k] = i + k < count ? __ldg(rows + i + k) : -1;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            code[k] = make_uint2(0, 0);
+            s8[k] = 0;
+            key[k] = make_uint4(0, 0, 0, 0);
+            if (r[k] >= 0 && r[k] < cache_rows) {
+                const uint8_t *row = cache + r[k] * cache_stride;
+                if (mine) {
+                    code[k] = __ldg(reinterpret_cast<const uint2 *>(row) + lane);
+                    s8[k] = __ldg(row + latent / 2 + 2 * ROPE + lane);
+                }
+                if (lane < 8) key[k] = __ldg(reinterpret_cast<const uint4 *>(row + latent / 2) + lane);
             }
-            if (lane < 8) key = __ldg(reinterpret_cast<const uint4 *>(row + latent / 2) + lane);
         }
-        uint32_t s;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(s8 | s8 << 8)));
-        const __half2 scale = *reinterpret_cast<const __half2 *>(&s);
-        uint4 *to = reinterpret_cast<uint4 *>(out + i * out_stride);
-        if (mine) {
-            to[2 * lane] = from_codes(code.x, scale);
-            to[2 * lane + 1] = from_codes(code.y, scale);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (i + k >= count) break;
+            uint32_t s;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(s8[k] | s8[k] << 8)));
+            const __half2 scale = *reinterpret_cast<const __half2 *>(&s);
+            uint4 *to = reinterpret_cast<uint4 *>(out + (i + k) * out_stride);
+            if (mine) {
+                to[2 * lane] = from_codes(code[k].x, scale);
+                to[2 * lane + 1] = from_codes(code[k].y, scale);
+            }
+            if (lane < 8) to[latent / 8 + lane] = key[k];
         }
-        if (lane < 8) to[latent / 8 + lane] = key;
     }
 }
 
@@ -254,9 +281,15 @@ cudaError_t launch_rows4(const uint8_t *cache, int64_t cache_stride, int32_t cac
                          const int32_t *rows, int32_t count, uint16_t *out, int64_t out_stride, int sms,
                          cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(count, sms, stream, &attr);
+    // Several rows a warp once there are twice as many as warps that run at once.
+    constexpr int R = 4;
+    const bool many = count > 2 * sms * (2048 / 32);
+    const cudaLaunchConfig_t cfg = config(many ? (count + R - 1) / R : count, sms, stream, &attr);
     void *args[] = {&cache, &cache_stride, &cache_rows, &latent, &rows, &count, &out, &out_stride};
-    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&rows4_kernel), args);
+    return cudaLaunchKernelExC(&cfg,
+                               many ? reinterpret_cast<const void *>(&rows4_kernel<R>)
+                                    : reinterpret_cast<const void *>(&rows4_kernel<1>),
+                               args);
 }
 
 }  // namespace topk::latent

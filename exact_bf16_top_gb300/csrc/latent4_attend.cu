@@ -72,7 +72,7 @@ struct Ctrl : Schedule<MAX_NT> {
     u64 unit_full[2][TURNS], unit_empty[2][3]; // a half's unit is in / read
     u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in / read
     u64 a_full[4], a_done[TURNS];              // a pair is in tensor memory / its scores are added and it is copied
-    u64 pair_full[3], summed[TURNS];           // a pair is in shared memory / its sums are added
+    u64 pair_full[4], summed[TURNS];           // a pair is in shared memory / its sums are added
     u64 key_full[KEY_SLOTS], key_done[BLOCKS]; // a block's key part is in tensor memory / its scores are added
     u64 s_full[2], s_empty[2];                 // scores written / read
     u64 row_full[BLOCKS];                      // a block's marks are in
@@ -946,7 +946,12 @@ __global__ void __launch_bounds__(Shape<NR>::NT, 1) attend4_kernel(const __grid_
 
 // ------------------------------------------------------------------ host side
 
-constexpr Costs COSTS = {1, 3, 3, 2, 1};
+// Blocks are twice the BF16 form's. Of eight settings at 200 sizes (1 to 150 tokens of 16
+// to 128 heads, 256 to 32768 rows) this takes the better side of each: shares against
+// the cluster, 1 token of 16 rows x 4 blocks 13.4 / 11.5 us (4 CTAs), x 16 14.1 / 13.5
+// (16); 8 tokens x 4 16.0 / 11.9; 1 of 64 rows x 16 17.6 / 21.8 (8), x 32 18.4 / 21.2;
+// pages of 64 rows x 32 21.2 / 28.6.
+constexpr Costs COSTS = {1, 3, 2, 2, 1};
 
 Device g_device[64];
 
