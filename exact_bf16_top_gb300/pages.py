@@ -62,10 +62,14 @@ def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_
         dev = block_table.get_device()
         n, pages = block_table.shape
         stride, t1 = block_table.stride()
-        fine = (dev >= 0 and block_table.dtype is _I32 and (t1 == 1 or pages <= 1) and _vector(lengths, n, dev)
-                and _vector(new_tokens, n, dev) and _vector(free_count, 1, dev)
-                and _vector(free_pages, free_pages.shape[0], dev))
-    except (AttributeError, ValueError, IndexError):
+        (size,), (count,) = free_pages.shape, free_count.shape
+        fine = (dev >= 0 and lengths.get_device() == new_tokens.get_device() == dev
+                and free_pages.get_device() == free_count.get_device() == dev
+                and block_table.dtype is lengths.dtype is new_tokens.dtype is _I32
+                and free_pages.dtype is free_count.dtype is _I32 and lengths.shape == new_tokens.shape == (n,)
+                and count == 1 and (t1 == 1 or pages <= 1) and lengths.is_contiguous()
+                and new_tokens.is_contiguous() and free_pages.is_contiguous())
+    except (AttributeError, ValueError):
         fine = False
     if not fine:
         try:
@@ -81,7 +85,7 @@ def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_
     block_rows = page_size if block_rows is None else int(block_rows)
     if n > MAX_REQUESTS or pages * page_size > MAX_WIDTH:
         raise ValueError(f"at most {MAX_REQUESTS} requests and {MAX_WIDTH} tokens in a request's pages")
-    if max(n * pages, n * q, abs(block_rows), page_size, free_pages.shape[0]) > MAX_ROWS:
+    if max(n * pages, n * q, abs(block_rows), page_size, size) > MAX_ROWS:
         raise ValueError("a length or count passes 31 bits")
     if n > 1 and stride < pages:
         raise ValueError("block_table's rows must not overlap")
@@ -105,12 +109,12 @@ def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_
             return page_step(block_table, lengths, new_tokens, free_pages, free_count, rows_per_request=q,
                              page_size=page_size, block_rows=block_rows, next_lengths=next_lengths,
                              next_free_count=next_free_count)
-    positions, slots, valid_len = torch.empty((3, n * q), dtype=_I32, device=block_table.device).unbind(0)
-    granted = torch.empty(n, dtype=_I32, device=block_table.device)
+    rows = n * q
+    positions, slots, valid_len, granted = block_table.new_empty(3 * rows + n).split_with_sizes((rows, rows, rows, n))
+    at = positions.data_ptr()
     args = _Args(block_table.data_ptr(), stride if n > 1 else pages, lengths.data_ptr(), new_tokens.data_ptr(),
                  free_pages.data_ptr(), free_count.data_ptr(), next_lengths.data_ptr(), next_free_count.data_ptr(),
-                 granted.data_ptr(), positions.data_ptr(), slots.data_ptr(), valid_len.data_ptr(), n, pages,
-                 free_pages.shape[0], page_size, block_rows, q)
+                 at + 12 * rows, at, at + 4 * rows, at + 8 * rows, n, pages, size, page_size, block_rows, q)
     status = (_package._lib or load()).page_step(args, _raw_stream(dev))
     if status:
         raise TopkError(status)
