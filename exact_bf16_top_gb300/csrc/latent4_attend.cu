@@ -11,7 +11,16 @@
 // sums'. So shared memory, which bounds the BF16 kernel, gives each block away once
 // instead of twice, and the scores run at 128 rows a step, ahead of the sums.
 // The key part stays BF16 and only goes to tensor memory. Warps have one job each
-// (softmax, rows, issue of either product) and meet at mbarriers only.
+// (softmax, copies, conversion, issue of either product) and meet at mbarriers only.
+//
+// Measured, latent part 512: 32 requests x 16 heads x 16384 rows 71 us (2.2 TB/s, the
+// rows in BF16 85 us), 128 tokens x 16 heads x 2048 listed rows 49 us (2.3 TB/s, 55), a
+// chunk of 509 tokens x 128 heads on 9000 rows 1.57 ms (0.79 PFLOP/s, 1.20 ms). What
+// bounds it is neither memory nor the tensor cores but the way of a block through the
+// warps, 3.1 to 3.5 us of 8.5 K warp instructions at 40 % of the issue slots: leaving
+// out any one part of it (the conversions, the exponentials, either product) takes a few
+// percent off. So where query rows are many the rows in BF16 are faster; these take 36 %
+// of the memory.
 
 #include <cuda_fp16.h>
 
@@ -24,13 +33,14 @@ namespace topk::latent {
 namespace {
 
 // Warps, each with one job, in groups of four: softmax, query rows and outputs (one
-// group, two of 64 query rows); cache rows from 4 bits to FP16 in tensor memory; values
-// from there to shared memory; and two for copies of cache rows as they are, two for the
-// tensor cores (scores, sums). No more than that: registers kept out of memory count for
-// more than warps (24 of them, two groups for either job, had 80 each; what did not fit
-// lay in a first-level cache of 28 KB that 24 warps' share: 32 requests x 16 heads x
-// 16384 took 73 us).
-constexpr int MAX_NT = 640;
+// group, two of 64 query rows); cache rows from 4 bits to FP16 in tensor memory (two, one
+// of 64 query rows); values from there to shared memory; and two warps for copies of
+// cache rows as they are, two for the tensor cores (scores, sums). 96 registers each.
+// (32 requests x 16 heads x 16384: 71 us; 24 warps of 80 registers, with two groups for
+// the values too, 73, for what did not fit lay in a first-level cache of 28 KB; 16 warps
+// of 128 with one group a job 72. A chunk of 509 tokens x 128 heads, one softmax group:
+// 2.05 ms instead of 1.78 before the other steps.)
+constexpr int NT = 640;
 constexpr int KEYS = 128;                    // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values
 constexpr int BLOCKS = 8, TURNS = 16;        // blocks; pairs and units that have barriers of their own: more than are
@@ -51,10 +61,10 @@ constexpr int SCALES = HALF * 32;            // bytes of a half's scales
 // (sums) and tensor memory (scores), blocks of weights and of scores, units on their way.
 template <int NR>
 struct Shape {
-    static constexpr int GROUPS = NR == 64 ? 2 : 1, CONVERT = 3 - GROUPS, SOFT = 128 * GROUPS, NT = 640;
+    static constexpr int GROUPS = NR == 64 ? 2 : 1, CONVERT = 3 - GROUPS, SOFT = 128 * GROUPS;
     static constexpr int CONVERT_WARP = SOFT / 32, COPY_WARP = CONVERT_WARP + 4 * CONVERT, SEND_WARP = COPY_WARP + 4,
                          SCORES_WARP = SEND_WARP + 2, SUMS_WARP = SCORES_WARP + 1;
-    static_assert(NT <= MAX_NT && NT == 32 * (SUMS_WARP + 1));
+    static_assert(NT == 32 * (SUMS_WARP + 1));
     static constexpr int PAIRS = 3, A_PAIRS = NR == 64 ? 2 : 4;
     static constexpr int WEIGHTS = NR == 64 ? 1 : 2, SCORES = NR == 64 ? 1 : 2;
     static constexpr int UNITS = NR == 64 ? 2 : 3, SCALE_SLOTS = NR == 64 ? 1 : 2;
@@ -68,7 +78,7 @@ struct Shape {
     static_assert(RINGS >= NR * LATENT_MAX * sizeof(float) + ROWS * MAX_CLUSTER * sizeof(float));
 };
 
-struct Ctrl : Schedule<MAX_NT> {
+struct Ctrl : Schedule<NT> {
     u64 unit_full[2][TURNS], unit_empty[2][3]; // a half's unit is in / read
     u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in / read
     u64 a_full[4], a_done[TURNS];              // a pair is in tensor memory / its scores are added and it is copied
@@ -266,9 +276,9 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
 // and more come by TMA, a box a unit (two of pages of 32 rows); listed rows by 16-byte
 // copies. (Rows read straight into registers, a row a lane, were held up at 7 KB on
 // their way per SM: the first-level cache, small beside this much shared memory, keeps a
-// line of 128 bytes for each 32 that come. 32 requests x 16 heads x 16384: 118 us. With
-// units a quarter of this size the sender was what all others waited for: a box or a
-// group of copies costs it 200 to 300 cycles.)
+// line of 128 bytes for each 32 that come: 32 requests x 16 heads x 16384 took 118 us.
+// With units of 32 bytes of each row the sender was what all others waited for: a box or
+// a group of copies costs it 200 to 300 cycles.)
 template <int NR>
 __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, const CUtensorMap *scales_map, Ctrl &c,
                           uint32_t raw) {
@@ -474,10 +484,10 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
 }
 
 // The sums' left operand: pairs out of tensor memory into shared memory, a chunk's rows
-// of 128 bytes swizzled as the products read them. What waits for its place waits in registers, so that tensor memory is free for the
-// pairs behind it. A scale of NaN makes every score of its row NaN, and with it the
-// weights of all that see the row; its values become zeros here, so that 0 x NaN does
-// not reach those that may not see it.
+// of 128 bytes swizzled as the products read them. What waits for its place waits in
+// registers, so that tensor memory is free for the pairs behind it. A scale of NaN makes
+// every score of its row NaN, and with it the weights of all that see the row; its
+// values become zeros here, so that 0 x NaN does not reach those that may not see it.
 template <int NR>
 __device__ void copy_values(const AttendParams &p, Ctrl &c, uint32_t pairs_at, uint32_t tmem) {
     using S = Shape<NR>;
@@ -865,7 +875,7 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
 }
 
 template <int NR>
-__global__ void __launch_bounds__(Shape<NR>::NT, 1) attend4_kernel(const __grid_constant__ AttendParams p,
+__global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ AttendParams p,
                                                         const __grid_constant__ CUtensorMap units_map,
                                                         const __grid_constant__ CUtensorMap scales_map) {
     using S = Shape<NR>;
@@ -912,7 +922,7 @@ __global__ void __launch_bounds__(Shape<NR>::NT, 1) attend4_kernel(const __grid_
     }
     grid_dependents_release();
     grid_dependency_wait();
-    make_schedule<KEYS, S::NT>(p, c);
+    make_schedule<KEYS, NT>(p, c);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -936,7 +946,7 @@ __global__ void __launch_bounds__(Shape<NR>::NT, 1) attend4_kernel(const __grid_
         cluster_arrive();
         cluster_wait();
         if (c.ranks > 1)
-            join_cluster<S::NT>(p, c, pairs,
+            join_cluster<NT>(p, c, pairs,
                              reinterpret_cast<float(*)[MAX_CLUSTER]>(pairs + NR * LATENT_MAX * sizeof(float)));
         __syncwarp();
         cluster_arrive();                      // no CTA leaves while others read its part
@@ -961,7 +971,7 @@ const void *attend_fn() {
 }
 
 cudaError_t device(Device *&out) {
-    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, MAX_NT, out);
+    return device(g_device, {attend_fn<16>(), attend_fn<32>(), attend_fn<64>()}, NT, out);
 }
 
 }  // namespace
@@ -1019,7 +1029,7 @@ cudaError_t launch_attend4(AttendParams p, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.grid, 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(plan.nr == 64 ? Shape<64>::NT : Shape<16>::NT), 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;

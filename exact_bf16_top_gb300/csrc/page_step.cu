@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ P
     const int32_t ctas = static_cast<int32_t>(gridDim.x), rank = static_cast<int32_t>(blockIdx.x);
     const int32_t q = a.rows_per_request, n = a.requests;
     const int32_t r0 = min(n, rank * p.slice), r1 = min(n, r0 + p.slice);
-    const int32_t rows = n * q, per = (rows + ctas - 1) / ctas;
+    const int32_t rows = n * q, per = rows / ctas + (rows % ctas != 0);
     const int32_t t0 = static_cast<int32_t>(min(static_cast<long long>(rows), static_cast<long long>(rank) * per));
     const int32_t t1 = t0 + min(rows - t0, per);
     if (tid == 0) s_taken = 0;

@@ -153,6 +153,18 @@ def test_many_steps_leave_every_page_owned_once():
         assert sorted(held + mine[2][:mine[3]]) == list(range(size))
 
 
+def test_about_as_many_rows_as_31_bits_count():
+    q = (2 ** 31 - 1) // 3
+    table, lengths, free, count = i32([[7, -1]] * 3), i32([1, 0, 64]), i32([5, 6]), i32([2])
+    got = tk.page_step(table, lengths, i32([2, 0, 1]), free, count, rows_per_request=q)
+    assert got.positions.numel() == 3 * q and got.granted.tolist() == [2, 0, 1]
+    for rows, want, pad in zip(got[:3], ((1, 2, 64), (449, 450, 6 * 64), (2, 3, 65)), (0, -1, 0)):
+        assert (*rows[:2].tolist(), rows[2 * q].item()) == want
+        assert rows[2:2 * q].min().item() == rows[2:2 * q].max().item() == pad
+        assert rows[2 * q + 1:].min().item() == rows[2 * q + 1:].max().item() == pad
+    assert table.tolist() == [[7, -1], [7, -1], [7, 6]] and lengths.tolist() == [3, 0, 65] and count.item() == 1
+
+
 def test_on_another_stream():
     a = case(64, 8, 4, 16, 9)
     table, lengths, new, free, count = a
