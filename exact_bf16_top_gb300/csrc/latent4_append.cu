@@ -63,10 +63,11 @@ __device__ __forceinline__ float largest(float m, float v) {
 }
 
 // v / s rounded to nearest, by Markstein's correction of a quotient from the rounded
-// reciprocal: the remainder is exact, and its share of s is added with one rounding.
+// reciprocal: the remainder is exact, and its share of s is taken off with one rounding
+// (of that sign, so that -0 stays -0).
 __device__ __forceinline__ float quotient(float v, float s, float over_s) {
     const float q = __fmul_rn(v, over_s);
-    return __fmaf_rn(__fmaf_rn(-q, s, v), over_s, q);
+    return __fmaf_rn(__fmaf_rn(q, s, -v), -over_s, q);
 }
 
 // A block's 16 values to its scale's e4m3 byte and 16 codes. Both quotients are rounded

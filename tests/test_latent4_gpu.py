@@ -135,6 +135,23 @@ def test_append_not_finite():
     assert torch.isnan(tk.latent4_rows(cache, slots[:2])[:, :512]).all()
 
 
+def test_append_keeps_the_sign_of_zeros():
+    # -0 and what rounds to it have code 8, +0 and what rounds to it code 0, whatever the scale.
+    x = torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda")
+    x[0, ::2] = -0.0
+    x[1] = torch.tensor([-0.0, 0.0, -0.125, 0.125, 6, -6, 1, -1] * 16)
+    x[2] = torch.tensor([-0.0, 0.0, 2.0 ** -133, -(2.0 ** -133), 1.5 * 2.0 ** 60, 0.0, 0.0, -0.0] * 16)
+    slots = torch.arange(3, device="cuda", dtype=torch.int32)
+    for weight in (None, torch.ones(128, dtype=torch.bfloat16, device="cuda")):
+        cache = torch.zeros(3, 224, dtype=torch.uint8, device="cuda")
+        tk.latent4_append(cache, x, torch.zeros(3, ROPE, dtype=torch.bfloat16, device="cuda"), slots, angles(4), slots,
+                          weight=weight, eps=1.0)
+        code = torch.stack((cache[:, :64] & 15, cache[:, :64] >> 4), -1).flatten(1)
+        small = x.abs() <= 0.125
+        assert torch.equal(code[small] & 7, torch.zeros_like(code[small]))
+        assert torch.equal(code >> 3 == 1, torch.signbit(x.float()))
+
+
 @pytest.mark.parametrize("interleaved", [True, False])
 def test_append_rotates_queries_in_place_and_works_without_them(interleaved):
     g, latent, tokens, heads = gen(64), 128, 50, 20
