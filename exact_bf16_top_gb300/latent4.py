@@ -15,7 +15,7 @@ import exact_bf16_top_gb300 as _package
 
 from . import TopkError, load
 from ._latent_abi import Append4
-from .latent import (_BF16, _I32, _U8, LATENTS, MAX_ROWS, ROPE, Form, _append, _check_stream, _paged, _raw_device,
+from .latent import (_BF16, _I32, _U8, LATENTS, MAX_ROWS, ROPE, Form, _append, _check_no_grad, _check_stream, _paged, _raw_device,
                      _raw_stream, _refuse, _row_stride, _selected, _workspace)
 
 
@@ -78,6 +78,8 @@ def latent4_rows(cache, rows, *, latent: int = 512, out=None, stream=None):
     elif not (isinstance(out, torch.Tensor) and out.dtype is _BF16 and out.get_device() == dev
               and out.shape == (count, width) and out.stride(1) == 1):
         raise ValueError("out must be a bfloat16 [rows, latent + 64] with unit inner stride on the cache's device")
+    elif out.requires_grad:
+        _check_no_grad()
     if count:
         status = (_package._lib or load()).latent4_rows(
             cache.data_ptr(), _row_stride(cached, columns, cache_stride, 32), cached, latent, rows.data_ptr(), count,

@@ -168,6 +168,18 @@ def test_append_rotates_queries_in_place_and_works_without_them(interleaved):
     assert torch.equal(apart, together) and all(torch.equal(caches[0], c) for c in caches)
 
 
+def test_rows_refuses_an_output_that_records_a_gradient():
+    cache = Q.random_cache(gen(1), 4, 128)
+    at = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    out = torch.zeros(2, 128 + ROPE, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError):
+        tk.latent4_rows(cache, at, latent=128, out=out)
+    assert not out.any()
+    with torch.no_grad():
+        tk.latent4_rows(cache, at, latent=128, out=out)
+    assert torch.equal(out, tk.latent4_rows(cache, at, latent=128))
+
+
 @pytest.mark.parametrize("latent", [128, 256, 384, 512])
 @pytest.mark.parametrize("count", [0, 1, 9, 1000, 40000])
 def test_rows(latent, count):
