@@ -111,7 +111,10 @@ struct Norm {
 // values that share a scale per lane, so that none of the rounding crosses lanes), or
 // up to 16 of a token's query heads. The sum of squares and the norm are pairs of
 // floats: a value next to a border of 4 bits takes the side that exact arithmetic
-// gives it, whatever the order of the sums.
+// gives it, whatever the order of the sums. Bound by that arithmetic: 8191 tokens of 512
+// values 8.4 us with the norm, 5.1 without (15 MB either way); with 16 heads' queries
+// (another 38 MB) 11.2. (By divisions and with one chain of sums 9.5 instead of 8.4.) One
+// token 2.2 us: the launch and two rounds of loads.
 __global__ void __launch_bounds__(NT) append4_kernel(const latent4_append_t a, uint32_t units, uint32_t groups,
                                                      const Norm norm) {
     grid_dependents_release();
@@ -199,8 +202,8 @@ __device__ __forceinline__ uint4 from_codes(uint32_t w, __half2 scale) {
 }
 
 // R rows of a warp at a time, all their loads together: 16 values of one scale per lane,
-// the key part by eight lanes. Bound by DRAM where rows are many (131071: see
-// launch_rows4), by the launch and two rounds of loads else.
+// the key part by eight lanes. Bound by DRAM where rows are many (131071 rows 35.5 us,
+// 5.8 TB/s), by the launch and two rounds of loads else (2048 rows 2.4 us).
 template <int R>
 __global__ void __launch_bounds__(NT) rows4_kernel(const uint8_t *__restrict__ cache, int64_t cache_stride,
                                                    int32_t cache_rows, int32_t latent, const int32_t *__restrict__ rows,
@@ -282,9 +285,11 @@ cudaError_t launch_rows4(const uint8_t *cache, int64_t cache_stride, int32_t cac
                          const int32_t *rows, int32_t count, uint16_t *out, int64_t out_stride, int sms,
                          cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    // Several rows a warp once there are twice as many as warps that run at once.
+    // Several rows a warp once there are three times as many as warps that run at once
+    // (latent 512, four rows a warp / one: 12000 rows 5.2 / 4.9 us, 20000 7.4 / 7.0, 30000
+    // 9.5 / 10.0, 60000 17.5 / 19.3, 131071 38.2 / 42.0, of a cache of 400000).
     constexpr int R = 4;
-    const bool many = count > 2 * sms * (2048 / 32);
+    const bool many = count > 3 * sms * (2048 / 32);
     const cudaLaunchConfig_t cfg = config(many ? (count + R - 1) / R : count, sms, stream, &attr);
     void *args[] = {&cache, &cache_stride, &cache_rows, &latent, &rows, &count, &out, &out_stride};
     return cudaLaunchKernelExC(&cfg,

@@ -15,8 +15,8 @@ import exact_bf16_top_gb300 as _package
 
 from . import TopkError, load
 from ._latent_abi import Append4
-from .latent import (_BF16, _I32, _U8, LATENTS, MAX_ROWS, ROPE, Form, _append, _check_no_grad, _check_stream, _paged, _raw_device,
-                     _raw_stream, _refuse, _row_stride, _selected, _workspace)
+from .latent import (_BF16, _I32, _U8, LATENTS, MAX_ROWS, ROPE, Form, _append, _check_no_grad, _check_stream, _paged,
+                     _raw_device, _raw_stream, _refuse, _row_stride, _selected, _workspace)
 
 
 def latent4_row_bytes(latent: int) -> int:
