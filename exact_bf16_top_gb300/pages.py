@@ -110,11 +110,13 @@ def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_
                              page_size=page_size, block_rows=block_rows, next_lengths=next_lengths,
                              next_free_count=next_free_count)
     rows = n * q
-    positions, slots, valid_len, granted = block_table.new_empty(3 * rows + n).split_with_sizes((rows, rows, rows, n))
-    at = positions.data_ptr()
+    device = block_table.device
+    positions, slots = torch.empty(rows, dtype=_I32, device=device), torch.empty(rows, dtype=_I32, device=device)
+    valid_len, granted = torch.empty(rows, dtype=_I32, device=device), torch.empty(n, dtype=_I32, device=device)
     args = _Args(block_table.data_ptr(), stride if n > 1 else pages, lengths.data_ptr(), new_tokens.data_ptr(),
                  free_pages.data_ptr(), free_count.data_ptr(), next_lengths.data_ptr(), next_free_count.data_ptr(),
-                 at + 12 * rows, at, at + 4 * rows, at + 8 * rows, n, pages, size, page_size, block_rows, q)
+                 granted.data_ptr(), positions.data_ptr(), slots.data_ptr(), valid_len.data_ptr(), n, pages, size,
+                 page_size, block_rows, q)
     status = (_package._lib or load()).page_step(args, _raw_stream(dev))
     if status:
         raise TopkError(status)
