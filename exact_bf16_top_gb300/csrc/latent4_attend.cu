@@ -48,10 +48,12 @@ constexpr int BLOCKS = 8, TURNS = 16;        // blocks; pairs and units that hav
                                              // not, and two phases of one barrier look like none)
 constexpr int KEY_SLOTS = 2;                 // blocks' key parts in tensor memory
 constexpr uint32_t FULL = 0xFFFFFFFFu;
-// Weights are FP16: the reference is set this far below the maximum and moves when a
-// weight passes 2^MOST, so that the largest weight of a row is 2^11 at least and what
-// FP16 rounds away below 2^-25 is less than 2^-36 of it.
-constexpr float BELOW = 11.0f, MOST = 15.0f;
+// Weights are FP16 (at most 65504): the reference is set this far below the maximum and
+// moves when a weight passes 2^MOST, so that the largest weight of a row is 2^8 at least
+// and what FP16 rounds away below 2^-25 is less than 2^-33 of it. A move stops the sums
+// until they are rescaled, so the two lie far apart (chunk of 509 tokens x 128 heads, 2^11
+// and 2^15: 1565 us, 2^11 and 2^15.9: 1479, 2^8 and 2^15.9: 1430, 2^4: 1430).
+constexpr float BELOW = 8.0f, MOST = 15.9f;
 
 constexpr int HALF = 64;                     // rows of a block that are sent for together
 constexpr int UNIT = HALF * 128;             // bytes of a unit as it comes: 128 bytes of each row of a half
@@ -212,14 +214,24 @@ __device__ __forceinline__ uint4 shared_vec(uint32_t addr) {
 
 // ------------------------------------------------------------------ the warps' parts
 
+// The larger of two pairs of BF16 values, numbers before NaN.
+__device__ __forceinline__ uint32_t larger_pair(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+
 // A softmax group's query rows into shared memory, eight threads a row: the latent part
 // as FP16, all of it times the power of two that brings the row's largest finite value
-// to [2^8, 2^9). Both are exact for values down to 2^-22 of it.
+// to [2^8, 2^9). Both are exact for values down to 2^-22 of it. (Through shared memory as
+// they are, for what is unrolled here is fetched from memory at the start of every
+// launch.)
 template <int NR>
 __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &tile, Ctrl &c, char *query, int group,
                                            int tid) {
     constexpr int SHARE = NR / Shape<NR>::GROUPS;
     const int piece = tid & 7, pairs = p.latent / 128;
+#pragma unroll 1
     for (int r = group * SHARE + (tid >> 3); r < (group + 1) * SHARE; r += 16) {
         const bool on = r < tile.rows;
         const int32_t flat = tile.base + (on ? r : 0), token = flat / p.heads, head = flat - token * p.heads;
@@ -228,14 +240,21 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
 #pragma unroll
         for (int k = 0; k <= LATENT_MAX / 64; ++k)
             v[k] = on && k <= 2 * pairs ? __ldg(reinterpret_cast<const uint4 *>(src + k * 64)) : make_uint4(0, 0, 0, 0);
-        uint32_t most = 0;
+        uint4 *mine = reinterpret_cast<uint4 *>(query + r * 128 + ((piece ^ (r & 7)) << 4));
+        uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k <= LATENT_MAX / 64; ++k) {
-            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = w[i] & 0x7F80u, hi = w[i] >> 16 & 0x7F80u;
-                most = max(most, max(lo == 0x7F80u ? 0u : lo, hi == 0x7F80u ? 0u : hi));
+            if (k <= 2 * pairs) mine[k * NR * 8] = v[k];
+            top = larger_pair(top, larger_pair(larger_pair(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu),
+                                               larger_pair(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu)));
+        }
+        uint32_t most = max(top & 0xFFFFu, top >> 16);
+        if (__any_sync(FULL, most == 0x7F80u)) [[unlikely]] {
+            most = 0;                          // an infinity: the largest of the others
+#pragma unroll 1
+            for (int k = 0; k < (2 * pairs + 1) * 8; ++k) {
+                const uint32_t h = reinterpret_cast<const uint16_t *>(mine + (k >> 3) * NR * 8)[k & 7] & 0x7FFFu;
+                most = max(most, h >= 0x7F80u ? 0u : h);
             }
         }
 #pragma unroll
@@ -246,23 +265,18 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
             const float u = p.scale * LOG2E * __uint_as_float((254u - up) << 23);
             c.unit[r] = fminf(fmaxf(u, -FLT_MAX), FLT_MAX);
         }
-        char *dst = query + r * 128 + ((piece ^ (r & 7)) << 4);
-#pragma unroll
-        for (int k = 0; k <= LATENT_MAX / 64; ++k) {
-            if (k > 2 * pairs) break;
-            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll 1
+        for (int k = 0; k <= 2 * pairs; ++k, mine += NR * 8) {
+            const uint4 x = *mine;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float a = __uint_as_float(w[i] << 16) * by, b = __uint_as_float(w[i] & 0xFFFF0000u) * by;
-                if (k < 2 * pairs) {
-                    const __half2 h = __floats2half2_rn(a, b);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                } else {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
+                const __half2 h = __floats2half2_rn(a, b);
+                const __nv_bfloat162 e = __floats2bfloat162_rn(a, b);
+                w[i] = k < 2 * pairs ? *reinterpret_cast<const uint32_t *>(&h) : *reinterpret_cast<const uint32_t *>(&e);
             }
-            *reinterpret_cast<uint4 *>(dst + k * NR * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+            *mine = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     __syncwarp();

@@ -245,6 +245,7 @@ __device__ __forceinline__ int32_t token_len(const AttendParams &p, int32_t toke
 __device__ __forceinline__ int32_t tile_len(const AttendParams &p, const Tile &t) {
     if (!p.paged) return p.k;
     int32_t n = 0;
+#pragma unroll 1
     for (int32_t i = t.token; i <= t.last; ++i) n = max(n, token_len(p, i));
     return n;
 }
@@ -344,6 +345,7 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<SI
     const int32_t t0 = min(p.tiles, tid * per), t1 = min(p.tiles, t0 + per);
     long long sum = 0;
     int32_t longest = 0;
+#pragma unroll 1
     for (int32_t t = t0; t < t1; ++t) {
         const int32_t n = blocks_of<KEYS>(tile_len(p, tile_at(p, t)));
         sum += n + p.tile_cost;
@@ -394,6 +396,7 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<SI
     }
     if (begin >= before && begin < before + sum) {
         long long at = before;
+#pragma unroll 1
         for (int32_t t = t0; t < t1; ++t) {
             const int32_t n = blocks_of<KEYS>(tile_len(p, tile_at(p, t))) + p.tile_cost;
             if (begin < at + n) {

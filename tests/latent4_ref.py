@@ -86,7 +86,7 @@ def attend(query, values, visible, scale, latent):
     query loses as FP16: nothing where a value is at least 2^-22 of its row's largest,
     else at most half a step of 2^-24 where the largest is at least 2^8, 2^-33 of it.
     Weights p are rounded to FP16: 2^-11 of themselves, or half a step of 2^-24 where
-    the largest is at least 2^11: 2^-36 of it, and so of their sum at most. The result
+    the largest is at least 2^8: 2^-25 / 2^8 = 2^-33 of it, and so of their sum at most. The result
     is rounded to BF16 once. 10 % for products of these, 2^-100 for what underflows.
     """
     tokens, heads, _ = query.shape
@@ -108,6 +108,6 @@ def attend(query, values, visible, scale, latent):
         lost = q.abs().amax(1, keepdim=True) * c.abs().sum(1).amax() * 2.0 ** -33
         d = ((q.abs() @ keys.abs().T).amax(1, keepdim=True) * 2.0 ** -16 + lost) * abs(scale)
         tol[t] = 1.1 * (R.U16 * out[t].abs() + (2.0 ** -11 + 2 * d + 2.0 ** -20) * (p @ c.abs())
-                        + 2.0 ** -36 * c.abs().sum(0)) + 2.0 ** -100
+                        + 2.0 ** -33 * c.abs().sum(0)) + 2.0 ** -100
         tol_lse[t] = d[:, 0] + 2.0 ** -20 * (1 + lse[t].abs())
     return out, lse, tol, tol_lse
