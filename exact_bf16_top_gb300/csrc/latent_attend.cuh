@@ -205,6 +205,14 @@ __device__ __forceinline__ float largest(float m, float a, float b) {
 
 // ------------------------------------------------------------------ the schedule
 
+// A tile is up to 64 consecutive (token, head) rows of one request (paged form)
+// or token (selected form).
+struct Tile {
+    int32_t base, rows;          // first flat row (token * heads + head), rows
+    int32_t token, last;         // first and last token
+    int32_t request;
+};
+
 // What a CTA (of NT threads at most) knows of its share of the blocks: part of its control block.
 template <int NT>
 struct Schedule {
@@ -213,14 +221,8 @@ struct Schedule {
     int32_t first_tile, first_unit;
     int32_t ranks;                             // CTAs of the cluster that have blocks
     long long begin, share, total;
-};
-
-// A tile is up to 64 consecutive (token, head) rows of one request (paged form)
-// or token (selected form).
-struct Tile {
-    int32_t base, rows;          // first flat row (token * heads + head), rows
-    int32_t token, last;         // first and last token
-    int32_t request;
+    Tile tile;                                 // the first one
+    int32_t len, low;
 };
 
 __device__ __forceinline__ Tile tile_at(const AttendParams &p, int32_t t) {
@@ -240,13 +242,17 @@ __device__ __forceinline__ int32_t token_len(const AttendParams &p, int32_t toke
     return min(max(p.valid_len[token], 0), p.width);
 }
 
-// Cache rows that a tile's longest row may see, and blocks of them (at least
-// one: a tile that sees nothing still writes its outputs).
-__device__ __forceinline__ int32_t tile_len(const AttendParams &p, const Tile &t) {
-    if (!p.paged) return p.k;
+// Cache rows that a tile's longest row may see (blocks of them: at least one, for a
+// tile that sees nothing still writes its outputs); low: its shortest row.
+__device__ __forceinline__ int32_t tile_len(const AttendParams &p, const Tile &t, int32_t &low) {
+    low = INT32_MAX;
     int32_t n = 0;
 #pragma unroll 1
-    for (int32_t i = t.token; i <= t.last; ++i) n = max(n, token_len(p, i));
+    for (int32_t i = t.token; i <= t.last; ++i) {
+        const int32_t v = token_len(p, i);
+        n = max(n, v);
+        low = min(low, v);
+    }
     return n;
 }
 
@@ -258,7 +264,7 @@ __host__ __device__ __forceinline__ int64_t split_cost(int64_t parts, int64_t ti
 template <int KEYS>
 __device__ __forceinline__ int32_t blocks_of(int32_t len) { return max(1, (len + KEYS - 1) / KEYS); }
 
-// As tile_len, by a whole warp; low: the tile's smallest length.
+// As tile_len, by a whole warp.
 __device__ __forceinline__ int32_t tile_len_warp(const AttendParams &p, const Tile &t, int lane, int32_t &low) {
     low = INT32_MAX;
     if (!p.paged) return p.k;
@@ -278,7 +284,9 @@ __device__ __forceinline__ int32_t tile_len_warp(const AttendParams &p, const Ti
 // query, first reference and outputs (854 tiles of 1 to 4 blocks: 97 us counted
 // as none, 72 as five). Or each CTA has one tile: a cluster's CTAs share one where
 // the host chose so, and pages whose tiles are about as many as the CTAs and about
-// as long as each other are not split, which only the lengths here can tell.
+// as long as each other are not split, which only the lengths here can tell. Whoever
+// makes the schedule leaves the first tile in it: a CTA begins with code that nobody
+// has fetched yet, of which six roles need not each have a copy.
 template <int KEYS>
 struct CursorOf {
     int32_t next_tile, next_unit;
@@ -286,14 +294,18 @@ struct CursorOf {
     Tile tile;
     int32_t b0, b1, blocks, len, low;   // the piece: blocks [b0, b1) of `blocks`
     int32_t u0, u1, units;              // the same with the tile's own cost in front
+    bool first = true;
     template <class Ctrl>
     __device__ CursorOf(const Ctrl &c)
-        : next_tile(c.first_tile), next_unit(c.first_unit),
-          left(min(c.begin + c.share, c.total) - c.begin) {}
+        : next_tile(c.first_tile), next_unit(c.first_unit), left(min(c.begin + c.share, c.total) - c.begin),
+          tile(c.tile), len(c.len), low(c.low) {}
     __device__ bool next(const AttendParams &p, int lane) {
         if (left <= 0) return false;
-        tile = tile_at(p, next_tile);
-        len = tile_len_warp(p, tile, lane, low);
+        if (!first) [[unlikely]] {
+            tile = tile_at(p, next_tile);
+            len = tile_len_warp(p, tile, lane, low);
+        }
+        first = false;
         blocks = blocks_of<KEYS>(len);
         units = blocks + p.tile_cost;
         u0 = next_unit;
@@ -315,10 +327,14 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<SI
     if (p.cluster) {                           // a tile per cluster, its blocks in equal runs
         if (warp == 0) {
             const int32_t tile = blockIdx.x / p.cluster, rank = blockIdx.x - tile * p.cluster;
+            const Tile first = tile_at(p, tile);
             int32_t low;
-            const int32_t n = blocks_of<KEYS>(tile_len_warp(p, tile_at(p, tile), lane, low));
+            const int32_t len = tile_len_warp(p, first, lane, low), n = blocks_of<KEYS>(len);
             const int32_t per = (n + p.cluster - 1) / p.cluster;
             if (lane == 0) {
+                c.tile = first;
+                c.len = len;
+                c.low = low;
                 c.first_tile = tile;
                 c.first_unit = rank * per;
                 c.begin = 0;
@@ -337,17 +353,24 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<SI
             c.begin = min(c.total, c.share * blockIdx.x);
             c.first_tile = static_cast<int32_t>(c.begin / n);
             c.first_unit = static_cast<int32_t>(c.begin % n);
+            c.tile = tile_at(p, c.first_tile);
+            c.len = p.k;
+            c.low = INT32_MAX;
         }
         __syncthreads();
         return;
     }
     const int32_t per = (p.tiles + NT - 1) / NT;
     const int32_t t0 = min(p.tiles, tid * per), t1 = min(p.tiles, t0 + per);
+    Tile tile;
+    int32_t len = 0, low = 0;
     long long sum = 0;
     int32_t longest = 0;
 #pragma unroll 1
     for (int32_t t = t0; t < t1; ++t) {
-        const int32_t n = blocks_of<KEYS>(tile_len(p, tile_at(p, t)));
+        tile = tile_at(p, t);
+        len = tile_len(p, tile, low);
+        const int32_t n = blocks_of<KEYS>(len);
         sum += n + p.tile_cost;
         longest = max(longest, n);
     }
@@ -376,11 +399,17 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<SI
     const int32_t ctas = static_cast<int32_t>(gridDim.x);
     if (p.tiles <= ctas && longest <= share + split_cost(ctas, p.tiles) / SPLIT_UNIT) {
         if (warp == 0) {                       // every tile to a CTA of its own
-            const int32_t tile = blockIdx.x;
-            int32_t n = 0, low;
-            if (tile < p.tiles) n = blocks_of<KEYS>(tile_len_warp(p, tile_at(p, tile), lane, low));
+            int32_t n = 0;
+            if (blockIdx.x < static_cast<unsigned>(p.tiles)) {
+                tile = tile_at(p, blockIdx.x);
+                len = tile_len_warp(p, tile, lane, low);
+                n = blocks_of<KEYS>(len);
+            }
             if (lane == 0) {
-                c.first_tile = tile;
+                c.tile = tile;
+                c.len = len;
+                c.low = low;
+                c.first_tile = blockIdx.x;
                 c.first_unit = 0;
                 c.begin = 0;
                 c.share = c.total = n;
@@ -398,8 +427,15 @@ __device__ __forceinline__ void make_schedule(const AttendParams &p, Schedule<SI
         long long at = before;
 #pragma unroll 1
         for (int32_t t = t0; t < t1; ++t) {
-            const int32_t n = blocks_of<KEYS>(tile_len(p, tile_at(p, t))) + p.tile_cost;
+            if (per > 1) {                     // (of a single tile they are known)
+                tile = tile_at(p, t);
+                len = tile_len(p, tile, low);
+            }
+            const int32_t n = blocks_of<KEYS>(len) + p.tile_cost;
             if (begin < at + n) {
+                c.tile = tile;
+                c.len = len;
+                c.low = low;
                 c.first_tile = t;
                 c.first_unit = static_cast<int32_t>(begin - at);
                 break;
