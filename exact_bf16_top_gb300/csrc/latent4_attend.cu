@@ -299,6 +299,7 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
     using S = Shape<NR>;
     const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - S::SEND_WARP, pairs = p.latent / 128;
     const int units = 1 + (pairs + 1) / 2;
+    const bool one = elected();
     const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
     const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT;
     Cursor at(c);
@@ -320,9 +321,12 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                 mask[h] = __ballot_sync(FULL, row[h] >= 0);
             }
             if (p.tiled) {
-                if (lane == 0) {
+                const uint32_t turn0 = turn, end = slot + units;
+                const int32_t first[2] = {__shfl_sync(FULL, row[0], 0), __shfl_sync(FULL, row[1], 0)};
+                if (one) {
                     // (rows of which there are none, and rows past the cache, come as zeros)
-                    const int32_t y0 = row[0] >= 0 ? row[0] : p.cache_rows, y1 = row[1] >= 0 ? row[1] : p.cache_rows;
+                    const int32_t y0 = first[0] >= 0 ? first[0] : p.cache_rows;
+                    const int32_t y1 = first[1] >= 0 ? first[1] : p.cache_rows;
                     for (int u = 0; u < units; ++u) {
                         u64 *full = &c.unit_full[half][turn % TURNS];
                         const uint32_t to = ring + slot * UNIT;
@@ -349,9 +353,9 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                     }
                 }
                 __syncwarp();
-                slot = __shfl_sync(FULL, slot, 0);
-                use = __shfl_sync(FULL, use, 0);
-                turn = __shfl_sync(FULL, turn, 0);
+                turn = turn0 + units;
+                slot = end % S::UNITS;
+                use = turn / S::UNITS;
                 continue;
             }
             // Eight lanes a row, four rows a copy: where this lane's copies come from.
