@@ -297,19 +297,19 @@ template <int NR>
 __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, const CUtensorMap *scales_map, Ctrl &c,
                           uint32_t raw) {
     using S = Shape<NR>;
-    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - S::SEND_WARP, pairs = p.latent / 128;
-    const int units = 1 + (pairs + 1) / 2;
+    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) - S::SEND_WARP;
+    const int pairs = p.latent / 128, units = 1 + (pairs + 1) / 2;
     const bool one = elected();
     const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
     const uint32_t ring = raw + half * S::RING, scales = ring + S::UNITS * UNIT;
     Cursor at(c);
-    uint32_t i = 0, turn = 0, slot = 0, use = 0;   // the block; the next unit, its place and the place's use
+    uint32_t i = 0, turn = 0;                  // the block and its first unit
     while (at.next(p, lane)) {
         const RowList list(p, at);
         int32_t now[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) now[h] = list.fetch(p, at.b0 * KEYS + half * HALF + h * 32 + lane);
-        for (int32_t b = at.b0; b < at.b1; ++b, ++i) {
+        for (int32_t b = at.b0; b < at.b1; ++b, ++i, turn += units) {
             const uint32_t s = i % S::SCALE_SLOTS;
             int32_t row[2];
             uint32_t mask[2];
@@ -321,31 +321,25 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                 mask[h] = __ballot_sync(FULL, row[h] >= 0);
             }
             if (p.tiled) {
-                const uint32_t turn0 = turn, end = slot + units;
-                const int32_t first[2] = {__shfl_sync(FULL, row[0], 0), __shfl_sync(FULL, row[1], 0)};
+                // (rows of which there are none, and rows past the cache, come as zeros)
+                const int32_t r0 = __shfl_sync(FULL, row[0], 0), r1 = __shfl_sync(FULL, row[1], 0);
+                const int32_t y0 = r0 >= 0 ? r0 : p.cache_rows, y1 = r1 >= 0 ? r1 : p.cache_rows;
                 if (one) {
-                    // (rows of which there are none, and rows past the cache, come as zeros)
-                    const int32_t y0 = first[0] >= 0 ? first[0] : p.cache_rows;
-                    const int32_t y1 = first[1] >= 0 ? first[1] : p.cache_rows;
                     for (int u = 0; u < units; ++u) {
-                        u64 *full = &c.unit_full[half][turn % TURNS];
-                        const uint32_t to = ring + slot * UNIT;
+                        const uint32_t t = turn + u, slot = t % S::UNITS;
                         const int x = u ? (u - 1) * 128 : p.latent / 2;
-                        await(&c.unit_empty[half][slot], (use + 1) & 1u, c);
+                        u64 *full = &c.unit_full[half][t % TURNS];
+                        await(&c.unit_empty[half][slot], (t / S::UNITS + 1) & 1u, c);
                         mbar_expect_tx(full, UNIT);
-                        copy_box(to, units_map, x, y0, full);
-                        if (p.tiled == 1) copy_box(to + UNIT / 2, units_map, x, y1, full);
-                        ++turn;
-                        if (++slot == S::UNITS) {
-                            slot = 0;
-                            ++use;
-                        }
+                        copy_box(ring + slot * UNIT, units_map, x, y0, full);
+                        if (p.tiled == 1) copy_box(ring + slot * UNIT + UNIT / 2, units_map, x, y1, full);
                         if (u == 0) {
                             full = &c.scales_full[half][s];
                             await(&c.scales_empty[half][s], (i / S::SCALE_SLOTS + 1) & 1u, c);
                             mbar_expect_tx(full, SCALES);
                             copy_box(scales + s * SCALES, scales_map, p.latent / 2 + 128, y0, full);
-                            if (p.tiled == 1) copy_box(scales + s * SCALES + SCALES / 2, scales_map, p.latent / 2 + 128, y1, full);
+                            if (p.tiled == 1)
+                                copy_box(scales + s * SCALES + SCALES / 2, scales_map, p.latent / 2 + 128, y1, full);
                             c.marks[i % BLOCKS][2 * half] = mask[0];
                             c.marks[i % BLOCKS][2 * half + 1] = mask[1];
                             arrive(&c.row_full[i % BLOCKS]);
@@ -353,9 +347,6 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                     }
                 }
                 __syncwarp();
-                turn = turn0 + units;
-                slot = end % S::UNITS;
-                use = turn / S::UNITS;
                 continue;
             }
             // Eight lanes a row, four rows a copy: where this lane's copies come from.
@@ -368,18 +359,13 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                 src[m] = cache + __shfl_sync(FULL, offset[m / 8], (4 * m + (lane >> 3)) & 31) + (lane & 7) * 16;
             const uint64_t mine = all >> (lane >> 3);   // bit 4 m: there is something to copy
             for (int u = 0; u < units; ++u) {
-                const uint32_t to = ring + slot * UNIT + (lane >> 3) * 128;
+                const uint32_t t = turn + u, slot = t % S::UNITS, to = ring + slot * UNIT + (lane >> 3) * 128;
                 const int x = u ? (u - 1) * 128 : p.latent / 2;
-                await_warp(&c.unit_empty[half][slot], use + 1, c);
+                await_warp(&c.unit_empty[half][slot], t / S::UNITS + 1, c);
 #pragma unroll
                 for (int m = 0; m < HALF / 4; ++m)
                     copy16(to + m * 512 + (((lane ^ (4 * m + (lane >> 3))) & 7) << 4), src[m] + x, mine >> 4 * m & 1u);
-                copies_arrive(&c.unit_full[half][turn % TURNS]);
-                ++turn;
-                if (++slot == S::UNITS) {
-                    slot = 0;
-                    ++use;
-                }
+                copies_arrive(&c.unit_full[half][t % TURNS]);
                 if (u == 0) {
                     await_warp(&c.scales_empty[half][s], i / S::SCALE_SLOTS + 1, c);
 #pragma unroll
