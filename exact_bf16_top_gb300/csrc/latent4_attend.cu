@@ -82,7 +82,7 @@ struct Shape {
 
 struct Ctrl : Schedule<NT> {
     u64 unit_full[2][TURNS], unit_empty[2][3]; // a half's unit is in / read
-    u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in / read
+    u64 scales_full[2][2], scales_empty[2][2]; // a half's scales are in (boxes: with the first values) / read
     u64 a_full[4], a_done[TURNS];              // a pair is in tensor memory / its scores are added and it is copied
     u64 pair_full[4], summed[TURNS];           // a pair is in shared memory / its sums are added
     u64 key_full[KEY_SLOTS], key_done[BLOCKS]; // a block's key part is in tensor memory / its scores are added
@@ -320,29 +320,30 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                 now[h] = list.fetch(p, j + KEYS);
                 mask[h] = __ballot_sync(FULL, row[h] >= 0);
             }
+            auto mark = [&]() {
+                c.marks[i % BLOCKS][2 * half] = mask[0];
+                c.marks[i % BLOCKS][2 * half + 1] = mask[1];
+                arrive(&c.row_full[i % BLOCKS]);
+            };
             if (p.tiled) {
                 // (rows of which there are none, and rows past the cache, come as zeros)
                 const int32_t r0 = __shfl_sync(FULL, row[0], 0), r1 = __shfl_sync(FULL, row[1], 0);
                 const int32_t y0 = r0 >= 0 ? r0 : p.cache_rows, y1 = r1 >= 0 ? r1 : p.cache_rows;
                 if (one) {
+                    mark();
                     for (int u = 0; u < units; ++u) {
                         const uint32_t t = turn + u, slot = t % S::UNITS;
                         const int x = u ? (u - 1) * 128 : p.latent / 2;
                         u64 *full = &c.unit_full[half][t % TURNS];
                         await(&c.unit_empty[half][slot], (t / S::UNITS + 1) & 1u, c);
-                        mbar_expect_tx(full, UNIT);
+                        if (u == 1) await(&c.scales_empty[half][s], (i / S::SCALE_SLOTS + 1) & 1u, c);
+                        mbar_expect_tx(full, u == 1 ? UNIT + SCALES : UNIT);
                         copy_box(ring + slot * UNIT, units_map, x, y0, full);
                         if (p.tiled == 1) copy_box(ring + slot * UNIT + UNIT / 2, units_map, x, y1, full);
-                        if (u == 0) {
-                            full = &c.scales_full[half][s];
-                            await(&c.scales_empty[half][s], (i / S::SCALE_SLOTS + 1) & 1u, c);
-                            mbar_expect_tx(full, SCALES);
-                            copy_box(scales + s * SCALES, scales_map, p.latent / 2 + 128, y0, full);
-                            if (p.tiled == 1)
-                                copy_box(scales + s * SCALES + SCALES / 2, scales_map, p.latent / 2 + 128, y1, full);
-                            c.marks[i % BLOCKS][2 * half] = mask[0];
-                            c.marks[i % BLOCKS][2 * half + 1] = mask[1];
-                            arrive(&c.row_full[i % BLOCKS]);
+                        if (u == 1) {
+                            const uint32_t to = scales + s * SCALES;
+                            copy_box(to, scales_map, p.latent / 2 + 128, y0, full);
+                            if (p.tiled == 1) copy_box(to + SCALES / 2, scales_map, p.latent / 2 + 128, y1, full);
                         }
                     }
                 }
@@ -376,20 +377,13 @@ __device__ void send_rows(const AttendParams &p, const CUtensorMap *units_map, c
                                all >> r & 1u);
                     }
                     copies_arrive(&c.scales_full[half][s]);
-                    if (lane == 0) {
-                        c.marks[i % BLOCKS][2 * half] = mask[0];
-                        c.marks[i % BLOCKS][2 * half + 1] = mask[1];
-                        arrive(&c.row_full[i % BLOCKS]);
-                    }
+                    if (lane == 0) mark();
                 }
             }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (p.tiled && c.abort) {
-        settle(c.unit_full[half], static_cast<int32_t>(turn) - 1, 1, TURNS);
-        settle(c.scales_full[half], static_cast<int32_t>(i) - 1, 1, S::SCALE_SLOTS);
-    }
+    if (p.tiled && c.abort) settle(c.unit_full[half], static_cast<int32_t>(turn) - 1, 1, TURNS);
 }
 
 // Units into tensor memory, a row a lane, each warp the rows of its own lanes there, 64
@@ -446,7 +440,7 @@ __device__ void convert_rows(const AttendParams &p, Ctrl &c, uint32_t raw, uint3
                 __syncwarp();
                 arrive_one(&c.key_full[key], lane);
             }
-            await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
+            if (!p.tiled) await_warp(&c.scales_full[half][s], i / S::SCALE_SLOTS, c);
 #pragma unroll 1
             for (int first = 0; first < pairs; first += 2) {
                 const uint32_t from = next_unit();
@@ -899,7 +893,7 @@ __global__ void __launch_bounds__(NT, 1) attend4_kernel(const __grid_constant__ 
             for (int s = 0; s < TURNS; ++s) mbar_init(&c.unit_full[h][s], p.tiled ? 1 : 32);
             for (int s = 0; s < S::UNITS; ++s) mbar_init(&c.unit_empty[h][s], 2 * S::CONVERT);
             for (int s = 0; s < S::SCALE_SLOTS; ++s) {
-                mbar_init(&c.scales_full[h][s], p.tiled ? 1 : 32);
+                mbar_init(&c.scales_full[h][s], 32);
                 mbar_init(&c.scales_empty[h][s], 2 * S::CONVERT);
             }
         }
