@@ -13,14 +13,15 @@
 // The key part stays BF16 and only goes to tensor memory. Warps have one job each
 // (softmax, copies, conversion, issue of either product) and meet at mbarriers only.
 //
-// Measured, latent part 512: 32 requests x 16 heads x 16384 rows 71 us (2.2 TB/s, the
-// rows in BF16 85 us), 128 tokens x 16 heads x 2048 listed rows 49 us (2.3 TB/s, 55), a
-// chunk of 509 tokens x 128 heads on 9000 rows 1.57 ms (0.79 PFLOP/s, 1.20 ms). What
-// bounds it is neither memory nor the tensor cores but the way of a block through the
-// warps, 3.1 to 3.5 us of 8.5 K warp instructions at 40 % of the issue slots: leaving
-// out any one part of it (the conversions, the exponentials, either product) takes a few
-// percent off. So where query rows are many the rows in BF16 are faster; these take 36 %
-// of the memory.
+// Measured, latent part 512: 32 requests x 16 heads x 16384 rows 61 us (2.6 TB/s; the
+// rows in BF16 82 us), 128 tokens x 16 heads x 2048 listed rows 48 us (2.4 TB/s; 55), a
+// chunk of 509 tokens x 128 heads on 9000 rows 1.42 ms (0.88 PFLOP/s; 1.20 ms). Neither
+// memory nor the tensor cores nor the issue slots are full: a block takes 4000 to 5500
+// cycles. With few query rows that is the time of the warps that send for its rows
+// (converters wait for them 1800 to 2400 cycles a block, they hardly ever for a place).
+// With 64 it is a loop: a block's last pairs find a place only when the sums of the one
+// before have read theirs, and its scores, softmax and sums come after. So where query
+// rows are many the rows in BF16 are faster; these take 36 % of the memory.
 
 #include <cuda_fp16.h>
 
@@ -36,10 +37,11 @@ namespace {
 // group, two of 64 query rows); cache rows from 4 bits to FP16 in tensor memory (two, one
 // of 64 query rows); values from there to shared memory; and two warps for copies of
 // cache rows as they are, two for the tensor cores (scores, sums). 96 registers each.
-// (32 requests x 16 heads x 16384: 71 us; 24 warps of 80 registers, with two groups for
-// the values too, 73, for what did not fit lay in a first-level cache of 28 KB; 16 warps
-// of 128 with one group a job 72. A chunk of 509 tokens x 128 heads, one softmax group:
-// 2.05 ms instead of 1.78 before the other steps.)
+// (32 requests x 16 heads x 16384: 61 us; 22 warps, two senders more, have 80 registers,
+// and what does not fit lies in a first-level cache of 28 KB: 71. Before the other steps:
+// 24 warps with two groups for the values too 73 instead of 71, 16 warps of 128 registers
+// with one group a job 72; a chunk of 509 tokens x 128 heads with one softmax group 2.05
+// ms instead of 1.78.)
 constexpr int NT = 640;
 constexpr int KEYS = 128;                    // cache rows of a block
 constexpr int CHUNK = KEYS * 128;            // bytes of a block's rows at 64 of their values

@@ -641,6 +641,45 @@ def test_repeats_are_bit_equal_and_streams_are_kept():
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+def test_two_calls_at_once():
+    # Split tiles and clusters of both forms on two streams, eagerly and as graphs replayed side by side, each call
+    # with scratch of its own; a shared one serves calls that follow each other on one stream.
+    query, cache, sel = selected_case(9, 64, 512, 2048, 9000, 31)
+    table = torch.arange(140, device="cuda", dtype=torch.int32)[None]
+    lens = torch.full((9,), 8960, dtype=torch.int32, device="cuda") - torch.arange(9, device="cuda").flip(0).int()
+    shared = tk.latent4_workspace()
+
+    def one(workspace=None):
+        return tk.latent4_attend_selected(query, cache, sel, SCALE, lse=True, workspace=workspace)
+
+    def other(workspace=None):
+        return tk.latent4_attend_paged(query, cache, lens, table, SCALE, rows_per_request=9, lse=True,
+                                       workspace=workspace)
+
+    want = (*one(), *other())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for call in (one, other):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held.append([call() for _ in range(3)])
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    eager = [[], []]
+    for i in range(12):
+        for k, call in enumerate((one, other)):
+            with torch.cuda.stream(streams[k]):
+                eager[k].append(call())
+                graphs[k].replay()
+    torch.cuda.synchronize()
+    both = [(one(shared), other(shared)) for _ in range(5)]
+    torch.cuda.synchronize()
+    for k in range(2):
+        for got in (*eager[k], *held[k], *(b[k] for b in both)):
+            assert torch.equal(got[0], want[2 * k]) and torch.equal(got[1], want[2 * k + 1])
+
+
 @pytest.mark.parametrize("latent", [128, 512])
 def test_a_paged_step_over_pages_in_four_bits(latent):
     """The operators as a server uses them, captured once and replayed: tables and slots, append, selection from the
