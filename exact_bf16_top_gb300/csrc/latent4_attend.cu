@@ -276,7 +276,8 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
                 const float a = __uint_as_float(w[i] << 16) * by, b = __uint_as_float(w[i] & 0xFFFF0000u) * by;
                 const __half2 h = __floats2half2_rn(a, b);
                 const __nv_bfloat162 e = __floats2bfloat162_rn(a, b);
-                w[i] = k < 2 * pairs ? *reinterpret_cast<const uint32_t *>(&h) : *reinterpret_cast<const uint32_t *>(&e);
+                w[i] = *reinterpret_cast<const uint32_t *>(&e);
+                if (k < 2 * pairs) w[i] = *reinterpret_cast<const uint32_t *>(&h);
             }
             *mine = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -623,7 +624,8 @@ __device__ void multiply_sums(const AttendParams &p, Ctrl &c, uint32_t pairs_at,
 // registers. Whether a score outgrows its reference is voted on before the exponentials:
 // the scores' place is free from then on.
 template <int NR>
-__device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_at, uint32_t weights_at, uint32_t tmem) {
+__device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_at, uint32_t weights_at,
+                       uint32_t tmem) {
     using S = Shape<NR>;
     constexpr int SHARE = NR / S::GROUPS, N = SHARE / 4;   // query rows of a group, of a thread
     const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, lane = tid & 31, w = tid >> 5, quad = lane & 3;

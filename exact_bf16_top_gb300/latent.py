@@ -92,8 +92,8 @@ def latent_append(cache, latent, key_rope, positions, cos_sin, slots, *, weight=
     """Writes tokens' rows into the cache (latent_bf16_append) and returns it.
 
     cache: CUDA bfloat16 [rows, latent + 64], written at ``slots`` (CUDA int32
-    [tokens], physical rows; a token whose slot lies outside the cache, e.g. -1,
-    is not written); latent: bfloat16 [tokens, 128 | 256 | 384 | 512]; key_rope:
+    [tokens], physical rows, distinct; a token whose slot lies outside the cache,
+    e.g. -1, is not written); latent: bfloat16 [tokens, 128 | 256 | 384 | 512]; key_rope:
     bfloat16 [tokens, 64]; positions: int32 [tokens]; cos_sin: float32
     [positions, 64], a position's 32 cosines then 32 sines; weight: None (no
     norm) or bfloat16 [latent], of x * weight / sqrt(mean(x^2) + eps);
@@ -173,8 +173,8 @@ def _selected(form, query, cache, selected, scale, latent, out, lse, workspace, 
                    (k, 0, 0, 1, 1, 1))
 
 
-def _paged(form, query, cache, valid_len, block_table, scale, page_size, block_rows, rows_per_request, width, latent, out,
-           lse, workspace, stream):
+def _paged(form, query, cache, valid_len, block_table, scale, page_size, block_rows, rows_per_request, width, latent,
+           out, lse, workspace, stream):
     try:
         dev = query.get_device()
         requests, pages = block_table.shape
@@ -249,8 +249,8 @@ def _attend(form, paged, dev, query, cache, scale, latent, out, lse, workspace, 
     lse_ptr = None if lse is None else lse.data_ptr()
     if tokens:
         args = Attend(query.data_ptr(), *_head_strides(query), cache.data_ptr(),
-                      _row_stride(rows, columns, cache_stride, form.granule), *pointers, out.data_ptr(), lse_ptr, None, 0, rows,
-                      tokens, heads, latent, *sizes, scale)
+                      _row_stride(rows, columns, cache_stride, form.granule), *pointers, out.data_ptr(), lse_ptr,
+                      None, 0, rows, tokens, heads, latent, *sizes, scale)
         lib = _package._lib or load()
         if workspace is None:
             n = getattr(lib, form.workspace)(args, paged)
