@@ -733,9 +733,12 @@ __device__ void soften(const AttendParams &p, Ctrl &c, char *query, char *pairs_
                     const float t = fmaxf(fmaxf(c.across[0][mine_row], c.across[1][mine_row]),
                                           fmaxf(c.across[2][mine_row], c.across[3][mine_row]));
                     const float old = c.ref[mine_row];
-                    const bool move = t > old + MOST;  // (of LOWEST: t > old)
-                    c.factor[mine_row] = move ? exp2_fast(old - (t - BELOW)) : 1.0f;
-                    if (move) c.ref[mine_row] = t - BELOW;
+                    // (Differences, as the exponents are: sums of large scores round. From 2^27 on t - BELOW
+                    // may lie 16 below t, where the weight would be infinite: then t itself is taken.)
+                    const bool move = t - old > MOST;  // (of LOWEST: t > old)
+                    const float below = t - BELOW, to = t - below > MOST ? t : below;
+                    c.factor[mine_row] = move ? exp2_fast(old - to) : 1.0f;
+                    if (move) c.ref[mine_row] = to;
                 }
                 group_sync(group);
 #pragma unroll
