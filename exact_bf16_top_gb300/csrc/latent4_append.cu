@@ -27,31 +27,39 @@ __device__ __forceinline__ Two add(Two a, Two b) {
     return {s, __fadd_rn(__fadd_rn(a.lo, b.lo), e)};
 }
 
-__device__ __forceinline__ Two times(Two a, Two b) {
-    const float h = __fmul_rn(a.hi, b.hi);
-    return {h, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -h)))};
+// a / n of such a number and a small whole one, over = 1 / n: to 2^-47, and exactly where
+// the quotient is a float.
+__device__ __forceinline__ Two share(Two a, float n, float over) {
+    const float h = __fmul_rn(a.hi, over);
+    return {h, __fmul_rn(__fadd_rn(__fmaf_rn(-h, n, a.hi), a.lo), over)};
 }
 
-// 1 / sqrt(x): Newton's step in pairs of floats on the hardware's estimate, whose
-// error of 2^-22 becomes 2^-44 (and stays none where there was none: rows whose mean
-// square is a power of four give values that lie on the borders).
-__device__ __forceinline__ Two over_sqrt(Two x) {
-    const float y = rsqrtf(x.hi);
-    const float p = __fmul_rn(y, y), pe = __fmaf_rn(y, y, -p);
-    const float q = __fmul_rn(x.hi, p), qe = __fmaf_rn(x.hi, p, -q);
-    const float e = __fadd_rn(1.0f, -q) - qe - x.hi * pe - x.lo * p;   // 1 - x y^2
-    const float d = y * __fmaf_rn(0.375f * e, e, 0.5f * e), r = __fadd_rn(y, d);   // (NaN of an infinite x)
-    return {r, __fadd_rn(d, -__fadd_rn(r, -y))};
+// sqrt(x), and 1 / sqrt(x) as a float. Two of Newton's steps on the hardware's estimate,
+// each from the exact remainder: to 2^-46, and exactly where the root is a float (a row
+// whose norm is a number of few digits has values that lie on the borders).
+struct Root {
+    Two g;
+    float over;
+};
+
+__device__ __forceinline__ Root root(Two x) {
+    const float y = rsqrtf(x.hi), half = 0.5f * y;
+    const float h = __fmul_rn(x.hi, y);      // (NaN of an infinite x and of 0)
+    const float hi = __fmaf_rn(__fadd_rn(__fmaf_rn(-h, h, x.hi), x.lo), half, h);
+    return {{hi, __fmul_rn(__fadd_rn(__fmaf_rn(-hi, hi, x.hi), x.lo), half)}, y};
 }
 
-// xw * r, rounded to odd: what is not a float becomes the neighbour whose last bit is
-// 1. Rounded further to any format of two bits less it gives what the exact product
-// would, ties included.
-__device__ __forceinline__ float times_odd(float xw, Two r) {
-    const float v = __fmul_rn(xw, r.hi);
-    const float e = __fmaf_rn(xw, r.lo, __fmaf_rn(xw, r.hi, -v));
+// xw / g, rounded to odd: what is not a float becomes the neighbour whose last bit is 1.
+// Rounded further to any format of two bits less it gives what the exact quotient would,
+// ties included. The quotient is rounded to nearest first, for which of its neighbours the
+// remainder then points to is certain (product with a reciprocal of two parts, which may
+// be off by 1.5 units, took the wrong side of a border now and then); -0 stays -0.
+__device__ __forceinline__ float over_odd(float xw, const Root &r) {
+    const float q = __fmul_rn(xw, r.over);
+    const float v = __fmaf_rn(__fmaf_rn(q, r.g.lo, __fmaf_rn(q, r.g.hi, -xw)), -r.over, q);
+    const float m = __fmaf_rn(v, r.g.lo, __fmaf_rn(v, r.g.hi, -xw));   // v g - xw
     uint32_t b = __float_as_uint(v);
-    if (e != 0.0f && !(b & 1u)) b += (__float_as_uint(e) ^ b) >> 31 ? FULL : 1u;   // (towards e; NaN stays NaN)
+    if (m != 0.0f && !(b & 1u)) b += (__float_as_uint(m) ^ b) >> 31 ? 1u : FULL;   // (away from m; NaN stays NaN)
     return __uint_as_float(b);
 }
 
@@ -104,7 +112,8 @@ __device__ __forceinline__ uint32_t to_codes(const float (&v)[16], uint32_t (&co
 }
 
 struct Norm {
-    Two share, eps;                          // 1 / latent, eps
+    float over;                              // 1 / latent
+    Two eps;
 };
 
 // One warp per unit of work, as in the BF16 form: a token's cache row (a block of 16
@@ -166,11 +175,11 @@ __global__ void __launch_bounds__(NT) append4_kernel(const latent4_append_t a, u
 #pragma unroll
             for (int o = 16; o; o >>= 1)
                 sum = add(sum, {__shfl_xor_sync(FULL, sum.hi, o), __shfl_xor_sync(FULL, sum.lo, o)});
-            const Two r = over_sqrt(add(times(sum, norm.share), norm.eps));
+            const Root r = root(add(share(sum, static_cast<float>(a.latent), norm.over), norm.eps));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[2 * i] = times_odd(__fmul_rn(v[2 * i], lo_f(g[i])), r);
-                v[2 * i + 1] = times_odd(__fmul_rn(v[2 * i + 1], hi_f(g[i])), r);
+                v[2 * i] = over_odd(__fmul_rn(v[2 * i], lo_f(g[i])), r);
+                v[2 * i + 1] = over_odd(__fmul_rn(v[2 * i + 1], hi_f(g[i])), r);
             }
         }
         uint32_t code[2];
@@ -276,7 +285,7 @@ cudaError_t launch_append4(const latent4_append_t &a, int sms, cudaStream_t stre
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(units, sms, stream, &attr);
     latent4_append_t arg = a;
-    Norm norm = {two(1.0 / a.latent), two(a.eps)};
+    Norm norm = {1.0f / static_cast<float>(a.latent), two(a.eps)};
     void *args[] = {&arg, &units, &groups, &norm};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&append4_kernel), args);
 }

@@ -41,8 +41,8 @@ extern "C" {
  *     key part       =   rotate(key_rope[t], positions[t])
  * and, for every token when query_rope is given, query[t][h][latent .. ) =
  * rotate(query_rope[t][h], positions[t]). The norm x * weight / sqrt(mean(x^2) + eps)
- * is carried to about 2^-44 (pairs of floats) and rounded to 4 bits once, so the
- * codes are those of exact arithmetic; sums of squares past 2^127 read back as NaN.
+ * is carried to about 2^-44 (pairs of floats; exactly where it is a number of few
+ * digits) and rounded to 4 bits once, so the codes are those of exact arithmetic; sums of squares past 2^127 read back as NaN.
  * eps is a double: as a float it would already move values next to a border.
  *
  * cache          device bytes, row r at cache + r * cache_stride; 32-byte aligned,

@@ -7,7 +7,8 @@ import torch
 import exact_bf16_top_gb300 as tk
 import latent4_ref as Q
 import latent_ref as R
-from test_latent_gpu import ROPE, clean_status, gen  # noqa: F401
+from test_latent4_gpu import check_append
+from test_latent_gpu import ROPE, clean_status, gen, normal  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -27,7 +28,8 @@ def check_large(query, cache, scale, latent, selected=None, valid=None, table=No
         out, lse = tk.latent4_attend_selected(query, cache, selected, scale, latent=latent, lse=True)
         visible = R.visible_selected(selected, cache.shape[0])
     else:
-        out, lse = tk.latent4_attend_paged(query, cache, valid, table, scale, rows_per_request=q, latent=latent, lse=True)
+        out, lse = tk.latent4_attend_paged(query, cache, valid, table, scale, rows_per_request=q, latent=latent,
+                                           lse=True)
         visible = R.visible_paged(valid, table, table.shape[1] * 64, 64, 64, q, cache.shape[0])
     values = Q.unpack(cache, latent)
     ref, rl, _, _ = Q.attend(query, values, visible, scale, latent)
@@ -112,3 +114,68 @@ def test_large_scores_whose_last_bit_is_odd(heads, power):
         check_forms(query, cache, latent, order)
         check_large(query, cache, LN2, latent, selected=order[:100].int().repeat(4, 1))
         query.neg_()
+
+
+# ------------------------------------------------------------------ values next to borders and on them
+
+def row_of_squares(latent, total):
+    """Whole numbers, the first 64 of them 1 or -1, whose squares add up to `total`."""
+    row = [1.0 if i % 3 else -1.0 for i in range(64)]
+    left = total - 64
+    while left:
+        assert len(row) < latent
+        row.append(float(min(int(left ** 0.5), 200)))
+        left -= int(row[-1]) ** 2
+    return row + [0.0] * (latent - len(row))
+
+
+@pytest.mark.parametrize("latent", [128, 256, 384, 512])
+@pytest.mark.parametrize("root", [6, 7, 9, 10, 11, 12, 13, 15, 18, 20, 21, 25, 27, 31])
+def test_append_norms_that_are_fractions(latent, root):
+    # The norm of a row is exactly root / 8 (times a power of two), and weights are that times a border: each value is
+    # a tie, or a tie of its block's scale.
+    weight = torch.zeros(latent, dtype=torch.float64)
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]).double()
+    weight[:16], weight[16:32] = border.repeat(2), border.repeat(2) * 2.0 ** -3
+    weight[32], weight[48] = 6 * 1.0625, 6 * 1.3125
+    weight *= root / 8
+    weight[weight.to(torch.bfloat16).double() != weight] = 0         # (a border times this root has too many digits)
+    assert (weight != 0).sum() >= 32
+    x = torch.tensor(row_of_squares(latent, latent * root * root // 64)).double()
+    x = x * torch.exp2(torch.arange(-9.0, 10.0).double())[:, None]
+    assert torch.equal(x.to(torch.bfloat16).double(), x)
+    check_append(x.to(torch.bfloat16).cuda(), weight.to(torch.bfloat16).cuda(), 0.0, root)
+
+
+def next_to_borders():
+    """(weight, border, eps): weight / sqrt(1 + eps) is a sixteenth to seven of a float's step from the border, and so
+    that the product with the two nearest floats' sum for the root's reciprocal, rounded to odd, lies beyond it."""
+    found = []
+    for border in (1.25, 1.75, 2.5, 3.5, 5.0, 6.375, 7.125, 7.875):
+        for w in range(128, 1024):
+            w = w / 128 if w < 256 else w // 2 / 64 if w < 512 else w // 4 / 32
+            for i in (-7, -5, -3, -2, -1, 1, 2, 3, 5, 7):
+                eps = (w / (border * (1 + i / 16 * 2.0 ** -23))) ** 2 - 1
+                if eps <= 0:
+                    continue
+                over = torch.tensor((1 + eps) ** -0.5, dtype=torch.float64)
+                high = over.float()
+                v = w * high
+                rest = w * over - v.double()
+                bits = v.view(torch.int32).item()
+                if rest != 0 and not bits & 1:
+                    bits += 1 if rest > 0 else -1
+                v = torch.tensor(bits, dtype=torch.int32).view(torch.float32).item()
+                if (v > border) != (w * over.item() > border):
+                    found.append((w, border, eps))
+    return sorted(set(found))
+
+
+def test_append_values_next_to_borders():
+    cases = next_to_borders()
+    assert len(cases) >= 20
+    for w, border, eps in cases:
+        weight = torch.zeros(128, device="cuda")
+        weight[0] = w                        # (next to a border of its block's scale, where it is one)
+        weight[16], weight[17] = w, 6 * (1 + eps) ** 0.5      # (next to a border of codes under a scale of 1)
+        check_append(torch.ones(4, 128, dtype=torch.bfloat16, device="cuda"), weight.to(torch.bfloat16), eps, 3)
