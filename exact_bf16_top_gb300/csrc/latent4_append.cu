@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
+#include <cmath>
 
 #include "latent_rotate.cuh"
 
@@ -114,7 +115,29 @@ __device__ __forceinline__ uint32_t to_codes(const float (&v)[16], uint32_t (&co
 struct Norm {
     float over;                              // 1 / latent
     Two eps;
+    Two part;                                // eps = part * 4^power, part in [1, 4)
+    int32_t power;
 };
+
+// Mean squares plus eps between these are as exact as what follows: no square, remainder
+// or product of the norm that counts is below the least float. A row outside them is
+// scaled by a power of two first.
+constexpr float LEAST_MEAN = 0x1p-60f, MOST_MEAN = 0x1p100f;
+
+// Brings a row's largest value, or the root of eps where that is larger, to [1, 2), exactly
+// (a lane's 16 values), and returns what eps is then.
+__device__ __forceinline__ Two scale_row(float (&v)[16], const Norm &norm) {
+    int32_t field = 127 + norm.power;        // exponent fields
+#pragma unroll
+    for (int i = 0; i < 16; ++i) field = max(field, static_cast<int32_t>(__float_as_uint(v[i]) >> 23 & 0xFFu));
+    field = min(max(__reduce_max_sync(FULL, field), 1), 253);
+    const float by = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], by);
+    const int32_t up = norm.power + 127 - field;
+    const float f = up < -60 ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 + 2 * min(up, 60)) << 23);
+    return {__fmul_rn(norm.part.hi, f), __fmul_rn(norm.part.lo, f)};
+}
 
 // One warp per unit of work, as in the BF16 form: a token's cache row (a block of 16
 // values that share a scale per lane, so that none of the rounding crosses lanes), or
@@ -165,17 +188,25 @@ __global__ void __launch_bounds__(NT) append4_kernel(const latent4_append_t a, u
             v[2 * i + 1] = hi_f(b[i]);
         }
         if (a.weight) {
-            Two sums[4];                     // (squares of BF16 are exact; four sums side by side)
+            Two mean, eps = norm.eps;
+#pragma unroll 1
+            for (bool scaled = false;; scaled = true) {
+                Two sums[4];                 // (squares that count are exact; four sums side by side)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const Two square = {__fmul_rn(v[i], v[i]), 0.0f};
-                sums[i % 4] = i < 4 ? square : add(sums[i % 4], square);
+                for (int i = 0; i < 16; ++i) {
+                    const Two square = {__fmul_rn(v[i], v[i]), 0.0f};
+                    sums[i % 4] = i < 4 ? square : add(sums[i % 4], square);
+                }
+                Two sum = add(add(sums[0], sums[1]), add(sums[2], sums[3]));
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    sum = add(sum, {__shfl_xor_sync(FULL, sum.hi, o), __shfl_xor_sync(FULL, sum.lo, o)});
+                mean = add(share(sum, static_cast<float>(a.latent), norm.over), eps);
+                const bool fine = (mean.hi >= LEAST_MEAN && mean.hi <= MOST_MEAN) || !(sum.hi <= FLT_MAX);
+                if (scaled || __all_sync(FULL, fine)) [[likely]] break;   // (a sum that overflows stays so: NaN)
+                eps = scale_row(v, norm);
             }
-            Two sum = add(add(sums[0], sums[1]), add(sums[2], sums[3]));
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                sum = add(sum, {__shfl_xor_sync(FULL, sum.hi, o), __shfl_xor_sync(FULL, sum.lo, o)});
-            const Root r = root(add(share(sum, static_cast<float>(a.latent), norm.over), norm.eps));
+            const Root r = root(mean);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[2 * i] = over_odd(__fmul_rn(v[2 * i], lo_f(g[i])), r);
@@ -285,7 +316,12 @@ cudaError_t launch_append4(const latent4_append_t &a, int sms, cudaStream_t stre
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(units, sms, stream, &attr);
     latent4_append_t arg = a;
-    Norm norm = {1.0f / static_cast<float>(a.latent), two(a.eps)};
+    int at = 0;
+    (void)std::frexp(a.eps, &at);            // eps in [2^(at - 1), 2^at)
+    const bool some = a.eps != 0.0 && std::isfinite(a.eps);
+    const int32_t power = some ? (at - 1 - ((at - 1) & 1)) / 2 : -1000;
+    Norm norm = {1.0f / static_cast<float>(a.latent), two(a.eps),
+                 two(some ? std::ldexp(a.eps, -2 * power) : a.eps), power};
     void *args[] = {&arg, &units, &groups, &norm};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&append4_kernel), args);
 }

@@ -179,3 +179,41 @@ def test_append_values_next_to_borders():
         weight[0] = w                        # (next to a border of its block's scale, where it is one)
         weight[16], weight[17] = w, 6 * (1 + eps) ** 0.5      # (next to a border of codes under a scale of 1)
         check_append(torch.ones(4, 128, dtype=torch.bfloat16, device="cuda"), weight.to(torch.bfloat16), eps, 3)
+
+
+# ------------------------------------------------------------------ norms of very small and very large rows
+
+@pytest.mark.parametrize("latent", [128, 384, 512])
+@pytest.mark.parametrize("power", [-133, -126, -120, -100, -80, -75, -64, -60, -50, -30, 30, 48, 52, 56])
+def test_append_norms_of_any_size(power, latent):
+    # Codes are those of exact arithmetic (check_append): rows of numbers of any size, with an eps of none, one that is
+    # as large as their mean square and others far from it on either side.
+    g = gen(latent + power)
+    x = (normal(g, 60, latent).double() * 2.0 ** power).to(torch.bfloat16)
+    x[5, 3:] = 0
+    x[5, :3] = 2.0 ** power
+    x[6] = 0
+    x[6, latent - 1] = -(2.0 ** power)
+    weight = (normal(g, latent).float() * 3).to(torch.bfloat16)
+    if power <= -126:
+        x[x.abs().amax(1) == 0, 0] = 2.0 ** -133                # (no row of zeros)
+    for eps in (0.0, 2.0 ** (2 * power), 2.0 ** (2 * power - 40), 3.0 * 2.0 ** (2 * power + 9), 1e-6):
+        check_append(x, weight, eps, power + 200)
+
+
+def test_append_norms_next_to_borders_at_any_size():
+    # Rows of +-2^i whose norm is exactly one: with weights that are borders, every value is a tie.
+    g = gen(16)
+    x = torch.where(torch.rand(190, 512, generator=g, device="cuda") < 0.5, -1.0, 1.0).double()
+    x = (x * torch.exp2(torch.arange(190, device="cuda").double()[:, None] - 133)).to(torch.bfloat16)
+    weight = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 64, device="cuda").to(torch.bfloat16)
+    check_append(x, weight, 0.0, 17)
+
+
+def test_append_an_eps_far_above_its_rows():
+    # x / sqrt(eps) of ordinary size needs an eps of the size of x^2; larger ones take the values to zero.
+    g = gen(18)
+    for power in (40, 56):
+        x = (normal(g, 40, 256).double() * 2.0 ** power).to(torch.bfloat16)
+        for eps in (2.0 ** (2 * power), 2.0 ** (2 * power + 8), 2.0 ** 127, 2.0 ** 130, 2.0 ** 200):
+            check_append(x, torch.full((256,), 3.0, device="cuda").to(torch.bfloat16), eps, 19)
