@@ -239,10 +239,14 @@ def _attend(form, paged, dev, query, cache, scale, latent, out, lse, workspace, 
     elif not (out.dtype is _BF16 and out.device == device and out.shape == (tokens, heads, latent)
               and out.is_contiguous()):
         raise ValueError("out must be a contiguous bfloat16 [tokens, heads, latent] on the query's device")
+    elif out.requires_grad:
+        _check_no_grad()
     if not isinstance(lse, torch.Tensor):
         lse = torch.empty((tokens, heads), dtype=_F32, device=device) if lse else None
     elif not (lse.dtype is _F32 and lse.device == device and lse.shape == (tokens, heads) and lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [tokens, heads] on the query's device")
+    elif lse.requires_grad:
+        _check_no_grad()
     if workspace is not None and not (workspace.dtype is _U8 and workspace.device == device
                                       and workspace.is_contiguous()):
         raise ValueError("workspace must be a uint8 tensor from latent_workspace() on the query's device")

@@ -217,3 +217,36 @@ def test_append_an_eps_far_above_its_rows():
         x = (normal(g, 40, 256).double() * 2.0 ** power).to(torch.bfloat16)
         for eps in (2.0 ** (2 * power), 2.0 ** (2 * power + 8), 2.0 ** 127, 2.0 ** 130, 2.0 ** 200):
             check_append(x, torch.full((256,), 3.0, device="cuda").to(torch.bfloat16), eps, 19)
+
+
+# ------------------------------------------------------------------ outputs that record a gradient
+
+@pytest.mark.parametrize("form", ["bf16", "4 bits"])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("which", ["out", "lse"])
+def test_attention_refuses_outputs_that_record_a_gradient(form, paged, which):
+    g = gen(1)
+    query = normal(g, 2, 3, 128 + ROPE)
+    cache = Q.random_cache(g, 64, 128) if form == "4 bits" else normal(g, 64, 128 + ROPE)
+    rows = torch.arange(64, dtype=torch.int32, device="cuda").expand(2, 64).contiguous()
+    valid, table = torch.tensor([64, 64], dtype=torch.int32, device="cuda"), rows[:1, :1].contiguous()
+    given = {"out": torch.zeros(2, 3, 128, dtype=torch.bfloat16, device="cuda"),
+             "lse": torch.zeros(2, 3, device="cuda")}
+
+    def call(**kw):
+        name = "latent4" if form == "4 bits" else "latent"
+        if paged:
+            return getattr(tk, f"{name}_attend_paged")(query, cache, valid, table, 0.1, latent=128, rows_per_request=2,
+                                                       **kw)
+        return getattr(tk, f"{name}_attend_selected")(query, cache, rows, 0.1, latent=128, **kw)
+
+    given[which].requires_grad_()
+    with pytest.raises(ValueError):
+        call(**given)
+    assert not given["out"].any() and not given["lse"].any()
+    with torch.no_grad():
+        call(**given)
+    want = call(lse=True)
+    assert torch.equal(given["out"], want[0]) and torch.equal(given["lse"], want[1])
+    given[which].requires_grad_(False)
+    call(**given)                            # (an output of its own that records none is taken)
