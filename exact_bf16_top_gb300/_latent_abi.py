@@ -35,7 +35,8 @@ class PageStep(ctypes.Structure):
     _fields_ = [("block_table", _P), ("table_stride", _L), ("lengths", _P), ("new_tokens", _P), ("free_pages", _P),
                 ("free_count", _P), ("next_lengths", _P), ("next_free_count", _P), ("granted", _P),
                 ("positions", _P), ("slots", _P), ("valid_len", _P), ("requests", _I), ("pages", _I),
-                ("free_size", _I), ("page_size", _I), ("block_rows", _I), ("rows_per_request", _I)]
+                ("free_size", _I), ("page_size", _I), ("block_rows", _I), ("rows_per_request", _I),
+                ("held", ctypes.c_size_t)]      # an address, 0 for none: the one that may be missing
 
 
 def declare(lib) -> None:

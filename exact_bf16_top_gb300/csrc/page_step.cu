@@ -31,14 +31,20 @@ __device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t shift) {
     return static_cast<int32_t>((static_cast<uint32_t>(tokens) + (1u << shift) - 1u) >> shift);
 }
 
+// Pages that request r, of this many tokens, has before the step.
+__device__ __forceinline__ int32_t owned_by(const Params &p, int32_t r, int32_t length) {
+    const int32_t reached = pages_of(length, p.page_shift);
+    return p.a.held ? max(reached, min(p.a.held[r], p.a.pages)) : reached;
+}
+
 __device__ __forceinline__ Request request_at(const Params &p, int32_t r) {
     const int32_t width = p.a.pages << p.page_shift, ask = p.a.new_tokens[r];
     Request x;
     x.length = min(max(p.a.lengths[r], 0), width);
-    x.owned = pages_of(x.length, p.page_shift);
+    x.owned = owned_by(p, r, x.length);
     x.add = min(max(ask, 0), p.a.rows_per_request);
     if (x.add > width - x.length) x.add = 0;
-    x.need = pages_of(x.length + x.add, p.page_shift) - x.owned;
+    x.need = max(pages_of(x.length + x.add, p.page_shift) - x.owned, 0);
     x.done = ask < 0;
     x.back = x.done ? x.owned : 0;
     return x;
@@ -46,8 +52,8 @@ __device__ __forceinline__ Request request_at(const Params &p, int32_t r) {
 
 // Every CTA of the (one) cluster goes over all requests, NT at a time: a prefix
 // sum of the pages they need, of which its own rows take theirs; so no CTA waits for
-// another's sums. What other CTAs still read (lengths, the count, the stack's top)
-// is written after the cluster's barrier, which is what makes the call work in
+// another's sums. What other CTAs still read (lengths, held pages, the count, the stack's
+// top) is written after the cluster's barrier, which is what makes the call work in
 // place without scratch of its own.
 // Bound by latency: two rounds of loads, a scan, what comes back to the stack and the
 // launch. 1 request of 1 token 2.7 us, 512 of 4 tokens with finished ones 7.9 us (a CTA's
@@ -55,7 +61,7 @@ __device__ __forceinline__ Request request_at(const Params &p, int32_t r) {
 __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ Params p) {
     extern __shared__ int32_t own[];         // the CTA's requests: next length, or ~ the place of the first page back
     __shared__ uint32_t s_first[NT];
-    __shared__ int32_t s_length[NT], s_add[NT], s_need[NT / 32], s_back[NT / 32], s_taken;
+    __shared__ int32_t s_length[NT], s_owned[NT], s_add[NT], s_need[NT / 32], s_back[NT / 32], s_taken;
     const page_step_t &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t ctas = static_cast<int32_t>(gridDim.x), rank = static_cast<int32_t>(blockIdx.x);
@@ -97,6 +103,7 @@ __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ P
         s_first[tid] = static_cast<uint32_t>(count) - 1u - static_cast<uint32_t>(need - x.need) +
                        static_cast<uint32_t>(x.owned);
         s_length[tid] = x.length;
+        s_owned[tid] = x.owned;
         s_add[tid] = add;
         if (r >= r0 && r < r1) {
             a.granted[r] = add;
@@ -110,8 +117,8 @@ __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ P
             const int32_t i = static_cast<int32_t>(in / static_cast<uint32_t>(q)), j = static_cast<int32_t>(in - i * q);
             int32_t pos = 0, slot = -1, valid = 0;
             if (j < s_add[i]) {
-                const int32_t length = s_length[i], owned = pages_of(length, p.page_shift);
-                pos = length + j;
+                const int32_t owned = s_owned[i];
+                pos = s_length[i] + j;
                 valid = pos + 1;
                 const int32_t at = pos >> p.page_shift, offset = pos & ((1 << p.page_shift) - 1);
                 int32_t *entry = a.block_table + (base + i) * a.table_stride + at;
@@ -141,10 +148,11 @@ __global__ void __launch_bounds__(NT) page_step_kernel(const __grid_constant__ P
             const int32_t next = own[r - r0];
             if (next < 0) {
                 const int32_t width = a.pages << p.page_shift;
-                back = pages_of(min(max(a.lengths[r], 0), width), p.page_shift);
+                back = owned_by(p, r, min(max(a.lengths[r], 0), width));
                 first = ~next;
             }
             a.next_lengths[r] = max(next, 0);
+            if (a.held) a.held[r] = next < 0 ? 0 : owned_by(p, r, next);
         }
         for (uint32_t m = __ballot_sync(FULL, back > 0); m; m &= m - 1) {
             const int from = __ffs(m) - 1;
@@ -179,7 +187,7 @@ topk_status_t check(const page_step_t *a) {
                           static_cast<const void *>(a->free_count), static_cast<const void *>(a->next_lengths),
                           static_cast<const void *>(a->next_free_count), static_cast<const void *>(a->granted),
                           static_cast<const void *>(a->positions), static_cast<const void *>(a->slots),
-                          static_cast<const void *>(a->valid_len)})
+                          static_cast<const void *>(a->valid_len), static_cast<const void *>(a->held)})
         if (reinterpret_cast<uintptr_t>(v) & 3u) return TOPK_ERR_ALIGN;
     return TOPK_OK;
 }

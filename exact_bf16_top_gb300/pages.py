@@ -40,7 +40,7 @@ def _vector(t, n: int, dev: int) -> bool:
 
 def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_per_request: int = 1,
               page_size: int = 64, block_rows: int | None = None, next_lengths=None, next_free_count=None,
-              stream=None) -> PageStep:
+              held=None, stream=None) -> PageStep:
     """Takes a batch's page tables one step further (page_step) -> PageStep.
 
     block_table: CUDA int32 [requests, pages], request r's first ceil(lengths[r]
@@ -57,6 +57,12 @@ def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_
     (default page_size). Row r * rows_per_request + j is request r's j-th new
     token: position lengths[r] + j, its slot, valid length position + 1; rows past
     granted[r] are padding (0, -1, 0), which the other operators leave out.
+
+    held: None, or int32 [requests], the pages that each request has, updated in
+    place (zeros to begin with will do). It is needed where lengths are lowered
+    between steps (drafted tokens that were rejected): a page behind a request's
+    last token stays its own, to be used next. Without it a request has what its
+    length says, and such a page would be nobody's.
     """
     try:
         dev = block_table.get_device()
@@ -97,18 +103,20 @@ def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_
         next_free_count = free_count
     elif not _vector(next_free_count, 1, dev):
         raise ValueError("next_free_count must be a contiguous int32 [1] on the tables' device")
+    if held is not None and not _vector(held, n, dev):
+        raise ValueError("held must be a contiguous int32 [requests] on the tables' device")
     if stream is not None:
         _check_stream(stream, dev)
     if _raw_device() != dev:
         with torch.cuda.device(dev):
             return page_step(block_table, lengths, new_tokens, free_pages, free_count, rows_per_request=q,
                              page_size=page_size, block_rows=block_rows, next_lengths=next_lengths,
-                             next_free_count=next_free_count, stream=stream)
+                             next_free_count=next_free_count, held=held, stream=stream)
     if stream is not None and stream != torch.cuda.current_stream(dev):
         with torch.cuda.stream(stream):     # new tensors belong to the stream that uses them
             return page_step(block_table, lengths, new_tokens, free_pages, free_count, rows_per_request=q,
                              page_size=page_size, block_rows=block_rows, next_lengths=next_lengths,
-                             next_free_count=next_free_count)
+                             next_free_count=next_free_count, held=held)
     rows = n * q
     device = block_table.device
     positions, slots = torch.empty(rows, dtype=_I32, device=device), torch.empty(rows, dtype=_I32, device=device)
@@ -116,7 +124,7 @@ def page_step(block_table, lengths, new_tokens, free_pages, free_count, *, rows_
     args = _Args(block_table.data_ptr(), stride if n > 1 else pages, lengths.data_ptr(), new_tokens.data_ptr(),
                  free_pages.data_ptr(), free_count.data_ptr(), next_lengths.data_ptr(), next_free_count.data_ptr(),
                  granted.data_ptr(), positions.data_ptr(), slots.data_ptr(), valid_len.data_ptr(), n, pages, size,
-                 page_size, block_rows, q)
+                 page_size, block_rows, q, 0 if held is None else held.data_ptr())
     status = (_package._lib or load()).page_step(args, _raw_stream(dev))
     if status:
         raise TopkError(status)

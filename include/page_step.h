@@ -25,6 +25,13 @@
  * with `page` the table's new entry position / page_size; else (a padded row) 0, -1
  * and 0: such a row is not appended and sees nothing. A slot past 31 bits or of a
  * negative page is -1.
+ *
+ * Lengths that go down between steps (drafted tokens that were rejected) need `held`:
+ * how many pages each request has. A request then has max(held, ceil(length /
+ * page_size)) pages: one behind its last token stays its own, is used before any of
+ * the stack, and goes back when the request is finished. Without `held` a request has
+ * what its length says, and a page that a lowered length no longer reaches would be in
+ * nobody's hands.
  */
 #ifndef PAGE_STEP_H
 #define PAGE_STEP_H
@@ -52,11 +59,13 @@ extern "C" {
  * granted           device int32 [requests]: tokens that a request got (0: refused,
  *                   finished or none asked for).
  * positions, slots, valid_len   device int32 [requests * rows_per_request].
+ * held              NULL, or device int32 [requests], clamped to [0, pages]: pages that
+ *                   each request has, updated in place (zeros to begin with will do).
  * page_size is a power of two, block_rows >= page_size. No other overlap of what is
  * written with anything else is allowed. Pages that come back past free_size are
  * dropped (they were never taken from this stack).
  *
- * Errors: TOPK_ERR_ARG (null pointer, negative count, more than
+ * Errors: TOPK_ERR_ARG (null pointer but for held, negative count, more than
  * PAGE_STEP_MAX_REQUESTS, a bad page size, block_rows, table stride or
  * rows_per_request, requests * pages or requests * rows_per_request past 31 bits),
  * TOPK_ERR_WIDTH (pages * page_size past PAGE_STEP_MAX_WIDTH), TOPK_ERR_ALIGN,
@@ -70,6 +79,7 @@ typedef struct {
     const int32_t *free_count;
     int32_t *next_lengths, *next_free_count, *granted, *positions, *slots, *valid_len;
     int32_t requests, pages, free_size, page_size, block_rows, rows_per_request;
+    int32_t *held;
 } page_step_t;
 
 topk_status_t page_step(const page_step_t *args, void *stream);

@@ -121,6 +121,12 @@ def test_step_refuses(lib, kw, status):
     assert lib.page_step(step_args(**kw), None) == status
 
 
+def test_step_held_may_be_missing_but_not_misaligned(lib):
+    assert PageStep().held == 0
+    assert lib.page_step(step_args(held=4098), None) == 2
+    assert lib.page_step(step_args(held=4096, lengths=None), None) == 1
+
+
 def test_nothing_to_do_and_no_arguments(lib):
     assert lib.latent4_append(append_args(tokens=0, cache=None, latents=None), None) == 0
     assert lib.latent4_attend_selected(attend_args(tokens=0, query=None, out=None), None) == 0
