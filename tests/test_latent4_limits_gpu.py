@@ -8,7 +8,7 @@ import exact_bf16_top_gb300 as tk
 import latent4_ref as Q
 import latent_ref as R
 from test_latent4_gpu import check_append
-from test_latent_gpu import ROPE, clean_status, gen, normal  # noqa: F401
+from test_latent_gpu import ROPE, SCALE, angles, clean_status, gen, normal  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +250,48 @@ def test_attention_refuses_outputs_that_record_a_gradient(form, paged, which):
     assert torch.equal(given["out"], want[0]) and torch.equal(given["lse"], want[1])
     given[which].requires_grad_(False)
     call(**given)                            # (an output of its own that records none is taken)
+
+
+# ------------------------------------------------------------------ caches past 4 GB
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+def test_pages_past_32_bit_offsets(page):
+    # 5 GB of cache, whole pages: the last 320 rows' bytes lie past 2^32. (Pages of 16 come by copies of rows, of 32 and
+    # 64 by boxes.)
+    rows, latent, edge = 12_500_032, 512, 320
+    assert rows % 64 == 0 and (rows - edge) * 416 > 2 ** 32
+    cache = torch.empty(rows, 416, dtype=torch.uint8, device="cuda")
+    g = gen(page)
+    cache[-edge:], cache[:edge] = Q.random_cache(g, edge, latent), Q.random_cache(g, edge, latent)
+    small = torch.cat((cache[:edge], cache[-edge:]))
+    n, last = edge // page, rows // page - edge // page
+    width = 240 // page
+    near = torch.randint(0, n, (2, width), generator=g, device="cuda").int()
+    table = torch.where(torch.arange(width, device="cuda") % 2 == 0, last + near, near)
+    moved = torch.where(table >= last, table - last + n, table)
+    valid = torch.tensor([width * page - 7, width * page, 150, 151], dtype=torch.int32, device="cuda")
+    for heads in (16, 64):
+        query = normal(g, 4, heads, 576)
+        out, lse = tk.latent4_attend_paged(query, cache, valid, table, SCALE, lse=True, rows_per_request=2,
+                                           page_size=page)
+        ref, rl, tol, tl = Q.attend(query, Q.unpack(small, latent),
+                                    R.visible_paged(valid, moved, width * page, page, page, 2, 2 * edge), SCALE, latent)
+        R.assert_close(out, ref, tol, "out")
+        R.assert_close(lse, rl, tl, "lse")
+    # What an append writes there: codes, scales and key parts, as in rows 0 and 1 and nothing beside them.
+    slot = torch.tensor([rows - 1, 0, rows - edge, 1], dtype=torch.int32, device="cuda")
+    x, key = normal(g, 4, latent), normal(g, 4, ROPE)
+    tk.latent4_append(cache, x, key, torch.zeros_like(slot), angles(2), slot)
+    to = torch.where(slot >= edge, slot - rows + 2 * edge, slot).long()
+    code, scale = Q.quantise(x.double())
+    got = torch.cat((cache[:edge], cache[-edge:]))
+    held = Q.unpack(got, latent)
+    level = torch.tensor(Q.LEVELS, dtype=torch.float64, device="cuda")[code]
+    want = torch.where(x < 0, -level, level) * Q.e4m3(scale).repeat_interleave(16, 1)
+    assert torch.equal(held[to, :latent], want)
+    assert torch.equal(held[to, latent:], key.double())         # (position 0 turns by nothing)
+    assert torch.equal(got[to, 384:].long(), scale)
+    assert torch.equal(tk.latent4_rows(cache, slot).double(), held[to])
+    rest = torch.ones(2 * edge, dtype=torch.bool, device="cuda")
+    rest[to] = False
+    assert torch.equal(got[rest], small[rest])
