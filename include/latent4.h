@@ -16,9 +16,13 @@
  *
  * Rounding to 4 bits, per 16 values v: s = e4m3(max |v| / 6), at least 2^-9 and at
  * most 448, and code = e2m1(v / s), both to the nearest, ties to the even code, past
- * 6 the largest. So values are off by at most s / 4 where |v| <= 2 s, s / 2 where
- * |v| <= 4 s and s above (with s rounded down, the largest may be off by up to 0.43 s
- * more: a / s <= 6.4). Sixteen values of which one is NaN or infinite read back as NaN.
+ * 6 the largest. With s from 2^-6 on and max |v| up to 2688 values are off by at most
+ * s / 4 where |v| <= 2 s, s / 2 where |v| <= 4 s and s above, where the largest is at
+ * most 6.375 s. Scales below 2^-6 are 2^-9 apart, so there the largest may be 9 s and off
+ * by 3 s; values below s / 4 become zero (below 2^-11 in any case), and values past 2688
+ * become 2688. A cache whose values are that small or large is better held times a
+ * power of two: as part of `weight`, taken out again of the query's latent part and of
+ * the outputs. Sixteen values of which one is NaN or infinite read back as NaN.
  */
 #ifndef LATENT4_H
 #define LATENT4_H

@@ -295,3 +295,36 @@ def test_pages_past_32_bit_offsets(page):
     rest = torch.ones(2 * edge, dtype=torch.bool, device="cuda")
     rest[to] = False
     assert torch.equal(got[rest], small[rest])
+
+
+# ------------------------------------------------------------------ what 4 bits keep
+
+def test_append_errors_are_within_the_stated_bounds():
+    # Per 16 values with the largest of size a, scale s. s of 2^-6 to 448 and a of 2688 at most: off by s / 4 up to 2 s,
+    # s / 2 up to 4 s, s above, 0.375 s the largest. Smaller scales: s / 4 and s / 2 as before, 3 s at most (s of
+    # 2^-9 stands for a up to 9 s). Past 2688: the largest value is 2688.
+    g, latent, n = gen(3), 512, 4000
+    x = normal(g, n, latent).double() * torch.exp2(torch.rand(n, 1, generator=g, device="cuda").double() * 24 - 14)
+    x[::2] = torch.rand(x[::2].shape, generator=g, device="cuda").double() * x[::2].abs().amax(1, keepdim=True)
+    at = torch.arange(1, 513, device="cuda").double()
+    x[1] = at * 2.0 ** -13                                       # blocks around every one of the small scales
+    x[3] = (at * 6 + 3) * 2.0 ** -11
+    x[5, ::16] = torch.linspace(2500, 3000, 32, device="cuda").double()
+    x = x.to(torch.bfloat16)
+    cache = torch.zeros(n, 416, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    tk.latent4_append(cache, x, normal(g, n, ROPE), slots, angles(2), slots)
+    held = Q.unpack(cache, latent)[:, :latent].view(n, 32, 16)
+    s = Q.e4m3(cache[:, 384:])[..., None]
+    v = x.double().view(n, 32, 16)
+    size, off = v.abs(), (held - v).abs()
+    a = size.amax(2, keepdim=True)
+    normal_scale = (s >= 2.0 ** -6) & (a <= 2688)
+    above = torch.where(normal_scale, torch.where(size == a, torch.where(size > 6 * s, 0.375 * s, s), s), 3 * s)
+    bound = torch.where(size <= 2 * s, s / 4, torch.where(size <= 4 * s, s / 2, above))
+    bound = torch.where((size > 6 * s) & (a > 2688), size - 2688, bound)
+    assert (off <= bound).all()
+    for kind in (normal_scale, s < 2.0 ** -6, a > 2688):
+        assert kind.sum() > 20
+    small = (s < 2.0 ** -6).expand_as(size)
+    assert (off[small] > 2 * s.expand_as(size)[small]).any()     # (the bound of ordinary scales does not hold there)
