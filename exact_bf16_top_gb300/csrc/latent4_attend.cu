@@ -264,7 +264,7 @@ __device__ __forceinline__ void load_query(const AttendParams &p, const Tile &ti
         const uint32_t up = min(262u - (most >> 7), 253u);       // exponent field of the factor: 2^(8 - exponent)
         const float by = __uint_as_float(up << 23);
         if (piece == 0) {
-            const float u = p.scale * LOG2E * __uint_as_float((254u - up) << 23);
+            const float u = p.scale * __uint_as_float((254u - up) << 23) * LOG2E;   // (so no scale overflows)
             c.unit[r] = fminf(fmaxf(u, -FLT_MAX), FLT_MAX);
         }
 #pragma unroll 1

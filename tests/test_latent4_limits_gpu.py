@@ -7,7 +7,7 @@ import torch
 import exact_bf16_top_gb300 as tk
 import latent4_ref as Q
 import latent_ref as R
-from test_latent4_gpu import check_append
+from test_latent4_gpu import check_append, check_selected, selected_case
 from test_latent_gpu import ROPE, SCALE, angles, clean_status, gen, normal  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -114,6 +114,15 @@ def test_large_scores_whose_last_bit_is_odd(heads, power):
         check_forms(query, cache, latent, order)
         check_large(query, cache, LN2, latent, selected=order[:100].int().repeat(4, 1))
         query.neg_()
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_the_largest_scales(heads):
+    # Queries of the least BF16 values with scales up to float32's largest: scores of ordinary size.
+    query, cache, sel = selected_case(2, heads, 256, 300, 900, 6)
+    query = (query.double() * 2.0 ** -130).to(torch.bfloat16)
+    for scale in (2.0 ** 126, 2.3e38, 2.5e38, -3.3e38, (2 - 2.0 ** -23) * 2.0 ** 127):
+        check_selected(query, cache, sel, 256, scale=torch.tensor(scale).float().item())
 
 
 # ------------------------------------------------------------------ values next to borders and on them
