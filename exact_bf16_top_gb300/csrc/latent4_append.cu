@@ -144,9 +144,10 @@ __device__ __forceinline__ Two scale_row(float (&v)[16], const Norm &norm) {
 // up to 16 of a token's query heads. The sum of squares and the norm are pairs of
 // floats: a value next to a border of 4 bits takes the side that exact arithmetic
 // gives it, whatever the order of the sums. Bound by that arithmetic: 8191 tokens of 512
-// values 8.4 us with the norm, 5.1 without (15 MB either way); with 16 heads' queries
-// (another 38 MB) 11.2. (By divisions and with one chain of sums 9.5 instead of 8.4.) One
-// token 2.2 us: the launch and two rounds of loads.
+// values 8.9 us with the norm, 4.7 without (15 MB either way); with 16 heads' queries
+// (another 34 MB) 13.8 and 10.6. (Products with a reciprocal in two parts took 0.6 us less,
+// and the wrong side of some borders; by divisions and with one chain of sums the rows took
+// 1.1 more.) One token 2.0 us: the launch and two rounds of loads.
 __global__ void __launch_bounds__(NT) append4_kernel(const latent4_append_t a, uint32_t units, uint32_t groups,
                                                      const Norm norm) {
     grid_dependents_release();

@@ -17,8 +17,9 @@
 // rows in BF16 82 us), 128 tokens x 16 heads x 2048 listed rows 48 us (2.4 TB/s; 55), a
 // chunk of 509 tokens x 128 heads on 9000 rows 1.42 ms (0.88 PFLOP/s; 1.20 ms). Neither
 // memory nor the tensor cores nor the issue slots are full: a block takes 4000 to 5500
-// cycles. With few query rows that is the time of the warps that send for its rows
-// (converters wait for them 1800 to 2400 cycles a block, they hardly ever for a place).
+// cycles. With few query rows that is the time until its rows are there (converters wait
+// for them 1800 to 2400 cycles a block, the warps that send for them hardly ever for a
+// place; the copies' issue alone is a quarter of a block).
 // With 64 it is a loop: a block's last pairs find a place only when the sums of the one
 // before have read theirs, and its scores, softmax and sums come after. So where query
 // rows are many the rows in BF16 are faster; these take 36 % of the memory.
@@ -52,7 +53,8 @@ constexpr int KEY_SLOTS = 2;                 // blocks' key parts in tensor memo
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 // Weights are FP16 (at most 65504): the reference is set this far below the maximum and
 // moves when a weight passes 2^MOST, so that the largest weight of a row is 2^8 at least
-// and what FP16 rounds away below 2^-25 is less than 2^-33 of it. A move stops the sums
+// and what FP16 rounds away below 2^-25 is less than 2^-33 of it (1 at least for scores past
+// 2^27 in log2 units, whose next weights are 2^-16 and 2^-32). A move stops the sums
 // until they are rescaled, so the two lie far apart (chunk of 509 tokens x 128 heads, 2^11
 // and 2^15: 1565 us, 2^11 and 2^15.9: 1479, 2^8 and 2^15.9: 1430, 2^4: 1430).
 constexpr float BELOW = 8.0f, MOST = 15.9f;

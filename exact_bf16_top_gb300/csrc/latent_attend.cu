@@ -10,14 +10,14 @@
 // it), and 16 rows cost little more than their share. Warps have one job each
 // (softmax, copies, issue of either product) and meet at mbarriers only.
 //
-// What bounds it. Few heads: DRAM (32 requests x 16 heads x up to 16384 tokens: 85
-// us, 5.2 TB/s). 64 rows a tile: shared memory. A block's operands leave it 36 x 4
+// What bounds it. Few heads: DRAM (32 requests x 16 heads x up to 16384 tokens: 83
+// us, 5.3 TB/s). 64 rows a tile: shared memory. A block's operands leave it 36 x 4
 // KB (scores) and 16 x 6 KB (sums) at 128 bytes a cycle and its rows come in once:
 // about 2500 cycles a block, what a chunk of 509 tokens x 128 heads over 9000 takes
-// (1.22 ms, 1.0 PFLOP/s; tensor pipes 66 % active). More rows a tile would halve
+// (1.20 ms, 1.0 PFLOP/s; tensor pipes 66 % active). More rows a tile would halve
 // that but neither their queries (74 KB for 64) nor their sums have room. Listed
 // rows (no TMA boxes) add the copies' latency: 3200 cycles a block at two blocks in
-// flight, tile ends included (512 tokens x 128 heads x 2048: 356 us).
+// flight, tile ends included (512 tokens x 128 heads x 2048: 359 us).
 
 #include <type_traits>
 
