@@ -47,8 +47,8 @@ extern "C" {
  * rotate(query_rope[t][h], positions[t]). The norm x * weight / sqrt(mean(x^2) + eps)
  * is carried to about 2^-44 (pairs of floats; exactly where it is a number of few
  * digits) and rounded to 4 bits once, so the codes are those of exact arithmetic, for
- * rows of any size down to the least BF16 values, with eps = 0 too (|weight| up to
- * 2^100). Sums of squares that overflow 32 bits (2^128) read back as NaN, and so do rows
+ * rows of any size down to the least BF16 values, with eps = 0 too (|weight| up to 2^60:
+ * past that x * weight may overflow). Sums of squares that overflow 32 bits (2^128) read back as NaN, and so do rows
  * of zeros with eps = 0. eps, at least 0, is a double: as a float it would already move
  * values next to a border.
  *

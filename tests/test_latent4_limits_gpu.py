@@ -219,6 +219,19 @@ def test_append_norms_next_to_borders_at_any_size():
     check_append(x, weight, 0.0, 17)
 
 
+@pytest.mark.parametrize("weight_power", [-60, -20, 20, 60])
+@pytest.mark.parametrize("power", [-133, -100, -61, -31, 0, 40, 51, 56])
+def test_append_weights_of_any_size(power, weight_power):
+    # What is too large for the scales stays at 448 * 6, what is too small is zero; products do not overflow on the way.
+    g = gen(power)
+    x = (normal(g, 40, 512).double() * 2.0 ** power).to(torch.bfloat16)
+    x[:, 0] = 2.0 ** max(power, -133)
+    weight = (normal(g, 512).double() * 2.0 ** (weight_power - 2)).clamp(-2.0 ** 60, 2.0 ** 60).to(torch.bfloat16)
+    weight[:64] = 2.0 ** -weight_power
+    for eps in (0.0, 2.0 ** (2 * power), 1e-6):
+        check_append(x, weight, eps, 21)
+
+
 def test_append_an_eps_far_above_its_rows():
     # x / sqrt(eps) of ordinary size needs an eps of the size of x^2; larger ones take the values to zero.
     g = gen(18)
